@@ -326,3 +326,20 @@ def sgemv_beam_traceback(parent, tok, count, seq, status=None, stream=None) -> N
     _check_tensor(seq, (beam_max, steps), "torch.int32", "seq")
     _check(_lib.sgemv_beam_traceback(steps, beam_max, _addr(parent), _addr(tok), _addr(count), _addr(seq),
                                      _addr(status), _stream(stream)), "sgemv_beam_traceback")
+
+
+# ---------------------------------------------------------------------------------------------- decode path
+
+_KV_NAMES = ("SGEMV_F16", "SGEMV_BF16", "SGEMV_F32", "KV_WORKSPACE", "EXPORTED_KV", "KvLayout", "KvQuery",
+             "sgemv_kv_layout_query", "sgemv_kv_plan", "sgemv_kv_append", "sgemv_kv_read", "sgemv_kv_attention",
+             "sgemv_logprobs", "kv_cache", "kv_workspace", "kv_attention", "logprobs")
+
+
+def __getattr__(name):
+    """The decode-path operators live in the module `kv`, which needs torch; it is imported on first use."""
+    if name in _KV_NAMES:
+        from . import kv
+        for n in _KV_NAMES:
+            globals()[n] = getattr(kv, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,258 @@
+"""Binding of the decode-path operators (include/sgemv_kv.h): the paged 4-bit KV cache and the
+log-probabilities of the head's logits.
+
+As in the package itself, each function carries the name of its C entry point and marshals arguments only:
+tensors are checked for type, shape and strides, and their addresses passed on. Nothing here allocates
+except the helpers `kv_cache`, `kv_workspace`, `kv_attention` and `logprobs`.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, _lib, _stream
+
+SGEMV_F16 = 0
+SGEMV_BF16 = 1
+SGEMV_F32 = 2
+
+KV_WORKSPACE = 32 << 20
+
+EXPORTED_KV = ("sgemv_kv_layout_query", "sgemv_kv_plan", "sgemv_kv_append", "sgemv_kv_read", "sgemv_kv_attention",
+               "sgemv_logprobs")
+
+_DTYPE = {torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32}
+
+
+class KvLayout(ctypes.Structure):
+    """sgemv_kv_layout: shape and byte layout of a paged 4-bit cache."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "dim", "group", "page", "n_pages", "reserved")] + \
+        [(n, ctypes.c_uint64) for n in ("sub_bytes", "head_bytes", "page_bytes", "total_bytes")]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_ if name != "reserved"}
+
+    def __repr__(self) -> str:
+        return f"KvLayout({self.as_dict()})"
+
+
+class KvQuery(ctypes.Structure):
+    """sgemv_kv_query: what sgemv_kv_attention reads and writes beside the cache."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "heads_q", "n_req", "n_tokens", "max_q", "window", "table_cols")] + \
+        [("scale", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("table_stride", "q_token_stride", "q_head_stride", "out_token_stride",
+                                       "out_head_stride")] + \
+        [(n, ctypes.c_void_p) for n in ("q_dev", "q_start_dev", "len_dev", "table_dev", "tree_dev", "out_dev", "lse_dev",
+                                        "workspace_dev")] + \
+        [("workspace_bytes", ctypes.c_uint64)]
+
+
+_c, _p, _i, _l = ctypes, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+_lib.sgemv_kv_layout_query.argtypes = [_i] * 5 + [_c.POINTER(KvLayout)]
+_lib.sgemv_kv_plan.argtypes = [_i, _i, _i, _p, _p, _p, _p, _i, _l] + [_p] * 7 + [_i, _p, _p]
+_lib.sgemv_kv_append.argtypes = [_c.POINTER(KvLayout), _p, _i, _p, _l, _l, _p, _l, _l, _p, _i, _p, _p]
+_lib.sgemv_kv_read.argtypes = [_c.POINTER(KvLayout), _p, _p, _i, _i, _p, _p, _p, _p]
+_lib.sgemv_kv_attention.argtypes = [_c.POINTER(KvLayout), _p, _c.POINTER(KvQuery), _p, _p]
+_lib.sgemv_logprobs.argtypes = [_p, _i, _i, _i, _l, _p, _i, _i] + [_p] * 8
+for _name in EXPORTED_KV:
+    getattr(_lib, _name).restype = ctypes.c_int
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _flat(t, dtype, numel, what):
+    """t is a contiguous CUDA tensor of dtype with numel elements (any number if None)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous CUDA {dtype} tensor")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
+
+
+def _rows(t, shape, dtype, what):
+    """t is a CUDA tensor [tokens, heads, dim] of dtype whose dims are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or t.stride(2) != 1:
+        raise ValueError(f"{what}: expected a CUDA {dtype} tensor {shape} with contiguous dims")
+
+
+def _status_ok(status):
+    if status is not None:
+        _flat(status, torch.int32, None, "status")
+
+
+def _cache_ok(layout, cache):
+    _flat(cache, torch.uint8, None, "cache")
+    if cache.numel() < layout.total_bytes:
+        raise ValueError(f"cache: need {layout.total_bytes} bytes")
+
+
+def _table_ok(table, n_req, what="table"):
+    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_req or \
+            (n_req > 0 and table.shape[1] > 1 and table.stride(1) != 1) or \
+            (n_req > 1 and table.stride(0) < table.shape[1]):
+        raise ValueError(f"{what}: expected a CUDA int32 tensor [{n_req}, columns] with contiguous rows")
+
+
+def sgemv_kv_layout_query(heads: int, dim: int, group: int, page: int, n_pages: int) -> KvLayout:
+    out = KvLayout()
+    _check(_lib.sgemv_kv_layout_query(heads, dim, group, page, n_pages, ctypes.byref(out)), "sgemv_kv_layout_query")
+    return out
+
+
+def sgemv_kv_plan(length, keep, add, table, free, free_count, page: int, out, status=None, stream=None) -> None:
+    """Block tables and slot maps of one step. length, keep (or None), add: int32 [n_req]; table: int32 [n_req, columns]
+    and free: int32 [n_pages], both updated; free_count: int32 [1]. out = (length int32 [n_req], free_count int32 [1],
+    q_start int32 [n_req + 1], slots int64 [n_slots], pos int32 [n_slots])."""
+    n = length.numel()
+    o_length, o_count, o_start, o_slots, o_pos = out
+    i32 = torch.int32
+    _flat(length, i32, n, "length")
+    if keep is not None:
+        _flat(keep, i32, n, "keep")
+    _flat(add, i32, n, "add")
+    _table_ok(table, n)
+    _flat(free, i32, None, "free")
+    _flat(free_count, i32, 1, "free_count")
+    _flat(o_length, i32, n, "out length")
+    _flat(o_count, i32, 1, "out free_count")
+    _flat(o_start, i32, n + 1, "out q_start")
+    _flat(o_slots, torch.int64, None, "out slots")
+    _flat(o_pos, i32, o_slots.numel(), "out pos")
+    _status_ok(status)
+    cols = table.shape[1]
+    _check(_lib.sgemv_kv_plan(n, page, free.numel(), length.data_ptr(), _ptr(keep), add.data_ptr(), table.data_ptr(), cols,
+                              max(table.stride(0), cols), free.data_ptr(), free_count.data_ptr(), o_length.data_ptr(),
+                              o_count.data_ptr(), o_start.data_ptr(), o_slots.data_ptr(), o_pos.data_ptr(),
+                              o_slots.numel(), _ptr(status), _stream(stream)), "sgemv_kv_plan")
+
+
+def sgemv_kv_append(layout: KvLayout, cache, k, v, slots, status=None, stream=None) -> None:
+    """Quantise k, v (fp16 or bf16 [tokens, heads, dim], any token and head strides) into the cache at slots (int64)."""
+    _cache_ok(layout, cache)
+    shape = (slots.numel(), layout.heads, layout.dim)
+    _rows(k, shape, k.dtype, "k")
+    _rows(v, shape, k.dtype, "v")
+    _flat(slots, torch.int64, None, "slots")
+    _status_ok(status)
+    _check(_lib.sgemv_kv_append(ctypes.byref(layout), cache.data_ptr(), _DTYPE.get(k.dtype, -1), k.data_ptr(), k.stride(0),
+                                k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), slots.numel(),
+                                _ptr(status), _stream(stream)), "sgemv_kv_append")
+
+
+def sgemv_kv_read(layout: KvLayout, cache, slots, k, v, status=None, stream=None) -> None:
+    """The cached values of the tokens at slots into k, v (fp16, bf16 or fp32, contiguous [tokens, heads, dim])."""
+    _cache_ok(layout, cache)
+    _flat(slots, torch.int64, None, "slots")
+    n = slots.numel() * layout.heads * layout.dim
+    _flat(k, k.dtype, n, "k")
+    _flat(v, k.dtype, n, "v")
+    _status_ok(status)
+    _check(_lib.sgemv_kv_read(ctypes.byref(layout), cache.data_ptr(), slots.data_ptr(), slots.numel(),
+                              _DTYPE.get(k.dtype, -1), k.data_ptr(), v.data_ptr(), _ptr(status), _stream(stream)),
+           "sgemv_kv_read")
+
+
+def sgemv_kv_attention(layout: KvLayout, cache, q, q_start, length, table, out, max_q: int, scale: float, workspace,
+                       lse=None, window: int = 0, tree=None, status=None, stream=None) -> None:
+    """Attention of the requests' new tokens over the cache. q, out: fp16 or bf16 [tokens, heads_q, dim] (any token and
+    head strides); q_start int32 [n_req + 1]; length int32 [n_req], new tokens included; table int32 [n_req, columns];
+    workspace: from kv_workspace(); lse: fp32 [tokens, heads_q] or None; tree: int64 [tokens] bit masks or None."""
+    _cache_ok(layout, cache)
+    n, n_req, dtype = q.shape[0], length.numel(), q.dtype
+    shape = (n, q.shape[1], layout.dim)
+    _rows(q, shape, dtype, "q")
+    _rows(out, shape, dtype, "out")
+    _flat(q_start, torch.int32, n_req + 1, "q_start")
+    _flat(length, torch.int32, n_req, "length")
+    _table_ok(table, n_req)
+    _flat(workspace, torch.uint8, None, "workspace")
+    if lse is not None:
+        _flat(lse, torch.float32, n * shape[1], "lse")
+    if tree is not None:
+        _flat(tree, torch.int64, n, "tree")
+    _status_ok(status)
+    cols = table.shape[1]
+    args = KvQuery(_DTYPE.get(dtype, -1), shape[1], n_req, n, max_q, window, cols, scale, max(table.stride(0), cols),
+                   q.stride(0), q.stride(1), out.stride(0), out.stride(1), q.data_ptr(), q_start.data_ptr(),
+                   length.data_ptr(), table.data_ptr(), _ptr(tree), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                   workspace.numel())
+    _check(_lib.sgemv_kv_attention(ctypes.byref(layout), cache.data_ptr(), ctypes.byref(args), _ptr(status),
+                                   _stream(stream)), "sgemv_kv_attention")
+
+
+def sgemv_logprobs(logits, out, tokens=None, status=None, stream=None) -> None:
+    """Log-probabilities of logits (fp16, bf16 or fp32 [rows, vocab], contiguous vocabulary). tokens: int32 [rows, n] or
+    None. out = (tok_logp fp32 [rows, n], lse fp32 [rows], entropy fp32 [rows], top_tok int32 [rows, top],
+    top_logp fp32 [rows, top], logp fp32 [rows, vocab]), any of them None; top is top_tok's width."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch.Tensor")
+    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected a CUDA tensor [rows, vocab] with a contiguous vocabulary")
+    rows, vocab = logits.shape
+    tok_logp, lse, entropy, top_tok, top_logp, logp = out
+    f32, n_tok, top = torch.float32, 0, 0
+    if (tokens is None) != (tok_logp is None) or (top_tok is None) != (top_logp is None):
+        raise ValueError("tokens and out tok_logp, and out top_tok and top_logp, come together")
+    if tokens is not None:
+        n_tok = tokens.shape[1] if tokens.dim() == 2 else 1
+        _flat(tokens, torch.int32, rows * n_tok, "tokens")
+        _flat(tok_logp, f32, rows * n_tok, "out tok_logp")
+    if top_tok is not None:
+        top = top_tok.shape[1]
+        _flat(top_tok, torch.int32, rows * top, "out top_tok")
+        _flat(top_logp, f32, rows * top, "out top_logp")
+    for t, n, what in ((lse, rows, "out lse"), (entropy, rows, "out entropy"), (logp, rows * vocab, "out logp")):
+        if t is not None:
+            _flat(t, f32, n, what)
+    _status_ok(status)
+    _check(_lib.sgemv_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), rows, vocab, max(logits.stride(0), vocab),
+                               _ptr(tokens), n_tok, top, _ptr(tok_logp), _ptr(lse), _ptr(entropy), _ptr(top_tok),
+                               _ptr(top_logp), _ptr(logp), _ptr(status), _stream(stream)), "sgemv_logprobs")
+
+
+# ---------------------------------------------------------------------------------------------- helpers
+
+def kv_cache(layout: KvLayout, device="cuda"):
+    """The bytes of a cache of this layout (uninitialised: what was never written is never used)."""
+    return torch.empty(layout.total_bytes, dtype=torch.uint8, device=device)
+
+
+def kv_workspace(device="cuda"):
+    """Workspace of sgemv_kv_attention, zeroed as its first call needs it; one for each stream that calls it."""
+    return torch.zeros(KV_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+def kv_attention(layout: KvLayout, cache, q, q_start, length, table, max_q: int, scale: float, workspace, window: int = 0,
+                 tree=None, status=None, stream=None):
+    """sgemv_kv_attention into a new contiguous tensor, which it returns."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    sgemv_kv_attention(layout, cache, q, q_start, length, table, out, max_q, scale, workspace, None, window, tree, status,
+                       stream)
+    return out
+
+
+def logprobs(logits, tokens=None, top: int = 0, full: bool = False, status=None, stream=None) -> dict:
+    """sgemv_logprobs into new tensors: {"lse", "entropy"} and, where asked for, {"tok_logp", "top_tok", "top_logp",
+    "logp"}."""
+    rows, vocab = logits.shape
+    f = dict(dtype=torch.float32, device=logits.device)
+    got = {"lse": torch.empty(rows, **f), "entropy": torch.empty(rows, **f)}
+    if tokens is not None:
+        got["tok_logp"] = torch.empty(tokens.shape, **f)
+    if top:
+        got["top_tok"] = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
+        got["top_logp"] = torch.empty((rows, top), **f)
+    if full:
+        got["logp"] = torch.empty((rows, vocab), **f)
+    sgemv_logprobs(logits, tuple(got.get(n) for n in ("tok_logp", "lse", "entropy", "top_tok", "top_logp", "logp")),
+                   tokens, status, stream)
+    return got
