@@ -136,7 +136,7 @@ typedef struct {
  * Rows of out past q_start[n_req] are not written. What the cache holds past len is never used.
  * Results do not depend on the order in which the GPU runs the call's parts: the same inputs give the same bits.
  * Device-reported: SGEMV_ERR_ARG (a request with q_start out of order or out of range, n > max_q, a negative
- * length; a page id outside the cache), SGEMV_ERR_SHAPE (len needs more than table_cols pages): such a request's
+ * length; a page id outside the cache), SGEMV_ERR_SHAPE (len needs more than table_cols pages, or passes 2^30): such a request's
  * rows are not written, keys of a page outside the cache are left out; SGEMV_ERR_TIMEOUT (a bounded wait for a
  * copy gave up: out is invalid).
  * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_FORMAT (layout fields), SGEMV_ERR_SHAPE (heads_q), SGEMV_ERR_ALIGN,
