@@ -15,11 +15,15 @@
 // mma.m16n8k16 and 8 rows of queries (query heads of a KV head x new tokens) the narrow one: with few rows this is half the
 // tensor work of the usual orientation, and the weights become the second product's operand with one movmatrix per 8 x 8.
 //
+// out = 0 and lse = -inf where a row sees nothing; a masked key's weight is set to 0, so what the cache holds there (a
+// scale that is not a number included) never enters a sum.
+//
 // Work: the 32-token tiles of all (request, row tile, head) segments form one list, split evenly over the CTAs and
-// again over their warps, whatever the lengths. A warp copies its tiles (two 16-token subtiles, contiguous in the
-// cache) into a ring of its own with the copy engine and keeps the softmax's reference, sum and O in registers. Segments
-// that cross warps are joined in shared memory, those that cross CTAs through the workspace by the last CTA to arrive,
-// always in the order of the keys: the same inputs give the same bits.
+// again over their warps, whatever the lengths (a segment counts kSwitch tiles more than it has). A warp copies its
+// tiles (two 16-token subtiles, contiguous in the cache) into a ring of its own with the copy engine, running ahead across
+// segments, and keeps the softmax's reference, sum and O in registers. Segments that cross warps are joined in shared
+// memory, those that cross CTAs through the workspace by the last CTA to arrive, always in the order of the keys: the
+// same inputs give the same bits.
 #pragma once
 
 #include "kv_common.cuh"
@@ -28,8 +32,10 @@ namespace sgemv {
 
 constexpr int kTileTok = 32;      // tokens of a tile
 constexpr int kMaxLen = 1 << 30;  // positions past the end of a tile stay in 32 bits
-constexpr float kWeightScale = 64.0f;   // weights go into fp16 times this
-constexpr float kMaxGrowth = 8.0f;      // the reference m follows the maximum when it is passed by more than this (log2)
+// Weights 2^(t - m) s' go into fp16: the largest is 2^kTop when the reference m is set, and m is set anew when one would pass
+// 2^kLimit (fp16 ends at 2^16). Weights below 2^(kTop - 20) of the largest lose bits, as fp16 subnormals.
+constexpr float kTop = 6.0f, kLimit = 15.0f;
+constexpr int kSwitch = 2;  // what taking up a segment costs, in tiles: counted when the work is split
 
 struct AttnParams {
     const uint8_t* cache;
@@ -116,6 +122,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -165,17 +176,109 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
     }
 }
 
+// Tiles of a request (all its segments), with what taking each up costs.
+template <int kRows>
+__device__ __forceinline__ int64_t units_of(const AttnParams& p, const Span& s) {
+    int64_t n = 0;
+    for (int row0 = 0; row0 < s.n * p.ratio; row0 += kRows) n += keys_of(p, s, row0, kRows).tiles + kSwitch;
+    return n * p.heads;
+}
+
+// The segment after s (there is one).
+template <int kRows>
+__device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
+    s.start += s.keys.tiles + kSwitch;
+    if (++s.head < p.heads) return;
+    s.head = 0;
+    s.row0 += kRows;
+    while (s.row0 >= s.span.n * p.ratio) {
+        s.span = span_of(p, ++s.r);
+        s.row0 = 0;
+    }
+    s.keys = keys_of(p, s.span, s.row0, kRows);
+}
+
+// The copies of one warp: a ring of stages, filled tile by tile along the warp's part of the list.
+template <int D, int G, int NT>
+struct Producer {
+    using S = AttnShape<D, G, NT>;
+    Segment* seg;          // shared memory, one a warp
+    uint64_t* bar;
+    uint8_t* ring;
+    int k, to;             // next tile of the segment, and where the warp's part of it ends
+    int ids, ids_at;       // page ids of 32 copies, one a lane, from tile ids_at; -1 past the keys, -2 outside the cache
+    uint32_t bad;          // two bits a stage: subtiles whose page is outside the cache
+    bool done;
+
+    // Copies the next tile into `stage`, by the whole warp. Where a page holds a tile's two subtiles it is one copy.
+    __device__ __forceinline__ void issue(const AttnParams& p, uint32_t stage, int64_t end, int lane) {
+        if (done) return;
+        if (k >= to) {
+            Segment s = *seg;
+            if (end <= s.start + kSwitch + s.keys.tiles + kSwitch) {
+                done = true;
+                return;
+            }
+            next_segment<S::kRows>(p, s);
+            __syncwarp();
+            if (lane == 0) *seg = s;
+            __syncwarp();
+            k = 0;
+            to = static_cast<int>(min(static_cast<int64_t>(s.keys.tiles), end - s.start - kSwitch));
+            ids_at = -64;
+        }
+        const bool two = p.page == kSub;  // a copy a subtile
+        const int lo = seg->keys.lo, hi = seg->keys.hi;
+        if (k >= ids_at + (two ? 16 : 32)) {
+            ids_at = k;
+            const int pos = lo + kTileTok * k + (two ? 16 : 32) * lane;
+            ids = -1;
+            if (pos < hi) {
+                ids = p.q.table_dev[seg->r * p.q.table_stride + (pos >> p.log2_page)];
+                if (ids < 0 || ids >= p.n_pages) {
+                    report(p.status, SGEMV_ERR_ARG);
+                    ids = -2;
+                }
+            }
+        }
+        const uint8_t* const base = p.cache + seg->head * p.head_bytes;
+        uint8_t* const dst = ring + stage * S::kStageBytes;
+        const int pos = lo + kTileTok * k;
+        if (!two) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, k - ids_at);
+            const uint32_t bytes = id < 0 ? 0 : (pos + kSub < hi ? S::kStageBytes : S::kSubBytes);
+            bad = (bad & ~(3u << (2 * stage))) | (id == -2 ? 3u << (2 * stage) : 0u);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar + stage, bytes);
+                if (bytes)
+                    bulk_g2s(dst, base + id * p.page_bytes + ((pos & (p.page - 1)) >> 4) * S::kSubBytes, bytes, bar + stage);
+            }
+        } else {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (k - ids_at) + (lane & 1));
+            const uint32_t want = __ballot_sync(0xFFFFFFFFu, lane < 2 && id >= 0);
+            const uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < 2 && id == -2);
+            bad = (bad & ~(3u << (2 * stage))) | (none << (2 * stage));
+            if (lane == 0) mbar_arrive_expect_tx(bar + stage, __popc(want) * S::kSubBytes);
+            __syncwarp();
+            if (lane < 2 && id >= 0) bulk_g2s(dst + lane * S::kSubBytes, base + id * p.page_bytes, S::kSubBytes, bar + stage);
+        }
+        ++k;
+    }
+};
+
 template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kernel(const AttnParams p) {
     using S = AttnShape<D, G, NT>;
     constexpr int kWords = S::kPanel / 32;   // 32-bit words of a K row and panel a lane holds
     constexpr int kMt = D / 16;              // 16-dim tiles of O^T
+    constexpr int kGr = S::kGroups;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_before[S::kThreads];
     __shared__ int64_t s_warp[S::kWarps];
     __shared__ __align__(8) uint64_t s_bar[S::kWarps][S::kStages];
+    __shared__ Segment s_ahead[S::kWarps];    // where each warp's copies are
     __shared__ Segment s_seg[2 * S::kWarps];  // of each warp's first and last partial
-    __shared__ int s_has[2 * S::kWarps];
+    __shared__ int s_has[2 * S::kWarps], s_list[2 * S::kWarps];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     if (lane == 0) {
@@ -186,15 +289,10 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     pdl_launch_dependents();
     pdl_wait();
 
-    // Tiles of every request; thread x has requests [x * run, (x + 1) * run).
+    // Units of every request; thread x has requests [x * run, (x + 1) * run).
     const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
-    const auto tiles_of = [&](const Span& s) {
-        int64_t n = 0;
-        for (int row0 = 0; row0 < s.n * p.ratio; row0 += S::kRows) n += keys_of(p, s, row0, S::kRows).tiles;
-        return n * p.heads;
-    };
     int64_t mine = 0;
-    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += tiles_of(span_of(p, r));
+    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += units_of<S::kRows>(p, span_of(p, r));
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -210,7 +308,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     }
     s_before[tid] = before;
     __syncthreads();
-    // A CTA takes a tile a warp at least: with little work fewer CTAs have less to join.
+    // A CTA takes a unit a warp at least: with little work fewer CTAs have less to join.
     const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (total + S::kWarps - 1) / S::kWarps));
     if (blockIdx.x >= ctas || total == 0) return;
     const int64_t cta0 = blockIdx.x * total / ctas, cta1 = (blockIdx.x + 1) * total / ctas;
@@ -220,11 +318,8 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     float* const slots = scratch + static_cast<int64_t>(gridDim.x) * S::kWarps * S::kPartial;  // two a CTA
     int* const arrived = static_cast<int*>(p.q.workspace_dev);
 
-    uint8_t* const ring = smem + warp * S::kStages * S::kStageBytes;
     Segment seg;
-    int at = 0;           // tile of the segment
-    uint32_t turn = 0;    // tiles this warp has waited for
-    bool dead = false;    // a copy never came
+    int from = 0, to = 0;   // the warp's tiles of the segment
     if (begin < end) {
         int lo = 0, hi = min(S::kThreads, (p.q.n_req + run - 1) / run) - 1;
         while (lo < hi) {
@@ -235,185 +330,193 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         seg.r = lo * run;
         for (;; ++seg.r) {
             seg.span = span_of(p, seg.r);
-            const int64_t n = tiles_of(seg.span);
+            const int64_t n = units_of<S::kRows>(p, seg.span);
             if (begin < seg.start + n) break;
             seg.start += n;
         }
         for (seg.row0 = 0;; seg.row0 += S::kRows) {
             seg.keys = keys_of(p, seg.span, seg.row0, S::kRows);
-            const int64_t n = static_cast<int64_t>(seg.keys.tiles) * p.heads;
+            const int64_t n = static_cast<int64_t>(seg.keys.tiles + kSwitch) * p.heads;
             if (begin < seg.start + n) break;
             seg.start += n;
         }
-        seg.head = static_cast<int>((begin - seg.start) / seg.keys.tiles);
-        seg.start += static_cast<int64_t>(seg.head) * seg.keys.tiles;
-        at = static_cast<int>(begin - seg.start);
+        seg.head = static_cast<int>((begin - seg.start) / (seg.keys.tiles + kSwitch));
+        seg.start += static_cast<int64_t>(seg.head) * (seg.keys.tiles + kSwitch);
+        from = static_cast<int>(max(static_cast<int64_t>(0), begin - seg.start - kSwitch));
+        to = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch)));
+    }
+    bool more = from < to;
+    bool dead = false;       // a copy never came
+    uint32_t stage = 0, parity = 0;  // of the tile waited for next
+    Producer<D, G, NT> ahead;
+    if (more) {
+        if (lane == 0) s_ahead[warp] = seg;
+        __syncwarp();
+        ahead.seg = &s_ahead[warp];
+        ahead.bar = s_bar[warp];
+        ahead.ring = smem + warp * S::kStages * S::kStageBytes;
+        ahead.k = from, ahead.to = to;
+        ahead.ids = -1, ahead.ids_at = -64;
+        ahead.bad = 0;
+        ahead.done = false;
+        for (int i = 0; i < S::kStages; ++i) ahead.issue(p, i, end, lane);
+    } else {
+        named_bar_sync(1, S::kThreads);  // see the same barrier below
     }
 
-    for (int64_t tile = begin; tile < end;) {
-        const int stop = static_cast<int>(min(static_cast<int64_t>(seg.keys.tiles), at + (end - tile)));
-        const int old = seg.span.len - seg.span.n;
-        const uint8_t* const base = p.cache + seg.head * p.head_bytes;
-        const int32_t* const table = p.q.table_dev + seg.r * p.q.table_stride;
-
-        // Page ids of the next 32 subtiles, one a lane; -1 past the keys, -2 for one outside the cache.
-        int ids = -1, ids_at = at - 16;
-        uint32_t bad = 0;  // two bits a stage: subtiles whose page is outside the cache
-        const auto issue = [&](int k, uint32_t stage) {
-            if (k >= ids_at + 16) {
-                ids_at = k;
-                const int pos = seg.keys.lo + 16 * (2 * k + lane);
-                ids = -1;
-                if (pos < seg.keys.hi) {
-                    ids = table[pos >> p.log2_page];
-                    if (ids < 0 || ids >= p.n_pages) {
-                        report(p.status, SGEMV_ERR_ARG);
-                        ids = -2;
-                    }
-                }
-            }
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (k - ids_at) + (lane & 1));
-            const uint32_t want = __ballot_sync(0xFFFFFFFFu, lane < 2 && id >= 0);
-            const uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < 2 && id == -2);
-            bad = (bad & ~(3u << (2 * stage))) | (none << (2 * stage));
-            if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][stage], __popc(want) * S::kSubBytes);
-            __syncwarp();
-            if (lane < 2 && id >= 0) {
-                const int pos = seg.keys.lo + 16 * (2 * k + lane);
-                bulk_g2s(ring + stage * S::kStageBytes + lane * S::kSubBytes,
-                         base + id * p.page_bytes + ((pos & (p.page - 1)) >> 4) * S::kSubBytes, S::kSubBytes, &s_bar[warp][stage]);
-            }
-        };
-        for (int k = 0; k < S::kStages && at + k < stop && !dead; ++k) issue(at + k, (turn + k) % S::kStages);
+    while (more) {
+        const int old = seg.span.len - seg.span.n, rows = seg.span.n * p.ratio;
 
         // Queries: lane (g, t) holds dims 32 t .. 32 t + 31 of each panel of row g (16 t .. where a panel has 64), scaled by a
-        // power of two that brings the row's largest into [2^9, 2^10); xs = sums over a group's dims.
+        // power of two that brings the tile's largest into [2^9, 2^10); nx = - sums over a group's dims, per column.
         uint32_t qb[NT][S::kPanels][2 * kWords][2];
-        float c[NT][2], xs[S::kGroups][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = seg.row0 + 8 * nt + g;
-            const bool live = row < seg.span.n * p.ratio;
-            const T* x = static_cast<const T*>(p.q.q_dev);
-            if (live) x += (seg.span.first + row / p.ratio) * p.q.q_token_stride + (seg.head * p.ratio + row % p.ratio) * p.q.q_head_stride;
-            uint4 raw[S::kPanels][kWords];
+        float nx[kGr][NT][2], c;
+        {
             float big = 0.0f;
+            const T* x[NT];
 #pragma unroll
-            for (int pn = 0; pn < S::kPanels; ++pn)
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = seg.row0 + 8 * nt + g;
+                x[nt] = row < rows ? static_cast<const T*>(p.q.q_dev) + (seg.span.first + row / p.ratio) * p.q.q_token_stride +
+                                         (seg.head * p.ratio + row % p.ratio) * p.q.q_head_stride
+                                   : nullptr;
+            }
+            const auto load = [&](int nt, int pn, int w) {
+                return x[nt] != nullptr ? *reinterpret_cast<const uint4*>(x[nt] + pn * 128 + 8 * (kWords * t + w)) : make_uint4(0, 0, 0, 0);
+            };
 #pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                    raw[pn][w] = live ? *reinterpret_cast<const uint4*>(x + pn * 128 + 8 * (kWords * t + w)) : make_uint4(0, 0, 0, 0);
-                    const T* h = reinterpret_cast<const T*>(&raw[pn][w]);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
-                }
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                for (int pn = 0; pn < S::kPanels; ++pn)
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const uint4 raw = load(nt, pn, w);
+                        const T* h = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
+                    }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
             const int be = static_cast<int>(__float_as_uint(big) >> 23);  // biased exponent; 0 and infinity are left alone
             const int sh = be == 0 || be == 255 ? 0 : min(max(127 + 9 - be, -100), 100);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-            float sum[S::kPanels];
+            c = p.scale_log2 * kTwo24 / up;
 #pragma unroll
-            for (int pn = 0; pn < S::kPanels; ++pn) {
-                sum[pn] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                    const T* h = reinterpret_cast<const T*>(&raw[pn][w]);
-                    float f[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = to_f32(h[j]) * up;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t e = pack_half2(f[2 * j], f[2 * j + 4]);
-                        const uint32_t o = pack_half2(f[2 * j + 1] * 0.0625f, f[2 * j + 5] * 0.0625f);
-                        qb[nt][pn][2 * w + j][0] = e;
-                        qb[nt][pn][2 * w + j][1] = o;
-                        const float2 fe = unpack_half2(e), fo = unpack_half2(o);
-                        sum[pn] += (fe.x + fe.y) + 16.0f * (fo.x + fo.y);
-                    }
-                }
-                sum[pn] += __shfl_xor_sync(0xFFFFFFFFu, sum[pn], 1);
-                if (!S::kSplit) sum[pn] += __shfl_xor_sync(0xFFFFFFFFu, sum[pn], 2);
-                sum[pn] *= 1.0f / kTwo24;
-            }
-            // from rows (g) to the columns 2t, 2t + 1 of the products
-            const float down = p.scale_log2 * kTwo24 / up;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                c[nt][j] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + j));
+            for (int nt = 0; nt < NT; ++nt) {
+                float sum[S::kPanels];
 #pragma unroll
                 for (int pn = 0; pn < S::kPanels; ++pn) {
-                    if constexpr (S::kSplit) {
-                        xs[2 * pn][nt][j] = __shfl_sync(0xFFFFFFFFu, sum[pn], 4 * (2 * t + j));
-                        xs[2 * pn + 1][nt][j] = __shfl_sync(0xFFFFFFFFu, sum[pn], 4 * (2 * t + j) + 2);
-                    } else {
-                        xs[pn][nt][j] = __shfl_sync(0xFFFFFFFFu, sum[pn], 4 * (2 * t + j));
+                    sum[pn] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const uint4 raw = load(nt, pn, w);
+                        const T* h = reinterpret_cast<const T*>(&raw);
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = to_f32(h[j]) * up;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t e = pack_half2(f[2 * j], f[2 * j + 4]);
+                            const uint32_t o = pack_half2(f[2 * j + 1] * 0.0625f, f[2 * j + 5] * 0.0625f);
+                            qb[nt][pn][2 * w + j][0] = e;
+                            qb[nt][pn][2 * w + j][1] = o;
+                            const float2 fe = unpack_half2(e), fo = unpack_half2(o);
+                            sum[pn] += (fe.x + fe.y) + 16.0f * (fo.x + fo.y);
+                        }
                     }
+                    sum[pn] += __shfl_xor_sync(0xFFFFFFFFu, sum[pn], 1);
+                    if (!S::kSplit) sum[pn] += __shfl_xor_sync(0xFFFFFFFFu, sum[pn], 2);
+                    sum[pn] *= -1.0f / kTwo24;
                 }
+                // from rows (g) to the columns 2t, 2t + 1 of the products
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int gr = 0; gr < kGr; ++gr)
+                        nx[gr][nt][j] = __shfl_sync(0xFFFFFFFFu, sum[S::kSplit ? gr / 2 : gr],
+                                                    4 * (2 * t + j) + (S::kSplit ? 2 * (gr & 1) : 0));
             }
         }
 
-        float o[kMt][NT][4], l[NT][2], zp[S::kGroups][NT][2], m[NT][2];
+        // o: V's integers times weights. zs: V's zero points times weights. l: this lane's tokens' weights. ref: the
+        // reference, and lim = ref + kLimit + what the scale adds, or -inf while nothing was seen.
+        float o[kMt][NT][4], zs[kGr][NT][4], l[NT][2], ref[NT][2], lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < kMt; ++i)
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+                for (int i = 0; i < kMt; ++i) o[i][nt][j] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                l[nt][j] = 0.0f, m[nt][j] = -INFINITY;
-#pragma unroll
-                for (int gr = 0; gr < S::kGroups; ++gr) zp[gr][nt][j] = 0.0f;
+                for (int gr = 0; gr < kGr; ++gr) zs[gr][nt][j] = 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) l[nt][j] = 0.0f, ref[nt][j] = 0.0f, lim[nt][j] = -INFINITY;
         }
-        // positions that every row of the segment sees
-        const int i0 = seg.row0 / p.ratio, i1 = min(seg.row0 + S::kRows - 1, seg.span.n * p.ratio - 1) / p.ratio;
-        const int clear1 = p.q.tree_dev != nullptr ? old : old + i0 + 1;
-        const int clear0 = p.q.window > 0 ? old + i1 - p.q.window + 1 : 0;
+        // tiles [plain0, plain1) hold positions that every row of the segment sees
+        int plain0 = 0, plain1;
+        {
+            const int i0 = seg.row0 / p.ratio, i1 = min(seg.row0 + S::kRows - 1, rows - 1) / p.ratio;
+            if (p.q.window > 0) plain0 = (max(seg.keys.lo, old + i1 - p.q.window + 1) - seg.keys.lo + kTileTok - 1) / kTileTok;
+            plain1 = (max(seg.keys.lo, p.q.tree_dev != nullptr ? old : old + i0 + 1) - seg.keys.lo) / kTileTok;
+        }
         const int ta = 4 * (g >> 1) + (g & 1);  // the token of row g of S^T; row g + 8 is token ta + 2
 
-        for (int k = at; k < stop; ++k, ++turn) {
-            const uint32_t stage = turn % S::kStages;
-            if (!dead && !mbar_wait(&s_bar[warp][stage], (turn / S::kStages) & 1)) {
-                report(p.status, SGEMV_ERR_TIMEOUT);
-                dead = true;
+        for (int k = from; k < to; ++k) {
+            {
+                const bool here = dead || mbar_try_wait(&s_bar[warp][stage], parity);
+                if (!__all_sync(0xFFFFFFFFu, here)) {
+                    const bool came = here || mbar_wait(&s_bar[warp][stage], parity);
+                    if (!__all_sync(0xFFFFFFFFu, came)) {
+                        report(p.status, SGEMV_ERR_TIMEOUT);
+                        dead = true;
+                        ahead.done = true;  // no more copies
+                    }
+                }
             }
-            dead = __any_sync(0xFFFFFFFFu, dead);
-            const uint8_t* const buf = ring + stage * S::kStageBytes;
+            const uint8_t* const buf = ahead.ring + stage * S::kStageBytes;
+            const bool plain = k >= plain0 && k < plain1 && ahead.bad == 0;
             const int pos0 = seg.keys.lo + k * kTileTok;
-            const bool plain = pos0 >= clear0 && pos0 + kTileTok <= clear1 && ((bad >> (2 * stage)) & 3u) == 0;
 
-            float sc[2][NT][4];   // scores: before c, then in log2
-            float vs[2][S::kGroups][2], vz[2][S::kGroups][2];  // of the lane's tokens ta, ta + 2: scale x 64, zero point
-            float ve[2][2];       // exponent of the largest scale of V
+            float sc[2][NT][4];    // t_j + log2 of the token's scale of V
+            float iv[2][2];        // one over that scale, of the lane's tokens ta, ta + 2
+            float fr[2][kGr][2];   // each group's scale of V over the token's largest
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint8_t* const sub = buf + u * S::kSubBytes;
-                // a token past the keys, or in a page outside the cache, may hold anything: s = 1, z = 0 for it
-                bool gone[2] = {false, false};
+                const uint8_t* const scales = sub + 16 * D + 4 * ta;
+                uint32_t kw[kGr][2], vw[kGr][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int gr = 0; gr < kGr; ++gr) {
+                        kw[gr][e] = *reinterpret_cast<const uint32_t*>(scales + 64 * gr + 8 * e);
+                        vw[gr][e] = *reinterpret_cast<const uint32_t*>(scales + 64 * (kGr + gr) + 8 * e);
+                    }
                 if (!plain) {
+                    // a token past the keys, or in a page outside the cache, may hold anything: s = 1, z = 0 for it
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        gone[e] = pos0 + 16 * u + ta + 2 * e >= seg.keys.hi || ((bad >> (2 * stage + u)) & 1u);
+                        if (pos0 + 16 * u + ta + 2 * e >= seg.keys.hi || ((ahead.bad >> (2 * stage + u)) & 1u)) {
+#pragma unroll
+                            for (int gr = 0; gr < kGr; ++gr) kw[gr][e] = vw[gr][e] = 0x00003C00u;
+                        }
                 }
+                float lv[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    ve[u][e] = -100.0f;
+                    float v = unpack_half2(vw[0][e]).x;
 #pragma unroll
-                    for (int gr = 0; gr < S::kGroups; ++gr) {
-                        uint32_t w = *reinterpret_cast<const uint32_t*>(sub + 16 * D + 64 * S::kGroups + 64 * gr + 4 * (ta + 2 * e));
-                        if (!plain && gone[e]) w = 0x00003C00u;
-                        const float2 f = unpack_half2(w);
-                        vs[u][gr][e] = f.x * kWeightScale;
-                        vz[u][gr][e] = f.y;
-                        ve[u][e] = fmaxf(ve[u][e], static_cast<float>(static_cast<int>((w & 0x7C00u) >> 10) - 15));
-                    }
+                    for (int gr = 1; gr < kGr; ++gr) v = fmaxf(v, unpack_half2(vw[gr][e]).x);
+                    lv[e] = log2_approx(v);
+                    iv[u][e] = exp2_approx(-lv[e]);
+#pragma unroll
+                    for (int gr = 0; gr < kGr; ++gr) fr[u][gr][e] = unpack_half2(vw[gr][e]).x * iv[u][e];
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sc[u][nt][j] = 0.0f;
+                    for (int j = 0; j < 4; ++j) sc[u][nt][j] = lv[j >> 1];
 #pragma unroll
                 for (int pn = 0; pn < S::kPanels; ++pn) {
                     uint32_t ka[kWords], kb[kWords];
@@ -457,53 +560,46 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                         const int gr = kSets * pn + h;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float2 f = unpack_half2(*reinterpret_cast<const uint32_t*>(sub + 16 * D + 64 * gr + 4 * (ta + 2 * e)));
-                            const float sz = f.x * f.y;
+                            const float2 f = unpack_half2(kw[gr][e]);
+                            const float kc = f.x * c;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j)
-                                    sc[u][nt][2 * e + j] += fmaf(f.x, acc[h][nt][2 * e + j], -sz * xs[gr][nt][j]);
+                                    sc[u][nt][2 * e + j] = fmaf(kc, fmaf(f.y, nx[gr][nt][j], acc[h][nt][2 * e + j]), sc[u][nt][2 * e + j]);
                         }
                     }
                 }
             }
-            float top[NT][2];
+            if (!plain) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    top[nt][j] = -INFINITY;
-                    const int row = seg.row0 + 8 * nt + 2 * t + j;
-                    int last = 0, first = 0;
-                    uint64_t tree = 0;
-                    if (!plain) {
-                        const int i = min(row, seg.span.n * p.ratio - 1) / p.ratio;
-                        last = old + i;
-                        if (p.q.window > 0) first = last - p.q.window + 1;
-                        if (p.q.tree_dev != nullptr) tree = p.q.tree_dev[seg.span.first + i];
-                    }
+                    for (int j = 0; j < 2; ++j) {
+                        const int i = min(seg.row0 + 8 * nt + 2 * t + j, rows - 1) / p.ratio;
+                        const int last = old + i, first = p.q.window > 0 ? last - p.q.window + 1 : 0;
+                        const uint64_t tree = p.q.tree_dev != nullptr ? p.q.tree_dev[seg.span.first + i] : 0;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& x = sc[u][nt][2 * e + j];
-                            x *= c[nt][j];
-                            if (!plain) {
+                            for (int e = 0; e < 2; ++e) {
                                 const int pos = pos0 + 16 * u + ta + 2 * e;
-                                bool see = pos < seg.keys.hi && !((bad >> (2 * stage + u)) & 1u);
+                                bool see = pos < seg.keys.hi && !((ahead.bad >> (2 * stage + u)) & 1u);
                                 if (p.q.tree_dev != nullptr) see = see && (pos < old || ((tree >> (pos - old)) & 1));
                                 else see = see && pos >= first && pos <= last;
-                                if (!see) x = -INFINITY;
+                                if (!see) sc[u][nt][2 * e + j] = -INFINITY;
                             }
-                            top[nt][j] = fmaxf(top[nt][j], x + ve[u][e]);
-                        }
-                }
+                    }
+            }
+            float top[NT][2];
             bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) grow = grow || top[nt][j] > m[nt][j] + kMaxGrowth;
+                for (int j = 0; j < 2; ++j) {
+                    top[nt][j] = fmaxf(fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][2 + j]), sc[1][nt][j]), sc[1][nt][2 + j]);
+                    grow = grow || top[nt][j] > lim[nt][j];
+                }
             if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -513,53 +609,58 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                        x = fmaxf(x, m[nt][j]);
-                        const float f = x == -INFINITY ? 1.0f : exp2_approx(m[nt][j] - x);
-                        m[nt][j] = x;
-                        l[nt][j] *= f;
+                        if (x > lim[nt][j]) {  // the same in the 8 lanes of a column
+                            const float f = lim[nt][j] == -INFINITY ? 1.0f : exp2_approx(ref[nt][j] - (x - kTop));
+                            ref[nt][j] = x - kTop;
+                            lim[nt][j] = x - kTop + kLimit;
+                            l[nt][j] *= f;
 #pragma unroll
-                        for (int gr = 0; gr < S::kGroups; ++gr) zp[gr][nt][j] *= f;
+                            for (int gr = 0; gr < kGr; ++gr) zs[gr][nt][j] *= f;
 #pragma unroll
-                        for (int i = 0; i < kMt; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
+                            for (int i = 0; i < kMt; ++i) o[i][nt][j] *= f, o[i][nt][2 + j] *= f;
+                        }
                     }
             }
             // weights, rounded to fp16 per group of V, and the second product
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* const sub = buf + u * S::kSubBytes + 8 * D;
-                uint32_t pb[S::kGroups][NT][2];
+                const uint8_t* const sub = buf + u * S::kSubBytes;
+                uint32_t pb[kGr][NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float ref = m[nt][j] == -INFINITY ? 0.0f : m[nt][j];
+                    for (int e = 0; e < 2; ++e) {
+                        const float p0 = exp2_approx(sc[u][nt][2 * e] - ref[nt][0]), p1 = exp2_approx(sc[u][nt][2 * e + 1] - ref[nt][1]);
+                        l[nt][0] = fmaf(p0, iv[u][e], l[nt][0]);
+                        l[nt][1] = fmaf(p1, iv[u][e], l[nt][1]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& x = sc[u][nt][2 * e + j];
-                            x = exp2_approx(x - ref);
-                            l[nt][j] += x;
-                        }
+                        for (int gr = 0; gr < kGr; ++gr)
+                            pb[gr][nt][e] = transpose8x8(kGr == 1 ? pack_half2(p0, p1) : pack_half2(p0 * fr[u][gr][e], p1 * fr[u][gr][e]));
                     }
+                // zero points: every row of this product's first operand holds tokens 4t .. 4t + 3, so its sums need no joining
 #pragma unroll
-                    for (int gr = 0; gr < S::kGroups; ++gr)
+                for (int gr = 0; gr < kGr; ++gr) {
+                    uint4 w = *reinterpret_cast<const uint4*>(sub + 16 * D + 64 * (kGr + gr) + 16 * t);
+                    if (!plain) {
+                        const int left = ((ahead.bad >> (2 * stage + u)) & 1u) ? 0 : seg.keys.hi - (pos0 + 16 * u + 4 * t);
+                        if (left < 1) w.x = 0;
+                        if (left < 2) w.y = 0;
+                        if (left < 3) w.z = 0;
+                        if (left < 4) w.w = 0;
+                    }
+                    const uint32_t a0 = __byte_perm(w.x, w.y, 0x7632), a2 = __byte_perm(w.z, w.w, 0x7632);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t w = pack_half2(sc[u][nt][2 * e] * vs[u][gr][e], sc[u][nt][2 * e + 1] * vs[u][gr][e]);
-                            const float2 f = unpack_half2(w);
-                            zp[gr][nt][0] = fmaf(f.x, vz[u][gr][e], zp[gr][nt][0]);
-                            zp[gr][nt][1] = fmaf(f.y, vz[u][gr][e], zp[gr][nt][1]);
-                            pb[gr][nt][e] = transpose8x8(w);
-                        }
+                    for (int nt = 0; nt < NT; ++nt) mma16816(zs[gr][nt], a0, 0, a2, 0, pb[gr][nt][0], pb[gr][nt][1]);
                 }
-                uint32_t vw[D / 16];
+                uint32_t vq[D / 16];
 #pragma unroll
                 for (int r = 0; r < D / 64; ++r)
-                    *reinterpret_cast<uint4*>(vw + 4 * r) = *reinterpret_cast<const uint4*>(sub + 512 * r + 16 * lane);
+                    *reinterpret_cast<uint4*>(vq + 4 * r) = *reinterpret_cast<const uint4*>(sub + 8 * D + 512 * r + 16 * lane);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t a = h ? vw[i] >> 8 : vw[i], b = h ? vw[D / 32 + i] >> 8 : vw[D / 32 + i];
+                        const uint32_t a = h ? vq[i] >> 8 : vq[i], b = h ? vq[D / 32 + i] >> 8 : vq[D / 32 + i];
                         const uint32_t a0 = a & 0x000F000Fu, a1 = a & 0x00F000F0u, a2 = b & 0x000F000Fu, a3 = b & 0x00F000F0u;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -568,32 +669,30 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                 }
             }
             __syncwarp();
-            if (k + S::kStages < stop && !dead) issue(k + S::kStages, stage);
+            ahead.issue(p, stage, end, lane);
+            if (++stage == S::kStages) stage = 0, parity ^= 1;
         }
 
         // the lanes' sums over their tokens
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
-#pragma unroll
-                    for (int gr = 0; gr < S::kGroups; ++gr) zp[gr][nt][j] += __shfl_xor_sync(0xFFFFFFFFu, zp[gr][nt][j], d);
-                }
-            }
-        const bool whole = at == 0 && stop == seg.keys.tiles;
-        const bool to_first = !whole && stop == seg.keys.tiles && tile + (stop - at) < end;  // more segments follow
-        float* const mine_p = to_first ? scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + warp) * S::kPartial
-                                       : reinterpret_cast<float*>(smem) + warp * S::kPartial;
-        if (!whole && !to_first) named_bar_sync(1, S::kThreads);  // every warp is done with its ring: partials go there
+                for (int d = 4; d < 32; d <<= 1) l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
+        const int64_t seg_end = seg.start + kSwitch + seg.keys.tiles;
+        const bool whole = from == 0 && to == seg.keys.tiles;
+        more = end > seg_end + kSwitch;  // a tile of the next segment is this warp's
+        // A partial that more work follows goes to global memory; the last one to where the rings were, once all are done.
+        if (!more) named_bar_sync(1, S::kThreads);
+        float* const part = more ? scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + warp) * S::kPartial
+                                 : reinterpret_cast<float*>(smem) + warp * S::kPartial;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int n = 8 * nt + 2 * t + j, row = seg.row0 + n;
-                const bool live = row < seg.span.n * p.ratio;
+                const bool live = row < rows;
                 int tok = 0, a = 0;
                 T* out = nullptr;
                 if (whole && live) out = out_row<T>(p, seg, row, tok, a);
@@ -603,39 +702,27 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int d = 16 * i + 8 * e + g;
-                        const float v = (o[i][nt][2 * e + j] * (e ? kTwo20 : kTwo24) - zp[16 * i / G][nt][j]) * (1.0f / kWeightScale);
-                        if (!whole) mine_p[n * S::kPitch + d] = v;
+                        const float v = o[i][nt][2 * e + j] * (e ? kTwo20 : kTwo24) - zs[16 * i / G][nt][j];
+                        if (!whole) part[n * S::kPitch + d] = v;
                         else if (live) out[d] = from_f32<T>(v * inv);
                     }
                 if (g == 0) {
-                    if (!whole) mine_p[S::kRows * S::kPitch + n] = m[nt][j], mine_p[S::kRows * S::kPitch + S::kRows + n] = l[nt][j];
-                    else if (live) write_lse(p, tok, a, m[nt][j], l[nt][j]);
+                    const float m = lim[nt][j] == -INFINITY ? -INFINITY : ref[nt][j];
+                    if (!whole) part[S::kRows * S::kPitch + n] = m, part[S::kRows * S::kPitch + S::kRows + n] = l[nt][j];
+                    else if (live) write_lse(p, tok, a, m, l[nt][j]);
                 }
             }
         if (!whole && lane == 0) {
-            const int slot = 2 * warp + (to_first ? 0 : 1);
+            const int slot = 2 * warp + (more ? 0 : 1);
             s_has[slot] = 1;
             s_seg[slot] = seg;
         }
-        if (!whole && !to_first) break;  // the warp's last segment, and the barrier is behind it
-        tile += stop - at;
-        at = 0;
-        if (tile < end) {
-            seg.start += seg.keys.tiles;
-            if (++seg.head == p.heads) {
-                seg.head = 0;
-                seg.row0 += S::kRows;
-                while (seg.row0 >= seg.span.n * p.ratio) {
-                    seg.span = span_of(p, ++seg.r);
-                    seg.row0 = 0;
-                }
-                seg.keys = keys_of(p, seg.span, seg.row0, S::kRows);
-            }
-        } else {
-            named_bar_sync(1, S::kThreads);  // the same barrier, for a warp that ends with a whole segment
+        if (more) {
+            next_segment<S::kRows>(p, seg);
+            from = 0;
+            to = static_cast<int>(min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch));
         }
     }
-    if (begin >= end) named_bar_sync(1, S::kThreads);  // and for one that had no tile
     __syncthreads();
 
     // Join the partials of each segment that this CTA's warps share, in the order of the warps.
@@ -645,30 +732,35 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             continue;
         }
         const Segment s = s_seg[i];
-        int idx[2 * S::kWarps], n = 0;
+        uint32_t which = 0;
         for (; i < 2 * S::kWarps && (!s_has[i] || s_seg[i].start == s.start); ++i)
-            if (s_has[i]) idx[n++] = i;
+            if (s_has[i]) which |= 1u << i;
+        const int n = __popc(which);
+        __syncthreads();
+        if (tid < 2 * S::kWarps && ((which >> tid) & 1u)) s_list[__popc(which & ((1u << tid) - 1u))] = tid;
+        __syncthreads();
         const auto part = [&](int x, int at) {
-            const float* q = (idx[x] & 1) ? reinterpret_cast<const float*>(smem) + (idx[x] >> 1) * S::kPartial
-                                          : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + (idx[x] >> 1)) * S::kPartial;
+            const int slot = s_list[x];
+            const float* q = (slot & 1) ? reinterpret_cast<const float*>(smem) + (slot >> 1) * S::kPartial
+                                        : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + (slot >> 1)) * S::kPartial;
             return q[at];
         };
-        const int64_t s_end = s.start + s.keys.tiles;
-        if (s.start >= cta0 && s_end <= cta1) {
+        const int64_t first = s.start + kSwitch, s_end = first + s.keys.tiles;
+        if (first >= cta0 && s_end <= cta1) {
             join<T, D, G, NT>(p, s, n, part, nullptr);
             continue;
         }
         const auto slot = [&](int64_t cta, bool tail) { return slots + (2 * cta + (tail ? 1 : 0)) * S::kPartial; };
-        join<T, D, G, NT>(p, s, n, part, slot(blockIdx.x, s.start >= cta0));
+        join<T, D, G, NT>(p, s, n, part, slot(blockIdx.x, first >= cta0));
         __threadfence();
         __syncthreads();
-        const int64_t from = ((s.start + 1) * ctas - 1) / total, to = (s_end * ctas - 1) / total;
-        if (tid == 0) s_last = atomicAdd(&arrived[from], 1) == static_cast<int>(to - from);
+        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = (s_end * ctas - 1) / total;
+        if (tid == 0) s_last = atomicAdd(&arrived[c0], 1) == static_cast<int>(c1 - c0);
         __syncthreads();
         if (s_last) {
             __threadfence();
-            join<T, D, G, NT>(p, s, static_cast<int>(to - from + 1), [&](int x, int at) { return __ldcg(slot(from + x, x == 0) + at); }, nullptr);
-            if (tid == 0) arrived[from] = 0;
+            join<T, D, G, NT>(p, s, static_cast<int>(c1 - c0 + 1), [&](int x, int at) { return __ldcg(slot(c0 + x, x == 0) + at); }, nullptr);
+            if (tid == 0) arrived[c0] = 0;
         }
         __syncthreads();
     }
