@@ -36,6 +36,7 @@ constexpr int kMaxLen = 1 << 30;  // positions past the end of a tile stay in 32
 // 2^kLimit (fp16 ends at 2^16). Weights below 2^(kTop - 20) of the largest lose bits, as fp16 subnormals.
 constexpr float kTop = 6.0f, kLimit = 15.0f;
 constexpr int kSwitch = 2;  // what taking up a segment costs, in tiles: counted when the work is split
+constexpr int kSpans = 256; // requests whose lengths are kept in shared memory
 
 struct AttnParams {
     const uint8_t* cache;
@@ -55,14 +56,16 @@ struct AttnShape {
     static constexpr int kSubBytes = 16 * D + 128 * kGroups;
     static constexpr int kStageBytes = 2 * kSubBytes;
     static constexpr int kWarps = (D == 256 || NT > 1) ? 8 : 16;
-    static constexpr int kStages = D == 64 ? 4 : 3;
+    static constexpr int kStages = D == 64 ? 4 : NT > 1 ? 3 : 2;
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;             // floats of a partial row: 4 more so that two rows are 8 banks apart
     static constexpr int kPartial = kRows * kPitch + 2 * kRows;  // floats of a partial: O, then m, then l
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kJoin = kWarps * kPartial * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kSmem = kRing + kWarps * kPartial * 4;  // the rings, then a partial a warp
+    // With at most so many tiles in all, a CTA's part of the list starts where a segment starts, if that segment has at
+    // most kShortSegment tiles: a join across CTAs costs more than it brings.
+    static constexpr int kFewTiles = 2 * kWarps, kShortSegment = 4 * kWarps;
 };
 
 // What request r asks for; n = 0 where there is nothing to do.
@@ -147,32 +150,61 @@ __device__ __forceinline__ void write_lse(const AttnParams& p, int tok, int a, f
         p.q.lse_dev[static_cast<int64_t>(tok) * p.q.heads_q + a] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-// Joins partials part(0) .. part(n - 1) of a segment, in order, by the whole CTA, into the output (dst null) or a partial.
-// val(i, x) is float x of partial i.
-template <typename T, int D, int G, int NT, typename Val>
-__device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int n, Val val, float* dst) {
+// Joins row `row` of partials val(0, ..) .. val(n - 1, ..) of a segment, in order, by one warp, into the output (dst null)
+// or a partial. val(i, x) are 4 floats from float x of partial i on, one(i, x) is float x.
+template <typename T, int D, int G, int NT, typename Val, typename One>
+__device__ __forceinline__ void join_row(const AttnParams& p, const Segment& s, int row, int n, int lane, Val val, One one, float* dst) {
     using S = AttnShape<D, G, NT>;
-    for (int e = threadIdx.x; e < S::kRows * D; e += S::kThreads) {
-        const int row = e / D, d = e % D;
-        if (s.row0 + row >= s.span.n * p.ratio) continue;
-        float m = -INFINITY;
-        for (int i = 0; i < n; ++i) m = fmaxf(m, val(i, S::kRows * S::kPitch + row));
-        float o = 0.0f, l = 0.0f;
-        for (int i = 0; i < n; ++i) {
-            const float mi = val(i, S::kRows * S::kPitch + row), li = val(i, S::kRows * S::kPitch + S::kRows + row);
-            const float f = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);
-            o = fmaf(val(i, row * S::kPitch + d), f, o);
-            l = fmaf(li, f, l);
+    if (s.row0 + row >= s.span.n * p.ratio) return;
+    constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, one(i, kM + row));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    constexpr int kVec = (D + 127) / 128;  // groups of 4 dims a lane has (where D is 64, both half warps have the same)
+    const int d0 = D == 64 ? 4 * (lane & 15) : 4 * lane;
+    float4 o[kVec];
+    float l = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float f = 0.0f, fl = 0.0f;
+        if (i0 + lane < n) {
+            const float mi = one(i0 + lane, kM + row), li = one(i0 + lane, kL + row);
+            f = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);
+            fl = li * f;
         }
+        const int cnt = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+            const float w = __shfl_sync(0xFFFFFFFFu, f, i);
+            l += __shfl_sync(0xFFFFFFFFu, fl, i);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                const float4 x = val(i0 + i, row * S::kPitch + 128 * v + d0);
+                o[v].x = fmaf(x.x, w, o[v].x);
+                o[v].y = fmaf(x.y, w, o[v].y);
+                o[v].z = fmaf(x.z, w, o[v].z);
+                o[v].w = fmaf(x.w, w, o[v].w);
+            }
+        }
+    }
+    int tok = 0, a = 0;
+    T* const out = dst == nullptr ? out_row<T>(p, s, s.row0 + row, tok, a) : nullptr;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+        const int d = 128 * v + d0;
         if (dst != nullptr) {
-            dst[row * S::kPitch + d] = o;
-            if (d == 0) dst[S::kRows * S::kPitch + row] = m, dst[S::kRows * S::kPitch + S::kRows + row] = l;
+            *reinterpret_cast<float4*>(dst + row * S::kPitch + d) = o[v];
         } else {
-            int tok, a;
-            T* out = out_row<T>(p, s, s.row0 + row, tok, a);
-            out[d] = from_f32<T>(l == 0.0f ? 0.0f : o / l);
-            if (d == 0) write_lse(p, tok, a, m, l);
+            const T h[4] = {from_f32<T>(o[v].x * inv), from_f32<T>(o[v].y * inv), from_f32<T>(o[v].z * inv), from_f32<T>(o[v].w * inv)};
+            *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
         }
+    }
+    if (lane == 0) {
+        if (dst != nullptr) dst[kM + row] = m, dst[kL + row] = l;
+        else write_lse(p, tok, a, m, l);
     }
 }
 
@@ -184,18 +216,53 @@ __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Span& s) 
     return n * p.heads;
 }
 
+// The requests' lengths, from shared memory where they fit.
+struct Spans {
+    const AttnParams& p;
+    const Span* cached;  // of every request, or null
+    __device__ __forceinline__ Span operator[](int r) const { return cached != nullptr ? cached[r] : span_of(p, r); }
+};
+
 // The segment after s (there is one).
 template <int kRows>
-__device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
+__device__ __forceinline__ void next_segment(const AttnParams& p, const Spans& spans, Segment& s) {
     s.start += s.keys.tiles + kSwitch;
     if (++s.head < p.heads) return;
     s.head = 0;
     s.row0 += kRows;
     while (s.row0 >= s.span.n * p.ratio) {
-        s.span = span_of(p, ++s.r);
+        s.span = spans[++s.r];
         s.row0 = 0;
     }
     s.keys = keys_of(p, s.span, s.row0, kRows);
+}
+
+// The segment that holds a unit. before: units before each thread's run of requests.
+template <int kRows>
+__device__ __forceinline__ Segment locate(const AttnParams& p, const Spans& spans, const int64_t* before, int runs, int run, int64_t unit) {
+    int lo = 0, hi = runs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= unit) lo = mid; else hi = mid - 1;
+    }
+    Segment s;
+    s.start = before[lo];
+    for (s.r = lo * run;; ++s.r) {
+        s.span = spans[s.r];
+        if (run == 1) break;
+        const int64_t n = units_of<kRows>(p, s.span);
+        if (unit < s.start + n) break;
+        s.start += n;
+    }
+    for (s.row0 = 0;; s.row0 += kRows) {
+        s.keys = keys_of(p, s.span, s.row0, kRows);
+        const int64_t n = static_cast<int64_t>(s.keys.tiles + kSwitch) * p.heads;
+        if (unit < s.start + n) break;
+        s.start += n;
+    }
+    s.head = static_cast<int>((unit - s.start) / (s.keys.tiles + kSwitch));
+    s.start += static_cast<int64_t>(s.head) * (s.keys.tiles + kSwitch);
+    return s;
 }
 
 // The copies of one warp: a ring of stages, filled tile by tile along the warp's part of the list.
@@ -206,12 +273,15 @@ struct Producer {
     uint64_t* bar;
     uint8_t* ring;
     int k, to;             // next tile of the segment, and where the warp's part of it ends
-    int ids, ids_at;       // page ids of 32 copies, one a lane, from tile ids_at; -1 past the keys, -2 outside the cache
+    int at;                // first tile of the copies that the lanes hold
+    const uint8_t* src;    // this lane's copy of those, its bytes, and what its tile's copies bring
+    uint32_t bytes, tx;
+    uint32_t wrong;        // lanes whose page is outside the cache
     uint32_t bad;          // two bits a stage: subtiles whose page is outside the cache
     bool done;
 
-    // Copies the next tile into `stage`, by the whole warp. Where a page holds a tile's two subtiles it is one copy.
-    __device__ __forceinline__ void issue(const AttnParams& p, uint32_t stage, int64_t end, int lane) {
+    // Copies the next tile into `stage`, by the whole warp: one copy where a page holds the tile's two subtiles, else two.
+    __device__ __forceinline__ void issue(const AttnParams& p, const Spans& spans, uint32_t stage, int64_t end, int lane) {
         if (done) return;
         if (k >= to) {
             Segment s = *seg;
@@ -219,48 +289,40 @@ struct Producer {
                 done = true;
                 return;
             }
-            next_segment<S::kRows>(p, s);
+            next_segment<S::kRows>(p, spans, s);
             __syncwarp();
             if (lane == 0) *seg = s;
             __syncwarp();
             k = 0;
             to = static_cast<int>(min(static_cast<int64_t>(s.keys.tiles), end - s.start - kSwitch));
-            ids_at = -64;
+            at = -64;
         }
-        const bool two = p.page == kSub;  // a copy a subtile
-        const int lo = seg->keys.lo, hi = seg->keys.hi;
-        if (k >= ids_at + (two ? 16 : 32)) {
-            ids_at = k;
-            const int pos = lo + kTileTok * k + (two ? 16 : 32) * lane;
-            ids = -1;
+        const int two = p.page == kSub;  // a copy a subtile
+        if (k >= at + (32 >> two)) {  // the next 32 copies, one a lane
+            at = k;
+            const int lo = seg->keys.lo, hi = seg->keys.hi;
+            const int pos = lo + kTileTok * k + (kTileTok >> two) * lane;
+            bytes = 0;
+            bool out = false;
             if (pos < hi) {
-                ids = p.q.table_dev[seg->r * p.q.table_stride + (pos >> p.log2_page)];
-                if (ids < 0 || ids >= p.n_pages) {
-                    report(p.status, SGEMV_ERR_ARG);
-                    ids = -2;
-                }
+                const int id = p.q.table_dev[seg->r * p.q.table_stride + (pos >> p.log2_page)];
+                out = id < 0 || id >= p.n_pages;
+                if (out) report(p.status, SGEMV_ERR_ARG);
+                else bytes = !two && pos + kSub < hi ? S::kStageBytes : S::kSubBytes;
+                src = p.cache + id * p.page_bytes + seg->head * p.head_bytes + ((pos & (p.page - 1)) >> 4) * S::kSubBytes;
             }
+            const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, bytes, 1);
+            tx = two ? bytes + next : bytes;
+            wrong = __ballot_sync(0xFFFFFFFFu, out);
         }
-        const uint8_t* const base = p.cache + seg->head * p.head_bytes;
-        uint8_t* const dst = ring + stage * S::kStageBytes;
-        const int pos = lo + kTileTok * k;
-        if (!two) {
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, k - ids_at);
-            const uint32_t bytes = id < 0 ? 0 : (pos + kSub < hi ? S::kStageBytes : S::kSubBytes);
-            bad = (bad & ~(3u << (2 * stage))) | (id == -2 ? 3u << (2 * stage) : 0u);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar + stage, bytes);
-                if (bytes)
-                    bulk_g2s(dst, base + id * p.page_bytes + ((pos & (p.page - 1)) >> 4) * S::kSubBytes, bytes, bar + stage);
-            }
-        } else {
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, 2 * (k - ids_at) + (lane & 1));
-            const uint32_t want = __ballot_sync(0xFFFFFFFFu, lane < 2 && id >= 0);
-            const uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < 2 && id == -2);
-            bad = (bad & ~(3u << (2 * stage))) | (none << (2 * stage));
-            if (lane == 0) mbar_arrive_expect_tx(bar + stage, __popc(want) * S::kSubBytes);
-            __syncwarp();
-            if (lane < 2 && id >= 0) bulk_g2s(dst + lane * S::kSubBytes, base + id * p.page_bytes, S::kSubBytes, bar + stage);
+        const int i = k - at;
+        if ((lane >> two) == i) {
+            if (!two || (lane & 1) == 0) mbar_arrive_expect_tx(bar + stage, tx);
+            if (bytes) bulk_g2s(ring + stage * S::kStageBytes + (two ? (lane & 1) * S::kSubBytes : 0), src, bytes, bar + stage);
+        }
+        if (wrong | bad) {
+            const uint32_t w = two ? (wrong >> (2 * i)) & 3u : ((wrong >> i) & 1u) * 3u;
+            bad = (bad & ~(3u << (2 * stage))) | (w << (2 * stage));
         }
         ++k;
     }
@@ -278,8 +340,9 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     __shared__ __align__(8) uint64_t s_bar[S::kWarps][S::kStages];
     __shared__ Segment s_ahead[S::kWarps];    // where each warp's copies are
     __shared__ Segment s_seg[2 * S::kWarps];  // of each warp's first and last partial
-    __shared__ int s_has[2 * S::kWarps], s_list[2 * S::kWarps];
-    __shared__ int s_last;
+    __shared__ int s_has[2 * S::kWarps], s_list[2 * S::kWarps + 1], s_first[2 * S::kWarps + 1], s_groups;
+    __shared__ Span s_span[kSpans];
+    __shared__ int s_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     if (lane == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(&s_bar[warp][i], 1);
@@ -292,7 +355,12 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     // Units of every request; thread x has requests [x * run, (x + 1) * run).
     const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
     int64_t mine = 0;
-    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += units_of<S::kRows>(p, span_of(p, r));
+    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) {
+        const Span s = span_of(p, r);
+        if (r < kSpans) s_span[r] = s;
+        mine += units_of<S::kRows>(p, s);
+    }
+    const Spans spans = {p, p.q.n_req <= kSpans ? s_span : nullptr};
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -308,10 +376,21 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     }
     s_before[tid] = before;
     __syncthreads();
-    // A CTA takes a unit a warp at least: with little work fewer CTAs have less to join.
-    const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (total + S::kWarps - 1) / S::kWarps));
+    // With little work fewer CTAs have less to join: half a unit a warp at least, and whole segments.
+    const bool few = total <= static_cast<int64_t>(S::kFewTiles) * gridDim.x;
+    const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (2 * total + S::kWarps - 1) / S::kWarps));
     if (blockIdx.x >= ctas || total == 0) return;
-    const int64_t cta0 = blockIdx.x * total / ctas, cta1 = (blockIdx.x + 1) * total / ctas;
+    const int runs = min(S::kThreads, (p.q.n_req + run - 1) / run);
+    const auto split = [&](int64_t cta) {  // first unit of a CTA
+        int64_t u = cta * total / ctas;
+        if (few && u > 0 && u < total) {
+            const Segment s = locate<S::kRows>(p, spans, s_before, runs, run, u);
+            if (s.keys.tiles <= S::kShortSegment) u = s.start;
+        }
+        return u;
+    };
+    const int64_t cta0 = split(blockIdx.x), cta1 = split(blockIdx.x + 1);
+    if (cta0 == cta1) return;
     const int64_t begin = cta0 + warp * (cta1 - cta0) / S::kWarps, end = cta0 + (warp + 1) * (cta1 - cta0) / S::kWarps;
 
     float* const scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096);
@@ -321,27 +400,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     Segment seg;
     int from = 0, to = 0;   // the warp's tiles of the segment
     if (begin < end) {
-        int lo = 0, hi = min(S::kThreads, (p.q.n_req + run - 1) / run) - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_before[mid] <= begin) lo = mid; else hi = mid - 1;
-        }
-        seg.start = s_before[lo];
-        seg.r = lo * run;
-        for (;; ++seg.r) {
-            seg.span = span_of(p, seg.r);
-            const int64_t n = units_of<S::kRows>(p, seg.span);
-            if (begin < seg.start + n) break;
-            seg.start += n;
-        }
-        for (seg.row0 = 0;; seg.row0 += S::kRows) {
-            seg.keys = keys_of(p, seg.span, seg.row0, S::kRows);
-            const int64_t n = static_cast<int64_t>(seg.keys.tiles + kSwitch) * p.heads;
-            if (begin < seg.start + n) break;
-            seg.start += n;
-        }
-        seg.head = static_cast<int>((begin - seg.start) / (seg.keys.tiles + kSwitch));
-        seg.start += static_cast<int64_t>(seg.head) * (seg.keys.tiles + kSwitch);
+        seg = locate<S::kRows>(p, spans, s_before, runs, run, begin);
         from = static_cast<int>(max(static_cast<int64_t>(0), begin - seg.start - kSwitch));
         to = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch)));
     }
@@ -356,12 +415,11 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         ahead.bar = s_bar[warp];
         ahead.ring = smem + warp * S::kStages * S::kStageBytes;
         ahead.k = from, ahead.to = to;
-        ahead.ids = -1, ahead.ids_at = -64;
-        ahead.bad = 0;
+        ahead.at = -64;
+        ahead.src = nullptr, ahead.bytes = ahead.tx = 0;
+        ahead.wrong = ahead.bad = 0;
         ahead.done = false;
-        for (int i = 0; i < S::kStages; ++i) ahead.issue(p, i, end, lane);
-    } else {
-        named_bar_sync(1, S::kThreads);  // see the same barrier below
+        for (int i = 0; i < S::kStages; ++i) ahead.issue(p, spans, i, end, lane);
     }
 
     while (more) {
@@ -478,6 +536,17 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             const bool plain = k >= plain0 && k < plain1 && ahead.bad == 0;
             const int pos0 = seg.keys.lo + k * kTileTok;
 
+            if (!plain) {
+                // a token past the keys, or in a page outside the cache, may hold anything: s = 1, z = 0 for it
+                if (pos0 + lane >= seg.keys.hi || ((ahead.bad >> (2 * stage + (lane >> 4))) & 1u)) {
+                    uint32_t* const w = reinterpret_cast<uint32_t*>(ahead.ring + stage * S::kStageBytes + (lane >> 4) * S::kSubBytes + 16 * D) + (lane & 15);
+#pragma unroll
+                    for (int gr = 0; gr < 2 * kGr; ++gr) w[16 * gr] = 0x00003C00u;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copy engine writes there next
+                __syncwarp();
+            }
+
             float sc[2][NT][4];    // t_j + log2 of the token's scale of V
             float iv[2][2];        // one over that scale, of the lane's tokens ta, ta + 2
             float fr[2][kGr][2];   // each group's scale of V over the token's largest
@@ -493,15 +562,6 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                         kw[gr][e] = *reinterpret_cast<const uint32_t*>(scales + 64 * gr + 8 * e);
                         vw[gr][e] = *reinterpret_cast<const uint32_t*>(scales + 64 * (kGr + gr) + 8 * e);
                     }
-                if (!plain) {
-                    // a token past the keys, or in a page outside the cache, may hold anything: s = 1, z = 0 for it
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (pos0 + 16 * u + ta + 2 * e >= seg.keys.hi || ((ahead.bad >> (2 * stage + u)) & 1u)) {
-#pragma unroll
-                            for (int gr = 0; gr < kGr; ++gr) kw[gr][e] = vw[gr][e] = 0x00003C00u;
-                        }
-                }
                 float lv[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -640,14 +700,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                 // zero points: every row of this product's first operand holds tokens 4t .. 4t + 3, so its sums need no joining
 #pragma unroll
                 for (int gr = 0; gr < kGr; ++gr) {
-                    uint4 w = *reinterpret_cast<const uint4*>(sub + 16 * D + 64 * (kGr + gr) + 16 * t);
-                    if (!plain) {
-                        const int left = ((ahead.bad >> (2 * stage + u)) & 1u) ? 0 : seg.keys.hi - (pos0 + 16 * u + 4 * t);
-                        if (left < 1) w.x = 0;
-                        if (left < 2) w.y = 0;
-                        if (left < 3) w.z = 0;
-                        if (left < 4) w.w = 0;
-                    }
+                    const uint4 w = *reinterpret_cast<const uint4*>(sub + 16 * D + 64 * (kGr + gr) + 16 * t);
                     const uint32_t a0 = __byte_perm(w.x, w.y, 0x7632), a2 = __byte_perm(w.z, w.w, 0x7632);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma16816(zs[gr][nt], a0, 0, a2, 0, pb[gr][nt][0], pb[gr][nt][1]);
@@ -669,7 +722,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                 }
             }
             __syncwarp();
-            ahead.issue(p, stage, end, lane);
+            ahead.issue(p, spans, stage, end, lane);
             if (++stage == S::kStages) stage = 0, parity ^= 1;
         }
 
@@ -683,86 +736,118 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         const int64_t seg_end = seg.start + kSwitch + seg.keys.tiles;
         const bool whole = from == 0 && to == seg.keys.tiles;
         more = end > seg_end + kSwitch;  // a tile of the next segment is this warp's
-        // A partial that more work follows goes to global memory; the last one to where the rings were, once all are done.
-        if (!more) named_bar_sync(1, S::kThreads);
-        float* const part = more ? scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + warp) * S::kPartial
-                                 : reinterpret_cast<float*>(smem) + warp * S::kPartial;
+        // A partial that more work follows goes to global memory, the warp's last one to its place in shared memory; rows that
+        // are whole are turned there, so that they leave in full lines.
+        float* const own = reinterpret_cast<float*>(smem + S::kRing) + warp * S::kPartial;
+        float* const part = whole || !more ? own : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + warp) * S::kPartial;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int n = 8 * nt + 2 * t + j, row = seg.row0 + n;
-                const bool live = row < rows;
-                int tok = 0, a = 0;
-                T* out = nullptr;
-                if (whole && live) out = out_row<T>(p, seg, row, tok, a);
-                const float inv = l[nt][j] == 0.0f ? 0.0f : 1.0f / l[nt][j];
+                const int n = 8 * nt + 2 * t + j;
 #pragma unroll
                 for (int i = 0; i < kMt; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = 16 * i + 8 * e + g;
-                        const float v = o[i][nt][2 * e + j] * (e ? kTwo20 : kTwo24) - zs[16 * i / G][nt][j];
-                        if (!whole) part[n * S::kPitch + d] = v;
-                        else if (live) out[d] = from_f32<T>(v * inv);
-                    }
+                    for (int e = 0; e < 2; ++e)
+                        part[n * S::kPitch + 16 * i + 8 * e + g] = fmaf(o[i][nt][2 * e + j], e ? kTwo20 : kTwo24, -zs[16 * i / G][nt][j]);
                 if (g == 0) {
-                    const float m = lim[nt][j] == -INFINITY ? -INFINITY : ref[nt][j];
-                    if (!whole) part[S::kRows * S::kPitch + n] = m, part[S::kRows * S::kPitch + S::kRows + n] = l[nt][j];
-                    else if (live) write_lse(p, tok, a, m, l[nt][j]);
+                    part[S::kRows * S::kPitch + n] = lim[nt][j] == -INFINITY ? -INFINITY : ref[nt][j];
+                    part[S::kRows * S::kPitch + S::kRows + n] = l[nt][j];
                 }
             }
+        if (whole) {
+            __syncwarp();
+            constexpr int kLanes = D < 128 ? 16 : 32;  // lanes of a row
+            for (int n = lane / kLanes; n < S::kRows && seg.row0 + n < rows; n += 32 / kLanes) {
+                int tok, a;
+                T* const out = out_row<T>(p, seg, seg.row0 + n, tok, a);
+                const float sum = own[S::kRows * S::kPitch + S::kRows + n], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int d = 4 * (lane % kLanes); d < D; d += 4 * kLanes) {
+                    const float4 x = *reinterpret_cast<const float4*>(own + n * S::kPitch + d);
+                    const T h[4] = {from_f32<T>(x.x * inv), from_f32<T>(x.y * inv), from_f32<T>(x.z * inv), from_f32<T>(x.w * inv)};
+                    *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
+                }
+                if (lane % kLanes == 0) write_lse(p, tok, a, own[S::kRows * S::kPitch + n], sum);
+            }
+            __syncwarp();
+        }
         if (!whole && lane == 0) {
             const int slot = 2 * warp + (more ? 0 : 1);
             s_has[slot] = 1;
             s_seg[slot] = seg;
         }
         if (more) {
-            next_segment<S::kRows>(p, seg);
+            next_segment<S::kRows>(p, spans, seg);
             from = 0;
             to = static_cast<int>(min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch));
         }
     }
     __syncthreads();
 
-    // Join the partials of each segment that this CTA's warps share, in the order of the warps.
-    for (int i = 0; i < 2 * S::kWarps;) {
-        if (!s_has[i]) {
-            ++i;
-            continue;
-        }
-        const Segment s = s_seg[i];
-        uint32_t which = 0;
-        for (; i < 2 * S::kWarps && (!s_has[i] || s_seg[i].start == s.start); ++i)
-            if (s_has[i]) which |= 1u << i;
-        const int n = __popc(which);
-        __syncthreads();
-        if (tid < 2 * S::kWarps && ((which >> tid) & 1u)) s_list[__popc(which & ((1u << tid) - 1u))] = tid;
-        __syncthreads();
-        const auto part = [&](int x, int at) {
-            const int slot = s_list[x];
-            const float* q = (slot & 1) ? reinterpret_cast<const float*>(smem) + (slot >> 1) * S::kPartial
-                                        : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + (slot >> 1)) * S::kPartial;
-            return q[at];
+    // Join the partials of each segment that this CTA's warps share, in the order of the warps, a row a warp: into the
+    // output, or into a partial of this CTA where the segment goes on in another.
+    const auto slot = [&](int64_t cta, bool tail) { return slots + (2 * cta + (tail ? 1 : 0)) * S::kPartial; };
+    const auto owned = [&](const Segment& s) {  // tiles before this CTA (1), after it (2)
+        return (s.start + kSwitch < cta0 ? 1 : 0) | (s.start + kSwitch + s.keys.tiles > cta1 ? 2 : 0);
+    };
+    if (warp == 0) {  // the partials in order, and where each segment's begin: lane x looks at slot x
+        const bool has = lane < 2 * S::kWarps && s_has[lane];
+        const uint32_t all = __ballot_sync(0xFFFFFFFFu, has), below = all & ((1u << lane) - 1u);
+        const bool head = has && (below == 0 || s_seg[31 - __clz(below)].start != s_seg[lane].start);
+        const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+        if (has) s_list[__popc(below)] = lane;
+        if (head) s_first[__popc(heads & ((1u << lane) - 1u))] = __popc(below);
+        if (lane == 0) s_groups = __popc(heads), s_first[__popc(heads)] = __popc(all);
+    }
+    __syncthreads();
+    const int groups = s_groups;
+    for (int item = warp; item < groups * S::kRows; item += S::kWarps) {
+        const int gr = item / S::kRows, row = item % S::kRows, first = s_first[gr];
+        const Segment& s = s_seg[s_list[first]];
+        const int over = owned(s);
+        const auto base = [&](int i) {
+            const int x = s_list[first + i];
+            return (x & 1) ? reinterpret_cast<const float*>(smem + S::kRing) + (x >> 1) * S::kPartial
+                           : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + (x >> 1)) * S::kPartial;
         };
-        const int64_t first = s.start + kSwitch, s_end = first + s.keys.tiles;
-        if (first >= cta0 && s_end <= cta1) {
-            join<T, D, G, NT>(p, s, n, part, nullptr);
-            continue;
-        }
-        const auto slot = [&](int64_t cta, bool tail) { return slots + (2 * cta + (tail ? 1 : 0)) * S::kPartial; };
-        join<T, D, G, NT>(p, s, n, part, slot(blockIdx.x, first >= cta0));
+        join_row<T, D, G, NT>(
+            p, s, row, s_first[gr + 1] - first, lane, [&](int i, int at) { return *reinterpret_cast<const float4*>(base(i) + at); },
+            [&](int i, int at) { return base(i)[at]; }, over ? slot(blockIdx.x, !(over & 1)) : nullptr);
+    }
+    // Segments that other CTAs share (the first and the last one of this CTA's): the last CTA to arrive joins their partials.
+    const Segment* cross[2] = {nullptr, nullptr};
+    if (groups > 0) {
+        const Segment* const a = &s_seg[s_list[0]];
+        const Segment* const b = &s_seg[s_list[s_first[groups - 1]]];
+        const int oa = owned(*a), ob = owned(*b);
+        if (oa & 1) cross[0] = a;
+        if (ob == 2) cross[1] = b;
+    }
+    if (cross[0] == nullptr && cross[1] == nullptr) return;
+    __threadfence();
+    __syncthreads();
+    const auto cta_of = [&](int64_t unit) {
+        // the CTA whose part holds a unit of a segment that CTAs share: its bounds are not moved within such a segment
+        return ((unit + 1) * ctas - 1) / total;
+    };
+    if (tid < 2 && (tid ? cross[1] : cross[0]) != nullptr) {
+        const Segment& s = tid ? *cross[1] : *cross[0];
+        const int64_t c0 = cta_of(s.start + kSwitch), c1 = cta_of(s.start + kSwitch + s.keys.tiles - 1);
+        s_last[tid] = atomicAdd(&arrived[c0], 1) == static_cast<int>(c1 - c0);
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x) {
+        if ((x ? cross[1] : cross[0]) == nullptr || !s_last[x]) continue;
         __threadfence();
-        __syncthreads();
-        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = (s_end * ctas - 1) / total;
-        if (tid == 0) s_last = atomicAdd(&arrived[c0], 1) == static_cast<int>(c1 - c0);
-        __syncthreads();
-        if (s_last) {
-            __threadfence();
-            join<T, D, G, NT>(p, s, static_cast<int>(c1 - c0 + 1), [&](int x, int at) { return __ldcg(slot(c0 + x, x == 0) + at); }, nullptr);
-            if (tid == 0) arrived[c0] = 0;
-        }
-        __syncthreads();
+        const Segment& s = x ? *cross[1] : *cross[0];
+        const int64_t c0 = cta_of(s.start + kSwitch), c1 = cta_of(s.start + kSwitch + s.keys.tiles - 1);
+        for (int row = warp; row < S::kRows; row += S::kWarps)
+            join_row<T, D, G, NT>(
+                p, s, row, static_cast<int>(c1 - c0 + 1), lane,
+                [&](int i, int at) { return __ldcg(reinterpret_cast<const float4*>(slot(c0 + i, i == 0) + at)); },
+                [&](int i, int at) { return __ldcg(slot(c0 + i, i == 0) + at); }, nullptr);
+        if (tid == 0) arrived[c0] = 0;
     }
 }
 
