@@ -66,27 +66,39 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without the Stream object that torch.cuda.current_stream() builds (2.9 us against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, t):
+    """The stream's handle; the current one of t's device if None."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _flat(t, dtype, numel, what):
     """t is a contiguous CUDA tensor of dtype with numel elements (any number if None)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
+            return
+    except AttributeError:
+        raise TypeError(f"{what}: expected a torch.Tensor") from None
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous CUDA {dtype} tensor")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
+    raise ValueError(f"{what}: expected {numel} elements, got {t.numel()}")
 
 
 def _rows(t, shape, dtype, what):
-    """t is a CUDA tensor [tokens, heads, dim] of dtype whose dims are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or t.stride(2) != 1:
-        raise ValueError(f"{what}: expected a CUDA {dtype} tensor {shape} with contiguous dims")
-
-
-def _status_ok(status):
-    if status is not None:
-        _flat(status, torch.int32, None, "status")
+    """t is a CUDA tensor [tokens, heads, dim] of dtype whose dims are contiguous: its token and head strides."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape:
+            stride = t.stride()
+            if stride[2] == 1:
+                return stride
+    except AttributeError:
+        raise TypeError(f"{what}: expected a torch.Tensor") from None
+    raise ValueError(f"{what}: expected a CUDA {dtype} tensor {tuple(shape)} with contiguous dims")
 
 
 def _cache_ok(layout, cache):
@@ -95,11 +107,14 @@ def _cache_ok(layout, cache):
         raise ValueError(f"cache: need {layout.total_bytes} bytes")
 
 
-def _table_ok(table, n_req, what="table"):
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n_req or \
-            (n_req > 0 and table.shape[1] > 1 and table.stride(1) != 1) or \
-            (n_req > 1 and table.stride(0) < table.shape[1]):
-        raise ValueError(f"{what}: expected a CUDA int32 tensor [{n_req}, columns] with contiguous rows")
+def _table_ok(table, n_req):
+    """Columns and row stride of a block table."""
+    if table.dtype is torch.int32 and table.is_cuda and table.dim() == 2:
+        rows, cols = table.shape
+        stride = table.stride()
+        if rows == n_req and (rows == 0 or cols < 2 or stride[1] == 1) and (rows < 2 or stride[0] >= cols):
+            return cols, max(stride[0], cols)
+    raise ValueError(f"table: expected a CUDA int32 tensor [{n_req}, columns] with contiguous rows")
 
 
 def sgemv_kv_layout_query(heads: int, dim: int, group: int, page: int, n_pages: int) -> KvLayout:
@@ -112,53 +127,61 @@ def sgemv_kv_plan(length, keep, add, table, free, free_count, page: int, out, st
     """Block tables and slot maps of one step. length, keep (or None), add: int32 [n_req]; table: int32 [n_req, columns]
     and free: int32 [n_pages], both updated; free_count: int32 [1]. out = (length int32 [n_req], free_count int32 [1],
     q_start int32 [n_req + 1], slots int64 [n_slots], pos int32 [n_slots])."""
-    n = length.numel()
     o_length, o_count, o_start, o_slots, o_pos = out
     i32 = torch.int32
-    _flat(length, i32, n, "length")
+    _flat(length, i32, None, "length")
+    n = length.numel()
     if keep is not None:
         _flat(keep, i32, n, "keep")
     _flat(add, i32, n, "add")
-    _table_ok(table, n)
+    cols, stride = _table_ok(table, n)
     _flat(free, i32, None, "free")
     _flat(free_count, i32, 1, "free_count")
     _flat(o_length, i32, n, "out length")
     _flat(o_count, i32, 1, "out free_count")
     _flat(o_start, i32, n + 1, "out q_start")
     _flat(o_slots, torch.int64, None, "out slots")
-    _flat(o_pos, i32, o_slots.numel(), "out pos")
-    _status_ok(status)
-    cols = table.shape[1]
-    _check(_lib.sgemv_kv_plan(n, page, free.numel(), length.data_ptr(), _ptr(keep), add.data_ptr(), table.data_ptr(), cols,
-                              max(table.stride(0), cols), free.data_ptr(), free_count.data_ptr(), o_length.data_ptr(),
-                              o_count.data_ptr(), o_start.data_ptr(), o_slots.data_ptr(), o_pos.data_ptr(),
-                              o_slots.numel(), _ptr(status), _stream(stream)), "sgemv_kv_plan")
+    n_slots = o_slots.numel()
+    _flat(o_pos, i32, n_slots, "out pos")
+    if status is not None:
+        _flat(status, i32, None, "status")
+    code = _lib.sgemv_kv_plan(n, page, free.numel(), length.data_ptr(), _ptr(keep), add.data_ptr(), table.data_ptr(), cols,
+                              stride, free.data_ptr(), free_count.data_ptr(), o_length.data_ptr(), o_count.data_ptr(),
+                              o_start.data_ptr(), o_slots.data_ptr(), o_pos.data_ptr(), n_slots, _ptr(status),
+                              _on(stream, length))
+    if code:
+        _check(code, "sgemv_kv_plan")
 
 
 def sgemv_kv_append(layout: KvLayout, cache, k, v, slots, status=None, stream=None) -> None:
     """Quantise k, v (fp16 or bf16 [tokens, heads, dim], any token and head strides) into the cache at slots (int64)."""
     _cache_ok(layout, cache)
-    shape = (slots.numel(), layout.heads, layout.dim)
-    _rows(k, shape, k.dtype, "k")
-    _rows(v, shape, k.dtype, "v")
     _flat(slots, torch.int64, None, "slots")
-    _status_ok(status)
-    _check(_lib.sgemv_kv_append(ctypes.byref(layout), cache.data_ptr(), _DTYPE.get(k.dtype, -1), k.data_ptr(), k.stride(0),
-                                k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), slots.numel(),
-                                _ptr(status), _stream(stream)), "sgemv_kv_append")
+    n, dtype = slots.numel(), k.dtype
+    shape = (n, layout.heads, layout.dim)
+    ks, vs = _rows(k, shape, dtype, "k"), _rows(v, shape, dtype, "v")
+    if status is not None:
+        _flat(status, torch.int32, None, "status")
+    code = _lib.sgemv_kv_append(ctypes.byref(layout), cache.data_ptr(), _DTYPE.get(dtype, -1), k.data_ptr(), ks[0], ks[1],
+                                v.data_ptr(), vs[0], vs[1], slots.data_ptr(), n, _ptr(status), _on(stream, slots))
+    if code:
+        _check(code, "sgemv_kv_append")
 
 
 def sgemv_kv_read(layout: KvLayout, cache, slots, k, v, status=None, stream=None) -> None:
     """The cached values of the tokens at slots into k, v (fp16, bf16 or fp32, contiguous [tokens, heads, dim])."""
     _cache_ok(layout, cache)
     _flat(slots, torch.int64, None, "slots")
-    n = slots.numel() * layout.heads * layout.dim
-    _flat(k, k.dtype, n, "k")
-    _flat(v, k.dtype, n, "v")
-    _status_ok(status)
-    _check(_lib.sgemv_kv_read(ctypes.byref(layout), cache.data_ptr(), slots.data_ptr(), slots.numel(),
-                              _DTYPE.get(k.dtype, -1), k.data_ptr(), v.data_ptr(), _ptr(status), _stream(stream)),
-           "sgemv_kv_read")
+    n, dtype = slots.numel(), k.dtype
+    size = n * layout.heads * layout.dim
+    _flat(k, dtype, size, "k")
+    _flat(v, dtype, size, "v")
+    if status is not None:
+        _flat(status, torch.int32, None, "status")
+    code = _lib.sgemv_kv_read(ctypes.byref(layout), cache.data_ptr(), slots.data_ptr(), n, _DTYPE.get(dtype, -1),
+                              k.data_ptr(), v.data_ptr(), _ptr(status), _on(stream, slots))
+    if code:
+        _check(code, "sgemv_kv_read")
 
 
 def sgemv_kv_attention(layout: KvLayout, cache, q, q_start, length, table, out, max_q: int, scale: float, workspace,
@@ -167,26 +190,28 @@ def sgemv_kv_attention(layout: KvLayout, cache, q, q_start, length, table, out, 
     head strides); q_start int32 [n_req + 1]; length int32 [n_req], new tokens included; table int32 [n_req, columns];
     workspace: from kv_workspace(); lse: fp32 [tokens, heads_q] or None; tree: int64 [tokens] bit masks or None."""
     _cache_ok(layout, cache)
-    n, n_req, dtype = q.shape[0], length.numel(), q.dtype
-    shape = (n, q.shape[1], layout.dim)
-    _rows(q, shape, dtype, "q")
-    _rows(out, shape, dtype, "out")
-    _flat(q_start, torch.int32, n_req + 1, "q_start")
-    _flat(length, torch.int32, n_req, "length")
-    _table_ok(table, n_req)
+    n, heads, _ = shape = q.shape
+    dtype, i32 = q.dtype, torch.int32
+    if shape[2] != layout.dim:
+        raise ValueError(f"q: expected rows of {layout.dim}")
+    qs, os = _rows(q, shape, dtype, "q"), _rows(out, shape, dtype, "out")
+    _flat(length, i32, None, "length")
+    n_req = length.numel()
+    _flat(q_start, i32, n_req + 1, "q_start")
+    cols, stride = _table_ok(table, n_req)
     _flat(workspace, torch.uint8, None, "workspace")
     if lse is not None:
-        _flat(lse, torch.float32, n * shape[1], "lse")
+        _flat(lse, torch.float32, n * heads, "lse")
     if tree is not None:
         _flat(tree, torch.int64, n, "tree")
-    _status_ok(status)
-    cols = table.shape[1]
-    args = KvQuery(_DTYPE.get(dtype, -1), shape[1], n_req, n, max_q, window, cols, scale, max(table.stride(0), cols),
-                   q.stride(0), q.stride(1), out.stride(0), out.stride(1), q.data_ptr(), q_start.data_ptr(),
-                   length.data_ptr(), table.data_ptr(), _ptr(tree), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                   workspace.numel())
-    _check(_lib.sgemv_kv_attention(ctypes.byref(layout), cache.data_ptr(), ctypes.byref(args), _ptr(status),
-                                   _stream(stream)), "sgemv_kv_attention")
+    if status is not None:
+        _flat(status, i32, None, "status")
+    args = KvQuery(_DTYPE.get(dtype, -1), heads, n_req, n, max_q, window, cols, scale, stride, qs[0], qs[1], os[0], os[1],
+                   q.data_ptr(), q_start.data_ptr(), length.data_ptr(), table.data_ptr(), _ptr(tree), out.data_ptr(),
+                   _ptr(lse), workspace.data_ptr(), workspace.numel())
+    code = _lib.sgemv_kv_attention(ctypes.byref(layout), cache.data_ptr(), ctypes.byref(args), _ptr(status), _on(stream, q))
+    if code:
+        _check(code, "sgemv_kv_attention")
 
 
 def sgemv_logprobs(logits, out, tokens=None, status=None, stream=None) -> None:
@@ -213,10 +238,13 @@ def sgemv_logprobs(logits, out, tokens=None, status=None, stream=None) -> None:
     for t, n, what in ((lse, rows, "out lse"), (entropy, rows, "out entropy"), (logp, rows * vocab, "out logp")):
         if t is not None:
             _flat(t, f32, n, what)
-    _status_ok(status)
-    _check(_lib.sgemv_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), rows, vocab, max(logits.stride(0), vocab),
+    if status is not None:
+        _flat(status, torch.int32, None, "status")
+    code = _lib.sgemv_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), rows, vocab, max(logits.stride(0), vocab),
                                _ptr(tokens), n_tok, top, _ptr(tok_logp), _ptr(lse), _ptr(entropy), _ptr(top_tok),
-                               _ptr(top_logp), _ptr(logp), _ptr(status), _stream(stream)), "sgemv_logprobs")
+                               _ptr(top_logp), _ptr(logp), _ptr(status), _on(stream, logits))
+    if code:
+        _check(code, "sgemv_logprobs")
 
 
 # ---------------------------------------------------------------------------------------------- helpers
