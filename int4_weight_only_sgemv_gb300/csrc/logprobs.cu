@@ -5,11 +5,17 @@
 // share it where rows are few or long, into shared memory (copy engine, several chunks in flight). Two passes over
 // shared memory follow:
 //  A  each thread's maximum and where it is, as the chunks arrive; from these the row's (or slice's) maximum, and a bound that
-//     at least `top` elements reach: each warp sorts its 32 maxima and gives its ceil(top / warps)-th; the bound is the lowest.
-//  B  the sums, and the elements that reach the bound (a little over `top` of them) into a list.
+//     at least `top` elements reach: each warp gives the ceil(top / warps)-th of its 32 maxima, the bound is the lowest.
+//  B  the sums. Then the vectors of the threads whose maximum reaches the bound, spread over all threads, are searched for the
+//     elements that do (a little over `top` of them), which go into a list.
 // An element's rank in the list is the number of larger ones; ties rank by the lower token, so keys are unique. If the list
 // overflows (a row made so that a few threads hold most of the large values), its own `top`-th entry is a better bound and
-// the pass is run again. Clusters hand their lists and sums to the first CTA through distributed shared memory.
+// the pass is run again. The CTAs of a cluster write their sums to each other, and their best to the first one, through
+// distributed shared memory, before the one barrier that they share.
+//
+// x - m is formed before it is scaled to log2 (two packed operations for two elements, where one multiply-add by a rounded
+// log2(e) m would do): the maximum's own weight is then 1 exactly, and a row with all its weight on one token has lp 0 and
+// entropy 0 there.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -24,11 +30,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kList = 2048;       // candidates
+constexpr int kList = 1024;       // candidates
 constexpr int kMaxTop = 64;
 constexpr int kMaxCluster = 8;
 constexpr int kChunks = 8;        // copies a slice is fetched with
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct LogprobParams {
     const void* logits;
@@ -45,11 +51,10 @@ struct LogprobParams {
     int staged;   // the slices fit in shared memory
 };
 
-// What a CTA of a cluster tells the first one.
+// What a CTA of a cluster tells the others: its maximum, the sums about it, and how many candidates it has.
 struct Slice {
     float m, s, e;
-    int n;                   // entries of best
-    uint64_t best[kMaxTop];  // keys, highest first
+    int n;
 };
 
 // Larger for a larger logit; equal logits by the lower token. -0 counts as +0. Never 0 for a real element.
@@ -76,12 +81,70 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// How many of the n keys are larger than k (key n is read too: 0).
+__device__ __forceinline__ int count_larger(const uint64_t* keys, int n, uint64_t k) {
+    int larger = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; j += 2) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(keys + j);
+        larger += (w.x > k) + (w.y > k);
+    }
+    return larger;
+}
+// The same for kMaxTop keys in descending order.
+__device__ __forceinline__ int count_larger_sorted(const uint64_t* keys, uint64_t k) {
+    int at = 0;
+#pragma unroll
+    for (int step = kMaxTop / 2; step > 0; step >>= 1)
+        if (keys[at + step - 1] > k) at += step;
+    return at + (keys[at] > k);
+}
+
+// Two binary32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts_of(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // 16 bytes of logits.
 template <typename T>
 struct Vec {
     static constexpr int kN = 16 / sizeof(T);
     uint4 w;
     __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(&w)[i]); }
+    // Elements 2i and 2i + 1, -inf and what is below kLow set to kLow (where the row's maximum is far above, both have weight 0).
+    static constexpr float kLow = sizeof(T) == 2 && std::is_same<T, __half>::value ? -65504.0f : -1e30f;
+    __device__ __forceinline__ float2 two(int i) const {
+        if constexpr (sizeof(T) == 2) {
+            using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+            const T low = from_f32<T>(kLow);
+            const T2 h = __hmax2(reinterpret_cast<const T2*>(&w)[i], T2(low, low));
+            return make_float2(to_f32(h.x), to_f32(h.y));
+        } else {
+            return make_float2(fmaxf(at(2 * i), kLow), fmaxf(at(2 * i + 1), kLow));
+        }
+    }
     __device__ __forceinline__ float max() const {  // NaN if one is
         if constexpr (sizeof(T) == 2) {
             using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
@@ -98,11 +161,13 @@ template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
     constexpr int kWarps = kThreads / 32, kN = Vec<T>::kN;
     extern __shared__ __align__(16) uint8_t s_data[];  // the slice
-    __shared__ uint64_t s_list[kList];
-    __shared__ Slice s_slice;
+    __shared__ __align__(16) uint64_t s_list[kList + 2];
+    __shared__ __align__(16) uint64_t s_best[kMaxCluster * kMaxTop];  // of each slice, highest first (in the first CTA)
+    __shared__ Slice s_slice[kMaxCluster];
     __shared__ float s_f[3][kWarps];
     __shared__ uint64_t s_key[kWarps];
-    __shared__ int s_count;
+    __shared__ uint16_t s_hot[kThreads];
+    __shared__ int s_count, s_nhot;
     __shared__ __align__(8) uint64_t s_bar[kChunks];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cg::cluster_group cluster = cg::this_cluster();
@@ -111,6 +176,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     if (tid < kChunks) mbar_init(&s_bar[tid], 1);
     if (tid == 0) mbar_fence_init();
     __syncthreads();
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // every CTA has started: see below
     pdl_launch_dependents();
     pdl_wait();
 
@@ -136,40 +202,50 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     };
     Vec<T>* const data = reinterpret_cast<Vec<T>*>(s_data);
     const auto get = [&](int v) { return p.staged ? data[v - v0] : fetch(v); };
-    // chunk c of the whole vectors; every thread waits for it before it reads one
-    const auto chunk_at = [&](int c) { return f0 + static_cast<int>(static_cast<int64_t>(f1 - f0) * c / kChunks); };
+    // chunk c of the whole vectors: a vector a thread or several
+    const int chunk = ((f1 - f0 + kChunks - 1) / kChunks + kThreads - 1) / kThreads * kThreads;
+    const auto chunk_at = [&](int c) { return min(f1, f0 + chunk * c); };
     if (p.staged) {
         if (tid < kChunks) {
             const int a = chunk_at(tid), b = chunk_at(tid + 1);
             mbar_arrive_expect_tx(&s_bar[tid], static_cast<uint32_t>(b - a) * 16);
             if (b > a) bulk_g2s(&data[a - v0], x + (static_cast<int64_t>(a) * kN - head), static_cast<uint32_t>(b - a) * 16, &s_bar[tid]);
         }
-        if (tid >= 32 && tid < 34) {  // the first and the last vector, where they are not whole
-            const int v = tid == 32 ? v0 : v1 - 1;
-            if (v >= v0 && v < v1 && !(v >= f0 && v < f1)) data[v - v0] = fetch(v);
-        }
-        __syncthreads();
     }
+    // The first and the last vector, where they are not whole: a thread each, from registers.
+    const int edge = tid == 32 && v0 < f0 ? v0 : (tid == 33 && f1 < v1 ? v1 - 1 : -1);
+    Vec<T> edge_x;
+    if (edge >= 0) edge_x = fetch(edge);
+    // a token asked for, a thread: needed at the end
+    int given = -1;
+    if (part == 0 && tid < p.n_tok) given = p.tokens[static_cast<int64_t>(row) * p.n_tok + tid];
 
     // A: maxima
     float tm = -INFINITY;
     int tv = -1;
-    const auto look = [&](int v) {
-        const float vm = get(v).max();
+    const auto look = [&](const Vec<T>& r, int v) {
+        const float vm = r.max();
         if (vm > tm || tv < 0) tv = v;
         tm = max_nan(tm, vm);
     };
-    bool came = true;
     if (p.staged) {
-        for (int c = 0; c < kChunks; ++c) {
-            came = came && mbar_wait(&s_bar[c], 0);
-            const int b = c == kChunks - 1 ? v1 : chunk_at(c + 1);
-            for (int v = (c == 0 ? v0 : chunk_at(c)) + tid; v < b; v += kThreads) look(v);
+        bool came = true;
+        int c = -1;  // chunks that are there
+        for (int v = f0 + tid; v < f1; v += kThreads) {
+            while (v >= chunk_at(c + 1) && c + 1 < kChunks) came = mbar_wait(&s_bar[++c], 0) && came;
+            look(data[v - v0], v);
         }
+        while (c + 1 < kChunks) came = mbar_wait(&s_bar[++c], 0) && came;
         if (!came) report(p.status, SGEMV_ERR_TIMEOUT);
     } else {
-        for (int v = v0 + tid; v < v1; v += kThreads) look(v);
+        for (int v = f0 + tid; v < f1; v += kThreads) look(fetch(v), v);
     }
+    if (edge >= 0) {
+        look(edge_x, edge);
+        if (p.staged) data[edge - v0] = edge_x;
+    }
+    T given_x = from_f32<T>(0.0f);
+    if (given >= 0 && given < p.vocab) given_x = x[given];
     // a thread's maximum is at least this key; 0 for a thread without a vector
     uint64_t key = tv >= 0 && tm == tm ? key_of(tm, tv * kN - head + kN - 1) : 0;
     float m = tm;
@@ -177,19 +253,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     if (lane == 0) s_f[0][warp] = m;
     if (p.top > 0) {
-        // the warp's maxima, descending over the lanes
-#pragma unroll
-        for (int len = 2; len <= 32; len <<= 1)
-#pragma unroll
-            for (int j = len >> 1; j > 0; j >>= 1) {
-                const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, key, j);
-                const bool keep_max = ((lane & j) == 0) == ((lane & len) == 0);
-                key = keep_max ? (key > o ? key : o) : (key < o ? key : o);
-            }
-        const int r = (p.top + kWarps - 1) / kWarps - 1;
-        if (lane == r) s_key[warp] = key;
+        // the warp's r-th largest: the largest is taken out r - 1 times
+        uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key), h = 0, l = 0;
+        for (int r = (p.top + kWarps - 1) / kWarps; r > 0; --r) {
+            h = __reduce_max_sync(0xFFFFFFFFu, hi);
+            l = __reduce_max_sync(0xFFFFFFFFu, hi == h ? lo : 0u);
+            if (hi == h && lo == l) hi = lo = 0;
+        }
+        if (lane == 0) s_key[warp] = static_cast<uint64_t>(h) << 32 | l;
     }
-    if (tid == 0) s_count = 0;
+    if (tid == 0) s_count = s_nhot = 0;
     __syncthreads();
     m = s_f[0][0];
     uint64_t bound = p.top > 0 ? s_key[0] : ~0ull;
@@ -201,30 +274,63 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     const bool usable = m < INFINITY;  // neither NaN nor +inf
 
     // B: sums and candidates. A slice of banned tokens alone (m = -inf) has sums of 0.
-    float s = 0.0f, e = 0.0f;
+    const bool near = m > 0.5f * Vec<T>::kLow && m < 1e30f;  // kLow is far below m, and kLow - m finite
+    uint64_t s2 = 0, e2 = 0;  // two sums each
     if (usable) {
-        for (bool again = false;; again = true) {
-            const float bv = bound == 0 ? -INFINITY : (p.top > 0 ? value_of(bound) : INFINITY);
-            for (int v = v0 + tid; v < v1; v += kThreads) {
-                const Vec<T> r = get(v);
-                if (!again && m > -INFINITY) {
+        if (p.top > 0 && tv >= 0 && tm >= (bound == 0 ? -INFINITY : value_of(bound))) s_hot[atomicAdd(&s_nhot, 1)] = static_cast<uint16_t>(tid);
+        if (m > -INFINITY) {
+            const uint64_t scale = pair(kLog2e, kLog2e), minus = pair(-m, -m);
+            const auto add = [&](const Vec<T>& r) {
+                if (near) {
+#pragma unroll
+                    for (int i = 0; i < kN / 2; ++i) {
+                        const float2 f = r.two(i);
+                        const uint64_t a = mul2(add2(pair(f.x, f.y), minus), scale);
+                        const float2 af = parts_of(a);
+                        const uint64_t w = pair(exp2_approx(af.x), exp2_approx(af.y));
+                        s2 = add2(s2, w);
+                        e2 = fma2(w, a, e2);
+                    }
+                } else {
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
-                        const float t = fmaxf(r.at(i) - m, -1e30f);
-                        const float w = exp2_approx(t * kLog2e);
-                        s += w;
-                        e = fmaf(w, t, e);
+                        const float a = fmaxf(r.at(i) - m, -1e30f) * kLog2e, w = exp2_approx(a);
+                        s2 = add2(s2, pair(w, 0.0f));
+                        e2 = fma2(pair(w, 0.0f), pair(a, 0.0f), e2);
                     }
                 }
-                if (p.top > 0 && r.max() >= bv) {
+            };
+            if (p.staged) {
+#pragma unroll 2
+                for (int v = f0 + tid; v < f1; v += kThreads) add(data[v - v0]);
+            } else {
+                for (int v = f0 + tid; v < f1; v += kThreads) add(fetch(v));
+            }
+            if (edge >= 0) add(edge_x);
+        }
+        __syncthreads();
+        // candidates: vector i of hot thread j, and the edges
+        const int hot = s_nhot, each = (f1 - f0 + kThreads - 1) / kThreads;
+        while (p.top > 0) {
+            const float bv = bound == 0 ? -INFINITY : value_of(bound);
+            for (int i = tid; i < hot * each + 2; i += kThreads) {
+                int v = i - hot * each == 0 ? (v0 < f0 ? v0 : -1) : (f1 < v1 ? v1 - 1 : -1);
+                if (i < hot * each) {
+                    v = f0 + s_hot[i / each] + i % each * kThreads;
+                    if (v >= f1) v = -1;
+                }
+                if (v < 0) continue;
+                const Vec<T> r = get(v);
+                uint32_t which = 0;
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const int tok = v * kN - head + i;
-                        const uint64_t k = key_of(r.at(i), tok);
-                        if (k >= bound && tok >= 0 && tok < p.vocab) {
-                            const int at = atomicAdd(&s_count, 1);
-                            if (at < kList) s_list[at] = k;
-                        }
+                for (int j = 0; j < kN; ++j) which |= r.at(j) >= bv ? 1u << j : 0u;
+                for (; which != 0; which &= which - 1) {
+                    const int j = __ffs(which) - 1, tok = v * kN - head + j;
+                    if (tok < 0 || tok >= p.vocab) continue;
+                    const uint64_t k = key_of(p.staged ? to_f32(reinterpret_cast<const T*>(&data[v - v0])[j]) : to_f32(x[tok]), tok);
+                    if (k >= bound) {
+                        const int at = atomicAdd(&s_count, 1);
+                        if (at < kList) s_list[at] = k;
                     }
                 }
             }
@@ -233,100 +339,89 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
             // too many: the list's own top-th key is a higher bound
             for (int i = tid; i < kList; i += kThreads) {
                 const uint64_t k = s_list[i];
-                int larger = 0;
-                for (int j = 0; j < kList; ++j) larger += s_list[j] > k;
-                if (larger == p.top - 1) s_key[0] = k;
+                if (count_larger(s_list, kList, k) == p.top - 1) s_key[0] = k;
             }
             __syncthreads();
             bound = s_key[0];
             if (tid == 0) s_count = 0;
             __syncthreads();
         }
+        const float2 sf = parts_of(s2), ef = parts_of(e2);
+        float s = sf.x + sf.y, e = ef.x + ef.y;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-            e += __shfl_xor_sync(0xFFFFFFFFu, e, d);
+        for (int j = 16; j > 0; j >>= 1) {
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, j);
+            e += __shfl_xor_sync(0xFFFFFFFFu, e, j);
         }
         if (lane == 0) s_f[1][warp] = s, s_f[2][warp] = e;
     }
+    if (tid == 0 && usable) s_list[s_count] = 0;
     __syncthreads();
+    if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the others' shared memory may be written
     const int cand = usable ? s_count : 0;
-    s = 0.0f, e = 0.0f;
-    if (usable)
-        for (int w = 0; w < kWarps; ++w) s += s_f[1][w], e += s_f[2][w];
+    if (tid < parts) {
+        Slice o = {m, 0.0f, 0.0f, min(cand, p.top)};
+        if (usable) {
+            for (int w = 0; w < kWarps; ++w) o.s += s_f[1][w], o.e += s_f[2][w];
+            o.e *= kLn2;
+        }
+        *cluster.map_shared_rank(&s_slice[part], tid) = o;
+    }
+    uint64_t* const best = cluster.map_shared_rank(&s_best[part * kMaxTop], 0);
     for (int i = tid; i < cand; i += kThreads) {
         const uint64_t k = s_list[i];
-        int larger = 0;
-        for (int j = 0; j < cand; ++j) larger += s_list[j] > k;
-        if (larger < p.top) s_slice.best[larger] = k;
+        const int larger = count_larger(s_list, cand, k);
+        if (larger < p.top) best[larger] = k;
     }
-    if (tid == 0) s_slice.m = m, s_slice.s = s, s_slice.e = e, s_slice.n = min(cand, p.top);
+    if (tid >= min(cand, p.top) && tid < kMaxTop) best[tid] = 0;
+    if (parts > 1) cluster.sync();
+    else __syncthreads();
 
     // The whole row's, in every CTA of its cluster.
-    float lse_m = m, sum = s, ent = e;
-    if (parts > 1) {
-        cluster.sync();
-        float pm[kMaxCluster];
+    float rm = s_slice[0].m, sum = 0.0f, ent = 0.0f;
+    for (int i = 1; i < parts; ++i) rm = max_nan(rm, s_slice[i].m);
+    const bool bad = !(rm < INFINITY), none = rm == -INFINITY;
+    if (!bad && !none)
         for (int i = 0; i < parts; ++i) {
-            pm[i] = cluster.map_shared_rank(&s_slice, i)->m;
-            lse_m = i == 0 ? pm[0] : max_nan(lse_m, pm[i]);
+            const Slice o = s_slice[i];
+            if (o.m == -INFINITY) continue;
+            const float t = o.m - rm, f = exp2_approx(t * kLog2e), si = o.s * f;  // sums about o.m, moved to rm
+            sum += si;
+            ent += si == 0.0f ? 0.0f : fmaf(si, t, o.e * f);
         }
-        sum = 0.0f, ent = 0.0f;
-        if (lse_m < INFINITY && lse_m > -INFINITY)
-            for (int i = 0; i < parts; ++i) {
-                if (pm[i] == -INFINITY) continue;
-                const Slice* o = cluster.map_shared_rank(&s_slice, i);
-                // sums about pm[i], moved to lse_m
-                const float d = pm[i] - lse_m, f = exp2_approx(d * kLog2e), si = o->s * f;
-                sum += si;
-                ent += si == 0.0f ? 0.0f : fmaf(si, d, o->e * f);
-            }
-        // the first CTA's list becomes all slices' best
-        if (part == 0) {
-            for (int i = tid; i < parts * p.top; i += kThreads) {
-                const Slice* o = cluster.map_shared_rank(&s_slice, i / p.top);
-                s_list[i] = i % p.top < o->n ? o->best[i % p.top] : 0;
-            }
-        }
-    } else {
-        __syncthreads();
-    }
-    const bool bad = !(lse_m < INFINITY), none = lse_m == -INFINITY;
     const float kNan = __int_as_float(0x7FC00000), log_s = logf(sum);
-    const auto lp = [&](float f) { return bad ? kNan : (none ? -INFINITY : (f - lse_m) - log_s); };
+    const auto lp = [&](float f) { return bad ? kNan : (none ? -INFINITY : (f - rm) - log_s); };
     if (part == 0) {
-        if (parts > 1) __syncthreads();
         if (tid == 0) {
             if (bad) report(p.status, SGEMV_ERR_NONFINITE);
-            if (p.lse != nullptr) p.lse[row] = bad ? kNan : (none ? -INFINITY : lse_m + log_s);
+            if (p.lse != nullptr) p.lse[row] = bad ? kNan : (none ? -INFINITY : rm + log_s);
             if (p.entropy != nullptr) p.entropy[row] = bad ? kNan : (none ? 0.0f : log_s - ent / sum);
         }
-        for (int j = tid; j < p.n_tok; j += kThreads) {
-            const int t = p.tokens[static_cast<int64_t>(row) * p.n_tok + j];
+        if (tid < p.n_tok) {
             float v = 0.0f;
-            if (t >= 0 && t < p.vocab) v = lp(to_f32(x[t]));
-            else if (t != -1) {
+            if (given >= 0 && given < p.vocab) v = lp(to_f32(given_x));
+            else if (given != -1) {
                 v = kNan;
                 report(p.status, SGEMV_ERR_ARG);
             }
-            p.tok_logp[static_cast<int64_t>(row) * p.n_tok + j] = v;
+            p.tok_logp[static_cast<int64_t>(row) * p.n_tok + tid] = v;
         }
+        int found = 0;  // entries of all lists
+        for (int i = 0; i < parts; ++i) found += s_slice[i].n;
+        if (bad) found = 0;
         const int64_t o = static_cast<int64_t>(row) * p.top;
-        const auto put = [&](int rank, uint64_t k) {
-            p.top_tok[o + rank] = bad || k == 0 ? -1 : token_of(k);
-            p.top_logp[o + rank] = bad ? kNan : (k == 0 ? -INFINITY : lp(value_of(k)));
-        };
-        if (parts == 1) {
-            for (int j = tid; j < p.top; j += kThreads) put(j, !bad && j < s_slice.n ? s_slice.best[j] : 0);
-        } else {
-            const int n = parts * p.top;
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t k = s_list[i];
-                int rank = 0;
-                for (int j = 0; j < n; ++j) rank += s_list[j] > k || (s_list[j] == k && j < i);  // only the empty ones are equal
-                if (rank < p.top) put(rank, bad ? 0 : k);
+        for (int i = tid; i < parts * p.top && found > 0; i += kThreads) {
+            int rank = i % p.top;
+            const uint64_t k = s_best[i / p.top * kMaxTop + rank];
+            if (k == 0) continue;
+            if (parts > 1) {
+                rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < parts; ++j) rank += count_larger_sorted(s_best + j * kMaxTop, k);
             }
+            if (rank < p.top) p.top_tok[o + rank] = token_of(k), p.top_logp[o + rank] = lp(value_of(k));
         }
+        for (int j = found + tid; j < p.top; j += kThreads) p.top_tok[o + j] = -1, p.top_logp[o + j] = bad ? kNan : -INFINITY;
     }
     if (p.logp != nullptr) {
         float* const out = p.logp + static_cast<int64_t>(row) * p.vocab;
@@ -338,7 +433,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
             for (int t = t0 + tid; t < t1; t += kThreads) out[t] = lp(to_f32(x[t]));
         }
     }
-    if (parts > 1) cluster.sync();  // the first CTA has read the others' shared memory
 }
 
 template <typename T, int kThreads>
@@ -376,7 +470,7 @@ cudaError_t launch_logprobs(LogprobParams p, int sms, cudaStream_t s) {
     const int64_t nv = (static_cast<int64_t>(p.vocab) + 2 * Vec<T>::kN - 2) / Vec<T>::kN;  // with any alignment
     // One CTA a row while two fit an SM; more where slices are longer, or rows too few to fill the GPU with slices of 4 KB.
     int parts = 1;
-    while (parts < kMaxCluster && (nv * 16 > 92 * 1024 * static_cast<int64_t>(parts) ||
+    while (parts < kMaxCluster && (nv * 16 > 98 * 1024 * static_cast<int64_t>(parts) ||
                                    (static_cast<int64_t>(p.rows) * parts * 2 <= sms && nv > 512 * parts)))
         parts *= 2;
     const int64_t slice = (nv + parts - 1) / parts * 16;
