@@ -57,17 +57,18 @@ struct Slice {
     int n;
 };
 
-// Larger for a larger logit; equal logits by the lower token. -0 counts as +0. Never 0 for a real element.
-__device__ __forceinline__ uint64_t key_of(float x, int tok) {
+// Larger for a larger value, -0 as +0, NaN (as max_nan gives it) above +inf; never 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
     uint32_t u = __float_as_uint(x);
     if ((u & 0x7FFFFFFFu) == 0) u = 0;
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return (static_cast<uint64_t>(u) << 32) | static_cast<uint32_t>(~tok);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint64_t key) {
-    const uint32_t u = static_cast<uint32_t>(key >> 32);
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+__device__ __forceinline__ float of_order(uint32_t u) { return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u); }
+// Larger for a larger logit; equal logits by the lower token. Never 0 for a real element.
+__device__ __forceinline__ uint64_t key_of(float x, int tok) {
+    return (static_cast<uint64_t>(order_of(x)) << 32) | static_cast<uint32_t>(~tok);
 }
+__device__ __forceinline__ float value_of(uint64_t key) { return of_order(static_cast<uint32_t>(key >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -158,13 +159,14 @@ struct Vec {
 };
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const LogprobParams p) {
     constexpr int kWarps = kThreads / 32, kN = Vec<T>::kN;
     extern __shared__ __align__(16) uint8_t s_data[];  // the slice
     __shared__ __align__(16) uint64_t s_list[kList + 2];
     __shared__ __align__(16) uint64_t s_best[kMaxCluster * kMaxTop];  // of each slice, highest first (in the first CTA)
     __shared__ Slice s_slice[kMaxCluster];
-    __shared__ float s_f[3][kWarps];
+    __shared__ float s_f[2][kWarps];
+    __shared__ uint32_t s_most[kWarps];
     __shared__ uint64_t s_key[kWarps];
     __shared__ uint16_t s_hot[kThreads];
     __shared__ int s_count, s_nhot;
@@ -172,7 +174,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = static_cast<int>(cluster.num_blocks()), part = static_cast<int>(cluster.block_rank());
-    const int row = blockIdx.x / parts;
     if (tid < kChunks) mbar_init(&s_bar[tid], 1);
     if (tid == 0) mbar_fence_init();
     __syncthreads();
@@ -180,45 +181,64 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     pdl_launch_dependents();
     pdl_wait();
 
-    // The row in vectors of 16 aligned bytes: vector v holds tokens kN v - head .. ; this CTA has [v0, v1).
-    const T* const x = static_cast<const T*>(p.logits) + row * p.stride;
-    const int head = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-    const int nv = (head + p.vocab + kN - 1) / kN;
-    const int v0 = static_cast<int>(static_cast<int64_t>(nv) * part / parts), v1 = static_cast<int>(static_cast<int64_t>(nv) * (part + 1) / parts);
-    const int f0 = max(v0, head > 0 ? 1 : 0), f1 = max(f0, min(v1, (head + p.vocab) / kN));  // whole ones
-    const auto fetch = [&](int v) {  // from global memory; -inf where there is no token
-        Vec<T> r;
-        if (v >= f0 && v < f1) {
-            r.w = *reinterpret_cast<const uint4*>(x + (static_cast<int64_t>(v) * kN - head));
-        } else {
-            T* h = reinterpret_cast<T*>(&r.w);
+    Vec<T>* const data = reinterpret_cast<Vec<T>*>(s_data);
+    // A row in vectors of 16 aligned bytes: vector v holds tokens kN v - head .. ; this CTA has [v0, v1), and [f0, f1) are whole.
+    struct Row {
+        const T* x;
+        int head, v0, v1, f0, f1, chunk;
+        __device__ __forceinline__ int chunk_at(int c) const { return min(f1, f0 + chunk * c); }
+        __device__ __forceinline__ Vec<T> fetch(int v, int vocab) const {  // from global memory; -inf where there is no token
+            Vec<T> r;
+            if (v >= f0 && v < f1) {
+                r.w = *reinterpret_cast<const uint4*>(x + (static_cast<int64_t>(v) * kN - head));
+            } else {
+                T* h = reinterpret_cast<T*>(&r.w);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int tok = v * kN - head + i;
-                h[i] = tok >= 0 && tok < p.vocab ? x[tok] : from_f32<T>(-INFINITY);
+                for (int i = 0; i < kN; ++i) {
+                    const int tok = v * kN - head + i;
+                    h[i] = tok >= 0 && tok < vocab ? x[tok] : from_f32<T>(-INFINITY);
+                }
             }
+            return r;
         }
+    };
+    // What a thread holds of a row from its start on: its vector, if the first or the last one is not whole (threads 32 and 33),
+    // and a token asked for.
+    struct Held {
+        int edge, given;
+        Vec<T> x;
+    };
+    const auto start = [&](int row, Held& held) {
+        Row r;
+        r.x = static_cast<const T*>(p.logits) + row * p.stride;
+        r.head = static_cast<int>((reinterpret_cast<uintptr_t>(r.x) & 15u) / sizeof(T));
+        const int nv = (r.head + p.vocab + kN - 1) / kN;
+        r.v0 = parts == 1 ? 0 : static_cast<int>(static_cast<int64_t>(nv) * part / parts);
+        r.v1 = parts == 1 ? nv : static_cast<int>(static_cast<int64_t>(nv) * (part + 1) / parts);
+        r.f0 = max(r.v0, r.head > 0 ? 1 : 0), r.f1 = max(r.f0, min(r.v1, (r.head + p.vocab) / kN));
+        r.chunk = ((r.f1 - r.f0 + kChunks - 1) / kChunks + kThreads - 1) / kThreads * kThreads;  // a vector a thread or several
+        if (p.staged && tid < kChunks) {
+            const int a = r.chunk_at(tid), b = r.chunk_at(tid + 1);
+            mbar_arrive_expect_tx(&s_bar[tid], static_cast<uint32_t>(b - a) * 16);
+            if (b > a)
+                bulk_g2s(&data[a - r.v0], r.x + (static_cast<int64_t>(a) * kN - r.head), static_cast<uint32_t>(b - a) * 16, &s_bar[tid]);
+        }
+        held.edge = tid == 32 && r.v0 < r.f0 ? r.v0 : (tid == 33 && r.f1 < r.v1 ? r.v1 - 1 : -1);
+        if (held.edge >= 0) held.x = r.fetch(held.edge, p.vocab);
+        held.given = part == 0 && tid < p.n_tok ? p.tokens[static_cast<int64_t>(row) * p.n_tok + tid] : -1;
         return r;
     };
-    Vec<T>* const data = reinterpret_cast<Vec<T>*>(s_data);
-    const auto get = [&](int v) { return p.staged ? data[v - v0] : fetch(v); };
-    // chunk c of the whole vectors: a vector a thread or several
-    const int chunk = ((f1 - f0 + kChunks - 1) / kChunks + kThreads - 1) / kThreads * kThreads;
-    const auto chunk_at = [&](int c) { return min(f1, f0 + chunk * c); };
-    if (p.staged) {
-        if (tid < kChunks) {
-            const int a = chunk_at(tid), b = chunk_at(tid + 1);
-            mbar_arrive_expect_tx(&s_bar[tid], static_cast<uint32_t>(b - a) * 16);
-            if (b > a) bulk_g2s(&data[a - v0], x + (static_cast<int64_t>(a) * kN - head), static_cast<uint32_t>(b - a) * 16, &s_bar[tid]);
-        }
-    }
-    // The first and the last vector, where they are not whole: a thread each, from registers.
-    const int edge = tid == 32 && v0 < f0 ? v0 : (tid == 33 && f1 < v1 ? v1 - 1 : -1);
-    Vec<T> edge_x;
-    if (edge >= 0) edge_x = fetch(edge);
-    // a token asked for, a thread: needed at the end
-    int given = -1;
-    if (part == 0 && tid < p.n_tok) given = p.tokens[static_cast<int64_t>(row) * p.n_tok + tid];
+
+    int row = blockIdx.x / parts;
+    const int rows_apart = gridDim.x / parts;
+    Held next_held = {-1, -1, {}};
+    Row next_row = start(row, next_held);
+    for (uint32_t parity = 0; row < p.rows; row += rows_apart, parity ^= 1) {
+    const Row r = next_row;
+    const Held held = next_held;
+    const T* const x = r.x;
+    const int head = r.head, v0 = r.v0, v1 = r.v1, f0 = r.f0, f1 = r.f1, edge = held.edge, given = held.given;
+    const auto get = [&](int v) { return p.staged ? data[v - v0] : r.fetch(v, p.vocab); };
 
     // A: maxima
     float tm = -INFINITY;
@@ -230,28 +250,29 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     };
     if (p.staged) {
         bool came = true;
-        int c = -1;  // chunks that are there
-        for (int v = f0 + tid; v < f1; v += kThreads) {
-            while (v >= chunk_at(c + 1) && c + 1 < kChunks) came = mbar_wait(&s_bar[++c], 0) && came;
-            look(data[v - v0], v);
+        for (int c = 0; c < kChunks; ++c) {
+            came = mbar_wait(&s_bar[c], parity) && came;
+            const int end = r.chunk_at(c + 1);
+#pragma unroll 2
+            for (int v = r.chunk_at(c) + tid; v < end; v += kThreads) look(data[v - v0], v);
         }
-        while (c + 1 < kChunks) came = mbar_wait(&s_bar[++c], 0) && came;
         if (!came) report(p.status, SGEMV_ERR_TIMEOUT);
     } else {
-        for (int v = f0 + tid; v < f1; v += kThreads) look(fetch(v), v);
+        for (int v = f0 + tid; v < f1; v += kThreads) look(r.fetch(v, p.vocab), v);
     }
     if (edge >= 0) {
-        look(edge_x, edge);
-        if (p.staged) data[edge - v0] = edge_x;
+        look(held.x, edge);
+        if (p.staged) {
+            data[edge - v0] = held.x;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next row's copies may write there
+        }
     }
     T given_x = from_f32<T>(0.0f);
     if (given >= 0 && given < p.vocab) given_x = x[given];
     // a thread's maximum is at least this key; 0 for a thread without a vector
     uint64_t key = tv >= 0 && tm == tm ? key_of(tm, tv * kN - head + kN - 1) : 0;
-    float m = tm;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    if (lane == 0) s_f[0][warp] = m;
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, order_of(tm));
+    if (lane == 0) s_most[warp] = most;
     if (p.top > 0) {
         // the warp's r-th largest: the largest is taken out r - 1 times
         uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key), h = 0, l = 0;
@@ -264,12 +285,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     }
     if (tid == 0) s_count = s_nhot = 0;
     __syncthreads();
-    m = s_f[0][0];
-    uint64_t bound = p.top > 0 ? s_key[0] : ~0ull;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        m = max_nan(m, s_f[0][w]);
-        if (p.top > 0) bound = min(bound, s_key[w]);
+    // (a warp's lanes read all warps' and reduce them again)
+    const float m = of_order(__reduce_max_sync(0xFFFFFFFFu, s_most[lane % kWarps]));
+    uint64_t bound = ~0ull;
+    if (p.top > 0) {
+        const uint64_t k = s_key[lane % kWarps];
+        const uint32_t hi = static_cast<uint32_t>(k >> 32), h = __reduce_min_sync(0xFFFFFFFFu, hi);
+        const uint32_t l = __reduce_min_sync(0xFFFFFFFFu, hi == h ? static_cast<uint32_t>(k) : 0xFFFFFFFFu);
+        bound = static_cast<uint64_t>(h) << 32 | l;
     }
     const bool usable = m < INFINITY;  // neither NaN nor +inf
 
@@ -280,11 +303,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
         if (p.top > 0 && tv >= 0 && tm >= (bound == 0 ? -INFINITY : value_of(bound))) s_hot[atomicAdd(&s_nhot, 1)] = static_cast<uint16_t>(tid);
         if (m > -INFINITY) {
             const uint64_t scale = pair(kLog2e, kLog2e), minus = pair(-m, -m);
-            const auto add = [&](const Vec<T>& r) {
+            const auto add = [&](const Vec<T>& y) {
                 if (near) {
 #pragma unroll
                     for (int i = 0; i < kN / 2; ++i) {
-                        const float2 f = r.two(i);
+                        const float2 f = y.two(i);
                         const uint64_t a = mul2(add2(pair(f.x, f.y), minus), scale);
                         const float2 af = parts_of(a);
                         const uint64_t w = pair(exp2_approx(af.x), exp2_approx(af.y));
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
                 } else {
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
-                        const float a = fmaxf(r.at(i) - m, -1e30f) * kLog2e, w = exp2_approx(a);
+                        const float a = fmaxf(y.at(i) - m, -1e30f) * kLog2e, w = exp2_approx(a);
                         s2 = add2(s2, pair(w, 0.0f));
                         e2 = fma2(pair(w, 0.0f), pair(a, 0.0f), e2);
                     }
@@ -304,26 +327,30 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
 #pragma unroll 2
                 for (int v = f0 + tid; v < f1; v += kThreads) add(data[v - v0]);
             } else {
-                for (int v = f0 + tid; v < f1; v += kThreads) add(fetch(v));
+                for (int v = f0 + tid; v < f1; v += kThreads) add(r.fetch(v, p.vocab));
             }
-            if (edge >= 0) add(edge_x);
+            if (edge >= 0) add(held.x);
         }
         __syncthreads();
         // candidates: vector i of hot thread j, and the edges
-        const int hot = s_nhot, each = (f1 - f0 + kThreads - 1) / kThreads;
+        const int hot = s_nhot, each = (f1 - f0 + kThreads - 1) / kThreads;  // vectors a thread has
+        const int lg = 32 - __clz(max(each, 1) - 1);                         // and the next power of two
         while (p.top > 0) {
             const float bv = bound == 0 ? -INFINITY : value_of(bound);
-            for (int i = tid; i < hot * each + 2; i += kThreads) {
-                int v = i - hot * each == 0 ? (v0 < f0 ? v0 : -1) : (f1 < v1 ? v1 - 1 : -1);
-                if (i < hot * each) {
-                    v = f0 + s_hot[i / each] + i % each * kThreads;
-                    if (v >= f1) v = -1;
+            for (int i = tid; i < ((hot + 2) << lg); i += kThreads) {
+                const int j0 = i >> lg, at = i & ((1 << lg) - 1);
+                int v = -1;
+                if (j0 < hot) {
+                    v = f0 + s_hot[j0] + at * kThreads;
+                    if (at >= each || v >= f1) v = -1;
+                } else if (at == 0) {
+                    v = j0 == hot ? (v0 < f0 ? v0 : -1) : (f1 < v1 ? v1 - 1 : -1);
                 }
                 if (v < 0) continue;
-                const Vec<T> r = get(v);
+                const Vec<T> y = get(v);
                 uint32_t which = 0;
 #pragma unroll
-                for (int j = 0; j < kN; ++j) which |= r.at(j) >= bv ? 1u << j : 0u;
+                for (int j = 0; j < kN; ++j) which |= y.at(j) >= bv ? 1u << j : 0u;
                 for (; which != 0; which &= which - 1) {
                     const int j = __ffs(which) - 1, tok = v * kN - head + j;
                     if (tok < 0 || tok >= p.vocab) continue;
@@ -353,16 +380,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
             s += __shfl_xor_sync(0xFFFFFFFFu, s, j);
             e += __shfl_xor_sync(0xFFFFFFFFu, e, j);
         }
-        if (lane == 0) s_f[1][warp] = s, s_f[2][warp] = e;
+        if (lane == 0) s_f[0][warp] = s, s_f[1][warp] = e;
     }
     if (tid == 0 && usable) s_list[s_count] = 0;
     __syncthreads();
+    // The row's data is not needed any more, but where it is written out whole: the next row's copies go on from here.
+    if (p.logp == nullptr && row + rows_apart < p.rows) next_row = start(row + rows_apart, next_held);
     if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the others' shared memory may be written
     const int cand = usable ? s_count : 0;
     if (tid < parts) {
         Slice o = {m, 0.0f, 0.0f, min(cand, p.top)};
         if (usable) {
-            for (int w = 0; w < kWarps; ++w) o.s += s_f[1][w], o.e += s_f[2][w];
+            for (int w = 0; w < kWarps; ++w) o.s += s_f[0][w], o.e += s_f[1][w];
             o.e *= kLn2;
         }
         *cluster.map_shared_rank(&s_slice[part], tid) = o;
@@ -377,7 +406,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     if (parts > 1) cluster.sync();
     else __syncthreads();
 
-    // The whole row's, in every CTA of its cluster.
+    // The whole row's, in every CTA of its cluster that writes something.
+    const int writers = p.logp != nullptr ? kThreads : (part == 0 ? max(max(1, p.n_tok), parts * p.top) : 0);
+    if ((tid & ~31) < writers) {
     float rm = s_slice[0].m, sum = 0.0f, ent = 0.0f;
     for (int i = 1; i < parts; ++i) rm = max_nan(rm, s_slice[i].m);
     const bool bad = !(rm < INFINITY), none = rm == -INFINITY;
@@ -433,10 +464,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
             for (int t = t0 + tid; t < t1; t += kThreads) out[t] = lp(to_f32(x[t]));
         }
     }
+    }
+    if (row + rows_apart < p.rows) {
+        __syncthreads();  // the lists and the data are free
+        if (p.logp != nullptr) next_row = start(row + rows_apart, next_held);
+    }
+    }
 }
 
 template <typename T, int kThreads>
-cudaError_t launch_rows(const LogprobParams& p, int parts, uint32_t smem, cudaStream_t s) {
+cudaError_t launch_rows(const LogprobParams& p, int parts, uint32_t smem, int sms, cudaStream_t s) {
     auto kern = logprobs_kernel<T, kThreads>;
     static std::atomic<int> attr_smem[64];  // per device: dynamic shared memory already enabled
     int dev = 0;
@@ -449,7 +486,10 @@ cudaError_t launch_rows(const LogprobParams& p, int parts, uint32_t smem, cudaSt
         attr_smem[dev].store(static_cast<int>(smem));
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * parts);
+    // resident CTAs: by threads (registers allow as many) and by shared memory, with the kernel's own and what each CTA costs
+    const int resident = sms * std::max(1, std::min(1024 / kThreads, static_cast<int>(228 * 1024 / (smem + 14 * 1024 + 512))));
+    // CTAs that have a row to themselves take several, one after another, with the next row's copies under way
+    cfg.gridDim = dim3(parts > 1 ? static_cast<unsigned>(p.rows) * parts : static_cast<unsigned>(std::min(p.rows, resident)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -477,8 +517,10 @@ cudaError_t launch_logprobs(LogprobParams p, int sms, cudaStream_t s) {
     p.staged = slice <= 196 * 1024;  // else the passes read global memory
     const uint32_t smem = p.staged ? static_cast<uint32_t>(slice) : 0;
     if (static_cast<int64_t>(p.rows) * parts > INT_MAX) return cudaErrorInvalidValue;
-    // four warps where a slice gives 16 no more than a vector a thread (then every element fits the list)
-    return slice >= 16 * 1024 ? launch_rows<T, 512>(p, parts, smem, s) : launch_rows<T, 128>(p, parts, smem, s);
+    // four warps where a slice gives 16 no more than a vector a thread (then every element fits the list); eight where there
+    // are rows enough to fill the GPU, since each warp of a row costs about 500 instructions whatever its length
+    if (slice < 16 * 1024) return launch_rows<T, 128>(p, parts, smem, sms, s);
+    return static_cast<int64_t>(p.rows) * parts > 2 * sms ? launch_rows<T, 256>(p, parts, smem, sms, s) : launch_rows<T, 512>(p, parts, smem, sms, s);
 }
 
 }  // namespace
