@@ -1,9 +1,12 @@
 // Attention over the paged 4-bit KV cache: the entry point (argument checks, choice of the kernel).
-#include "kv_decode.cuh"
+#include <climits>
+
+#include "kv_chunk.cuh"
 
 namespace sgemv {
 cudaError_t launch_decode_f16(int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
 cudaError_t launch_decode_bf16(int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
+cudaError_t launch_chunk(int dtype, int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
 }  // namespace sgemv
 
 using namespace sgemv;
@@ -51,7 +54,11 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     rc = device_info(&di);
     if (rc != SGEMV_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = q.dtype == SGEMV_F16 ? launch_decode_f16(layout->dim, layout->group, p, di.sm_count, s)
-                                               : launch_decode_bf16(layout->dim, layout->group, p, di.sm_count, s);
+    // Requests with many rows go to the chunk kernel, whose tensor memory holds dims up to 128.
+    const bool chunks = layout->dim <= 128 && static_cast<int64_t>(q.max_q) * p.ratio > kChunkMinRows;
+    p.max_rows = chunks ? kChunkMinRows : INT_MAX;
+    cudaError_t e = q.dtype == SGEMV_F16 ? launch_decode_f16(layout->dim, layout->group, p, di.sm_count, s)
+                                         : launch_decode_bf16(layout->dim, layout->group, p, di.sm_count, s);
+    if (e == cudaSuccess && chunks) e = launch_chunk(q.dtype, layout->dim, layout->group, p, di.sm_count, s);
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }

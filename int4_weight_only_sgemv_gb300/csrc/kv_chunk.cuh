@@ -1,0 +1,613 @@
+// Attention over the paged 4-bit KV cache: the kernel of prompt chunks (requests with many rows of queries).
+//
+// With many rows the products bound the work, not the cache's bytes: 4 D operations a (row, key) against D / 2 + 4 bytes a
+// key. So they go to the 5th-generation tensor cores, S = x K^T and O += P V with 128 x 128 x 16 instructions, and one
+// CTA holds two 128-row tiles of queries against each 128-key tile that it unpacks, which halves the unpacking a product
+// needs. Roles, by warp:
+//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory in 32-column pieces (once
+//             for the maximum, once for the weights), weights back to tensor memory in fp16, over S
+//   8-11      unpack: raw subtiles -> K's integers q - z [key][dim] and V [dim][key] in fp16, both swizzled for the tensor cores,
+//             two buffers each, and K's scales
+//   12        issues the products      13  issues the copies of raw subtiles (copy engine, 64 keys a stage)
+// The two row tiles alternate, so that the products of one run while the other's softmax does.
+//
+// Roundings: scores have none but the sums' in 32 bits: x is fp16 (scaled by a power of two a row, exact), K's integers are exact,
+// and the softmax multiplies a column by its scale. Where a key has two groups, each has sums of its own (and a tile is 64 keys).
+// The weights are rounded to fp16, 11 bits, as in the decode kernel. V's values (q - z) s have up to 15 bits: they are formed as
+// ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale need be kept a column. The softmax's reference m
+// moves only when the maximum passes it by 2^9 (kLimit - kTop), so O is rarely rescaled.
+//
+// Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the last CTA to arrive joins.
+#pragma once
+
+#include "kv_decode.cuh"
+
+namespace sgemv {
+
+constexpr int kChunkMinRows = 64;  // requests with more rows (new tokens x query heads of a KV head) come here
+
+template <int D, int G>
+struct ChunkShape {
+    static constexpr int kGroups = D / G;
+    static constexpr int kSubBytes = 16 * D + 128 * kGroups;
+    static constexpr int kRows = 256, kTile = 128;                // rows of a CTA and of a row tile
+    static constexpr int kKeys = 128 / kGroups;                   // keys of a tile: kGroups sums of it are 128 columns
+    static constexpr int kHalves = kKeys / 64;                    // raw stages of a tile
+    static constexpr int kRawSubs = 4, kRawStages = 3;            // subtiles of a raw stage
+    static constexpr int kRawBytes = kRawSubs * kSubBytes;
+    static constexpr int kAtoms = D / 64;                         // 128-byte columns of a row of x or K
+    static constexpr int kQBytes = kTile * D * 2, kKBytes = kKeys * D * 2, kVBytes = D * kKeys * 2;
+    static constexpr int kThreads = 14 * 32;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + kRawStages * kRawBytes;
+    static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
+    static constexpr int kCols = 512;                             // tensor memory: S0, S1, O0, O1
+};
+
+__device__ __forceinline__ void tc_alloc(uint32_t* smem_slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_slot)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// d += a b (or d = a b): both operands in shared memory, or a in tensor memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+                 : "memory");
+}
+#define SGEMV_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define SGEMV_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+// 32 columns of this warp's 32 lanes, one lane a thread.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : SGEMV_R8(r, 0), SGEMV_R8(r, 8), SGEMV_R8(r, 16), SGEMV_R8(r, 24)
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+                 SGEMV_I8(r, 0), SGEMV_I8(r, 8), SGEMV_I8(r, 16), SGEMV_I8(r, 24)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 SGEMV_I8(r, 0), SGEMV_I8(r, 8)
+                 : "memory");
+}
+#undef SGEMV_R8
+#undef SGEMV_I8
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Operand descriptor: rows of 128 bytes (64 fp16 along the product's inner axis), 128-byte swizzle, 8 rows every 1024 bytes.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// fp16 operands, 32-bit sums, both operands with the inner axis contiguous, 128 x n.
+__host__ __device__ constexpr uint32_t tc_idesc(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n / 8) << 17) | ((128u / 16u) << 24);
+}
+
+// Segments (row tile pairs x heads) of a request that comes here.
+template <int kRows>
+__device__ __forceinline__ int64_t chunk_segments(const AttnParams& p, const Span& s) {
+    const int rows = s.n * p.ratio;
+    return rows > kChunkMinRows ? static_cast<int64_t>((rows + kRows - 1) / kRows) * p.heads : 0;
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(const AttnParams p) {
+    using S = ChunkShape<D, G>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t* const s_q = smem;
+    uint8_t* const s_k = s_q + 2 * S::kQBytes;
+    uint8_t* const s_v = s_k + 2 * S::kKBytes;
+    uint8_t* const s_raw = s_v + 2 * S::kVBytes;
+    __shared__ __align__(16) float s_scale[2][S::kGroups][S::kKeys];  // of K's groups
+    __shared__ __align__(8) uint64_t raw_full[S::kRawStages], raw_free[S::kRawStages], k_full[2], k_free[2], v_full[2], v_free[2];
+    __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int64_t s_sum[14];
+    __shared__ int s_req, s_bad, s_last;
+    __shared__ int64_t s_before;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < S::kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 128), mbar_init(&k_free[i], 1);
+            mbar_init(&v_full[i], 128), mbar_init(&v_free[i], 1);
+            mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
+        }
+        mbar_init(&q_full, 256);
+        mbar_fence_init();
+        s_req = -1, s_bad = 0;
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // The request whose segment this CTA has. Thread x has requests [x * run, (x + 1) * run).
+    const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
+    int64_t mine = 0;
+    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += chunk_segments<S::kRows>(p, span_of(p, r));
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+    for (int w = 0; w < 14; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    // fewer segments than SMs are split over the keys (the workspace has a partial for each of kMaxCtas CTAs)
+    const int splits = total == 0 || total * 2 > kMaxCtas ? 1 : static_cast<int>(kMaxCtas / total);
+    if (blockIdx.x >= total * splits) return;
+    // heavier segments (more keys before them) first
+    const int64_t want = total - 1 - blockIdx.x / splits;
+    const int part = blockIdx.x % splits;
+    if (want >= before && want < before + mine) {
+        for (int r = tid * run;; ++r) {
+            const int64_t n = chunk_segments<S::kRows>(p, span_of(p, r));
+            if (want < before + n) {
+                s_req = r, s_before = before;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    const int req = s_req;
+    const Span sp = span_of(p, req);
+    const int in_req = static_cast<int>(want - s_before);
+    const int head = in_req % p.heads, row0 = in_req / p.heads * S::kRows, rows = sp.n * p.ratio, old = sp.len - sp.n;
+    Keys keys = keys_of(p, sp, row0, S::kRows);
+    keys.lo = keys.lo / S::kKeys * S::kKeys;
+    const int all_tiles = max(1, (keys.hi - keys.lo + S::kKeys - 1) / S::kKeys);
+    const int parts = min(splits, max(1, all_tiles / 2));  // two tiles a split at least
+    if (part >= parts) return;
+    const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * part / parts);
+    const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (part + 1) / parts) - tile0;
+    const int key0 = keys.lo + tile0 * S::kKeys;
+    const int32_t* const table = p.q.table_dev + req * p.q.table_stride;
+    // page ids outside the cache are looked for beforehand
+    for (int b = (key0 >> p.log2_page) + tid; b << p.log2_page < min(keys.hi, key0 + tiles * S::kKeys); b += S::kThreads) {
+        const int id = table[b];
+        if (id < 0 || id >= p.n_pages) {
+            report(p.status, SGEMV_ERR_ARG);
+            s_bad = 1;
+        }
+    }
+    if (warp == 12) tc_alloc(&s_tmem, S::kCols);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = s_tmem;
+    const bool any_bad = s_bad != 0;
+    const auto lost = [&](int pos) {  // the page of a position is outside the cache
+        const int id = table[pos >> p.log2_page];
+        return id < 0 || id >= p.n_pages;
+    };
+    bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (dead || mbar_wait(bar, parity)) return;
+        dead = true;
+        report(p.status, SGEMV_ERR_TIMEOUT);
+    };
+    const int halves = S::kHalves * tiles;  // raw stages of this CTA
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------------------------------- softmax
+        const int x = warp >> 2, r = tid & 127, row = row0 + 128 * x + r;
+        const bool live = row < rows;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
+        const int i = min(row, rows - 1) / p.ratio;
+        // x: this thread's row, to shared memory; dims in the order 0 4 1 5 2 6 3 7 of each 8, as K's nibbles come out
+        float c;
+        {
+            const T* src = static_cast<const T*>(p.q.q_dev) + (sp.first + i) * p.q.q_token_stride +
+                           (head * p.ratio + min(row, rows - 1) % p.ratio) * p.q.q_head_stride;
+            float big = 0.0f;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                const uint4 w = *reinterpret_cast<const uint4*>(src + d);
+                const T* h = reinterpret_cast<const T*>(&w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
+            }
+            const int be = static_cast<int>(__float_as_uint(big) >> 23);
+            const int sh = be == 0 || be == 255 ? 0 : min(max(127 + 9 - be, -100), 100);
+            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), p.scale_log2);
+            c = p.scale_log2 / up;  // not negative
+            uint8_t* const dst = s_q + x * S::kQBytes + r * 128;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                uint4 w = live ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+                const T* h = reinterpret_cast<const T*>(&w);
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = to_f32(h[j]) * up;
+                const uint4 o = make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7]));
+                *reinterpret_cast<uint4*>(dst + d / 64 * (128 * 128) + (((d / 8) & 7) ^ (r & 7)) * 16) = o;
+            }
+            fence_async();
+            mbar_arrive(&q_full);
+        }
+        const int last = old + i, first = p.q.window > 0 ? last - p.q.window + 1 : 0;
+        const uint64_t tree = p.q.tree_dev != nullptr ? p.q.tree_dev[sp.first + i] : 0;
+        // positions [clear0, clear1) are seen by every row of this row tile
+        const int ia = min(row0 + 128 * x, rows - 1) / p.ratio, ib = min(row0 + 128 * x + 127, rows - 1) / p.ratio;
+        const int clear1 = any_bad ? 0 : (p.q.tree_dev != nullptr ? old : old + ia + 1);
+        const int clear0 = p.q.window > 0 ? old + ib - p.q.window + 1 : 0;
+        float ref = 0.0f, lim = -INFINITY, l = 0.0f;
+        for (int j = 0; j < tiles; ++j) {
+            const int pos0 = key0 + j * S::kKeys;
+            wait(&s_full[x], j & 1);
+            wait(&k_full[j & 1], (j >> 1) & 1);  // long since: makes the scales visible
+            __syncwarp();
+            tc_after_sync();
+            const bool plain = pos0 >= clear0 && pos0 + S::kKeys <= clear1;
+            // columns 32 q .. of this row: sums times scales, -inf where masked
+            const auto scores = [&](float (&s)[32], int q) {
+                uint32_t raw[S::kGroups][32];
+#pragma unroll
+                for (int gr = 0; gr < S::kGroups; ++gr) tc_ld32(raw[gr], ts + gr * S::kKeys + 32 * q);
+                tc_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 32; n += 4) {
+#pragma unroll
+                    for (int gr = 0; gr < S::kGroups; ++gr) {
+                        const float4 f = *reinterpret_cast<const float4*>(&s_scale[j & 1][gr][32 * q + n]);
+                        const float k[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = __uint_as_float(raw[gr][n + e]);
+                            s[n + e] = gr == 0 ? a * k[e] : fmaf(a, k[e], s[n + e]);
+                        }
+                    }
+                }
+                if (plain) return;
+                const int at = pos0 + 32 * q;
+#pragma unroll
+                for (int n = 0; n < 32; ++n) {
+                    const int pos = at + n;
+                    bool see = pos < keys.hi;
+                    if (p.q.tree_dev != nullptr) see = see && (pos < old || ((tree >> (pos - old)) & 1));
+                    else see = see && pos >= first && pos <= last;
+                    if (any_bad) see = see && !lost(pos);
+                    if (!see) s[n] = -INFINITY;
+                }
+            };
+            float top = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < S::kKeys / 32; ++q) {
+                float s[32];
+                scores(s, q);
+#pragma unroll
+                for (int n = 0; n < 32; n += 2) top = fmaxf(fmaxf(top, s[n]), s[n + 1]);
+            }
+            if (top != -INFINITY) top *= c;
+            const bool grow = top > lim;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                float f = 1.0f;
+                if (grow) {
+                    if (lim != -INFINITY) f = exp2_approx(ref - (top - kTop));
+                    ref = top - kTop;
+                    lim = top - kTop + kLimit;
+                    l *= f;
+                }
+                if (j > 0) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tc_ld32(o, to + 32 * q);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                        tc_st32(to + 32 * q, o);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < S::kKeys / 32; ++q) {
+                float s[32];
+                uint32_t w[16];
+                scores(s, q);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    float a = exp2_approx(fmaf(s[2 * n], c, -ref)), b = exp2_approx(fmaf(s[2 * n + 1], c, -ref));
+                    if (!plain) {  // c may be 0
+                        if (s[2 * n] == -INFINITY) a = 0.0f;
+                        if (s[2 * n + 1] == -INFINITY) b = 0.0f;
+                    }
+                    l += a + b;
+                    w[n] = pack_half2(a, b);
+                }
+                tc_st16(ts + 16 * q, w);
+            }
+            tc_wait_st();
+            tc_before_sync();
+            mbar_arrive(&p_full[x]);
+        }
+        wait(&o_full[x], 0);
+        __syncwarp();
+        tc_after_sync();
+        const float m = lim == -INFINITY ? -INFINITY : ref;
+        float* const slot = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) +
+                                             static_cast<int64_t>(blockIdx.x) * S::kPartial : nullptr;
+        int tok = 0, a = 0;
+        T* out = nullptr;
+        if (live) {
+            tok = sp.first + row / p.ratio, a = head * p.ratio + row % p.ratio;
+            out = static_cast<T*>(p.q.out_dev) + tok * p.q.out_token_stride + a * p.q.out_head_stride;
+        }
+        const float inv = l == 0.0f ? 0.0f : 2.0f / l;  // V is halved
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tc_ld32(o, to + 32 * q);
+            tc_wait_ld();
+            if (!live) continue;
+#pragma unroll
+            for (int n = 0; n < 32; n += 8) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[n + e]);
+                if (slot != nullptr) {
+                    float* const d = slot + (128 * x + r) * D + 32 * q + n;
+                    *reinterpret_cast<float4*>(d) = make_float4(2.0f * f[0], 2.0f * f[1], 2.0f * f[2], 2.0f * f[3]);
+                    *reinterpret_cast<float4*>(d + 4) = make_float4(2.0f * f[4], 2.0f * f[5], 2.0f * f[6], 2.0f * f[7]);
+                } else {
+                    T h[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[e] = from_f32<T>(f[e] * inv);
+                    *reinterpret_cast<uint4*>(out + 32 * q + n) = *reinterpret_cast<const uint4*>(h);
+                }
+            }
+        }
+        if (slot != nullptr) {
+            slot[S::kRows * D + 128 * x + r] = m;
+            slot[S::kRows * (D + 1) + 128 * x + r] = l;
+        } else if (live) {
+            write_lse(p, tok, a, m, l);
+        }
+        tc_before_sync();
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------------------------------- unpack
+        const int w = warp - 8, g = lane >> 2, t = lane & 3;
+        const __half2 half2_half = __floats2half2_rn(0.5f, 0.5f), half2_32nd = __floats2half2_rn(0.03125f, 0.03125f);
+        const __half2 half2_16th = __floats2half2_rn(0.0625f, 0.0625f);
+        // (nibble - zero) / 2 of bits 0 (hi false) or 4 of each half of a word, exactly; then times s, for V the scale
+        const auto value = [&](uint32_t a, bool hi, __half2 zero, __half2 s) {
+            const uint32_t m = hi ? 0x00F000F0u : 0x000F000Fu;
+            const uint32_t b = (a & m) | 0x64006400u;  // 1024 + q, or 1024 + 16 q
+            const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&b), hi ? half2_32nd : half2_half, zero);
+            const __half2 f = __hmul2(v, s);
+            return *reinterpret_cast<const uint32_t*>(&f);
+        };
+        // nibble - zero of the same bits, exactly
+        const auto whole = [&](uint32_t a, bool hi, __half2 zero) {
+            const uint32_t b = (a & (hi ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+            const __half2 n = *reinterpret_cast<const __half2*>(&b);
+            const __half2 f = hi ? __hfma2(n, half2_16th, zero) : __hadd2(n, zero);
+            return *reinterpret_cast<const uint32_t*>(&f);
+        };
+        for (int h = 0; h < halves; ++h) {
+            const int stage = h % S::kRawStages, j = h / S::kHalves, buf = j & 1;
+            const bool ends = h % S::kHalves == S::kHalves - 1;  // the tile
+            const uint32_t phase = (h / S::kRawStages) & 1;
+            const int pos = key0 + 64 * h + 16 * w;  // this warp's subtile
+            wait(&raw_full[stage], phase);
+            if (h % S::kHalves == 0 && j >= 2) {  // after the tile that had the buffers, its softmax included
+                wait(&k_free[buf], ((j >> 1) - 1) & 1);
+                wait(&v_free[buf], ((j >> 1) - 1) & 1);
+            }
+            __syncwarp();
+            const uint8_t* const sub = s_raw + stage * S::kRawBytes + w * S::kSubBytes;
+            const bool odd = pos + kSub > keys.hi || any_bad;
+            const auto scales = [&](const uint8_t* at, int token) {  // a token that there is not: 0
+                uint32_t sz = *reinterpret_cast<const uint32_t*>(at + 4 * token);
+                if (odd && (pos + token >= keys.hi || (any_bad && lost(pos + token)))) sz = 0;
+                return sz;
+            };
+            const int col = 64 * (h % S::kHalves) + 16 * w;  // key of the tile
+            // K: 8 lanes a token and atom, each a word of 8 dims
+            {
+                uint8_t* const dst = s_k + buf * S::kKBytes;
+#pragma unroll
+                for (int n = 0; n < 4 * S::kAtoms; ++n) {
+                    const int token = 4 * (n % 4) + (lane >> 3), atom = n / 4, wd = lane & 7;
+                    const int d = 64 * atom + 8 * wd;
+                    constexpr int P = D < 128 ? D : 128;
+                    const uint32_t a = *reinterpret_cast<const uint32_t*>(sub + d / P * 8 * P + token * (P / 2) + d % P / 2);
+                    const uint32_t sz = scales(sub + 16 * D + 64 * (64 * atom / G), token);
+                    const __half2 z = __half2half2(__ushort_as_half(static_cast<unsigned short>(sz >> 16)));
+                    const __half2 z0 = __hsub2(__floats2half2_rn(-1024.0f, -1024.0f), z), z1 = __hsub2(__floats2half2_rn(-64.0f, -64.0f), z);
+                    const uint4 o = make_uint4(whole(a, false, z0), whole(a, true, z1), whole(a >> 8, false, z0), whole(a >> 8, true, z1));
+                    const int row = col + token;
+                    *reinterpret_cast<uint4*>(dst + atom * (S::kKeys * 128) + row * 128 + ((wd ^ (row & 7)) * 16)) = o;
+                    if (wd == 0 && 64 * atom % G == 0)
+                        s_scale[buf][64 * atom / G][row] = __half2float(__ushort_as_half(static_cast<unsigned short>(sz & 0xFFFFu)));
+                }
+                fence_async();
+                if (ends) mbar_arrive(&k_full[buf]);
+            }
+            // V: lane (g, t) has tokens 4t .. 4t + 3 of dims g + 8n + 32i
+            {
+                uint8_t* const dst = s_v + buf * S::kVBytes;
+                uint32_t vq[D / 16];
+#pragma unroll
+                for (int r = 0; r < D / 64; ++r)
+                    *reinterpret_cast<uint4*>(vq + 4 * r) = *reinterpret_cast<const uint4*>(sub + 8 * D + 512 * r + 16 * lane);
+#pragma unroll
+                for (int gr = 0; gr < S::kGroups; ++gr) {
+                    __half2 s[2], z0[2], z1[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a = scales(sub + 16 * D + 64 * (S::kGroups + gr), 4 * t + 2 * e);
+                        const uint32_t b = scales(sub + 16 * D + 64 * (S::kGroups + gr), 4 * t + 2 * e + 1);
+                        const uint32_t sw = __byte_perm(a, b, 0x5410), zw = __byte_perm(a, b, 0x7632);
+                        s[e] = *reinterpret_cast<const __half2*>(&sw);
+                        const __half2 z = *reinterpret_cast<const __half2*>(&zw);
+                        z0[e] = __hfma2(z, __floats2half2_rn(-0.5f, -0.5f), __floats2half2_rn(-512.0f, -512.0f));
+                        z1[e] = __hfma2(z, __floats2half2_rn(-0.5f, -0.5f), __floats2half2_rn(-32.0f, -32.0f));
+                    }
+#pragma unroll
+                    for (int ii = 0; ii < G / 32; ++ii) {
+                        const int i = gr * (G / 32) + ii;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const uint32_t a = n < 2 ? vq[i] : vq[i] >> 8, b = n < 2 ? vq[D / 32 + i] : vq[D / 32 + i] >> 8;
+                            const uint2 o = make_uint2(value(a, n & 1, (n & 1) ? z1[0] : z0[0], s[0]), value(b, n & 1, (n & 1) ? z1[1] : z0[1], s[1]));
+                            const int d = 32 * i + 8 * n + g, k = col + 4 * t;  // row and key
+                            *reinterpret_cast<uint2*>(dst + k / 64 * (D * 128) + d * 128 + ((((k % 64) / 8) ^ (d & 7)) * 16) + (k % 8) * 2) = o;
+                        }
+                    }
+                }
+                fence_async();
+                if (ends) mbar_arrive(&v_full[buf]);
+            }
+            mbar_arrive(&raw_free[stage]);
+        }
+    } else if (warp == 12) {
+        // ---------------------------------------------------------------------------------------- products
+        if (lane == 0) {
+            const uint32_t q_at = smem_addr(s_q), k_at = smem_addr(s_k), v_at = smem_addr(s_v);
+            const auto scores = [&](int x, int buf) {
+                if (dead) return;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_ss(tmem + 128 * x + kk / (G / 16) * S::kKeys, tc_desc(q_at + x * S::kQBytes + kk / 4 * (128 * 128) + kk % 4 * 32),
+                              tc_desc(k_at + buf * S::kKBytes + kk / 4 * (S::kKeys * 128) + kk % 4 * 32), tc_idesc(S::kKeys), kk % (G / 16) > 0);
+            };
+            const auto outputs = [&](int x, int buf, bool add) {
+                if (dead) return;
+#pragma unroll
+                for (int kk = 0; kk < S::kKeys / 16; ++kk)
+                    tc_mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk,
+                              tc_desc(v_at + buf * S::kVBytes + kk / 4 * (D * 128) + kk % 4 * 32), tc_idesc(D), add || kk > 0);
+            };
+            wait(&q_full, 0);
+            wait(&k_full[0], 0);
+            tc_after_sync();
+            scores(0, 0);
+            tc_commit(&s_full[0]);
+            scores(1, 0);
+            tc_commit(&s_full[1]);
+            tc_commit(&k_free[0]);
+            for (int j = 0; j < tiles; ++j) {
+                const int buf = j & 1, next = buf ^ 1;
+                const bool more = j + 1 < tiles;
+                wait(&v_full[buf], (j >> 1) & 1);
+                for (int x = 0; x < 2; ++x) {
+                    wait(&p_full[x], j & 1);
+                    tc_after_sync();
+                    outputs(x, buf, j > 0);
+                    if (x == 1) tc_commit(&v_free[buf]);
+                    if (more) {
+                        if (x == 0) {
+                            wait(&k_full[next], ((j + 1) >> 1) & 1);
+                            tc_after_sync();
+                        }
+                        scores(x, next);
+                        tc_commit(&s_full[x]);
+                        if (x == 1) tc_commit(&k_free[next]);
+                    } else {
+                        tc_commit(&o_full[x]);
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------------------------- copies
+        const int per = min(p.page, 64);  // keys of a copy
+        const uint8_t* const base = p.cache + head * p.head_bytes;
+        for (int h = 0; h < halves; ++h) {
+            const int stage = h % S::kRawStages;
+            if (h >= S::kRawStages) wait(&raw_free[stage], (h / S::kRawStages - 1) & 1);
+            const int pos = key0 + 64 * h + lane * per;  // of this lane's copy
+            uint32_t bytes = 0;
+            const uint8_t* src = nullptr;
+            if (lane * per < 64 && pos < keys.hi) {
+                const int id = table[pos >> p.log2_page];
+                if (id >= 0 && id < p.n_pages) {
+                    bytes = ((min(keys.hi, pos + per) - pos + kSub - 1) / kSub) * S::kSubBytes;
+                    src = base + id * p.page_bytes + ((pos & (p.page - 1)) / kSub) * S::kSubBytes;
+                }
+            }
+            uint32_t sum = bytes;
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            if (dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], sum);
+            __syncwarp();
+            if (bytes) bulk_g2s(s_raw + stage * S::kRawBytes + lane * (per / kSub) * S::kSubBytes, src, bytes, &raw_full[stage]);
+        }
+    }
+    __syncwarp();
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp == 12) tc_dealloc(tmem, S::kCols);
+    if (parts == 1) return;
+
+    // Join the splits of the segment: the last CTA to arrive, a row a warp, in the order of the keys.
+    int* const arrived = static_cast<int*>(p.q.workspace_dev);
+    const int64_t seg = blockIdx.x / splits;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(&arrived[seg], 1) == parts - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const float* const slots = reinterpret_cast<const float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) + seg * splits * S::kPartial;
+    for (int r = warp; r < S::kRows && row0 + r < rows; r += 14) {
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(slots + i * S::kPartial + S::kRows * D + r));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        float o[D / 32], l = 0.0f;
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) o[v] = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float* const q = slots + i * S::kPartial;
+            const float mi = __ldcg(q + S::kRows * D + r), li = __ldcg(q + S::kRows * (D + 1) + r);
+            if (mi == -INFINITY && li == 0.0f) continue;
+            const float f = mi == -INFINITY ? 1.0f : exp2_approx(mi - m);
+            l = fmaf(li, f, l);
+#pragma unroll
+            for (int v = 0; v < D / 32; ++v) o[v] = fmaf(__ldcg(q + r * D + 32 * v + lane), f, o[v]);
+        }
+        const int row = row0 + r, tok = sp.first + row / p.ratio, a = head * p.ratio + row % p.ratio;
+        T* const out = static_cast<T*>(p.q.out_dev) + tok * p.q.out_token_stride + a * p.q.out_head_stride;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) out[32 * v + lane] = from_f32<T>(o[v] * inv);
+        if (lane == 0) write_lse(p, tok, a, m, l);
+    }
+    if (tid == 0) arrived[seg] = 0;
+}
+
+}  // namespace sgemv

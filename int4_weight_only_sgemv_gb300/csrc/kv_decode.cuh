@@ -36,6 +36,7 @@ constexpr int kMaxLen = 1 << 30;  // positions past the end of a tile stay in 32
 // 2^kLimit (fp16 ends at 2^16). Weights below 2^(kTop - 20) of the largest lose bits, as fp16 subnormals.
 constexpr float kTop = 6.0f, kLimit = 15.0f;
 constexpr int kSwitch = 2;  // what taking up a segment costs, in tiles: counted when the work is split
+constexpr int kMaxCtas = 152; // CTAs that the workspace has room for
 constexpr int kSpans = 256; // requests whose lengths are kept in shared memory
 
 struct AttnParams {
@@ -44,6 +45,7 @@ struct AttnParams {
     sgemv_kv_query q;
     int32_t* status;
     int heads, page, log2_page, n_pages, ratio;
+    int max_rows;      // requests with more rows a KV head are the chunk kernel's
     float scale_log2;  // scale * log2(e)
 };
 
@@ -83,6 +85,13 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int r) {
         report(p.status, SGEMV_ERR_SHAPE);
         s.n = 0;
     }
+    return s;
+}
+
+// The same for the decode kernel.
+__device__ __forceinline__ Span decode_span(const AttnParams& p, int r) {
+    Span s = span_of(p, r);
+    if (static_cast<int64_t>(s.n) * p.ratio > p.max_rows) s.n = 0;
     return s;
 }
 
@@ -220,7 +229,7 @@ __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Span& s) 
 struct Spans {
     const AttnParams& p;
     const Span* cached;  // of every request, or null
-    __device__ __forceinline__ Span operator[](int r) const { return cached != nullptr ? cached[r] : span_of(p, r); }
+    __device__ __forceinline__ Span operator[](int r) const { return cached != nullptr ? cached[r] : decode_span(p, r); }
 };
 
 // The segment after s (there is one).
@@ -356,7 +365,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
     int64_t mine = 0;
     for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) {
-        const Span s = span_of(p, r);
+        const Span s = decode_span(p, r);
         if (r < kSpans) s_span[r] = s;
         mine += units_of<S::kRows>(p, s);
     }

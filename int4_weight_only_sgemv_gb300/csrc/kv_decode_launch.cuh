@@ -1,6 +1,8 @@
 // Launcher of decode_kernel<T, ...>, shared by the translation units of the two query types.
 #pragma once
 
+#include <algorithm>
+
 #include "kv_decode.cuh"
 
 namespace sgemv {
@@ -8,7 +10,7 @@ namespace sgemv {
 template <typename T, int D, int G, int NT>
 cudaError_t launch_decode_shape(const AttnParams& p, int sms, cudaStream_t s) {
     using S = AttnShape<D, G, NT>;
-    static_assert(4096 + 4 * (152 * (S::kWarps + 2)) * S::kPartial <= SGEMV_KV_WORKSPACE, "workspace");
+    static_assert(4096 + 4 * (kMaxCtas * (S::kWarps + 2)) * S::kPartial <= SGEMV_KV_WORKSPACE, "workspace");
     auto kern = decode_kernel<T, D, G, NT>;
     static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
     int dev = 0;
@@ -20,13 +22,13 @@ cudaError_t launch_decode_shape(const AttnParams& p, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr_set[dev].store(1);
     }
-    const int grid = sms < 152 ? sms : 152;  // the workspace has room for so many
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     return launch_pdl(kern, dim3(grid), dim3(S::kThreads), S::kSmem, s, p);
 }
 
 template <typename T, int D, int G>
 cudaError_t launch_decode_rows(const AttnParams& p, int sms, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(p.q.max_q) * p.ratio;
+    const int64_t rows = std::min(static_cast<int64_t>(p.q.max_q) * p.ratio, static_cast<int64_t>(p.max_rows));
     if (rows <= 8) return launch_decode_shape<T, D, G, 1>(p, sms, s);
     if constexpr (D == 256) return launch_decode_shape<T, D, G, 1>(p, sms, s);
     if constexpr (D == 128) return launch_decode_shape<T, D, G, 2>(p, sms, s);
