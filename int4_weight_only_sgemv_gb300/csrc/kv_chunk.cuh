@@ -4,8 +4,8 @@
 // key. So they go to the 5th-generation tensor cores, S = x K^T and O += P V with 128 x 128 x 16 instructions, and one
 // CTA holds two 128-row tiles of queries against each 128-key tile that it unpacks, which halves the unpacking a product
 // needs. Roles, by warp:
-//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory in 32-column pieces (once
-//             for the maximum, once for the weights), weights back to tensor memory in fp16, over S
+//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory in 32-column pieces, weights
+//             back to tensor memory in fp16, over S
 //   8-11      unpack: raw subtiles -> K's integers q - z [key][dim] and V [dim][key] in fp16, both swizzled for the tensor cores,
 //             two buffers each, and K's scales
 //   12        issues the products      13  issues the copies of raw subtiles (copy engine, 64 keys a stage)
@@ -14,8 +14,11 @@
 // Roundings: scores have none but the sums' in 32 bits: x is fp16 (scaled by a power of two a row, exact), K's integers are exact,
 // and the softmax multiplies a column by its scale. Where a key has two groups, each has sums of its own (and a tile is 64 keys).
 // The weights are rounded to fp16, 11 bits, as in the decode kernel. V's values (q - z) s have up to 15 bits: they are formed as
-// ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale need be kept a column. The softmax's reference m
-// moves only when the maximum passes it by 2^9 (kLimit - kTop), so O is rarely rescaled.
+// ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale need be kept a column.
+//
+// The softmax reads a score once: a piece's weights are formed against the reference m that the row has, which moves only when
+// a weight would pass 2^kLimit, and then by whole powers of two, so that O, the sum and the weights already written for the
+// tile are rescaled exactly (but for fp16 subnormals). A pass of its own for the tile's maximum cost 2800 of 9200 cycles a tile.
 //
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the last CTA to arrive joins.
 #pragma once
@@ -73,6 +76,11 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                  : SGEMV_R8(r, 0), SGEMV_R8(r, 8), SGEMV_R8(r, 16), SGEMV_R8(r, 24)
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : SGEMV_R8(r, 0), SGEMV_R8(r, 8)
                  : "r"(addr));
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             const int be = static_cast<int>(__float_as_uint(big) >> 23);
             const int sh = be == 0 || be == 255 ? 0 : min(max(127 + 9 - be, -100), 100);
             const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), p.scale_log2);
-            c = p.scale_log2 / up;  // not negative
+            c = fmaxf(p.scale_log2 / up, 1e-30f);  // above 0, so that -inf stays -inf
             uint8_t* const dst = s_q + x * S::kQBytes + r * 128;
 #pragma unroll 4
             for (int d = 0; d < D; d += 8) {
@@ -259,7 +267,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         const int ia = min(row0 + 128 * x, rows - 1) / p.ratio, ib = min(row0 + 128 * x + 127, rows - 1) / p.ratio;
         const int clear1 = any_bad ? 0 : (p.q.tree_dev != nullptr ? old : old + ia + 1);
         const int clear0 = p.q.window > 0 ? old + ib - p.q.window + 1 : 0;
-        float ref = 0.0f, lim = -INFINITY, l = 0.0f;
+        float ref = 0.0f, lim = -INFINITY;  // lim = ref + kLimit, or -inf while nothing was seen
+        uint64_t l2 = 0;                    // two sums
         for (int j = 0; j < tiles; ++j) {
             const int pos0 = key0 + j * S::kKeys;
             wait(&s_full[x], j & 1);
@@ -267,80 +276,90 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             tc_after_sync();
             const bool plain = pos0 >= clear0 && pos0 + S::kKeys <= clear1;
-            // columns 32 q .. of this row: sums times scales, -inf where masked
-            const auto scores = [&](float (&s)[32], int q) {
+#pragma unroll 1
+            for (int q = 0; q < S::kKeys / 32; ++q) {
+                // columns 32 q .. of this row: sums times scales, -inf where masked
                 uint32_t raw[S::kGroups][32];
 #pragma unroll
                 for (int gr = 0; gr < S::kGroups; ++gr) tc_ld32(raw[gr], ts + gr * S::kKeys + 32 * q);
                 tc_wait_ld();
+                float s[32];
+                const float* const scale = &s_scale[j & 1][0][32 * q];
 #pragma unroll
                 for (int n = 0; n < 32; n += 4) {
 #pragma unroll
                     for (int gr = 0; gr < S::kGroups; ++gr) {
-                        const float4 f = *reinterpret_cast<const float4*>(&s_scale[j & 1][gr][32 * q + n]);
-                        const float k[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = __uint_as_float(raw[gr][n + e]);
-                            s[n + e] = gr == 0 ? a * k[e] : fmaf(a, k[e], s[n + e]);
-                        }
+                        const float4 f = *reinterpret_cast<const float4*>(scale + gr * S::kKeys + n);
+                        const uint64_t k0 = pair(f.x, f.y), k1 = pair(f.z, f.w);
+                        const uint64_t a0 = pair(__uint_as_float(raw[gr][n]), __uint_as_float(raw[gr][n + 1]));
+                        const uint64_t a1 = pair(__uint_as_float(raw[gr][n + 2]), __uint_as_float(raw[gr][n + 3]));
+                        const float2 t0 = parts_of(gr == 0 ? mul2(a0, k0) : fma2(a0, k0, pair(s[n], s[n + 1])));
+                        const float2 t1 = parts_of(gr == 0 ? mul2(a1, k1) : fma2(a1, k1, pair(s[n + 2], s[n + 3])));
+                        s[n] = t0.x, s[n + 1] = t0.y, s[n + 2] = t1.x, s[n + 3] = t1.y;
                     }
                 }
-                if (plain) return;
-                const int at = pos0 + 32 * q;
+                if (!plain) {
+                    const int at = pos0 + 32 * q;
+                    uint32_t see = 0;
+#pragma unroll 1
+                    for (int n = 0; n < 32; ++n) {
+                        const int pos = at + n;
+                        bool ok = pos < keys.hi;
+                        if (p.q.tree_dev != nullptr) ok = ok && (pos < old || ((tree >> (pos - old)) & 1));
+                        else ok = ok && pos >= first && pos <= last;
+                        if (any_bad) ok = ok && !lost(pos);
+                        see |= ok ? 1u << n : 0u;
+                    }
 #pragma unroll
-                for (int n = 0; n < 32; ++n) {
-                    const int pos = at + n;
-                    bool see = pos < keys.hi;
-                    if (p.q.tree_dev != nullptr) see = see && (pos < old || ((tree >> (pos - old)) & 1));
-                    else see = see && pos >= first && pos <= last;
-                    if (any_bad) see = see && !lost(pos);
-                    if (!see) s[n] = -INFINITY;
+                    for (int n = 0; n < 32; ++n)
+                        if (!((see >> n) & 1u)) s[n] = -INFINITY;
                 }
-            };
-            float top = -INFINITY;
+                float top = s[0];
 #pragma unroll
-            for (int q = 0; q < S::kKeys / 32; ++q) {
-                float s[32];
-                scores(s, q);
-#pragma unroll
-                for (int n = 0; n < 32; n += 2) top = fmaxf(fmaxf(top, s[n]), s[n + 1]);
-            }
-            if (top != -INFINITY) top *= c;
-            const bool grow = top > lim;
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                float f = 1.0f;
-                if (grow) {
-                    if (lim != -INFINITY) f = exp2_approx(ref - (top - kTop));
-                    ref = top - kTop;
-                    lim = top - kTop + kLimit;
-                    l *= f;
-                }
-                if (j > 0) {
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tc_ld32(o, to + 32 * q);
+                for (int n = 1; n < 31; n += 2) top = fmaxf(fmaxf(top, s[n]), s[n + 1]);
+                top = fmaxf(top, s[31]) * c;
+                if (__any_sync(0xFFFFFFFFu, top > lim)) {
+                    float f = 1.0f;
+                    if (top > lim) {
+                        const float up = lim == -INFINITY ? top - kTop - ref : ceilf(top - kTop - ref);
+                        if (lim != -INFINITY) f = exp2_approx(-up);
+                        ref += up;
+                        lim = ref + kLimit;
+                    }
+                    l2 = mul2(l2, pair(f, f));
+                    const __half2 fh = __float2half2_rn(f);  // f is a power of two (0 below fp16's)
+#pragma unroll 1
+                    for (int d = 0; d < q; ++d) {  // the tile's weights so far
+                        uint32_t w[16];
+                        tc_ld16(w, ts + 16 * d);
                         tc_wait_ld();
 #pragma unroll
-                        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-                        tc_st32(to + 32 * q, o);
+                        for (int n = 0; n < 16; ++n) {
+                            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w[n]), fh);
+                            w[n] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        tc_st16(ts + 16 * d, w);
                     }
-                }
-            }
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int d = 0; d < D / 32; ++d) {
+                            uint32_t o[32];
+                            tc_ld32(o, to + 32 * d);
+                            tc_wait_ld();
 #pragma unroll
-            for (int q = 0; q < S::kKeys / 32; ++q) {
-                float s[32];
+                            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                            tc_st32(to + 32 * d, o);
+                        }
+                    }
+                    tc_wait_st();
+                }
                 uint32_t w[16];
-                scores(s, q);
+                const uint64_t cc = pair(c, c), rr = pair(-ref, -ref);
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    float a = exp2_approx(fmaf(s[2 * n], c, -ref)), b = exp2_approx(fmaf(s[2 * n + 1], c, -ref));
-                    if (!plain) {  // c may be 0
-                        if (s[2 * n] == -INFINITY) a = 0.0f;
-                        if (s[2 * n + 1] == -INFINITY) b = 0.0f;
-                    }
-                    l += a + b;
+                    const float2 t = parts_of(fma2(pair(s[2 * n], s[2 * n + 1]), cc, rr));
+                    const float a = exp2_approx(t.x), b = exp2_approx(t.y);
+                    l2 = add2(l2, pair(a, b));
                     w[n] = pack_half2(a, b);
                 }
                 tc_st16(ts + 16 * q, w);
@@ -352,7 +371,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         wait(&o_full[x], 0);
         __syncwarp();
         tc_after_sync();
-        const float m = lim == -INFINITY ? -INFINITY : ref;
+        const float2 lf = parts_of(l2);
+        const float m = lim == -INFINITY ? -INFINITY : ref, l = lf.x + lf.y;
         float* const slot = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) +
                                              static_cast<int64_t>(blockIdx.x) * S::kPartial : nullptr;
         int tok = 0, a = 0;
