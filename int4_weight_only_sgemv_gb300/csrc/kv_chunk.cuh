@@ -1,24 +1,22 @@
 // Attention over the paged 4-bit KV cache: the kernel of prompt chunks (requests with many rows of queries).
 //
 // With many rows the products bound the work, not the cache's bytes: 4 D operations a (row, key) against D / 2 + 4 bytes a
-// key. So they go to the 5th-generation tensor cores, S = x K^T and O += P V with 128 x 128 x 16 instructions, and one
-// CTA holds two 128-row tiles of queries against each 128-key tile that it unpacks, which halves the unpacking a product
+// key. So they go to the 5th-generation tensor cores, S = x K^T with 128 x 64 x 16 and O += P V with 128 x D x 16 instructions, and
+// one CTA holds two 128-row tiles of queries against each 64-key tile that it unpacks, which halves the unpacking a product
 // needs. Roles, by warp:
-//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory in 32-column pieces, weights
-//             back to tensor memory in fp16, over S
+//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory, weights back to tensor
+//             memory in fp16, over S
 //   8-11      unpack: raw subtiles -> K's integers q - z [key][dim] and V [dim][key] in fp16, both swizzled for the tensor cores,
-//             two buffers each, and K's scales
+//             four buffers each, and K's scales
 //   12        issues the products      13  issues the copies of raw subtiles (copy engine, 64 keys a stage)
-// The two row tiles alternate, so that the products of one run while the other's softmax does.
+// S has two buffers a row tile in tensor memory (2 x 2 x 64 columns beside 2 x D of O), so that the next tile's scores are there
+// when a softmax is done with one: with 128-key tiles and one buffer each softmax waited 2100 of 6100 cycles a tile for its
+// scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
 //
 // Roundings: scores have none but the sums' in 32 bits: x is fp16 (scaled by a power of two a row, exact), K's integers are exact,
-// and the softmax multiplies a column by its scale. Where a key has two groups, each has sums of its own (and a tile is 64 keys).
-// The weights are rounded to fp16, 11 bits, as in the decode kernel. V's values (q - z) s have up to 15 bits: they are formed as
-// ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale need be kept a column.
-//
-// The softmax reads a score once: a piece's weights are formed against the reference m that the row has, which moves only when
-// a weight would pass 2^kLimit, and then by whole powers of two, so that O, the sum and the weights already written for the
-// tile are rescaled exactly (but for fp16 subnormals). A pass of its own for the tile's maximum cost 2800 of 9200 cycles a tile.
+// and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
+// values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale
+// need be kept a column. The softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
 //
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the last CTA to arrive joins.
 #pragma once
@@ -34,14 +32,15 @@ struct ChunkShape {
     static constexpr int kGroups = D / G;
     static constexpr int kSubBytes = 16 * D + 128 * kGroups;
     static constexpr int kRows = 256, kTile = 128;                // rows of a CTA and of a row tile
-    static constexpr int kKeys = 128 / kGroups;                   // keys of a tile: kGroups sums of it are 128 columns
-    static constexpr int kHalves = kKeys / 64;                    // raw stages of a tile
+    static constexpr int kKeys = 64;                              // keys of a tile
+    static constexpr int kSBufs = 2 / kGroups;                    // buffers of S
+    static constexpr int kBufs = 4;                               // of K and V
     static constexpr int kRawSubs = 4, kRawStages = 3;            // subtiles of a raw stage
     static constexpr int kRawBytes = kRawSubs * kSubBytes;
     static constexpr int kAtoms = D / 64;                         // 128-byte columns of a row of x or K
     static constexpr int kQBytes = kTile * D * 2, kKBytes = kKeys * D * 2, kVBytes = D * kKeys * 2;
     static constexpr int kThreads = 14 * 32;
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + kRawStages * kRawBytes;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + kBufs * (kKBytes + kVBytes) + kRawStages * kRawBytes;
     static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
     static constexpr int kCols = 512;                             // tensor memory: S0, S1, O0, O1
 };
@@ -103,6 +102,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {  // true in one lane of the warp
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Operand descriptor: rows of 128 bytes (64 fp16 along the product's inner axis), 128-byte swizzle, 8 rows every 1024 bytes.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
@@ -126,11 +131,12 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* const s_q = smem;
     uint8_t* const s_k = s_q + 2 * S::kQBytes;
-    uint8_t* const s_v = s_k + 2 * S::kKBytes;
-    uint8_t* const s_raw = s_v + 2 * S::kVBytes;
-    __shared__ __align__(16) float s_scale[2][S::kGroups][S::kKeys];  // of K's groups
-    __shared__ __align__(8) uint64_t raw_full[S::kRawStages], raw_free[S::kRawStages], k_full[2], k_free[2], v_full[2], v_free[2];
-    __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    uint8_t* const s_v = s_k + S::kBufs * S::kKBytes;
+    uint8_t* const s_raw = s_v + S::kBufs * S::kVBytes;
+    __shared__ __align__(16) float s_scale[S::kBufs][S::kGroups][S::kKeys];  // of K's groups
+    __shared__ __align__(8) uint64_t raw_full[S::kRawStages], raw_free[S::kRawStages];
+    __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_free[S::kBufs];
+    __shared__ __align__(8) uint64_t q_full, s_full[2][2], p_full[2][2], o_full[2][2];
     __shared__ uint32_t s_tmem;
     __shared__ int64_t s_sum[14];
     __shared__ int s_req, s_bad, s_last;
@@ -138,11 +144,12 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S::kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 128);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&k_full[i], 128), mbar_init(&k_free[i], 1);
             mbar_init(&v_full[i], 128), mbar_init(&v_free[i], 1);
-            mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
         }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&s_full[i >> 1][i & 1], 1), mbar_init(&p_full[i >> 1][i & 1], 128), mbar_init(&o_full[i >> 1][i & 1], 1);
         mbar_init(&q_full, 256);
         mbar_fence_init();
         s_req = -1, s_bad = 0;
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     Keys keys = keys_of(p, sp, row0, S::kRows);
     keys.lo = keys.lo / S::kKeys * S::kKeys;
     const int all_tiles = max(1, (keys.hi - keys.lo + S::kKeys - 1) / S::kKeys);
-    const int parts = min(splits, max(1, all_tiles / 2));  // two tiles a split at least
+    const int parts = min(splits, max(1, all_tiles / 4));  // a few tiles a split at least
     if (part >= parts) return;
     const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * part / parts);
     const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (part + 1) / parts) - tile0;
@@ -221,14 +228,13 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         dead = true;
         report(p.status, SGEMV_ERR_TIMEOUT);
     };
-    const int halves = S::kHalves * tiles;  // raw stages of this CTA
 
     if (warp < 8) {
         // ---------------------------------------------------------------------------------------- softmax
         const int x = warp >> 2, r = tid & 127, row = row0 + 128 * x + r;
         const bool live = row < rows;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
+        const uint32_t to = tmem + lanes + 256 + 128 * x;
         const int i = min(row, rows - 1) / p.ratio;
         // x: this thread's row, to shared memory; dims in the order 0 4 1 5 2 6 3 7 of each 8, as K's nibbles come out
         float c;
@@ -270,105 +276,109 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         float ref = 0.0f, lim = -INFINITY;  // lim = ref + kLimit, or -inf while nothing was seen
         uint64_t l2 = 0;                    // two sums
         for (int j = 0; j < tiles; ++j) {
-            const int pos0 = key0 + j * S::kKeys;
-            wait(&s_full[x], j & 1);
-            wait(&k_full[j & 1], (j >> 1) & 1);  // long since: makes the scales visible
+            const int pos0 = key0 + j * S::kKeys, b = j % S::kSBufs;
+            const uint32_t ts = tmem + lanes + 128 * x + 64 * b;
+            wait(&s_full[x][b], (j / S::kSBufs) & 1);
+            wait(&k_full[j % S::kBufs], (j / S::kBufs) & 1);  // long since: makes the scales visible
             __syncwarp();
             tc_after_sync();
             const bool plain = pos0 >= clear0 && pos0 + S::kKeys <= clear1;
-#pragma unroll 1
-            for (int q = 0; q < S::kKeys / 32; ++q) {
-                // columns 32 q .. of this row: sums times scales, -inf where masked
-                uint32_t raw[S::kGroups][32];
+            // this row's scores: sums times scales, -inf where masked
+            float s[64];
+            {
+                const float* const scale = &s_scale[j % S::kBufs][0][0];
+                if constexpr (S::kGroups == 1) {
+                    uint32_t raw[2][32];
+                    tc_ld32(raw[0], ts);
+                    tc_ld32(raw[1], ts + 32);
+                    tc_wait_ld();
 #pragma unroll
-                for (int gr = 0; gr < S::kGroups; ++gr) tc_ld32(raw[gr], ts + gr * S::kKeys + 32 * q);
-                tc_wait_ld();
-                float s[32];
-                const float* const scale = &s_scale[j & 1][0][32 * q];
-#pragma unroll
-                for (int n = 0; n < 32; n += 4) {
-#pragma unroll
-                    for (int gr = 0; gr < S::kGroups; ++gr) {
-                        const float4 f = *reinterpret_cast<const float4*>(scale + gr * S::kKeys + n);
-                        const uint64_t k0 = pair(f.x, f.y), k1 = pair(f.z, f.w);
-                        const uint64_t a0 = pair(__uint_as_float(raw[gr][n]), __uint_as_float(raw[gr][n + 1]));
-                        const uint64_t a1 = pair(__uint_as_float(raw[gr][n + 2]), __uint_as_float(raw[gr][n + 3]));
-                        const float2 t0 = parts_of(gr == 0 ? mul2(a0, k0) : fma2(a0, k0, pair(s[n], s[n + 1])));
-                        const float2 t1 = parts_of(gr == 0 ? mul2(a1, k1) : fma2(a1, k1, pair(s[n + 2], s[n + 3])));
+                    for (int n = 0; n < 64; n += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(scale + n);
+                        const uint32_t* const r4 = &raw[n / 32][n % 32];
+                        const float2 t0 = parts_of(mul2(pair(__uint_as_float(r4[0]), __uint_as_float(r4[1])), pair(f.x, f.y)));
+                        const float2 t1 = parts_of(mul2(pair(__uint_as_float(r4[2]), __uint_as_float(r4[3])), pair(f.z, f.w)));
                         s[n] = t0.x, s[n + 1] = t0.y, s[n + 2] = t1.x, s[n + 3] = t1.y;
                     }
-                }
-                if (!plain) {
-                    const int at = pos0 + 32 * q;
-                    uint32_t see = 0;
-#pragma unroll 1
-                    for (int n = 0; n < 32; ++n) {
-                        const int pos = at + n;
-                        bool ok = pos < keys.hi;
-                        if (p.q.tree_dev != nullptr) ok = ok && (pos < old || ((tree >> (pos - old)) & 1));
-                        else ok = ok && pos >= first && pos <= last;
-                        if (any_bad) ok = ok && !lost(pos);
-                        see |= ok ? 1u << n : 0u;
-                    }
+                } else {
 #pragma unroll
-                    for (int n = 0; n < 32; ++n)
-                        if (!((see >> n) & 1u)) s[n] = -INFINITY;
-                }
-                float top = s[0];
-#pragma unroll
-                for (int n = 1; n < 31; n += 2) top = fmaxf(fmaxf(top, s[n]), s[n + 1]);
-                top = fmaxf(top, s[31]) * c;
-                if (__any_sync(0xFFFFFFFFu, top > lim)) {
-                    float f = 1.0f;
-                    if (top > lim) {
-                        const float up = lim == -INFINITY ? top - kTop - ref : ceilf(top - kTop - ref);
-                        if (lim != -INFINITY) f = exp2_approx(-up);
-                        ref += up;
-                        lim = ref + kLimit;
-                    }
-                    l2 = mul2(l2, pair(f, f));
-                    const __half2 fh = __float2half2_rn(f);  // f is a power of two (0 below fp16's)
-#pragma unroll 1
-                    for (int d = 0; d < q; ++d) {  // the tile's weights so far
-                        uint32_t w[16];
-                        tc_ld16(w, ts + 16 * d);
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t raw[2][32];
+                        tc_ld32(raw[0], ts + 32 * q);
+                        tc_ld32(raw[1], ts + 64 + 32 * q);
                         tc_wait_ld();
 #pragma unroll
-                        for (int n = 0; n < 16; ++n) {
-                            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w[n]), fh);
-                            w[n] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                        tc_st16(ts + 16 * d, w);
-                    }
-                    if (j > 0) {
-#pragma unroll 1
-                        for (int d = 0; d < D / 32; ++d) {
-                            uint32_t o[32];
-                            tc_ld32(o, to + 32 * d);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-                            tc_st32(to + 32 * d, o);
+                        for (int n = 0; n < 32; n += 2) {
+                            const float2 f = *reinterpret_cast<const float2*>(scale + 32 * q + n);
+                            const float2 g = *reinterpret_cast<const float2*>(scale + S::kKeys + 32 * q + n);
+                            const uint64_t a = mul2(pair(__uint_as_float(raw[0][n]), __uint_as_float(raw[0][n + 1])), pair(f.x, f.y));
+                            const float2 t = parts_of(fma2(pair(__uint_as_float(raw[1][n]), __uint_as_float(raw[1][n + 1])), pair(g.x, g.y), a));
+                            s[32 * q + n] = t.x, s[32 * q + n + 1] = t.y;
                         }
                     }
-                    tc_wait_st();
                 }
+            }
+            if (!plain) {
+                uint64_t see = 0;
+#pragma unroll 1
+                for (int n = 0; n < 64; ++n) {
+                    const int pos = pos0 + n;
+                    bool ok = pos < keys.hi;
+                    if (p.q.tree_dev != nullptr) ok = ok && (pos < old || ((tree >> (pos - old)) & 1));
+                    else ok = ok && pos >= first && pos <= last;
+                    if (any_bad) ok = ok && !lost(pos);
+                    see |= ok ? 1ull << n : 0ull;
+                }
+#pragma unroll
+                for (int n = 0; n < 64; ++n)
+                    if (!((see >> n) & 1u)) s[n] = -INFINITY;
+            }
+            float top = fmaxf(s[0], s[63]), top1 = s[1];
+#pragma unroll
+            for (int n = 2; n < 62; n += 4) top = fmaxf(fmaxf(top, s[n]), s[n + 1]), top1 = fmaxf(fmaxf(top1, s[n + 2]), s[n + 3]);
+            top = fmaxf(fmaxf(top, top1), s[62]) * c;
+            if (__any_sync(0xFFFFFFFFu, top > lim)) {
+                float f = 1.0f;
+                if (top > lim) {
+                    if (lim != -INFINITY) f = exp2_approx(ref - (top - kTop));
+                    ref = top - kTop;
+                    lim = ref + kLimit;
+                }
+                l2 = mul2(l2, pair(f, f));
+                if (j > 0) {
+                    // O holds every tile before this one. (The tile before that is known to be in: this one's scores came after it.)
+                    wait(&o_full[x][(j - 1) % S::kSBufs], ((j - 1) / S::kSBufs) & 1);
+                    __syncwarp();
+                    tc_after_sync();
+#pragma unroll 1
+                    for (int d = 0; d < D / 32; ++d) {
+                        uint32_t o[32];
+                        tc_ld32(o, to + 32 * d);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                        tc_st32(to + 32 * d, o);
+                    }
+                }
+            }
+            const uint64_t cc = pair(c, c), rr = pair(-ref, -ref);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
                 uint32_t w[16];
-                const uint64_t cc = pair(c, c), rr = pair(-ref, -ref);
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    const float2 t = parts_of(fma2(pair(s[2 * n], s[2 * n + 1]), cc, rr));
-                    const float a = exp2_approx(t.x), b = exp2_approx(t.y);
-                    l2 = add2(l2, pair(a, b));
-                    w[n] = pack_half2(a, b);
+                    const float2 t = parts_of(fma2(pair(s[32 * q + 2 * n], s[32 * q + 2 * n + 1]), cc, rr));
+                    const float a = exp2_approx(t.x), e = exp2_approx(t.y);
+                    l2 = add2(l2, pair(a, e));
+                    w[n] = pack_half2(a, e);
                 }
                 tc_st16(ts + 16 * q, w);
             }
             tc_wait_st();
             tc_before_sync();
-            mbar_arrive(&p_full[x]);
+            mbar_arrive(&p_full[x][b]);
         }
-        wait(&o_full[x], 0);
+        wait(&o_full[x][(tiles - 1) % S::kSBufs], ((tiles - 1) / S::kSBufs) & 1);
         __syncwarp();
         tc_after_sync();
         const float2 lf = parts_of(l2);
@@ -432,15 +442,13 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             const __half2 f = hi ? __hfma2(n, half2_16th, zero) : __hadd2(n, zero);
             return *reinterpret_cast<const uint32_t*>(&f);
         };
-        for (int h = 0; h < halves; ++h) {
-            const int stage = h % S::kRawStages, j = h / S::kHalves, buf = j & 1;
-            const bool ends = h % S::kHalves == S::kHalves - 1;  // the tile
-            const uint32_t phase = (h / S::kRawStages) & 1;
-            const int pos = key0 + 64 * h + 16 * w;  // this warp's subtile
-            wait(&raw_full[stage], phase);
-            if (h % S::kHalves == 0 && j >= 2) {  // after the tile that had the buffers, its softmax included
-                wait(&k_free[buf], ((j >> 1) - 1) & 1);
-                wait(&v_free[buf], ((j >> 1) - 1) & 1);
+        for (int j = 0; j < tiles; ++j) {
+            const int stage = j % S::kRawStages, buf = j % S::kBufs;
+            const int pos = key0 + S::kKeys * j + 16 * w;  // this warp's subtile
+            wait(&raw_full[stage], (j / S::kRawStages) & 1);
+            if (j >= S::kBufs) {  // after the tile that had the buffers, its softmax included
+                wait(&k_free[buf], (j / S::kBufs - 1) & 1);
+                wait(&v_free[buf], (j / S::kBufs - 1) & 1);
             }
             __syncwarp();
             const uint8_t* const sub = s_raw + stage * S::kRawBytes + w * S::kSubBytes;
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 if (odd && (pos + token >= keys.hi || (any_bad && lost(pos + token)))) sz = 0;
                 return sz;
             };
-            const int col = 64 * (h % S::kHalves) + 16 * w;  // key of the tile
+            const int col = 16 * w;  // key of the tile
             // K: 8 lanes a token and atom, each a word of 8 dims
             {
                 uint8_t* const dst = s_k + buf * S::kKBytes;
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                         s_scale[buf][64 * atom / G][row] = __half2float(__ushort_as_half(static_cast<unsigned short>(sz & 0xFFFFu)));
                 }
                 fence_async();
-                if (ends) mbar_arrive(&k_full[buf]);
+                mbar_arrive(&k_full[buf]);
             }
             // V: lane (g, t) has tokens 4t .. 4t + 3 of dims g + 8n + 32i
             {
@@ -505,56 +513,66 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                     }
                 }
                 fence_async();
-                if (ends) mbar_arrive(&v_full[buf]);
+                mbar_arrive(&v_full[buf]);
             }
             mbar_arrive(&raw_free[stage]);
         }
     } else if (warp == 12) {
         // ---------------------------------------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t q_at = smem_addr(s_q), k_at = smem_addr(s_k), v_at = smem_addr(s_v);
-            const auto scores = [&](int x, int buf) {
-                if (dead) return;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_ss(tmem + 128 * x + kk / (G / 16) * S::kKeys, tc_desc(q_at + x * S::kQBytes + kk / 4 * (128 * 128) + kk % 4 * 32),
-                              tc_desc(k_at + buf * S::kKBytes + kk / 4 * (S::kKeys * 128) + kk % 4 * 32), tc_idesc(S::kKeys), kk % (G / 16) > 0);
-            };
-            const auto outputs = [&](int x, int buf, bool add) {
-                if (dead) return;
-#pragma unroll
-                for (int kk = 0; kk < S::kKeys / 16; ++kk)
-                    tc_mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk,
-                              tc_desc(v_at + buf * S::kVBytes + kk / 4 * (D * 128) + kk % 4 * 32), tc_idesc(D), add || kk > 0);
-            };
-            wait(&q_full, 0);
-            wait(&k_full[0], 0);
+        // The whole warp goes through the loop, with values that the compiler can see are the same in its lanes (they end up in
+        // uniform registers, which the instruction reads); one lane issues. Issued from a branch of one lane, with descriptors
+        // formed anew, an instruction took 115 cycles to issue, more than it takes to run.
+        const int n_tiles = __shfl_sync(0xFFFFFFFFu, tiles, 0);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t q_desc = tc_desc(smem_addr(s_q)), k_desc = tc_desc(smem_addr(s_k)), v_desc = tc_desc(smem_addr(s_v));
+        const auto hold = [&](uint64_t* bar, uint32_t parity) {
+            wait(bar, parity);
+            dead = __any_sync(0xFFFFFFFFu, dead);
             tc_after_sync();
-            scores(0, 0);
-            tc_commit(&s_full[0]);
-            scores(1, 0);
-            tc_commit(&s_full[1]);
-            tc_commit(&k_free[0]);
-            for (int j = 0; j < tiles; ++j) {
-                const int buf = j & 1, next = buf ^ 1;
-                const bool more = j + 1 < tiles;
-                wait(&v_full[buf], (j >> 1) & 1);
-                for (int x = 0; x < 2; ++x) {
-                    wait(&p_full[x], j & 1);
-                    tc_after_sync();
-                    outputs(x, buf, j > 0);
-                    if (x == 1) tc_commit(&v_free[buf]);
-                    if (more) {
-                        if (x == 0) {
-                            wait(&k_full[next], ((j + 1) >> 1) & 1);
-                            tc_after_sync();
-                        }
-                        scores(x, next);
-                        tc_commit(&s_full[x]);
-                        if (x == 1) tc_commit(&k_free[next]);
-                    } else {
-                        tc_commit(&o_full[x]);
+        };
+        const auto scores = [&](int x, int j) {  // of tile j, once its K is there
+            const int buf = j % S::kBufs, b = j % S::kSBufs;
+            if (elect_one()) {
+                const uint64_t qd = q_desc + x * (S::kQBytes >> 4), kd = k_desc + buf * (S::kKBytes >> 4);
+                const uint32_t to = tm + 128 * x + 64 * b;
+                if (!dead) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_ss(to + 64 * (kk / (G / 16)), qd + ((kk / 4 * (128 * 128) + kk % 4 * 32) >> 4),
+                                  kd + ((kk / 4 * (S::kKeys * 128) + kk % 4 * 32) >> 4), tc_idesc(S::kKeys), kk % (G / 16) > 0);
+                }
+                tc_commit(&s_full[x][b]);
+                if (x == 1) tc_commit(&k_free[buf]);
+            }
+            __syncwarp();
+        };
+        hold(&q_full, 0);
+        for (int j = 0; j < min(S::kSBufs, n_tiles); ++j) {
+            hold(&k_full[j], 0);
+            scores(0, j);
+            scores(1, j);
+        }
+        for (int j = 0; j < n_tiles; ++j) {
+            const int buf = j % S::kBufs, b = j % S::kSBufs, next = j + S::kSBufs;
+            hold(&v_full[buf], (j / S::kBufs) & 1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                hold(&p_full[x][b], (j / S::kSBufs) & 1);
+                if (elect_one()) {
+                    const uint64_t vd = v_desc + buf * (S::kVBytes >> 4);
+                    const uint32_t to = tm + 256 + 128 * x, from = tm + 128 * x + 64 * b;
+                    if (!dead) {
+                        tc_mma_ts(to, from, vd, tc_idesc(D), j > 0);
+#pragma unroll
+                        for (int kk = 1; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, from + 8 * kk, vd + (kk * 32 >> 4), tc_idesc(D), true);
                     }
+                    tc_commit(&o_full[x][b]);
+                    if (x == 1) tc_commit(&v_free[buf]);
+                }
+                __syncwarp();
+                if (next < n_tiles) {  // over the weights just used: the products run in the order of their issue
+                    if (x == 0) hold(&k_full[next % S::kBufs], (next / S::kBufs) & 1);
+                    scores(x, next);
                 }
             }
         }
@@ -562,10 +580,10 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         // ---------------------------------------------------------------------------------------- copies
         const int per = min(p.page, 64);  // keys of a copy
         const uint8_t* const base = p.cache + head * p.head_bytes;
-        for (int h = 0; h < halves; ++h) {
-            const int stage = h % S::kRawStages;
-            if (h >= S::kRawStages) wait(&raw_free[stage], (h / S::kRawStages - 1) & 1);
-            const int pos = key0 + 64 * h + lane * per;  // of this lane's copy
+        for (int j = 0; j < tiles; ++j) {
+            const int stage = j % S::kRawStages;
+            if (j >= S::kRawStages) wait(&raw_free[stage], (j / S::kRawStages - 1) & 1);
+            const int pos = key0 + S::kKeys * j + lane * per;  // of this lane's copy
             uint32_t bytes = 0;
             const uint8_t* src = nullptr;
             if (lane * per < 64 && pos < keys.hi) {
