@@ -8,7 +8,7 @@
 //             memory in fp16, over S
 //   8-11      unpack: raw subtiles -> K's integers q - z [key][dim] and V [dim][key] in fp16, both swizzled for the tensor cores,
 //             four buffers each, and K's scales
-//   12        issues the products      13  issues the copies of raw subtiles (copy engine, 64 keys a stage)
+//   12, 13    issue the products, a row tile each      14  issues the copies of raw subtiles (copy engine, 64 keys a stage)
 // S has two buffers a row tile in tensor memory (2 x 2 x 64 columns beside 2 x D of O), so that the next tile's scores are there
 // when a softmax is done with one: with 128-key tiles and one buffer each softmax waited 2100 of 6100 cycles a tile for its
 // scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
@@ -39,7 +39,7 @@ struct ChunkShape {
     static constexpr int kRawBytes = kRawSubs * kSubBytes;
     static constexpr int kAtoms = D / 64;                         // 128-byte columns of a row of x or K
     static constexpr int kQBytes = kTile * D * 2, kKBytes = kKeys * D * 2, kVBytes = D * kKeys * 2;
-    static constexpr int kThreads = 14 * 32;
+    static constexpr int kWarps = 15, kThreads = 32 * kWarps;
     static constexpr int kSmem = 1024 + 2 * kQBytes + kBufs * (kKBytes + kVBytes) + kRawStages * kRawBytes;
     static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
     static constexpr int kCols = 512;                             // tensor memory: S0, S1, O0, O1
@@ -138,15 +138,15 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_free[S::kBufs];
     __shared__ __align__(8) uint64_t q_full, s_full[2][2], p_full[2][2], o_full[2][2];
     __shared__ uint32_t s_tmem;
-    __shared__ int64_t s_sum[14];
+    __shared__ int64_t s_sum[S::kWarps];
     __shared__ int s_req, s_bad, s_last;
     __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < S::kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 128);
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(&k_full[i], 128), mbar_init(&k_free[i], 1);
-            mbar_init(&v_full[i], 128), mbar_init(&v_free[i], 1);
+            mbar_init(&k_full[i], 128), mbar_init(&k_free[i], 2);
+            mbar_init(&v_full[i], 128), mbar_init(&v_free[i], 2);
         }
         for (int i = 0; i < 4; ++i)
             mbar_init(&s_full[i >> 1][i & 1], 1), mbar_init(&p_full[i >> 1][i & 1], 128), mbar_init(&o_full[i >> 1][i & 1], 1);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     int64_t total = 0, before = incl - mine;
-    for (int w = 0; w < 14; ++w) {
+    for (int w = 0; w < S::kWarps; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
     }
@@ -517,64 +517,60 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             }
             mbar_arrive(&raw_free[stage]);
         }
-    } else if (warp == 12) {
+    } else if (warp < 14) {
         // ---------------------------------------------------------------------------------------- products
-        // The whole warp goes through the loop, with values that the compiler can see are the same in its lanes (they end up in
-        // uniform registers, which the instruction reads); one lane issues. Issued from a branch of one lane, with descriptors
-        // formed anew, an instruction took 115 cycles to issue, more than it takes to run.
+        // A warp a row tile. The whole warp goes through the loop, with values that the compiler can see are the same in its lanes
+        // (they end up in uniform registers, which the instruction reads); one lane issues. Issued from a branch of one lane, with
+        // descriptors formed anew, an instruction took 115 cycles to issue, more than it takes to run; with one warp for both row
+        // tiles, 80.
+        const int x = __shfl_sync(0xFFFFFFFFu, warp - 12, 0);
         const int n_tiles = __shfl_sync(0xFFFFFFFFu, tiles, 0);
-        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const uint64_t q_desc = tc_desc(smem_addr(s_q)), k_desc = tc_desc(smem_addr(s_k)), v_desc = tc_desc(smem_addr(s_v));
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128 * x;
+        const uint64_t q_desc = tc_desc(smem_addr(s_q) + x * S::kQBytes), k_desc = tc_desc(smem_addr(s_k)), v_desc = tc_desc(smem_addr(s_v));
         const auto hold = [&](uint64_t* bar, uint32_t parity) {
             wait(bar, parity);
             dead = __any_sync(0xFFFFFFFFu, dead);
             tc_after_sync();
         };
-        const auto scores = [&](int x, int j) {  // of tile j, once its K is there
+        const auto scores = [&](int j) {  // of tile j, once its K is there
             const int buf = j % S::kBufs, b = j % S::kSBufs;
             if (elect_one()) {
-                const uint64_t qd = q_desc + x * (S::kQBytes >> 4), kd = k_desc + buf * (S::kKBytes >> 4);
-                const uint32_t to = tm + 128 * x + 64 * b;
+                const uint64_t kd = k_desc + buf * (S::kKBytes >> 4);
+                const uint32_t to = tm + 64 * b;
                 if (!dead) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_ss(to + 64 * (kk / (G / 16)), qd + ((kk / 4 * (128 * 128) + kk % 4 * 32) >> 4),
+                        tc_mma_ss(to + 64 * (kk / (G / 16)), q_desc + ((kk / 4 * (128 * 128) + kk % 4 * 32) >> 4),
                                   kd + ((kk / 4 * (S::kKeys * 128) + kk % 4 * 32) >> 4), tc_idesc(S::kKeys), kk % (G / 16) > 0);
                 }
                 tc_commit(&s_full[x][b]);
-                if (x == 1) tc_commit(&k_free[buf]);
+                tc_commit(&k_free[buf]);
             }
             __syncwarp();
         };
         hold(&q_full, 0);
         for (int j = 0; j < min(S::kSBufs, n_tiles); ++j) {
             hold(&k_full[j], 0);
-            scores(0, j);
-            scores(1, j);
+            scores(j);
         }
         for (int j = 0; j < n_tiles; ++j) {
             const int buf = j % S::kBufs, b = j % S::kSBufs, next = j + S::kSBufs;
             hold(&v_full[buf], (j / S::kBufs) & 1);
+            if (next < n_tiles) hold(&k_full[next % S::kBufs], (next / S::kBufs) & 1);
+            hold(&p_full[x][b], (j / S::kSBufs) & 1);
+            if (elect_one()) {
+                const uint64_t vd = v_desc + buf * (S::kVBytes >> 4);
+                const uint32_t to = tm + 256, from = tm + 64 * b;
+                if (!dead) {
+                    tc_mma_ts(to, from, vd, tc_idesc(D), j > 0);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                hold(&p_full[x][b], (j / S::kSBufs) & 1);
-                if (elect_one()) {
-                    const uint64_t vd = v_desc + buf * (S::kVBytes >> 4);
-                    const uint32_t to = tm + 256 + 128 * x, from = tm + 128 * x + 64 * b;
-                    if (!dead) {
-                        tc_mma_ts(to, from, vd, tc_idesc(D), j > 0);
-#pragma unroll
-                        for (int kk = 1; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, from + 8 * kk, vd + (kk * 32 >> 4), tc_idesc(D), true);
-                    }
-                    tc_commit(&o_full[x][b]);
-                    if (x == 1) tc_commit(&v_free[buf]);
+                    for (int kk = 1; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, from + 8 * kk, vd + (kk * 32 >> 4), tc_idesc(D), true);
                 }
-                __syncwarp();
-                if (next < n_tiles) {  // over the weights just used: the products run in the order of their issue
-                    if (x == 0) hold(&k_full[next % S::kBufs], (next / S::kBufs) & 1);
-                    scores(x, next);
-                }
+                tc_commit(&o_full[x][b]);
+                tc_commit(&v_free[buf]);
             }
+            __syncwarp();
+            if (next < n_tiles) scores(next);  // over the weights just used: the products run in the order of their issue
         }
     } else {
         // ---------------------------------------------------------------------------------------- copies
@@ -620,7 +616,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     if (!s_last) return;
     __threadfence();
     const float* const slots = reinterpret_cast<const float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) + seg * splits * S::kPartial;
-    for (int r = warp; r < S::kRows && row0 + r < rows; r += 14) {
+    for (int r = warp; r < S::kRows && row0 + r < rows; r += S::kWarps) {
         float m = -INFINITY;
         for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(slots + i * S::kPartial + S::kRows * D + r));
 #pragma unroll
