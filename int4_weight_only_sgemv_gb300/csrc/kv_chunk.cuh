@@ -6,9 +6,12 @@
 // needs. Roles, by warp:
 //   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, S from tensor memory, weights back to tensor
 //             memory in fp16, over S
-//   8-11      unpack: raw subtiles -> K's integers q - z [key][dim] and V [dim][key] in fp16, both swizzled for the tensor cores,
-//             four buffers each, and K's scales
-//   12, 13    issue the products, a row tile each      14  issues the copies of raw subtiles (copy engine, 64 keys a stage)
+//   8-11      unpack K: raw subtiles -> the integers q - z [key][dim] in fp16, swizzled for the tensor cores, four buffers, and
+//             the scales
+//   12-15     unpack V [dim][key] likewise
+//   16, 17    issue the products, a row tile each      18  issues the copies of raw subtiles (copy engine, 64 keys a stage)
+// (with one warp a subtile for both K and V, unpacking was what a tile waited for: 2150 of 2850 cycles). Registers go from the
+// other warps to the softmax's (setmaxnreg), whose rows' 64 scores stay in them.
 // S has two buffers a row tile in tensor memory (2 x 2 x 64 columns beside 2 x D of O), so that the next tile's scores are there
 // when a softmax is done with one: with 128-key tiles and one buffer each softmax waited 2100 of 6100 cycles a tile for its
 // scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
@@ -39,7 +42,9 @@ struct ChunkShape {
     static constexpr int kRawBytes = kRawSubs * kSubBytes;
     static constexpr int kAtoms = D / 64;                         // 128-byte columns of a row of x or K
     static constexpr int kQBytes = kTile * D * 2, kKBytes = kKeys * D * 2, kVBytes = D * kKeys * 2;
-    static constexpr int kWarps = 15, kThreads = 32 * kWarps;
+    static constexpr int kWarps = 20, kThreads = 32 * kWarps;
+    // Registers a thread at launch, and after the split: 8 warps each, and 4. 8 kSoftmax + 8 kUnpack + 4 kOther = 20 kLaunch.
+    static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsUnpack = 80, kRegsOther = 64;
     static constexpr int kSmem = 1024 + 2 * kQBytes + kBufs * (kKBytes + kVBytes) + kRawStages * kRawBytes;
     static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
     static constexpr int kCols = 512;                             // tensor memory: S0, S1, O0, O1
@@ -102,6 +107,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// By every warp of a warpgroup: more registers a thread (once others have given theirs), or fewer.
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 __device__ __forceinline__ bool elect_one() {  // true in one lane of the warp
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -143,7 +154,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < S::kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 128);
+        for (int i = 0; i < S::kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 256);
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&k_full[i], 128), mbar_init(&k_free[i], 2);
             mbar_init(&v_full[i], 128), mbar_init(&v_free[i], 2);
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             s_bad = 1;
         }
     }
-    if (warp == 12) tc_alloc(&s_tmem, S::kCols);
+    if (warp == 16) tc_alloc(&s_tmem, S::kCols);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -230,6 +241,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     };
 
     if (warp < 8) {
+        regs_inc<S::kRegsSoftmax>();
         // ---------------------------------------------------------------------------------------- softmax
         const int x = warp >> 2, r = tid & 127, row = row0 + 128 * x + r;
         const bool live = row < rows;
@@ -278,8 +290,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         for (int j = 0; j < tiles; ++j) {
             const int pos0 = key0 + j * S::kKeys, b = j % S::kSBufs;
             const uint32_t ts = tmem + lanes + 128 * x + 64 * b;
-            wait(&s_full[x][b], (j / S::kSBufs) & 1);
-            wait(&k_full[j % S::kBufs], (j / S::kBufs) & 1);  // long since: makes the scales visible
+            wait(&s_full[x][b], (j / S::kSBufs) & 1);  // (the products waited for K, its scales with it)
             __syncwarp();
             tc_after_sync();
             const bool plain = pos0 >= clear0 && pos0 + S::kKeys <= clear1;
@@ -422,9 +433,13 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             write_lse(p, tok, a, m, l);
         }
         tc_before_sync();
-    } else if (warp < 12) {
+        __syncwarp();
+        regs_dec<S::kRegs>();  // every warp has the launch's number again
+    } else if (warp < 16) {
+        regs_dec<S::kRegsUnpack>();
         // ---------------------------------------------------------------------------------------- unpack
-        const int w = warp - 8, g = lane >> 2, t = lane & 3;
+        const bool keys_not_values = warp < 12;
+        const int w = warp & 3, g = lane >> 2, t = lane & 3;
         const __half2 half2_half = __floats2half2_rn(0.5f, 0.5f), half2_32nd = __floats2half2_rn(0.03125f, 0.03125f);
         const __half2 half2_16th = __floats2half2_rn(0.0625f, 0.0625f);
         // (nibble - zero) / 2 of bits 0 (hi false) or 4 of each half of a word, exactly; then times s, for V the scale
@@ -446,8 +461,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             const int stage = j % S::kRawStages, buf = j % S::kBufs;
             const int pos = key0 + S::kKeys * j + 16 * w;  // this warp's subtile
             wait(&raw_full[stage], (j / S::kRawStages) & 1);
-            if (j >= S::kBufs) {  // after the tile that had the buffers, its softmax included
-                wait(&k_free[buf], (j / S::kBufs - 1) & 1);
+            if (j >= S::kBufs) {  // after the tile that had the buffers; for K's scales, after its softmax too
+                if (keys_not_values) wait(&k_free[buf], (j / S::kBufs - 1) & 1);
                 wait(&v_free[buf], (j / S::kBufs - 1) & 1);
             }
             __syncwarp();
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             };
             const int col = 16 * w;  // key of the tile
             // K: 8 lanes a token and atom, each a word of 8 dims
-            {
+            if (keys_not_values) {
                 uint8_t* const dst = s_k + buf * S::kKBytes;
 #pragma unroll
                 for (int n = 0; n < 4 * S::kAtoms; ++n) {
@@ -481,7 +496,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 mbar_arrive(&k_full[buf]);
             }
             // V: lane (g, t) has tokens 4t .. 4t + 3 of dims g + 8n + 32i
-            {
+            if (!keys_not_values) {
                 uint8_t* const dst = s_v + buf * S::kVBytes;
                 uint32_t vq[D / 16];
 #pragma unroll
@@ -517,13 +532,17 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             }
             mbar_arrive(&raw_free[stage]);
         }
-    } else if (warp < 14) {
+        __syncwarp();
+        regs_inc<S::kRegs>();
+    } else {
+        regs_dec<S::kRegsOther>();
+        if (warp < 18) {
         // ---------------------------------------------------------------------------------------- products
         // A warp a row tile. The whole warp goes through the loop, with values that the compiler can see are the same in its lanes
         // (they end up in uniform registers, which the instruction reads); one lane issues. Issued from a branch of one lane, with
         // descriptors formed anew, an instruction took 115 cycles to issue, more than it takes to run; with one warp for both row
         // tiles, 80.
-        const int x = __shfl_sync(0xFFFFFFFFu, warp - 12, 0);
+        const int x = __shfl_sync(0xFFFFFFFFu, warp - 16, 0);
         const int n_tiles = __shfl_sync(0xFFFFFFFFu, tiles, 0);
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128 * x;
         const uint64_t q_desc = tc_desc(smem_addr(s_q) + x * S::kQBytes), k_desc = tc_desc(smem_addr(s_k)), v_desc = tc_desc(smem_addr(s_v));
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             if (next < n_tiles) scores(next);  // over the weights just used: the products run in the order of their issue
         }
-    } else {
+        } else if (warp == 18) {
         // ---------------------------------------------------------------------------------------- copies
         const int per = min(p.page, 64);  // keys of a copy
         const uint8_t* const base = p.cache + head * p.head_bytes;
@@ -598,12 +617,15 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             if (bytes) bulk_g2s(s_raw + stage * S::kRawBytes + lane * (per / kSub) * S::kSubBytes, src, bytes, &raw_full[stage]);
         }
+        }
+        __syncwarp();
+        regs_inc<S::kRegs>();
     }
     __syncwarp();
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    if (warp == 12) tc_dealloc(tmem, S::kCols);
+    if (warp == 16) tc_dealloc(tmem, S::kCols);
     if (parts == 1) return;
 
     // Join the splits of the segment: the last CTA to arrive, a row a warp, in the order of the keys.
