@@ -84,8 +84,9 @@ int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* len_dev, cons
  *                  one past the cache is skipped and reported (SGEMV_ERR_ARG). Slots are distinct.
  *   status_dev   : nullable; SGEMV_ERR_NONFINITE if a row holds inf or NaN, or a range too wide for an fp16 scale;
  *                  such a group is stored as zeros.
- * Every byte of a token's 16 * dim / 16 + scales is written, none of its neighbours'.
- * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_FORMAT (layout fields), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
+ * Every byte of a written token's nibbles and scales is set, none of its neighbours'.
+ * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_FORMAT (layout fields), SGEMV_ERR_ALIGN, SGEMV_ERR_SHAPE (n_tokens * heads
+ * past 2^31 - 1 rows of 128), SGEMV_ERR_CUDA.
  */
 int sgemv_kv_append(const sgemv_kv_layout* layout, void* cache_dev, int dtype, const void* k_dev,
                     int64_t k_token_stride, int64_t k_head_stride, const void* v_dev, int64_t v_token_stride,

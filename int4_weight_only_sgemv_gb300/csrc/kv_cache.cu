@@ -1,8 +1,10 @@
 // The paged 4-bit KV cache: its layout, writing K and V rows into it, and reading them back.
 //
-// Work unit of both kernels: one panel of min(dim, 128) dims of one (token, head), by width / 4 lanes: a warp, or
-// a half warp where dim is 64. Lane l holds dims 4l .. 4l+3 of the panel, so a quantisation group of 64 or 128
-// is 16 or 32 neighbouring lanes and its range is a few shuffles.
+// Both kernels move bytes, each input and output once. Work unit: one panel of min(dim, 128) dims of one (token, head), by
+// width / 8 lanes with 8 dims each: 16-byte loads and stores on the wide side, 4 bytes of K nibbles, and V's nibbles through a
+// 4 x 4 byte transpose over 4 lanes (two shuffles), since a 16-bit word of V holds one nibble from each of them. With 4 dims a
+// lane and a division an element the append was bound by its instructions (prompt of 20011 tokens, 8 heads of 128: append
+// and read 110 us together).
 #include <climits>
 
 #include "kv_common.cuh"
@@ -24,46 +26,74 @@ struct CacheParams {
     void* v_out;
     uint64_t sub_bytes, head_bytes, page_bytes;
     int64_t n_slots;  // slots of the cache
-    int64_t units;
-    int heads, page, n_tokens;
+    uint32_t units;
+    int heads, log2_page, n_tokens;
 };
 
-// Quantises the 4 values of this lane with the group of `lanes` neighbouring lanes: nibbles (first dim lowest),
-// scale and zero point. Binary32, no fused multiply-add, division rounded to nearest.
-__device__ __forceinline__ uint32_t quantise(const float (&x)[4], int lanes, __half& s16, float& z, bool& bad) {
-    float mn = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), 0.0f);
-    float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), 0.0f);
-    // fminf and fmaxf drop NaN: it is looked for by itself
-    int nan = (x[0] != x[0]) | (x[1] != x[1]) | (x[2] != x[2]) | (x[3] != x[3]);
-    for (int d = 1; d < lanes; d <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, d));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, d);
+template <typename T>
+struct Two;
+template <>
+struct Two<__half> { using type = __half2; };
+template <>
+struct Two<__nv_bfloat16> { using type = __nv_bfloat162; };
+
+// Quantises the 8 values of this lane with the group of kLanes neighbouring lanes: nibbles (first dim lowest), scale and zero
+// point, in binary32 without fused multiply-adds but for the quotients. A quotient v / s is formed from the reciprocal r of s as
+// t = v r, t + r (v - t s), the remainder exact in one fused multiply-add (Markstein's correction). The rounded integer is that
+// of the correctly rounded quotient: v and s have 11 bits at most, so a quotient that is not half way between two integers
+// is at least 2^-13 of its size away from there, and one that is half way comes out exactly.
+template <typename T, int kLanes>
+__device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s16, float& z, bool& bad) {
+    using T2 = typename Two<T>::type;
+    const T2* h = reinterpret_cast<const T2*>(&raw);
+    // the largest value and the largest negated value, exactly, NaN if one is
+    T2 hi = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    T2 lo = __hmax2_nan(__hmax2_nan(__hneg2(h[0]), __hneg2(h[1])), __hmax2_nan(__hneg2(h[2]), __hneg2(h[3])));
+    T2 m = __hmax2_nan(T2(hi.x, lo.x), T2(hi.y, lo.y));
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) {
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&m), d);
+        m = __hmax2_nan(m, *reinterpret_cast<const T2*>(&o));
     }
-    s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
-    bad = nan || __hisinf(s16) || isinf(mn) || isinf(mx);
+    const float mx = to_f32(m.x), mn = -to_f32(m.y);
+    bad = !(mx < INFINITY) || !(mn > -INFINITY);
+    const float top = fmaxf(mx, 0.0f), bottom = fminf(mn, 0.0f);
+    s16 = __float2half_rn(__fdiv_rn(__fsub_rn(top, bottom), 15.0f));
+    bad = bad || __hisinf(s16);
     if (bad || __half2float(s16) == 0.0f) s16 = __float2half_rn(1.0f);
-    const float s = __half2float(s16);
-    if (bad) {
-        z = 0.0f;
-        return 0;
-    }
-    z = fminf(fmaxf(rintf(__fdiv_rn(-mn, s)), 0.0f), 15.0f) + 0.0f;  // + 0: never -0
+    z = 0.0f;
+    if (bad) return 0;
+    const float s = __half2float(s16), r = __frcp_rn(s);
+    const auto whole = [&](float v) {
+        const float t = __fmul_rn(v, r);
+        return rintf(fmaf(r, fmaf(-t, s, v), t));
+    };
+    z = fminf(fmaxf(whole(-bottom), 0.0f), 15.0f) + 0.0f;  // + 0: never -0
     uint32_t q = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float f = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(x[j], s)), z), 0.0f), 15.0f);
-        q |= static_cast<uint32_t>(f) << (4 * j);
+    for (int j = 0; j < 8; ++j) {
+        const float v = to_f32(reinterpret_cast<const T*>(&raw)[j]);
+        q |= static_cast<uint32_t>(fminf(fmaxf(whole(v) + z, 0.0f), 15.0f)) << (4 * j);
     }
     return q;
 }
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const T* h = reinterpret_cast<const T*>(&w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = to_f32(h[j]);
+// Lane n of 4 neighbouring ones holds the bytes b[n][0..3]; afterwards b[0..3][n].
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
+    uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+    w = (lane & 1) ? __byte_perm(w, o, 0x3715) : __byte_perm(w, o, 0x6240);
+    o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+    return (lane & 2) ? __byte_perm(w, o, 0x3276) : __byte_perm(w, o, 0x5410);
+}
+// The low nibbles of 4 bytes as a 16-bit word, and back.
+__device__ __forceinline__ uint32_t pack_nibbles(uint32_t x) {
+    x &= 0x0F0F0F0Fu;
+    x = (x | (x >> 4)) & 0x00FF00FFu;
+    return (x | (x >> 8)) & 0xFFFFu;
+}
+__device__ __forceinline__ uint32_t spread_nibbles(uint32_t x) {
+    x = (x | (x << 8)) & 0x00FF00FFu;
+    return (x | (x << 4)) & 0x0F0F0F0Fu;
 }
 
 // Byte offset in a subtile of the 16-bit word of V with dims c + 8n + 32i (n = 0..3) of token tau.
@@ -73,116 +103,112 @@ __device__ __forceinline__ uint32_t v_word(int tau, int c, int i) {
     return 8 * D + (w >> 2) * 512 + (4 * c + (tau >> 2)) * 16 + (w & 3) * 4 + (tau & 1) * 2;
 }
 
+// Where a unit's lane works.
+template <int D>
+struct Place {
+    static constexpr int kPanel = D < 128 ? D : 128, kPanels = D / kPanel, kLanes = kPanel / 8;
+    uint32_t tok;
+    int lane, panel, head, tau;
+    int64_t slot;   // -1: nothing there
+    bool in;        // a unit of the call (a warp's last ones may not be: they still take part in the shuffles)
+    uint8_t* sub;
+    __device__ __forceinline__ explicit Place(const CacheParams& p) {
+        const uint32_t unit = blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
+        lane = threadIdx.x % kLanes;
+        in = unit < p.units;
+        panel = unit % kPanels;
+        tok = unit / kPanels / static_cast<uint32_t>(p.heads);
+        head = static_cast<int>(unit / kPanels - tok * static_cast<uint32_t>(p.heads));
+        slot = in ? p.slots[tok] : -1;
+        if (slot >= p.n_slots) {
+            report(p.status, SGEMV_ERR_ARG);
+            slot = -1;
+        }
+        if (slot < 0) slot = -1;
+        const int at = static_cast<int>(slot) & ((1 << p.log2_page) - 1);
+        tau = at % kSub;
+        sub = p.cache + static_cast<uint64_t>(slot >> p.log2_page) * p.page_bytes + head * p.head_bytes + (at / kSub) * p.sub_bytes;
+    }
+};
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int kPanel = D < 128 ? D : 128, kPanels = D / kPanel, kLanes = kPanel / 4;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x) / kLanes;
-    const bool in = unit < p.units;  // a half warp may be past the end: it still takes part in the shuffles
-    const int panel = static_cast<int>(unit % kPanels);
-    const int head = static_cast<int>(unit / kPanels % p.heads);
-    const int64_t tok = unit / kPanels / p.heads;
-    int64_t slot = in ? p.slots[tok] : -1;
-    if (slot >= p.n_slots) {
-        report(p.status, SGEMV_ERR_ARG);
-        slot = -1;
-    }
-    float x[4] = {}, y[4] = {};
-    if (slot >= 0) {
-        load4(static_cast<const T*>(p.k) + tok * p.k_token + head * p.k_head + panel * kPanel + 4 * lane, x);
-        load4(static_cast<const T*>(p.v) + tok * p.v_token + head * p.v_head + panel * kPanel + 4 * lane, y);
+    const Place<D> at(p);
+    constexpr int kPanel = Place<D>::kPanel;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (at.slot >= 0) {
+        const int d = at.panel * kPanel + 8 * at.lane;
+        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at.tok * p.k_token + at.head * p.k_head + d);
+        y = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + at.tok * p.v_token + at.head * p.v_head + d);
     }
     __half ks, vs;
     float kz, vz;
     bool kbad, vbad;
-    const uint32_t kq = quantise(x, G / 4, ks, kz, kbad);
-    const uint32_t vq = quantise(y, G / 4, vs, vz, vbad);
-    // V's word (i, c) takes the nibbles c + 8n + 32i: lane 8i + 2n + c / 4 of the panel, place c % 4
-    const int c = lane & 7, i = lane >> 3;
-    const int first = (threadIdx.x & 31) - lane + 8 * i + (c >> 2);
-    uint32_t vw = 0;
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-        vw |= ((__shfl_sync(0xFFFFFFFFu, vq, first + 2 * n) >> (4 * (c & 3))) & 15u) << (4 * n);
-    if (slot < 0) return;
+    const uint32_t kq = quantise<T, G / 8>(x, ks, kz, kbad);
+    // lane l holds dims 8l .. of block l / 4, n = l % 4: byte c / 2 of its nibbles is dims c, c + 1
+    const uint32_t vb = transpose_bytes(quantise<T, G / 8>(y, vs, vz, vbad), at.lane);
+    if (at.slot < 0) return;
     if (kbad || vbad) report(p.status, SGEMV_ERR_NONFINITE);
-    const int at = static_cast<int>(slot % p.page);
-    uint8_t* sub = p.cache + static_cast<uint64_t>(slot / p.page) * p.page_bytes + head * p.head_bytes +
-                   (at / kSub) * p.sub_bytes;
-    const int tau = at % kSub;
-    *reinterpret_cast<uint16_t*>(sub + panel * 8 * kPanel + tau * (kPanel / 2) + 2 * lane) = static_cast<uint16_t>(kq);
-    *reinterpret_cast<uint16_t*>(sub + v_word<D>(tau, c, i + 4 * panel)) = static_cast<uint16_t>(vw);
-    if (lane % (G / 4) == 0) {
-        const int grp = panel * (kPanel / G) + lane / (G / 4);
+    *reinterpret_cast<uint32_t*>(at.sub + at.panel * 8 * kPanel + at.tau * (kPanel / 2) + 4 * at.lane) = kq;
+    const int c = 2 * (at.lane & 3), i = (at.lane >> 2) + 4 * at.panel;
+    *reinterpret_cast<uint16_t*>(at.sub + v_word<D>(at.tau, c, i)) = static_cast<uint16_t>(pack_nibbles(vb));
+    *reinterpret_cast<uint16_t*>(at.sub + v_word<D>(at.tau, c + 1, i)) = static_cast<uint16_t>(pack_nibbles(vb >> 4));
+    if (at.lane % (G / 8) == 0) {
+        const int grp = at.panel * (kPanel / G) + at.lane / (G / 8);
         const __half2 k2 = __halves2half2(ks, __float2half_rn(kz)), v2 = __halves2half2(vs, __float2half_rn(vz));
-        *reinterpret_cast<__half2*>(sub + 16 * D + 64 * grp + 4 * tau) = k2;
-        *reinterpret_cast<__half2*>(sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * tau) = v2;
+        *reinterpret_cast<__half2*>(at.sub + 16 * D + 64 * grp + 4 * at.tau) = k2;
+        *reinterpret_cast<__half2*>(at.sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * at.tau) = v2;
     }
 }
 
+// The 8 values of nibbles q, each rounded once.
 template <typename T>
-__device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
-    T h[4];
+__device__ __forceinline__ void store8(T* p, uint32_t q, float s, float z) {
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = from_f32<T>(x[j]);
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
-    else *reinterpret_cast<float4*>(p) = make_float4(h[0], h[1], h[2], h[3]);
+    for (int j = 0; j < 8; ++j) f[j] = (static_cast<float>((q >> (4 * j)) & 15u) - z) * s;
+    if constexpr (sizeof(T) == 2) {
+        T h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = from_f32<T>(f[j]);
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
 }
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int kPanel = D < 128 ? D : 128, kPanels = D / kPanel, kLanes = kPanel / 4;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x) / kLanes;
-    const bool in = unit < p.units;
-    const int panel = static_cast<int>(unit % kPanels);
-    const int head = static_cast<int>(unit / kPanels % p.heads);
-    const int64_t tok = unit / kPanels / p.heads;
-    int64_t slot = in ? p.slots[tok] : -1;
-    if (slot >= p.n_slots) {
-        report(p.status, SGEMV_ERR_ARG);
-        slot = -1;
+    const Place<D> at(p);
+    constexpr int kPanel = Place<D>::kPanel;
+    uint32_t kq = 0, vb = 0;
+    float2 kf = make_float2(0.0f, 0.0f), vf = kf;  // scale, zero point
+    if (at.slot >= 0) {
+        kq = *reinterpret_cast<const uint32_t*>(at.sub + at.panel * 8 * kPanel + at.tau * (kPanel / 2) + 4 * at.lane);
+        const int c = 2 * (at.lane & 3), i = (at.lane >> 2) + 4 * at.panel;
+        const uint32_t lo = *reinterpret_cast<const uint16_t*>(at.sub + v_word<D>(at.tau, c, i));
+        const uint32_t hi = *reinterpret_cast<const uint16_t*>(at.sub + v_word<D>(at.tau, c + 1, i));
+        const int grp = at.panel * (kPanel / G) + at.lane / (G / 8);
+        kf = __half22float2(*reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * grp + 4 * at.tau));
+        vf = __half22float2(*reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * at.tau));
+        vb = spread_nibbles(lo) | (spread_nibbles(hi) << 4);
     }
-    uint32_t kq = 0, vw = 0;
-    float ks = 0.0f, kz = 0.0f, vs = 0.0f, vz = 0.0f;
-    const int c = lane & 7, i = lane >> 3;
-    if (slot >= 0) {
-        const int at = static_cast<int>(slot % p.page);
-        const uint8_t* sub = p.cache + static_cast<uint64_t>(slot / p.page) * p.page_bytes + head * p.head_bytes +
-                             (at / kSub) * p.sub_bytes;
-        const int tau = at % kSub;
-        kq = *reinterpret_cast<const uint16_t*>(sub + panel * 8 * kPanel + tau * (kPanel / 2) + 2 * lane);
-        vw = *reinterpret_cast<const uint16_t*>(sub + v_word<D>(tau, c, i + 4 * panel));
-        const int grp = panel * (kPanel / G) + lane / (G / 4);
-        const __half2 k2 = *reinterpret_cast<const __half2*>(sub + 16 * D + 64 * grp + 4 * tau);
-        const __half2 v2 = *reinterpret_cast<const __half2*>(sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * tau);
-        ks = __low2float(k2), kz = __high2float(k2), vs = __low2float(v2), vz = __high2float(v2);
-    }
-    // dim 4 lane + j of the panel is nibble n = lane / 2 % 4 of the word (i = lane / 8, c = 4 (lane % 2) + j)
-    const int base = (threadIdx.x & 31) - lane;
-    float x[4], y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w = __shfl_sync(0xFFFFFFFFu, vw, base + (lane & ~7) + 4 * (lane & 1) + j);
-        x[j] = (static_cast<float>((kq >> (4 * j)) & 15u) - kz) * ks;
-        y[j] = (static_cast<float>((w >> (4 * ((lane >> 1) & 3))) & 15u) - vz) * vs;
-    }
-    if (!in) return;
-    const int64_t o = (tok * p.heads + head) * D + panel * kPanel + 4 * lane;
-    store4(static_cast<T*>(p.k_out) + o, x);
-    store4(static_cast<T*>(p.v_out) + o, y);
+    const uint32_t vq = transpose_bytes(vb, at.lane);
+    if (!at.in) return;
+    const int64_t o = (static_cast<int64_t>(at.tok) * p.heads + at.head) * D + at.panel * kPanel + 8 * at.lane;
+    store8(static_cast<T*>(p.k_out) + o, kq, kf.x, kf.y);
+    store8(static_cast<T*>(p.v_out) + o, vq, vf.x, vf.y);
 }
 
 template <typename T, bool kAppend>
 cudaError_t launch_cache(const sgemv_kv_layout& L, const CacheParams& p, cudaStream_t s) {
-    const int lanes = L.dim < 128 ? L.dim / 4 : 32;
-    const int64_t blocks = (p.units * lanes + kCacheThreads - 1) / kCacheThreads;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const unsigned units = kCacheThreads / (L.dim < 128 ? L.dim / 8 : 16);  // of a CTA
+    const dim3 grid((p.units + units - 1) / units);
 #define SGEMV_KV_CASE(D, G)                                                                                   \
     if (L.dim == D && L.group == G) {                                                                         \
         if constexpr (kAppend) return launch_pdl(append_kernel<T, D, G>, grid, dim3(kCacheThreads), 0, s, p); \
@@ -197,6 +223,9 @@ cudaError_t launch_cache(const sgemv_kv_layout& L, const CacheParams& p, cudaStr
     return cudaErrorInvalidValue;
 }
 
+// Units of a call fit 31 bits (a unit's K and V take 256 bytes at least: no GPU holds so many).
+bool too_many(const sgemv_kv_layout& L, int n) { return static_cast<int64_t>(n) * L.heads * (L.dim > 128 ? 2 : 1) > INT_MAX; }
+
 CacheParams params_of(const sgemv_kv_layout& L, const void* cache, const int64_t* slots, int n, int32_t* status) {
     CacheParams p = {};
     p.cache = const_cast<uint8_t*>(static_cast<const uint8_t*>(cache));
@@ -207,9 +236,9 @@ CacheParams params_of(const sgemv_kv_layout& L, const void* cache, const int64_t
     p.page_bytes = L.page_bytes;
     p.n_slots = static_cast<int64_t>(L.n_pages) * L.page;
     p.heads = L.heads;
-    p.page = L.page;
+    while ((1 << p.log2_page) < L.page) ++p.log2_page;
     p.n_tokens = n;
-    p.units = static_cast<int64_t>(n) * L.heads * (L.dim > 128 ? L.dim / 128 : 1);
+    p.units = static_cast<uint32_t>(n) * L.heads * (L.dim > 128 ? L.dim / 128 : 1);
     return p;
 }
 
@@ -259,6 +288,7 @@ int sgemv_kv_append(const sgemv_kv_layout* layout, void* cache_dev, int dtype, c
     if (rc != SGEMV_OK) return rc;
     if ((dtype != SGEMV_F16 && dtype != SGEMV_BF16) || n_tokens < 0) return SGEMV_ERR_ARG;
     if (n_tokens == 0) return SGEMV_OK;
+    if (too_many(*layout, n_tokens)) return SGEMV_ERR_SHAPE;
     if (cache_dev == nullptr || k_dev == nullptr || v_dev == nullptr || slots_dev == nullptr) return SGEMV_ERR_ARG;
     if (!is_aligned(cache_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(slots_dev, 8) ||
         !is_aligned(status_dev, 4) || k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8)
@@ -282,6 +312,7 @@ int sgemv_kv_read(const sgemv_kv_layout* layout, const void* cache_dev, const in
     if (rc != SGEMV_OK) return rc;
     if (dtype < SGEMV_F16 || dtype > SGEMV_F32 || n_tokens < 0) return SGEMV_ERR_ARG;
     if (n_tokens == 0) return SGEMV_OK;
+    if (too_many(*layout, n_tokens)) return SGEMV_ERR_SHAPE;
     if (cache_dev == nullptr || k_dev == nullptr || v_dev == nullptr || slots_dev == nullptr) return SGEMV_ERR_ARG;
     if (!is_aligned(cache_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(slots_dev, 8) ||
         !is_aligned(status_dev, 4))
