@@ -64,16 +64,19 @@ __device__ __forceinline__ uint32_t quantise(const uint4& raw, __half& s16, floa
     z = 0.0f;
     if (bad) return 0;
     const float s = __half2float(s16), r = __frcp_rn(s);
-    const auto whole = [&](float v) {
+    // the quotient rounded to an integer, as the low bits of kMagic plus it (ties to even, as the addition rounds)
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+    const auto rounded = [&](float v) {
         const float t = __fmul_rn(v, r);
-        return rintf(fmaf(r, fmaf(-t, s, v), t));
+        return __fadd_rn(fmaf(r, fmaf(-t, s, v), t), kMagic);
     };
-    z = fminf(fmaxf(whole(-bottom), 0.0f), 15.0f) + 0.0f;  // + 0: never -0
+    z = fminf(fmaxf(rounded(-bottom) - kMagic, 0.0f), 15.0f) + 0.0f;  // + 0: never -0
+    const int zero = __float_as_int(z + kMagic) - 2 * __float_as_int(kMagic);
     uint32_t q = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float v = to_f32(reinterpret_cast<const T*>(&raw)[j]);
-        q |= static_cast<uint32_t>(fminf(fmaxf(whole(v) + z, 0.0f), 15.0f)) << (4 * j);
+        q += static_cast<uint32_t>(__viaddmin_s32_relu(__float_as_int(rounded(v)), zero, 15)) * (1u << (4 * j));
     }
     return q;
 }
@@ -163,20 +166,46 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheParams
     }
 }
 
-// The 8 values of nibbles q, each rounded once.
+// The 8 values of nibbles q, each rounded once. q - z comes out of the fp16 numbers 1024 + q and 1024 + 16 q exactly, dims j and
+// j + 4 at a time.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, uint32_t q, float s, float z) {
-    float f[8];
+__device__ __forceinline__ void store8(T* p, uint32_t q, __half2 sz) {
+    const __half2 z = __high2half2(sz), s = __low2half2(sz);
+    const __half2 z0 = __hsub2(__floats2half2_rn(-1024.0f, -1024.0f), z), z1 = __hsub2(__floats2half2_rn(-64.0f, -64.0f), z);
+    const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
+    __half2 h[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = (static_cast<float>((q >> (4 * j)) & 15u) - z) * s;
-    if constexpr (sizeof(T) == 2) {
-        T h[8];
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = (((j & 2) ? q >> 8 : q) & ((j & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+        const __half2 n = *reinterpret_cast<const __half2*>(&w);
+        h[j] = (j & 1) ? __hfma2(n, sixteenth, z1) : __hadd2(n, z0);
+    }
+    if constexpr (std::is_same<T, __half>::value) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = from_f32<T>(f[j]);
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+        for (int j = 0; j < 4; ++j) {
+            const __half2 f = __hmul2(h[j], s);
+            w[j] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                                                  __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
     } else {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        const float sf = __low2float(sz);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = __half22float2(h[j]);
+            f[j] = t.x * sf, f[j + 4] = t.y * sf;
+        }
+        if constexpr (sizeof(T) == 2) {
+            T o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = from_f32<T>(f[j]);
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+        } else {
+            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        }
     }
 }
 
@@ -187,22 +216,22 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheParams p
     const Place<D> at(p);
     constexpr int kPanel = Place<D>::kPanel;
     uint32_t kq = 0, vb = 0;
-    float2 kf = make_float2(0.0f, 0.0f), vf = kf;  // scale, zero point
+    __half2 kf = __floats2half2_rn(0.0f, 0.0f), vf = kf;  // scale, zero point
     if (at.slot >= 0) {
         kq = *reinterpret_cast<const uint32_t*>(at.sub + at.panel * 8 * kPanel + at.tau * (kPanel / 2) + 4 * at.lane);
         const int c = 2 * (at.lane & 3), i = (at.lane >> 2) + 4 * at.panel;
         const uint32_t lo = *reinterpret_cast<const uint16_t*>(at.sub + v_word<D>(at.tau, c, i));
         const uint32_t hi = *reinterpret_cast<const uint16_t*>(at.sub + v_word<D>(at.tau, c + 1, i));
         const int grp = at.panel * (kPanel / G) + at.lane / (G / 8);
-        kf = __half22float2(*reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * grp + 4 * at.tau));
-        vf = __half22float2(*reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * at.tau));
+        kf = *reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * grp + 4 * at.tau);
+        vf = *reinterpret_cast<const __half2*>(at.sub + 16 * D + 64 * (D / G) + 64 * grp + 4 * at.tau);
         vb = spread_nibbles(lo) | (spread_nibbles(hi) << 4);
     }
     const uint32_t vq = transpose_bytes(vb, at.lane);
     if (!at.in) return;
     const int64_t o = (static_cast<int64_t>(at.tok) * p.heads + at.head) * D + at.panel * kPanel + 8 * at.lane;
-    store8(static_cast<T*>(p.k_out) + o, kq, kf.x, kf.y);
-    store8(static_cast<T*>(p.v_out) + o, vq, vf.x, vf.y);
+    store8(static_cast<T*>(p.k_out) + o, kq, kf);
+    store8(static_cast<T*>(p.v_out) + o, vq, vf);
 }
 
 template <typename T, bool kAppend>
