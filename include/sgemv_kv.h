@@ -68,7 +68,7 @@ int sgemv_kv_layout_query(int heads, int dim, int group, int page, int n_pages, 
  * run out). A page id outside 0..n_pages-1 found in the table or the stack: SGEMV_ERR_ARG, and -1 in that
  * token's slot.
  * Pointers are 4-byte aligned (slots: 8-byte). n_req 0 and n_slots 0 are allowed.
- * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
+ * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page; n_req above 16384), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* len_dev, const int32_t* keep_dev,
                   const int32_t* add_dev, int32_t* table_dev, int table_cols, int64_t table_stride, int32_t* free_dev,

@@ -1,8 +1,12 @@
 // Block tables and slot maps of one step from the requests' lengths.
 //
-// Every CTA scans all requests by itself (three counts each), so no CTA waits for another; the outputs are then
-// spread over the whole grid. Nothing that is read is written: pages that change hands are found by their rank
-// among the given-up and the handed-out pages, not by the order in which threads reach the stack.
+// Every CTA scans all requests by itself (three counts each, prefix sums in shared memory), so no CTA waits for another; the
+// outputs are then spread over the whole grid, a token or a page a thread, which finds its request by a binary search.
+// Nothing that is read is written: pages that change hands are found by their rank among the given-up and the handed-out
+// pages, not by the order in which threads reach the stack.
+//
+// Bound by latency: a launch, two rounds of dependent loads and the scan. With the prefix sums of runs of requests alone, and
+// a walk through global memory from there, 4096 requests took 27 us.
 #include <algorithm>
 
 #include "kv_common.cuh"
@@ -11,7 +15,10 @@ namespace sgemv {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxReq = 16384;  // three prefix sums of so many requests fit in shared memory
+
+// Place of request r in shared memory: one word more every 32, so that threads with 8 (or 4, 16) requests each hit all banks.
+__host__ __device__ constexpr int padded(int r) { return r + (r >> 5); }
 
 struct PlanParams {
     const int32_t* len;
@@ -27,159 +34,150 @@ struct PlanParams {
     int64_t* slots;
     int32_t* pos;
     int32_t* status;
-    int n_req, page, n_pages, table_cols, n_slots;
+    int n_req, log2_page, n_pages, table_cols, n_slots;
 };
 
-// What one request (or a run of them) adds, gives up and is handed.
-struct Counts {
-    int64_t add, gone, come;
-};
-
-struct Request {
-    int len, keep, add, held, need;  // pages held before and needed after
-};
-
-__device__ __forceinline__ Request request(const PlanParams& p, int r) {
-    Request q;
-    q.len = p.len[r];
-    q.keep = p.keep != nullptr ? p.keep[r] : q.len;
-    q.add = p.add[r];
-    q.held = static_cast<int>((static_cast<int64_t>(q.len) + p.page - 1) / p.page);
-    q.need = static_cast<int>((static_cast<int64_t>(q.keep) + q.add + p.page - 1) / p.page);
-    return q;
+// Pages of n tokens.
+__device__ __forceinline__ int pages_of(const PlanParams& p, int64_t n) {
+    return static_cast<int>((n + (1 << p.log2_page) - 1) >> p.log2_page);
 }
 
-__device__ __forceinline__ Counts counts(const Request& q) {
-    return {q.add, q.held > q.need ? q.held - q.need : 0, q.need > q.held ? q.need - q.held : 0};
-}
-
-// The last i in [0, n) with a[i] <= x (a[0] <= x).
-__device__ __forceinline__ int find(const int64_t* a, int n, int64_t x) {
+// The last r in [0, n) with a[r] <= x (a[0] <= x): of requests with the same prefix sum the last, which is the one that is not empty.
+__device__ __forceinline__ int find(const int32_t* a, int n, int x) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a[mid] <= x) lo = mid; else hi = mid - 1;
+        if (a[padded(mid)] <= x) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-    __shared__ int64_t s_add[kPlanThreads], s_gone[kPlanThreads], s_come[kPlanThreads];
+template <int kPlanThreads>
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams p) {
+    extern __shared__ int32_t s_sums[];  // of tokens, of pages given up, of pages handed out, before each request
+    int32_t* const s_add = s_sums;
+    int32_t* const s_gone = s_add + padded(p.n_req);
+    int32_t* const s_come = s_gone + padded(p.n_req);
     __shared__ int64_t s_warp[3][kPlanThreads / 32];
     __shared__ int s_err;
     pdl_launch_dependents();
-    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // thread t has the requests [t * run, (t + 1) * run)
-    const int run = (p.n_req + kPlanThreads - 1) / kPlanThreads;
     if (tid == 0) s_err = 0;
     __syncthreads();
-    Counts sum = {0, 0, 0};
-    const int r0 = static_cast<int>(min(static_cast<int64_t>(tid) * run, static_cast<int64_t>(p.n_req)));
-    const int r1 = min(r0 + run, p.n_req);
-    for (int r = r0; r < r1; ++r) {
-        const Request q = request(p, r);
-        if (q.len < 0 || q.keep < 0 || q.keep > q.len || q.add < 0 || static_cast<int64_t>(q.keep) + q.add > INT32_MAX)
-            s_err = SGEMV_ERR_ARG;
-        else if (max(q.held, q.need) > p.table_cols)
-            atomicCAS(&s_err, 0, SGEMV_ERR_SHAPE);
-        const Counts c = counts(q);
-        sum.add += c.add, sum.gone += c.gone, sum.come += c.come;
-    }
-    // exclusive prefix sums over the threads
-    Counts incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t a = __shfl_up_sync(0xFFFFFFFFu, incl.add, d), g = __shfl_up_sync(0xFFFFFFFFu, incl.gone, d),
-                      c = __shfl_up_sync(0xFFFFFFFFu, incl.come, d);
-        if (lane >= d) incl.add += a, incl.gone += g, incl.come += c;
-    }
-    if (lane == 31) s_warp[0][warp] = incl.add, s_warp[1][warp] = incl.gone, s_warp[2][warp] = incl.come;
-    __syncthreads();
-    Counts before = {0, 0, 0}, all = {0, 0, 0};
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before.add += s_warp[0][w], before.gone += s_warp[1][w], before.come += s_warp[2][w];
-        all.add += s_warp[0][w], all.gone += s_warp[1][w], all.come += s_warp[2][w];
-    }
-    before.add += incl.add - sum.add, before.gone += incl.gone - sum.gone, before.come += incl.come - sum.come;
-    s_add[tid] = before.add, s_gone[tid] = before.gone, s_come[tid] = before.come;
-    __syncthreads();
+    pdl_wait();
     const int n_free = *p.free_count;
+#pragma unroll 4
+    for (int r = tid; r < p.n_req; r += kPlanThreads) {
+        const int len = p.len[r], keep = p.keep != nullptr ? p.keep[r] : len, add = p.add[r];
+        const int64_t total = static_cast<int64_t>(keep) + add;
+        const int held = pages_of(p, len), need = pages_of(p, total);
+        if (len < 0 || keep < 0 || keep > len || add < 0 || total > INT32_MAX) s_err = SGEMV_ERR_ARG;
+        else if (max(held, need) > p.table_cols) atomicCAS(&s_err, 0, SGEMV_ERR_SHAPE);
+        s_add[padded(r)] = add;
+        s_gone[padded(r)] = max(held - need, 0);
+        s_come[padded(r)] = max(need - held, 0);
+    }
+    __syncthreads();
+    // exclusive prefix sums: thread t has the requests [t * run, (t + 1) * run)
+    const int run = (p.n_req + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = min(tid * run, p.n_req), r1 = min(r0 + run, p.n_req);
+    int64_t sum[3] = {0, 0, 0}, incl[3];
+    for (int r = r0; r < r1; ++r) sum[0] += s_add[padded(r)], sum[1] += s_gone[padded(r)], sum[2] += s_come[padded(r)];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) incl[x] = sum[x];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl[x], d);
+            if (lane >= d) incl[x] += o;
+        }
+    if (lane == 31)
+        for (int x = 0; x < 3; ++x) s_warp[x][warp] = incl[x];
+    __syncthreads();
+    int64_t before[3], all[3] = {0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        before[x] = incl[x] - sum[x];
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) before[x] += s_warp[x][w];
+            all[x] += s_warp[x][w];
+        }
+    }
+    int32_t at[3] = {static_cast<int32_t>(before[0]), static_cast<int32_t>(before[1]), static_cast<int32_t>(before[2])};
+    for (int r = r0; r < r1; ++r) {
+        const int i = padded(r);
+        const int32_t a = s_add[i], g = s_gone[i], c = s_come[i];
+        s_add[i] = at[0], s_gone[i] = at[1], s_come[i] = at[2];
+        at[0] += a, at[1] += g, at[2] += c;
+    }
+    __syncthreads();
     int err = s_err;
-    if (err == 0 && (all.add > p.n_slots || n_free < 0 || n_free > p.n_pages)) err = SGEMV_ERR_ARG;
-    if (err == 0 && (all.come - all.gone > n_free || all.gone - all.come > p.n_pages - n_free)) err = SGEMV_ERR_SHAPE;
+    if (err == 0 && (all[0] > p.n_slots || n_free < 0 || n_free > p.n_pages)) err = SGEMV_ERR_ARG;
+    if (err == 0 && (all[2] - all[1] > n_free || all[1] - all[2] > p.n_pages - n_free)) err = SGEMV_ERR_SHAPE;
     const bool ok = err == 0;
-    if (!ok && blockIdx.x == 0 && tid == 0) report(p.status, err);
+    const int tokens = ok ? static_cast<int>(all[0]) : 0, gone = ok ? static_cast<int>(all[1]) : 0, come = ok ? static_cast<int>(all[2]) : 0;
 
-    // per request: thread t's run by CTA t % grid
-    if (tid % gridDim.x == blockIdx.x) {
-        int64_t at = before.add;
-        for (int r = r0; r < r1; ++r) {
-            const Request q = request(p, r);
-            p.q_start[r] = ok ? static_cast<int32_t>(at) : 0;
-            p.len_out[r] = ok ? q.keep + q.add : q.len;
-            at += q.add;
-        }
+    const int first = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
+    if (first == 0) {
+        if (!ok) report(p.status, err);
+        p.q_start[p.n_req] = tokens;
+        *p.free_count_out = n_free + gone - come;
     }
-    if (blockIdx.x == 0 && tid == 0) {
-        p.q_start[p.n_req] = ok ? static_cast<int32_t>(all.add) : 0;
-        *p.free_count_out = ok ? static_cast<int32_t>(n_free + all.gone - all.come) : n_free;
+    for (int r = first; r < p.n_req; r += stride) {
+        const int len = p.len[r];
+        p.q_start[r] = ok ? s_add[padded(r)] : 0;
+        p.len_out[r] = ok ? (p.keep != nullptr ? p.keep[r] : len) + p.add[r] : len;
     }
-
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-    const int n_run = run > 0 ? min(kPlanThreads, (p.n_req + run - 1) / run) : 0;
-
-    // the i-th page that a request gives up
-    const auto given = [&](int64_t i) {
-        const int t = find(s_gone, n_run, i);
-        int64_t at = s_gone[t];
-        for (int r = t * run;; ++r) {
-            const Request q = request(p, r);
-            const int64_t n = counts(q).gone;
-            if (i < at + n) return p.table[r * p.table_stride + q.need + (i - at)];
-            at += n;
-        }
+    // the i-th page that a request gives up: block need + (i - its first) of it
+    const auto given = [&](int i) {
+        const int r = find(s_gone, p.n_req, i);
+        const int need = pages_of(p, static_cast<int64_t>(p.keep != nullptr ? p.keep[r] : p.len[r]) + p.add[r]);
+        return p.table[r * p.table_stride + need + (i - s_gone[padded(r)])];
     };
     // the i-th page that a request is handed
-    const auto handed = [&](int64_t i) {
-        return i < all.gone ? given(i) : p.free[n_free - 1 - (i - all.gone)];
-    };
-    if (ok) {
-        for (int64_t i = first; i < all.come; i += stride) {
-            const int t = find(s_come, n_run, i);
-            int64_t at = s_come[t];
-            int r = t * run;
-            Request q = request(p, r);
-            while (i >= at + counts(q).come) {
-                at += counts(q).come;
-                q = request(p, ++r);
-            }
-            p.table[r * p.table_stride + q.held + (i - at)] = handed(i);
-        }
-        for (int64_t i = all.come + first; i < all.gone; i += stride) p.free[n_free + i - all.come] = given(i);
+    const auto handed = [&](int i) { return i < gone ? given(i) : p.free[n_free - 1 - (i - gone)]; };
+    for (int i = first; i < come; i += stride) {
+        const int r = find(s_come, p.n_req, i);
+        p.table[r * p.table_stride + pages_of(p, p.len[r]) + (i - s_come[padded(r)])] = handed(i);
     }
-    for (int64_t i = first; i < p.n_slots; i += stride) {
+    for (int i = come + first; i < gone; i += stride) p.free[n_free + i - come] = given(i);
+#pragma unroll 2
+    for (int i = first; i < p.n_slots; i += stride) {
         int64_t slot = -1;
         int pos = -1;
-        if (ok && i < all.add) {
-            const int t = find(s_add, n_run, i);
-            int64_t at = s_add[t], come = s_come[t];
-            int r = t * run;
-            Request q = request(p, r);
-            while (i >= at + q.add) {
-                at += q.add, come += counts(q).come;
-                q = request(p, ++r);
-            }
-            pos = q.keep + static_cast<int>(i - at);
-            const int b = pos / p.page;
-            const int id = b < q.held ? p.table[r * p.table_stride + b] : handed(come + (b - q.held));
-            if (id >= 0 && id < p.n_pages) slot = static_cast<int64_t>(id) * p.page + pos % p.page;
+        if (i < tokens) {
+            const int r = find(s_add, p.n_req, i);
+            const int len = p.len[r];
+            pos = (p.keep != nullptr ? p.keep[r] : len) + (i - s_add[padded(r)]);
+            const int b = pos >> p.log2_page, held = pages_of(p, len);
+            const int id = b < held ? p.table[r * p.table_stride + b] : handed(s_come[padded(r)] + (b - held));
+            if (id >= 0 && id < p.n_pages) slot = (static_cast<int64_t>(id) << p.log2_page) + (pos & ((1 << p.log2_page) - 1));
             else report(p.status, SGEMV_ERR_ARG);
         }
         p.slots[i] = slot;
         p.pos[i] = pos;
     }
+}
+
+template <int kPlanThreads>
+int launch_plan(const PlanParams& p, const DeviceInfo& di, cudaStream_t s) {
+    const uint32_t smem = static_cast<uint32_t>(padded(p.n_req)) * 12;
+    if (smem > 44 * 1024) {  // the kernel has some of its own
+        static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SGEMV_ERR_CUDA;
+        if (attr_set[dev].load() == 0) {
+            if (cudaFuncSetAttribute(plan_kernel<kPlanThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     padded(kPlanMaxReq) * 12) != cudaSuccess)
+                return SGEMV_ERR_CUDA;
+            attr_set[dev].store(1);
+        }
+    }
+    // a token a thread, up to a CTA an SM
+    const int grid = std::max(1, std::min(di.sm_count, (std::max(p.n_req, p.n_slots) + kPlanThreads - 1) / kPlanThreads));
+    return launch_pdl(plan_kernel<kPlanThreads>, dim3(grid), dim3(kPlanThreads), smem, s, p) == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }
 
 }  // namespace
@@ -195,6 +193,7 @@ extern "C" int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* le
                              int n_slots, int32_t* status_dev, void* stream) {
     if (n_req < 0 || n_slots < 0 || table_cols < 1 || table_stride < table_cols || n_pages < 1) return SGEMV_ERR_ARG;
     if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return SGEMV_ERR_SHAPE;
+    if (n_req > kPlanMaxReq) return SGEMV_ERR_SHAPE;
     const void* must[] = {free_dev, free_count_dev, free_count_out_dev, q_start_dev};
     for (const void* q : must)
         if (q == nullptr) return SGEMV_ERR_ARG;
@@ -227,11 +226,12 @@ extern "C" int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* le
     p.pos = pos_dev;
     p.status = status_dev;
     p.n_req = n_req;
-    p.page = page;
+    p.log2_page = 0;
+    while ((1 << p.log2_page) < page) ++p.log2_page;
     p.n_pages = n_pages;
     p.table_cols = table_cols;
     p.n_slots = n_slots;
-    const int grid = std::max(1, std::min(di.sm_count, (std::max(n_req, n_slots) + kPlanThreads - 1) / kPlanThreads));
-    const cudaError_t e = launch_pdl(plan_kernel, dim3(grid), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), p);
-    return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
+    // a decode step of up to 256 requests is all latency: fewer warps to bring together; more work needs them
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return n_req <= 256 && n_slots <= 4096 ? launch_plan<256>(p, di, st) : launch_plan<1024>(p, di, st);
 }

@@ -78,7 +78,8 @@ def _on(stream, t):
 
 
 def _flat(t, dtype, numel, what):
-    """t is a contiguous CUDA tensor of dtype with numel elements (any number if None)."""
+    """t is a contiguous CUDA tensor of dtype with numel elements (any number if None). (sgemv_kv_plan and sgemv_kv_attention,
+    whose calls are short and have many tensors, ask the same in place first: a call here costs as much as the questions.)"""
     try:
         if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (numel is None or t.numel() == numel):
             return
@@ -129,22 +130,36 @@ def sgemv_kv_plan(length, keep, add, table, free, free_count, page: int, out, st
     q_start int32 [n_req + 1], slots int64 [n_slots], pos int32 [n_slots])."""
     o_length, o_count, o_start, o_slots, o_pos = out
     i32 = torch.int32
-    _flat(length, i32, None, "length")
-    n = length.numel()
-    if keep is not None:
-        _flat(keep, i32, n, "keep")
-    _flat(add, i32, n, "add")
-    cols, stride = _table_ok(table, n)
-    _flat(free, i32, None, "free")
-    _flat(free_count, i32, 1, "free_count")
-    _flat(o_length, i32, n, "out length")
-    _flat(o_count, i32, 1, "out free_count")
-    _flat(o_start, i32, n + 1, "out q_start")
-    _flat(o_slots, torch.int64, None, "out slots")
-    n_slots = o_slots.numel()
-    _flat(o_pos, i32, n_slots, "out pos")
-    if status is not None:
-        _flat(status, i32, None, "status")
+    try:
+        if length.dtype is not i32 or not length.is_cuda or not length.is_contiguous():
+            _flat(length, i32, None, "length")
+        n = length.numel()
+        if keep is not None:
+            if keep.dtype is not i32 or not keep.is_cuda or not keep.is_contiguous() or keep.numel() != n:
+                _flat(keep, i32, n, "keep")
+        if add.dtype is not i32 or not add.is_cuda or not add.is_contiguous() or add.numel() != n:
+            _flat(add, i32, n, "add")
+        cols, stride = _table_ok(table, n)
+        if free.dtype is not i32 or not free.is_cuda or not free.is_contiguous():
+            _flat(free, i32, None, "free")
+        if free_count.dtype is not i32 or not free_count.is_cuda or not free_count.is_contiguous() or \
+                free_count.numel() != 1:
+            _flat(free_count, i32, 1, "free_count")
+        if o_length.dtype is not i32 or not o_length.is_cuda or not o_length.is_contiguous() or o_length.numel() != n:
+            _flat(o_length, i32, n, "out length")
+        if o_count.dtype is not i32 or not o_count.is_cuda or not o_count.is_contiguous() or o_count.numel() != 1:
+            _flat(o_count, i32, 1, "out free_count")
+        if o_start.dtype is not i32 or not o_start.is_cuda or not o_start.is_contiguous() or o_start.numel() != n + 1:
+            _flat(o_start, i32, n + 1, "out q_start")
+        if o_slots.dtype is not torch.int64 or not o_slots.is_cuda or not o_slots.is_contiguous():
+            _flat(o_slots, torch.int64, None, "out slots")
+        n_slots = o_slots.numel()
+        if o_pos.dtype is not i32 or not o_pos.is_cuda or not o_pos.is_contiguous() or o_pos.numel() != n_slots:
+            _flat(o_pos, i32, n_slots, "out pos")
+        if status is not None:
+            _flat(status, i32, None, "status")
+    except AttributeError:
+        raise TypeError("sgemv_kv_plan: expected torch.Tensors") from None
     code = _lib.sgemv_kv_plan(n, page, free.numel(), length.data_ptr(), _ptr(keep), add.data_ptr(), table.data_ptr(), cols,
                               stride, free.data_ptr(), free_count.data_ptr(), o_length.data_ptr(), o_count.data_ptr(),
                               o_start.data_ptr(), o_slots.data_ptr(), o_pos.data_ptr(), n_slots, _ptr(status),
@@ -189,23 +204,33 @@ def sgemv_kv_attention(layout: KvLayout, cache, q, q_start, length, table, out, 
     """Attention of the requests' new tokens over the cache. q, out: fp16 or bf16 [tokens, heads_q, dim] (any token and
     head strides); q_start int32 [n_req + 1]; length int32 [n_req], new tokens included; table int32 [n_req, columns];
     workspace: from kv_workspace(); lse: fp32 [tokens, heads_q] or None; tree: int64 [tokens] bit masks or None."""
-    _cache_ok(layout, cache)
-    n, heads, _ = shape = q.shape
-    dtype, i32 = q.dtype, torch.int32
-    if shape[2] != layout.dim:
-        raise ValueError(f"q: expected rows of {layout.dim}")
-    qs, os = _rows(q, shape, dtype, "q"), _rows(out, shape, dtype, "out")
-    _flat(length, i32, None, "length")
-    n_req = length.numel()
-    _flat(q_start, i32, n_req + 1, "q_start")
-    cols, stride = _table_ok(table, n_req)
-    _flat(workspace, torch.uint8, None, "workspace")
-    if lse is not None:
-        _flat(lse, torch.float32, n * heads, "lse")
-    if tree is not None:
-        _flat(tree, torch.int64, n, "tree")
-    if status is not None:
-        _flat(status, i32, None, "status")
+    i32 = torch.int32
+    try:
+        if cache.dtype is not torch.uint8 or not cache.is_cuda or not cache.is_contiguous() or \
+                cache.numel() < layout.total_bytes:
+            _cache_ok(layout, cache)
+        n, heads, _ = shape = q.shape
+        dtype = q.dtype
+        if shape[2] != layout.dim:
+            raise ValueError(f"q: expected rows of {layout.dim}")
+        qs, os = _rows(q, shape, dtype, "q"), _rows(out, shape, dtype, "out")
+        if length.dtype is not i32 or not length.is_cuda or not length.is_contiguous():
+            _flat(length, i32, None, "length")
+        n_req = length.numel()
+        if q_start.dtype is not i32 or not q_start.is_cuda or not q_start.is_contiguous() or \
+                q_start.numel() != n_req + 1:
+            _flat(q_start, i32, n_req + 1, "q_start")
+        cols, stride = _table_ok(table, n_req)
+        if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+            _flat(workspace, torch.uint8, None, "workspace")
+        if lse is not None:
+            _flat(lse, torch.float32, n * heads, "lse")
+        if tree is not None:
+            _flat(tree, torch.int64, n, "tree")
+        if status is not None:
+            _flat(status, i32, None, "status")
+    except AttributeError:
+        raise TypeError("sgemv_kv_attention: expected torch.Tensors") from None
     args = KvQuery(_DTYPE.get(dtype, -1), heads, n_req, n, max_q, window, cols, scale, stride, qs[0], qs[1], os[0], os[1],
                    q.data_ptr(), q_start.data_ptr(), length.data_ptr(), table.data_ptr(), _ptr(tree), out.data_ptr(),
                    _ptr(lse), workspace.data_ptr(), workspace.numel())
