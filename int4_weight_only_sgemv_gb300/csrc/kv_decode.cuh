@@ -167,7 +167,10 @@ __device__ __forceinline__ void join_row(const AttnParams& p, const Segment& s, 
     if (s.row0 + row >= s.span.n * p.ratio) return;
     constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, one(i, kM + row));
+    float m0 = -INFINITY, l0 = 0.0f;  // of partial `lane`
+    if (lane < n) m0 = one(lane, kM + row), l0 = one(lane, kL + row);
+    m = m0;
+    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, one(i, kM + row));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     constexpr int kVec = (D + 127) / 128;  // groups of 4 dims a lane has (where D is 64, both half warps have the same)
@@ -177,14 +180,12 @@ __device__ __forceinline__ void join_row(const AttnParams& p, const Segment& s, 
 #pragma unroll
     for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i0 = 0; i0 < n; i0 += 32) {
-        float f = 0.0f, fl = 0.0f;
-        if (i0 + lane < n) {
-            const float mi = one(i0 + lane, kM + row), li = one(i0 + lane, kL + row);
-            f = mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);
-            fl = li * f;
-        }
+        float mi = m0, li = l0;
+        if (i0 > 0 && i0 + lane < n) mi = one(i0 + lane, kM + row), li = one(i0 + lane, kL + row);
+        const float f = i0 + lane >= n ? 0.0f : (mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m));
+        const float fl = i0 + lane < n ? li * f : 0.0f;
         const int cnt = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < cnt; ++i) {
             const float w = __shfl_sync(0xFFFFFFFFu, f, i);
             l += __shfl_sync(0xFFFFFFFFu, fl, i);
@@ -414,10 +415,27 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         to = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch)));
     }
     bool more = from < to;
+    // The queries of a segment, raw: row g of each 8, this lane's dims (see below).
+    uint4 raw_q[NT][S::kPanels][kWords];
+    const auto load_queries = [&] {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = seg.row0 + 8 * nt + g;
+            const bool live = row < seg.span.n * p.ratio;
+            const T* x = static_cast<const T*>(p.q.q_dev);
+            if (live) x += (seg.span.first + row / p.ratio) * p.q.q_token_stride + (seg.head * p.ratio + row % p.ratio) * p.q.q_head_stride;
+#pragma unroll
+            for (int pn = 0; pn < S::kPanels; ++pn)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    raw_q[nt][pn][w] = live ? *reinterpret_cast<const uint4*>(x + pn * 128 + 8 * (kWords * t + w)) : make_uint4(0, 0, 0, 0);
+        }
+    };
     bool dead = false;       // a copy never came
     uint32_t stage = 0, parity = 0;  // of the tile waited for next
     Producer<D, G, NT> ahead;
     if (more) {
+        load_queries();  // under way while the copies are set up
         if (lane == 0) s_ahead[warp] = seg;
         __syncwarp();
         ahead.seg = &s_ahead[warp];
@@ -440,25 +458,13 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         float nx[kGr][NT][2], c;
         {
             float big = 0.0f;
-            const T* x[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = seg.row0 + 8 * nt + g;
-                x[nt] = row < rows ? static_cast<const T*>(p.q.q_dev) + (seg.span.first + row / p.ratio) * p.q.q_token_stride +
-                                         (seg.head * p.ratio + row % p.ratio) * p.q.q_head_stride
-                                   : nullptr;
-            }
-            const auto load = [&](int nt, int pn, int w) {
-                return x[nt] != nullptr ? *reinterpret_cast<const uint4*>(x[nt] + pn * 128 + 8 * (kWords * t + w)) : make_uint4(0, 0, 0, 0);
-            };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int pn = 0; pn < S::kPanels; ++pn)
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
-                        const uint4 raw = load(nt, pn, w);
-                        const T* h = reinterpret_cast<const T*>(&raw);
+                        const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
                     }
@@ -476,8 +482,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                     sum[pn] = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
-                        const uint4 raw = load(nt, pn, w);
-                        const T* h = reinterpret_cast<const T*>(&raw);
+                        const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
                         float f[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] = to_f32(h[j]) * up;
@@ -786,11 +791,21 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             s_has[slot] = 1;
             s_seg[slot] = seg;
         }
+        __syncwarp();
         if (more) {
             next_segment<S::kRows>(p, spans, seg);
             from = 0;
             to = static_cast<int>(min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch));
+            load_queries();
         }
+    }
+    // A warp's first partial comes back from global memory into its ring, so that the joins read shared memory only.
+    if (s_has[2 * warp]) {
+        static_assert(S::kPartial * 4 <= S::kStages * S::kStageBytes, "a partial in a warp's ring");
+        const float4* const src = reinterpret_cast<const float4*>(scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + warp) * S::kPartial);
+        float4* const dst = reinterpret_cast<float4*>(smem + warp * S::kStages * S::kStageBytes);
+#pragma unroll 8
+        for (int i = lane; i < S::kPartial / 4; i += 32) dst[i] = src[i];
     }
     __syncthreads();
 
@@ -818,7 +833,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         const auto base = [&](int i) {
             const int x = s_list[first + i];
             return (x & 1) ? reinterpret_cast<const float*>(smem + S::kRing) + (x >> 1) * S::kPartial
-                           : scratch + (static_cast<int64_t>(blockIdx.x) * S::kWarps + (x >> 1)) * S::kPartial;
+                           : reinterpret_cast<const float*>(smem + (x >> 1) * S::kStages * S::kStageBytes);
         };
         join_row<T, D, G, NT>(
             p, s, row, s_first[gr + 1] - first, lane, [&](int i, int at) { return *reinterpret_cast<const float4*>(base(i) + at); },
