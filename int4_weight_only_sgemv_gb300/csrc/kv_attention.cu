@@ -49,6 +49,9 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     while ((1 << p.log2_page) < layout->page) ++p.log2_page;
     p.n_pages = layout->n_pages;
     p.ratio = q.heads_q / layout->heads;
+    p.log2_ratio = 0;
+    while ((1 << p.log2_ratio) < p.ratio) ++p.log2_ratio;
+    if ((1 << p.log2_ratio) != p.ratio) p.log2_ratio = -1;
     p.scale_log2 = q.scale * 1.44269504088896340736f;
     DeviceInfo di;
     rc = device_info(&di);

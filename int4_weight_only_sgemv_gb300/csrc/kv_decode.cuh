@@ -35,7 +35,8 @@ constexpr int kMaxLen = 1 << 30;  // positions past the end of a tile stay in 32
 // Weights 2^(t - m) s' go into fp16: the largest is 2^kTop when the reference m is set, and m is set anew when one would pass
 // 2^kLimit (fp16 ends at 2^16). Weights below 2^(kTop - 20) of the largest lose bits, as fp16 subnormals.
 constexpr float kTop = 6.0f, kLimit = 15.0f;
-constexpr int kSwitch = 2;  // what taking up a segment costs, in tiles: counted when the work is split
+constexpr int kSwitch = 4;  // what taking up a segment costs, in tiles: counted when the work is split (1: 114 us, 2: 107, 3: 104.3, 4: 104.7
+                            // for a batch of 64 requests of 1 to 16384 keys; one request of 262144: 65.0 with 3, 64.1 with 4)
 constexpr int kMaxCtas = 152; // CTAs that the workspace has room for
 constexpr int kSpans = 256; // requests whose lengths are kept in shared memory
 
@@ -45,6 +46,7 @@ struct AttnParams {
     sgemv_kv_query q;
     int32_t* status;
     int heads, page, log2_page, n_pages, ratio;
+    int log2_ratio;    // -1 where ratio is not a power of two
     int max_rows;      // requests with more rows a KV head are the chunk kernel's
     float scale_log2;  // scale * log2(e)
 };
@@ -57,8 +59,9 @@ struct AttnShape {
     static constexpr bool kSplit = G < kPanel;       // a panel holds two groups
     static constexpr int kSubBytes = 16 * D + 128 * kGroups;
     static constexpr int kStageBytes = 2 * kSubBytes;
-    static constexpr int kWarps = (D == 256 || NT > 1) ? 8 : 16;
-    static constexpr int kStages = D == 64 ? 4 : NT > 1 ? 3 : 2;
+    // 12 warps have 168 registers a thread: the 128 of 16 warps spilled (104.3 against 102.6 us for the batch of 64 requests).
+    static constexpr int kWarps = (D == 256 || (NT > 1 && D > 64)) ? 8 : 12;
+    static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;             // floats of a partial row: 4 more so that two rows are 8 banks apart
     static constexpr int kPartial = kRows * kPitch + 2 * kRows;  // floats of a partial: O, then m, then l
@@ -67,8 +70,19 @@ struct AttnShape {
     static constexpr int kSmem = kRing + kWarps * kPartial * 4;  // the rings, then a partial a warp
     // With at most so many tiles in all, a CTA's part of the list starts where a segment starts, if that segment has at
     // most kShortSegment tiles: a join across CTAs costs more than it brings.
-    static constexpr int kFewTiles = 2 * kWarps, kShortSegment = 4 * kWarps;
+    static constexpr int kFewTiles = 2 * kWarps, kShortSegment = 2 * kWarps;
 };
+
+// Token of a row of a request, and its query head among those of the KV head.
+__device__ __forceinline__ int token_of_row(const AttnParams& p, int row) {
+    return p.log2_ratio >= 0 ? row >> p.log2_ratio : row / p.ratio;
+}
+__device__ __forceinline__ int head_of_row(const AttnParams& p, int row) { return row - token_of_row(p, row) * p.ratio; }
+
+// a / b, a >= 0, b > 0; a 64-bit division costs several times a 32-bit one.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 
 // What request r asks for; n = 0 where there is nothing to do.
 struct Span {
@@ -101,7 +115,7 @@ struct Keys {
 };
 
 __device__ __forceinline__ Keys keys_of(const AttnParams& p, const Span& s, int row0, int rows) {
-    const int i0 = row0 / p.ratio, i1 = min(row0 + rows - 1, s.n * p.ratio - 1) / p.ratio;
+    const int i0 = token_of_row(p, row0), i1 = token_of_row(p, min(row0 + rows - 1, s.n * p.ratio - 1));
     const int old = s.len - s.n;
     Keys k;
     k.hi = p.q.tree_dev != nullptr ? s.len : max(0, old + i1 + 1);
@@ -150,8 +164,8 @@ constexpr float kTwo24 = 16777216.0f, kTwo20 = 1048576.0f;
 // Writes row R (of its request) of a finished segment: dims and logarithm of the sum.
 template <typename T>
 __device__ __forceinline__ T* out_row(const AttnParams& p, const Segment& s, int row, int& tok, int& a) {
-    tok = s.span.first + row / p.ratio;
-    a = s.head * p.ratio + row % p.ratio;
+    tok = s.span.first + token_of_row(p, row);
+    a = s.head * p.ratio + head_of_row(p, row);
     return static_cast<T*>(p.q.out_dev) + tok * p.q.out_token_stride + a * p.q.out_head_stride;
 }
 __device__ __forceinline__ void write_lse(const AttnParams& p, int tok, int a, float m, float l) {
@@ -159,62 +173,39 @@ __device__ __forceinline__ void write_lse(const AttnParams& p, int tok, int a, f
         p.q.lse_dev[static_cast<int64_t>(tok) * p.q.heads_q + a] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-// Joins row `row` of partials val(0, ..) .. val(n - 1, ..) of a segment, in order, by one warp, into the output (dst null)
-// or a partial. val(i, x) are 4 floats from float x of partial i on, one(i, x) is float x.
-template <typename T, int D, int G, int NT, typename Val, typename One>
-__device__ __forceinline__ void join_row(const AttnParams& p, const Segment& s, int row, int n, int lane, Val val, One one, float* dst) {
+// Joining n partials of a row, in order, takes two steps: what each partial counts, 2^(its reference - the largest), then the sums
+// of O, 4 dims a thread. (In one step, a warp a row, whose loads and sums follow one another, the 96 rows of a CTA took
+// 23000 cycles.)
+__device__ __forceinline__ float join_weight(float mi, float li, float m) {
+    return mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);  // (1: li is not a number, and shows)
+}
+// val(i): 4 dims of partial i, weight(i) what it counts. Into the output (dst null) or a partial. kFlight partials' loads are under
+// way at once: partials of other CTAs come from L2.
+template <typename T, int D, int G, int NT, int kFlight, typename Val, typename Weight>
+__device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s, int row, int d, int n, float m, float l, Val val, Weight weight,
+                                          float* dst) {
     using S = AttnShape<D, G, NT>;
-    if (s.row0 + row >= s.span.n * p.ratio) return;
     constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
-    float m = -INFINITY;
-    float m0 = -INFINITY, l0 = 0.0f;  // of partial `lane`
-    if (lane < n) m0 = one(lane, kM + row), l0 = one(lane, kL + row);
-    m = m0;
-    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, one(i, kM + row));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    constexpr int kVec = (D + 127) / 128;  // groups of 4 dims a lane has (where D is 64, both half warps have the same)
-    const int d0 = D == 64 ? 4 * (lane & 15) : 4 * lane;
-    float4 o[kVec];
-    float l = 0.0f;
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float mi = m0, li = l0;
-        if (i0 > 0 && i0 + lane < n) mi = one(i0 + lane, kM + row), li = one(i0 + lane, kL + row);
-        const float f = i0 + lane >= n ? 0.0f : (mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m));
-        const float fl = i0 + lane < n ? li * f : 0.0f;
-        const int cnt = min(32, n - i0);
-#pragma unroll 8
-        for (int i = 0; i < cnt; ++i) {
-            const float w = __shfl_sync(0xFFFFFFFFu, f, i);
-            l += __shfl_sync(0xFFFFFFFFu, fl, i);
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const float4 x = val(i0 + i, row * S::kPitch + 128 * v + d0);
-                o[v].x = fmaf(x.x, w, o[v].x);
-                o[v].y = fmaf(x.y, w, o[v].y);
-                o[v].z = fmaf(x.z, w, o[v].z);
-                o[v].w = fmaf(x.w, w, o[v].w);
-            }
-        }
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll kFlight
+    for (int i = 0; i < n; ++i) {
+        const float4 x = val(i);
+        const float f = weight(i);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
     }
-    int tok = 0, a = 0;
-    T* const out = dst == nullptr ? out_row<T>(p, s, s.row0 + row, tok, a) : nullptr;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-        const int d = 128 * v + d0;
-        if (dst != nullptr) {
-            *reinterpret_cast<float4*>(dst + row * S::kPitch + d) = o[v];
-        } else {
-            const T h[4] = {from_f32<T>(o[v].x * inv), from_f32<T>(o[v].y * inv), from_f32<T>(o[v].z * inv), from_f32<T>(o[v].w * inv)};
-            *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
-        }
-    }
-    if (lane == 0) {
-        if (dst != nullptr) dst[kM + row] = m, dst[kL + row] = l;
-        else write_lse(p, tok, a, m, l);
+    if (dst != nullptr) {
+        *reinterpret_cast<float4*>(dst + row * S::kPitch + d) = o;
+        if (d == 0) dst[kM + row] = m, dst[kL + row] = l;
+    } else {
+        int tok, a;
+        T* const out = out_row<T>(p, s, s.row0 + row, tok, a);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const T h[4] = {from_f32<T>(o.x * inv), from_f32<T>(o.y * inv), from_f32<T>(o.z * inv), from_f32<T>(o.w * inv)};
+        *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
+        if (d == 0) write_lse(p, tok, a, m, l);
     }
 }
 
@@ -270,7 +261,7 @@ __device__ __forceinline__ Segment locate(const AttnParams& p, const Spans& span
         if (unit < s.start + n) break;
         s.start += n;
     }
-    s.head = static_cast<int>((unit - s.start) / (s.keys.tiles + kSwitch));
+    s.head = static_cast<int>(quotient(unit - s.start, s.keys.tiles + kSwitch));
     s.start += static_cast<int64_t>(s.head) * (s.keys.tiles + kSwitch);
     return s;
 }
@@ -352,6 +343,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     __shared__ Segment s_seg[2 * S::kWarps];  // of each warp's first and last partial
     __shared__ int s_has[2 * S::kWarps], s_list[2 * S::kWarps + 1], s_first[2 * S::kWarps + 1], s_groups;
     __shared__ Span s_span[kSpans];
+    __shared__ float s_weight[2 * S::kWarps][S::kRows], s_m[2 * S::kWarps][S::kRows], s_l[2 * S::kWarps][S::kRows];
     __shared__ int s_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     if (lane == 0) {
@@ -391,8 +383,9 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     const int64_t ctas = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (2 * total + S::kWarps - 1) / S::kWarps));
     if (blockIdx.x >= ctas || total == 0) return;
     const int runs = min(S::kThreads, (p.q.n_req + run - 1) / run);
+    const int64_t each = quotient(total, ctas), rest = total - each * ctas;  // the first `rest` CTAs take a unit more
     const auto split = [&](int64_t cta) {  // first unit of a CTA
-        int64_t u = cta * total / ctas;
+        int64_t u = cta * each + min(cta, rest);
         if (few && u > 0 && u < total) {
             const Segment s = locate<S::kRows>(p, spans, s_before, runs, run, u);
             if (s.keys.tiles <= S::kShortSegment) u = s.start;
@@ -401,7 +394,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     };
     const int64_t cta0 = split(blockIdx.x), cta1 = split(blockIdx.x + 1);
     if (cta0 == cta1) return;
-    const int64_t begin = cta0 + warp * (cta1 - cta0) / S::kWarps, end = cta0 + (warp + 1) * (cta1 - cta0) / S::kWarps;
+    const int64_t begin = cta0 + ((warp * (cta1 - cta0)) / S::kWarps), end = cta0 + (((warp + 1) * (cta1 - cta0)) / S::kWarps);
 
     float* const scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096);
     float* const slots = scratch + static_cast<int64_t>(gridDim.x) * S::kWarps * S::kPartial;  // two a CTA
@@ -423,7 +416,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             const int row = seg.row0 + 8 * nt + g;
             const bool live = row < seg.span.n * p.ratio;
             const T* x = static_cast<const T*>(p.q.q_dev);
-            if (live) x += (seg.span.first + row / p.ratio) * p.q.q_token_stride + (seg.head * p.ratio + row % p.ratio) * p.q.q_head_stride;
+            if (live) x += (seg.span.first + token_of_row(p, row)) * p.q.q_token_stride + (seg.head * p.ratio + head_of_row(p, row)) * p.q.q_head_stride;
 #pragma unroll
             for (int pn = 0; pn < S::kPanels; ++pn)
 #pragma unroll
@@ -435,7 +428,6 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     uint32_t stage = 0, parity = 0;  // of the tile waited for next
     Producer<D, G, NT> ahead;
     if (more) {
-        load_queries();  // under way while the copies are set up
         if (lane == 0) s_ahead[warp] = seg;
         __syncwarp();
         ahead.seg = &s_ahead[warp];
@@ -451,6 +443,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
 
     while (more) {
         const int old = seg.span.len - seg.span.n, rows = seg.span.n * p.ratio;
+        load_queries();
 
         // Queries: lane (g, t) holds dims 32 t .. 32 t + 31 of each panel of row g (16 t .. where a panel has 64), scaled by a
         // power of two that brings the tile's largest into [2^9, 2^10); nx = - sums over a group's dims, per column.
@@ -528,7 +521,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         // tiles [plain0, plain1) hold positions that every row of the segment sees
         int plain0 = 0, plain1;
         {
-            const int i0 = seg.row0 / p.ratio, i1 = min(seg.row0 + S::kRows - 1, rows - 1) / p.ratio;
+            const int i0 = token_of_row(p, seg.row0), i1 = token_of_row(p, min(seg.row0 + S::kRows - 1, rows - 1));
             if (p.q.window > 0) plain0 = (max(seg.keys.lo, old + i1 - p.q.window + 1) - seg.keys.lo + kTileTok - 1) / kTileTok;
             plain1 = (max(seg.keys.lo, p.q.tree_dev != nullptr ? old : old + i0 + 1) - seg.keys.lo) / kTileTok;
         }
@@ -650,7 +643,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int i = min(seg.row0 + 8 * nt + 2 * t + j, rows - 1) / p.ratio;
+                        const int i = token_of_row(p, min(seg.row0 + 8 * nt + 2 * t + j, rows - 1));
                         const int last = old + i, first = p.q.window > 0 ? last - p.q.window + 1 : 0;
                         const uint64_t tree = p.q.tree_dev != nullptr ? p.q.tree_dev[seg.span.first + i] : 0;
 #pragma unroll
@@ -796,7 +789,6 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             next_segment<S::kRows>(p, spans, seg);
             from = 0;
             to = static_cast<int>(min(static_cast<int64_t>(seg.keys.tiles), end - seg.start - kSwitch));
-            load_queries();
         }
     }
     // A warp's first partial comes back from global memory into its ring, so that the joins read shared memory only.
@@ -809,7 +801,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     }
     __syncthreads();
 
-    // Join the partials of each segment that this CTA's warps share, in the order of the warps, a row a warp: into the
+    // Join the partials of each segment that this CTA's warps share, in the order of the warps: into the
     // output, or into a partial of this CTA where the segment goes on in another.
     const auto slot = [&](int64_t cta, bool tail) { return slots + (2 * cta + (tail ? 1 : 0)) * S::kPartial; };
     const auto owned = [&](const Segment& s) {  // tiles before this CTA (1), after it (2)
@@ -826,18 +818,35 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     }
     __syncthreads();
     const int groups = s_groups;
-    for (int item = warp; item < groups * S::kRows; item += S::kWarps) {
-        const int gr = item / S::kRows, row = item % S::kRows, first = s_first[gr];
+    constexpr int kQuads = D / 4, kItems = S::kRows * kQuads, kM = S::kRows * S::kPitch, kL = kM + S::kRows;
+    const auto partial = [&](int i) {  // i-th of the list
+        const int x = s_list[i];
+        return (x & 1) ? reinterpret_cast<const float*>(smem + S::kRing) + (x >> 1) * S::kPartial
+                       : reinterpret_cast<const float*>(smem + (x >> 1) * S::kStages * S::kStageBytes);
+    };
+    for (int item = tid; item < groups * S::kRows; item += S::kThreads) {
+        const int gr = item / S::kRows, row = item % S::kRows;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+        for (int i = s_first[gr]; i < s_first[gr + 1]; ++i) m = fmaxf(m, partial(i)[kM + row]);
+#pragma unroll 4
+        for (int i = s_first[gr]; i < s_first[gr + 1]; ++i) {
+            const float li = partial(i)[kL + row], f = join_weight(partial(i)[kM + row], li, m);
+            s_weight[i][row] = f;
+            l = fmaf(li, f, l);
+        }
+        s_m[gr][row] = m, s_l[gr][row] = l;
+    }
+    __syncthreads();
+    for (int item = tid; item < groups * kItems; item += S::kThreads) {
+        const int gr = item / kItems, row = item % kItems / kQuads, d = 4 * (item % kQuads), first = s_first[gr];
         const Segment& s = s_seg[s_list[first]];
+        if (s.row0 + row >= s.span.n * p.ratio) continue;
         const int over = owned(s);
-        const auto base = [&](int i) {
-            const int x = s_list[first + i];
-            return (x & 1) ? reinterpret_cast<const float*>(smem + S::kRing) + (x >> 1) * S::kPartial
-                           : reinterpret_cast<const float*>(smem + (x >> 1) * S::kStages * S::kStageBytes);
-        };
-        join_row<T, D, G, NT>(
-            p, s, row, s_first[gr + 1] - first, lane, [&](int i, int at) { return *reinterpret_cast<const float4*>(base(i) + at); },
-            [&](int i, int at) { return base(i)[at]; }, over ? slot(blockIdx.x, !(over & 1)) : nullptr);
+        join_quad<T, D, G, NT, 4>(
+            p, s, row, d, s_first[gr + 1] - first, s_m[gr][row], s_l[gr][row],
+            [&](int i) { return *reinterpret_cast<const float4*>(partial(first + i) + row * S::kPitch + d); },
+            [&](int i) { return s_weight[first + i][row]; }, over ? slot(blockIdx.x, !(over & 1)) : nullptr);
     }
     // Segments that other CTAs share (the first and the last one of this CTA's): the last CTA to arrive joins their partials.
     const Segment* cross[2] = {nullptr, nullptr};
@@ -853,7 +862,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     __syncthreads();
     const auto cta_of = [&](int64_t unit) {
         // the CTA whose part holds a unit of a segment that CTAs share: its bounds are not moved within such a segment
-        return ((unit + 1) * ctas - 1) / total;
+        return unit < rest * (each + 1) ? quotient(unit, each + 1) : rest + quotient(unit - rest * (each + 1), each);
     };
     if (tid < 2 && (tid ? cross[1] : cross[0]) != nullptr) {
         const Segment& s = tid ? *cross[1] : *cross[0];
@@ -866,11 +875,38 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         __threadfence();
         const Segment& s = x ? *cross[1] : *cross[0];
         const int64_t c0 = cta_of(s.start + kSwitch), c1 = cta_of(s.start + kSwitch + s.keys.tiles - 1);
-        for (int row = warp; row < S::kRows; row += S::kWarps)
-            join_row<T, D, G, NT>(
-                p, s, row, static_cast<int>(c1 - c0 + 1), lane,
-                [&](int i, int at) { return __ldcg(reinterpret_cast<const float4*>(slot(c0 + i, i == 0) + at)); },
-                [&](int i, int at) { return __ldcg(slot(c0 + i, i == 0) + at); }, nullptr);
+        const int n = static_cast<int>(c1 - c0 + 1);
+        const auto part = [&](int i) { return slot(c0 + i, i == 0); };
+        float* const weights = reinterpret_cast<float*>(smem);  // [row][kMaxCtas]
+        static_assert(S::kRows * kMaxCtas * 4 <= S::kRing, "weights in the rings");
+        for (int row = warp; row < S::kRows; row += S::kWarps) {
+            float m = -INFINITY, l = 0.0f;
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(part(i) + kM + row));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                float fl = 0.0f;
+                if (i0 + lane < n) {
+                    const float li = __ldcg(part(i0 + lane) + kL + row), f = join_weight(__ldcg(part(i0 + lane) + kM + row), li, m);
+                    weights[row * kMaxCtas + i0 + lane] = f;
+                    fl = li * f;
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) fl += __shfl_xor_sync(0xFFFFFFFFu, fl, d);
+                l += fl;
+            }
+            if (lane == 0) s_m[0][row] = m, s_l[0][row] = l;
+        }
+        __syncthreads();
+        for (int item = tid; item < kItems; item += S::kThreads) {
+            const int row = item / kQuads, d = 4 * (item % kQuads);
+            if (s.row0 + row >= s.span.n * p.ratio) continue;
+            join_quad<T, D, G, NT, 10>(
+                p, s, row, d, n, s_m[0][row], s_l[0][row],
+                [&](int i) { return __ldcg(reinterpret_cast<const float4*>(part(i) + row * S::kPitch + d)); },
+                [&](int i) { return weights[row * kMaxCtas + i]; }, nullptr);
+        }
+        __syncthreads();  // the weights' place
         if (tid == 0) arrived[c0] = 0;
     }
 }

@@ -31,9 +31,7 @@ cudaError_t launch_decode_rows(const AttnParams& p, int sms, cudaStream_t s) {
     const int64_t rows = std::min(static_cast<int64_t>(p.q.max_q) * p.ratio, static_cast<int64_t>(p.max_rows));
     if (rows <= 8) return launch_decode_shape<T, D, G, 1>(p, sms, s);
     if constexpr (D == 256) return launch_decode_shape<T, D, G, 1>(p, sms, s);
-    if constexpr (D == 128) return launch_decode_shape<T, D, G, 2>(p, sms, s);
-    if constexpr (D == 64)
-        return rows <= 16 ? launch_decode_shape<T, D, G, 2>(p, sms, s) : launch_decode_shape<T, D, G, 4>(p, sms, s);
+    else return launch_decode_shape<T, D, G, 2>(p, sms, s);  // more rows are more row tiles
 }
 
 template <typename T>
