@@ -6,7 +6,7 @@
 namespace sgemv {
 cudaError_t launch_decode_f16(int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
 cudaError_t launch_decode_bf16(int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
-cudaError_t launch_chunk(int dtype, int dim, int group, const AttnParams& p, int sms, cudaStream_t s);
+cudaError_t launch_chunk(int dtype, int dim, int group, const AttnParams& p, cudaStream_t s);
 }  // namespace sgemv
 
 using namespace sgemv;
@@ -62,6 +62,6 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     p.max_rows = chunks ? kChunkMinRows : INT_MAX;
     cudaError_t e = q.dtype == SGEMV_F16 ? launch_decode_f16(layout->dim, layout->group, p, di.sm_count, s)
                                          : launch_decode_bf16(layout->dim, layout->group, p, di.sm_count, s);
-    if (e == cudaSuccess && chunks) e = launch_chunk(q.dtype, layout->dim, layout->group, p, di.sm_count, s);
+    if (e == cudaSuccess && chunks) e = launch_chunk(q.dtype, layout->dim, layout->group, p, s);
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }

@@ -9,7 +9,7 @@ namespace sgemv {
 namespace {
 
 template <typename T, int D, int G>
-cudaError_t launch_chunk_shape(const AttnParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t s) {
     using S = ChunkShape<D, G>;
     static_assert(4096 + 4ull * kMaxCtas * S::kPartial <= SGEMV_KV_WORKSPACE, "workspace");
     auto kern = chunk_kernel<T, D, G>;
@@ -31,17 +31,17 @@ cudaError_t launch_chunk_shape(const AttnParams& p, int sms, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_chunk_type(int dim, int group, const AttnParams& p, int sms, cudaStream_t s) {
-    if (dim == 64) return launch_chunk_shape<T, 64, 64>(p, sms, s);
-    if (group == 64) return launch_chunk_shape<T, 128, 64>(p, sms, s);
-    return launch_chunk_shape<T, 128, 128>(p, sms, s);
+cudaError_t launch_chunk_type(int dim, int group, const AttnParams& p, cudaStream_t s) {
+    if (dim == 64) return launch_chunk_shape<T, 64, 64>(p, s);
+    if (group == 64) return launch_chunk_shape<T, 128, 64>(p, s);
+    return launch_chunk_shape<T, 128, 128>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk(int dtype, int dim, int group, const AttnParams& p, int sms, cudaStream_t s) {
-    return dtype == SGEMV_F16 ? launch_chunk_type<__half>(dim, group, p, sms, s)
-                              : launch_chunk_type<__nv_bfloat16>(dim, group, p, sms, s);
+cudaError_t launch_chunk(int dtype, int dim, int group, const AttnParams& p, cudaStream_t s) {
+    return dtype == SGEMV_F16 ? launch_chunk_type<__half>(dim, group, p, s)
+                              : launch_chunk_type<__nv_bfloat16>(dim, group, p, s);
 }
 
 }  // namespace sgemv

@@ -82,11 +82,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
                  : SGEMV_R8(r, 0), SGEMV_R8(r, 8), SGEMV_R8(r, 16), SGEMV_R8(r, 24)
                  : "r"(addr));
 }
-__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : SGEMV_R8(r, 0), SGEMV_R8(r, 8)
-                 : "r"(addr));
-}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
@@ -168,10 +163,34 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     pdl_launch_dependents();
     pdl_wait();
 
-    // The request whose segment this CTA has. Thread x has requests [x * run, (x + 1) * run).
+    // The request whose segment this CTA has. Thread x has requests [x * run, (x + 1) * run); where that is one each, they are taken
+    // by descending length, so that the longest segments do not come last (16 requests of up to 2048 tokens: 381 us in
+    // index order, 335 so).
     const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
     int64_t mine = 0;
-    for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += chunk_segments<S::kRows>(p, span_of(p, r));
+    int* const s_len = reinterpret_cast<int*>(s_q);  // until the queries come
+    int* const s_order = s_len + S::kThreads;
+    int* const s_count = s_order + S::kThreads;
+    if (run == 1) {
+        int count = 0;
+        if (tid < p.q.n_req) {
+            const Span s = span_of(p, tid);
+            count = static_cast<int>(chunk_segments<S::kRows>(p, s));
+            s_len[tid] = count > 0 ? s.len : -1;
+        }
+        __syncthreads();
+        if (tid < p.q.n_req) {
+            const int len = s_len[tid];
+            int rank = 0;
+            for (int r = 0; r < p.q.n_req; ++r) rank += s_len[r] > len || (s_len[r] == len && r < tid);
+            s_order[rank] = tid;
+            s_count[rank] = count;
+        }
+        __syncthreads();
+        if (tid < p.q.n_req) mine = s_count[tid];
+    } else {
+        for (int r = tid * run; r < min((tid + 1) * run, p.q.n_req); ++r) mine += chunk_segments<S::kRows>(p, span_of(p, r));
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -188,24 +207,24 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     // fewer segments than SMs are split over the keys (the workspace has a partial for each of kMaxCtas CTAs)
     const int splits = total == 0 || total * 2 > kMaxCtas ? 1 : static_cast<int>(kMaxCtas / total);
     if (blockIdx.x >= total * splits) return;
-    // heavier segments (more keys before them) first
-    const int64_t want = total - 1 - blockIdx.x / splits;
+    const int64_t want = blockIdx.x / splits;
     const int part = blockIdx.x % splits;
     if (want >= before && want < before + mine) {
-        for (int r = tid * run;; ++r) {
+        int r = run == 1 ? s_order[tid] : tid * run;
+        for (; run > 1; ++r) {
             const int64_t n = chunk_segments<S::kRows>(p, span_of(p, r));
-            if (want < before + n) {
-                s_req = r, s_before = before;
-                break;
-            }
+            if (want < before + n) break;
             before += n;
         }
+        s_req = r, s_before = before;
     }
     __syncthreads();
     const int req = s_req;
     const Span sp = span_of(p, req);
     const int in_req = static_cast<int>(want - s_before);
-    const int head = in_req % p.heads, row0 = in_req / p.heads * S::kRows, rows = sp.n * p.ratio, old = sp.len - sp.n;
+    // within a request the last rows, which see the most keys, come first
+    const int rows = sp.n * p.ratio, old = sp.len - sp.n;
+    const int head = in_req % p.heads, row0 = ((rows + S::kRows - 1) / S::kRows - 1 - in_req / p.heads) * S::kRows;
     Keys keys = keys_of(p, sp, row0, S::kRows);
     keys.lo = keys.lo / S::kKeys * S::kKeys;
     const int all_tiles = max(1, (keys.hi - keys.lo + S::kKeys - 1) / S::kKeys);
