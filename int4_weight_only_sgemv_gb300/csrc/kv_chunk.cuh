@@ -18,8 +18,8 @@
 //
 // Roundings: scores have none but the sums' in 32 bits: x is fp16 (scaled by a power of two a row, exact), K's integers are exact,
 // and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
-// values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to 11 bits, so that no scale
-// need be kept a column. The softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
+// values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to 11 bits (in units of a power of two
+// that follows from the segment's largest scale), so that no scale need be kept a column. The softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
 //
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the last CTA to arrive joins.
 #pragma once
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     __shared__ __align__(8) uint64_t q_full, s_full[2][2], p_full[2][2], o_full[2][2];
     __shared__ uint32_t s_tmem;
     __shared__ int64_t s_sum[S::kWarps];
-    __shared__ int s_req, s_bad, s_last;
+    __shared__ int s_req, s_bad, s_last, s_vmax;
     __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             mbar_init(&s_full[i >> 1][i & 1], 1), mbar_init(&p_full[i >> 1][i & 1], 128), mbar_init(&o_full[i >> 1][i & 1], 1);
         mbar_init(&q_full, 256);
         mbar_fence_init();
-        s_req = -1, s_bad = 0;
+        s_req = -1, s_bad = 0, s_vmax = 0;
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -234,13 +234,28 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (part + 1) / parts) - tile0;
     const int key0 = keys.lo + tile0 * S::kKeys;
     const int32_t* const table = p.q.table_dev + req * p.q.table_stride;
-    // page ids outside the cache are looked for beforehand
-    for (int b = (key0 >> p.log2_page) + tid; b << p.log2_page < min(keys.hi, key0 + tiles * S::kKeys); b += S::kThreads) {
-        const int id = table[b];
-        if (id < 0 || id >= p.n_pages) {
-            report(p.status, SGEMV_ERR_ARG);
-            s_bad = 1;
+    // Beforehand: page ids outside the cache, and the largest of V's scales (1% of the time of a long segment).
+    {
+        int big = 0;
+        const int end = min(keys.hi, key0 + tiles * S::kKeys);
+#pragma unroll 4
+        for (int pos = key0 + tid; pos < end; pos += S::kThreads) {
+            const int id = table[pos >> p.log2_page];
+            if (id < 0 || id >= p.n_pages) {
+                report(p.status, SGEMV_ERR_ARG);
+                s_bad = 1;
+                continue;
+            }
+            const uint8_t* const at = p.cache + id * p.page_bytes + head * p.head_bytes + ((pos & (p.page - 1)) / kSub) * S::kSubBytes +
+                                      16 * D + 64 * S::kGroups + 4 * (pos % kSub);
+#pragma unroll
+            for (int gr = 0; gr < S::kGroups; ++gr) {
+                const int bits = *reinterpret_cast<const unsigned short*>(at + 64 * gr);
+                if (bits < 0x7C00) big = max(big, bits);  // (what a masked position holds need not be a number)
+            }
         }
+        big = __reduce_max_sync(0xFFFFFFFFu, big);
+        if (lane == 0 && big != 0) atomicMax(&s_vmax, big);
     }
     if (warp == 16) tc_alloc(&s_tmem, S::kCols);
     tc_before_sync();
@@ -248,6 +263,9 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     tc_after_sync();
     const uint32_t tmem = s_tmem;
     const bool any_bad = s_bad != 0;
+    // V's values are held in units of 2^vexp, which brings the largest scale to 2^11 .. 2^12: 15 s / 2 stays below fp16's end
+    // whatever the scale, and small ones are not lost to subnormals.
+    const int vexp = max(-14, min(4, (s_vmax >> 10) - 15 - 11));
     const auto lost = [&](int pos) {  // the page of a position is outside the cache
         const int id = table[pos >> p.log2_page];
         return id < 0 || id >= p.n_pages;
@@ -421,7 +439,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             tok = sp.first + row / p.ratio, a = head * p.ratio + row % p.ratio;
             out = static_cast<T*>(p.q.out_dev) + tok * p.q.out_token_stride + a * p.q.out_head_stride;
         }
-        const float inv = l == 0.0f ? 0.0f : 2.0f / l;  // V is halved
+        const float unit = __uint_as_float(static_cast<uint32_t>(127 + vexp + 1) << 23);  // and halved
+        const float inv = l == 0.0f ? 0.0f : unit / l;
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -435,8 +454,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[n + e]);
                 if (slot != nullptr) {
                     float* const d = slot + (128 * x + r) * D + 32 * q + n;
-                    *reinterpret_cast<float4*>(d) = make_float4(2.0f * f[0], 2.0f * f[1], 2.0f * f[2], 2.0f * f[3]);
-                    *reinterpret_cast<float4*>(d + 4) = make_float4(2.0f * f[4], 2.0f * f[5], 2.0f * f[6], 2.0f * f[7]);
+                    *reinterpret_cast<float4*>(d) = make_float4(unit * f[0], unit * f[1], unit * f[2], unit * f[3]);
+                    *reinterpret_cast<float4*>(d + 4) = make_float4(unit * f[4], unit * f[5], unit * f[6], unit * f[7]);
                 } else {
                     T h[8];
 #pragma unroll
@@ -460,6 +479,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         const bool keys_not_values = warp < 12;
         const int w = warp & 3, g = lane >> 2, t = lane & 3;
         const __half2 half2_half = __floats2half2_rn(0.5f, 0.5f), half2_32nd = __floats2half2_rn(0.03125f, 0.03125f);
+        const __half2 up = __float2half2_rn(__uint_as_float(static_cast<uint32_t>(127 - vexp) << 23));
         const __half2 half2_16th = __floats2half2_rn(0.0625f, 0.0625f);
         // (nibble - zero) / 2 of bits 0 (hi false) or 4 of each half of a word, exactly; then times s, for V the scale
         const auto value = [&](uint32_t a, bool hi, __half2 zero, __half2 s) {
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                         const uint32_t a = scales(sub + 16 * D + 64 * (S::kGroups + gr), 4 * t + 2 * e);
                         const uint32_t b = scales(sub + 16 * D + 64 * (S::kGroups + gr), 4 * t + 2 * e + 1);
                         const uint32_t sw = __byte_perm(a, b, 0x5410), zw = __byte_perm(a, b, 0x7632);
-                        s[e] = *reinterpret_cast<const __half2*>(&sw);
+                        s[e] = __hmul2(*reinterpret_cast<const __half2*>(&sw), up);
                         const __half2 z = *reinterpret_cast<const __half2*>(&zw);
                         z0[e] = __hfma2(z, __floats2half2_rn(-0.5f, -0.5f), __floats2half2_rn(-512.0f, -512.0f));
                         z1[e] = __hfma2(z, __floats2half2_rn(-0.5f, -0.5f), __floats2half2_rn(-32.0f, -32.0f));

@@ -461,3 +461,95 @@ def test_attention_refusals(env):
         sg.sgemv_kv_attention(c.L, c.cache[:100], **ok)
     with pytest.raises(ValueError):
         sg.sgemv_kv_attention(c.L, c.cache, **{**ok, "lse": torch.zeros(3, device="cuda")})
+
+
+@pytest.mark.parametrize("n_req", [300, 700])
+def test_attention_many_requests(env, n_req):
+    """More requests than either kernel keeps in shared memory; every hundredth is a prompt chunk, some are empty."""
+    rng = np.random.default_rng(n_req)
+    reqs = []
+    for r in range(n_req):
+        old, n = int(rng.integers(0, 60)), int(rng.integers(0, 3))
+        reqs.append((old + 70, 70) if r % 100 == 50 else (old + n, n))
+    c = Case(env, 64, 64, 16, 2, 1, "float16", reqs)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dim,group,dtype", [(64, 64, "float16"), (128, 64, "bfloat16"), (128, 128, "float16")])
+def test_attention_prompt_without_some_pages(env, dim, group, dtype):
+    """Page ids outside the cache in a prompt chunk: reported, their keys are left out, all else is as it was."""
+    sg, torch = env
+    c = Case(env, dim, group, 16, 1, 2, dtype, [(90, 60), (200, 75)])
+    good = c.run()
+    lost = [1, 7]
+    keep = c.table.copy()
+    c.table[1, lost] = [-5, c.L.n_pages]
+    st = _status(torch)
+    out, lse = c.run(status=st)
+    assert int(st.item()) == sg.SGEMV_ERR_ARG
+    assert np.array_equal(out[:60], good[0][:60]) and np.array_equal(lse[:60], good[1][:60])
+    # the formula on the keys that are left
+    j = np.arange(200)
+    slots = keep[1][j // 16].astype(np.int64) * 16 + j % 16
+    k, v, kmag, vmag = okv.values(c.O, c.cache.cpu().numpy(), slots, 0)
+    q = c.q.double().cpu().numpy()
+    u = 2.0 ** -11 if dtype == "float16" else 2.0 ** -8
+    for i in range(75):
+        see = (j <= 125 + i) & ~np.isin(j // 16, lost)
+        for a in range(2):
+            s = k[see] @ q[60 + i, a] * c.scale
+            e = np.exp(s - s.max())
+            score = 2 * dim * 2.0 ** -24 * (kmag[see] @ np.abs(q[60 + i, a])).max() * c.scale
+            ref, weight = e @ v[see] / e.sum(), e @ vmag[see] / e.sum()
+            tol = u * np.abs(ref) + weight * (2.0 ** -11 + 2.0 ** -14 + score) + 2.0 ** -24
+            assert np.all(np.abs(out[60 + i, a] - ref) <= tol)
+            want = s.max() + np.log(e.sum())
+            assert abs(lse[60 + i, a] - want) <= score + 2.0 ** -20 + 2.0 ** -22 * abs(want)
+
+
+@pytest.mark.parametrize("vscale", [1e-6, 1e-3, 7e4])
+def test_attention_prompt_extreme_values(env, vscale):
+    """V whose scales are at either end of fp16, and so large that the values themselves are far outside it."""
+    c = Case(env, 128, 128, 16, 1, 4, "bfloat16", [(200, 1), (150, 70)], vscale=vscale)
+    c.check(*c.run())
+
+
+def test_attention_prompt_sharp_scores(env):
+    """One key takes nearly all the weight, and the maximum moves along the keys of a prompt chunk."""
+    c = Case(env, 128, 128, 32, 2, 4, "float16", [(500, 100), (260, 40)])
+    c.q *= 30
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11])
+def test_attention_scale_of_any_sign(env, scale):
+    c = Case(env, 128, 64, 32, 2, 4, "float16", [(300, 90), (260, 1), (40, 3)])
+    c.scale = scale
+    c.check(*c.run())
+
+
+def test_attention_rows_do_not_meet(env):
+    """A query that is not a number makes its own row so, and no other."""
+    c = Case(env, 128, 128, 32, 1, 4, "float16", [(300, 90), (260, 4)])
+    good = c.run()
+    c.q[17, 2, 5] = float("nan")
+    c.q[91, 1, 70] = float("nan")
+    out, lse = c.run()
+    bad = np.zeros(lse.shape, dtype=bool)
+    bad[17, 2] = bad[91, 1] = True
+    assert np.isnan(out[bad]).all()
+    assert np.array_equal(out[~bad], good[0][~bad]) and np.array_equal(lse[~bad], good[1][~bad])
+
+
+def test_attention_prompt_beyond_32_bit_offsets(env):
+    sg, torch = env
+    c = Case(env, 64, 64, 64, 8, 2, "float16", [(300, 90)])
+    first = c.run()
+    far = (5 << 30) // c.L.page_bytes
+    big = sg.sgemv_kv_layout_query(8, 64, 64, 64, far + c.L.n_pages)
+    cache = torch.empty(big.total_bytes, dtype=torch.uint8, device="cuda")
+    cache[far * c.L.page_bytes:] = c.cache
+    c.table = np.where(c.table >= 0, c.table + far, -1)
+    c.cache, c.L = cache, big
+    again = c.run()
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])

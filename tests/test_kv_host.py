@@ -143,3 +143,14 @@ def test_plan_oracle_keeps_pages_distinct():
         used = [table[r][b] for r in range(n) for b in range(-(-length[r] // page))]
         assert sorted(used + free[:count]) == list(range(pages))
         assert len(set(slots)) == len(slots)
+
+
+def test_size_refusals(sg):
+    """Sizes past what the kernels index."""
+    plan = lambda n: sg._lib.sgemv_kv_plan(n, 16, 9, A, None, A + 64, A, 3, 3, A, A, A + 128, A + 256, A, A, A, 5, None, None)  # noqa: E731
+    assert plan(16385) == sg.SGEMV_ERR_SHAPE
+    L = sg.sgemv_kv_layout_query(1, 128, 128, 64, 10)
+    q = sg.KvQuery(dtype=0, heads_q=64, n_req=2, n_tokens=1 << 25, max_q=1, window=0, table_cols=4, scale=0.1, table_stride=4,
+                   q_token_stride=8192, q_head_stride=128, out_token_stride=8192, out_head_stride=128, q_dev=A, q_start_dev=A,
+                   len_dev=A, table_dev=A, tree_dev=None, out_dev=A, lse_dev=A, workspace_dev=A, workspace_bytes=sg.KV_WORKSPACE)
+    assert sg._lib.sgemv_kv_attention(ctypes.byref(L), A, ctypes.byref(q), None, None) == sg.SGEMV_ERR_SHAPE
