@@ -173,28 +173,43 @@ __device__ __forceinline__ void write_lse(const AttnParams& p, int tok, int a, f
         p.q.lse_dev[static_cast<int64_t>(tok) * p.q.heads_q + a] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-// Joining n partials of a row, in order, takes two steps: what each partial counts, 2^(its reference - the largest), then the sums
-// of O, 4 dims a thread. (In one step, a warp a row, whose loads and sums follow one another, the 96 rows of a CTA took
-// 23000 cycles.)
+// Joining n partials of a row, in order: 4 dims a thread, which forms the reference and what each partial counts, 2^(its
+// reference - the joint one), for itself. So a join is as long as its loads, and kFlight partials' are under way at once. (With the
+// weights formed first, by a warp a row, the join across CTAs took 14000 to 20000 cycles, mostly waiting for one load after another.)
 __device__ __forceinline__ float join_weight(float mi, float li, float m) {
     return mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);  // (1: li is not a number, and shows)
 }
-// val(i): 4 dims of partial i, weight(i) what it counts. Into the output (dst null) or a partial. kFlight partials' loads are under
-// way at once: partials of other CTAs come from L2.
-template <typename T, int D, int G, int NT, int kFlight, typename Val, typename Weight>
-__device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s, int row, int d, int n, float m, float l, Val val, Weight weight,
-                                          float* dst) {
+// get(i, m, l, x): partial i's reference, sum and 4 dims. Into the output (dst null) or a partial.
+template <typename T, int D, int G, int NT, int kFlight, typename Get>
+__device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s, int row, int d, int n, Get get, float* dst) {
     using S = AttnShape<D, G, NT>;
     constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll kFlight
-    for (int i = 0; i < n; ++i) {
-        const float4 x = val(i);
-        const float f = weight(i);
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kFlight) {
+        float mi[kFlight], li[kFlight];
+        float4 x[kFlight];
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            mi[j] = -INFINITY, li[j] = 0.0f, x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i0 + j < n) get(i0 + j, mi[j], li[j], x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) top = fmaxf(top, mi[j]);
+        const float before = join_weight(m, l, top);
+        m = top;
+        l *= before, o.x *= before, o.y *= before, o.z *= before, o.w *= before;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            const float f = join_weight(mi[j], li[j], top);
+            l = fmaf(li[j], f, l);
+            o.x = fmaf(x[j].x, f, o.x);
+            o.y = fmaf(x[j].y, f, o.y);
+            o.z = fmaf(x[j].z, f, o.z);
+            o.w = fmaf(x[j].w, f, o.w);
+        }
     }
     if (dst != nullptr) {
         *reinterpret_cast<float4*>(dst + row * S::kPitch + d) = o;
@@ -343,8 +358,7 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
     __shared__ Segment s_seg[2 * S::kWarps];  // of each warp's first and last partial
     __shared__ int s_has[2 * S::kWarps], s_list[2 * S::kWarps + 1], s_first[2 * S::kWarps + 1], s_groups;
     __shared__ Span s_span[kSpans];
-    __shared__ float s_weight[2 * S::kWarps][S::kRows], s_m[2 * S::kWarps][S::kRows], s_l[2 * S::kWarps][S::kRows];
-    __shared__ int s_last[2];
+    __shared__ int s_parts[2], s_cta[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     if (lane == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(&s_bar[warp][i], 1);
@@ -824,29 +838,18 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         return (x & 1) ? reinterpret_cast<const float*>(smem + S::kRing) + (x >> 1) * S::kPartial
                        : reinterpret_cast<const float*>(smem + (x >> 1) * S::kStages * S::kStageBytes);
     };
-    for (int item = tid; item < groups * S::kRows; item += S::kThreads) {
-        const int gr = item / S::kRows, row = item % S::kRows;
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-        for (int i = s_first[gr]; i < s_first[gr + 1]; ++i) m = fmaxf(m, partial(i)[kM + row]);
-#pragma unroll 4
-        for (int i = s_first[gr]; i < s_first[gr + 1]; ++i) {
-            const float li = partial(i)[kL + row], f = join_weight(partial(i)[kM + row], li, m);
-            s_weight[i][row] = f;
-            l = fmaf(li, f, l);
-        }
-        s_m[gr][row] = m, s_l[gr][row] = l;
-    }
-    __syncthreads();
     for (int item = tid; item < groups * kItems; item += S::kThreads) {
         const int gr = item / kItems, row = item % kItems / kQuads, d = 4 * (item % kQuads), first = s_first[gr];
         const Segment& s = s_seg[s_list[first]];
         if (s.row0 + row >= s.span.n * p.ratio) continue;
         const int over = owned(s);
-        join_quad<T, D, G, NT, 4>(
-            p, s, row, d, s_first[gr + 1] - first, s_m[gr][row], s_l[gr][row],
-            [&](int i) { return *reinterpret_cast<const float4*>(partial(first + i) + row * S::kPitch + d); },
-            [&](int i) { return s_weight[first + i][row]; }, over ? slot(blockIdx.x, !(over & 1)) : nullptr);
+        join_quad<T, D, G, NT, 6>(
+            p, s, row, d, s_first[gr + 1] - first,
+            [&](int i, float& m, float& l, float4& x) {
+                const float* const q = partial(first + i);
+                m = q[kM + row], l = q[kL + row], x = *reinterpret_cast<const float4*>(q + row * S::kPitch + d);
+            },
+            over ? slot(blockIdx.x, !(over & 1)) : nullptr);
     }
     // Segments that other CTAs share (the first and the last one of this CTA's): the last CTA to arrive joins their partials.
     const Segment* cross[2] = {nullptr, nullptr};
@@ -858,57 +861,37 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         if (ob == 2) cross[1] = b;
     }
     if (cross[0] == nullptr && cross[1] == nullptr) return;
-    __threadfence();
     __syncthreads();
-    const auto cta_of = [&](int64_t unit) {
-        // the CTA whose part holds a unit of a segment that CTAs share: its bounds are not moved within such a segment
-        return unit < rest * (each + 1) ? quotient(unit, each + 1) : rest + quotient(unit - rest * (each + 1), each);
-    };
-    if (tid < 2 && (tid ? cross[1] : cross[0]) != nullptr) {
-        const Segment& s = tid ? *cross[1] : *cross[0];
-        const int64_t c0 = cta_of(s.start + kSwitch), c1 = cta_of(s.start + kSwitch + s.keys.tiles - 1);
-        s_last[tid] = atomicAdd(&arrived[c0], 1) == static_cast<int>(c1 - c0);
+    if (tid < 2) {
+        s_parts[tid] = 0;
+        if ((tid ? cross[1] : cross[0]) != nullptr) {
+            const auto cta_of = [&](int64_t unit) {
+                // the CTA whose part holds a unit of a segment that CTAs share: its bounds are not moved within such a segment
+                return unit < rest * (each + 1) ? quotient(unit, each + 1) : rest + quotient(unit - rest * (each + 1), each);
+            };
+            const Segment& s = tid ? *cross[1] : *cross[0];
+            const int c0 = static_cast<int>(cta_of(s.start + kSwitch)), c1 = static_cast<int>(cta_of(s.start + kSwitch + s.keys.tiles - 1));
+            __threadfence();
+            if (atomicAdd(&arrived[c0], 1) == c1 - c0) s_parts[tid] = c1 - c0 + 1, s_cta[tid] = c0;
+            __threadfence();
+        }
     }
     __syncthreads();
-    for (int x = 0; x < 2; ++x) {
-        if ((x ? cross[1] : cross[0]) == nullptr || !s_last[x]) continue;
-        __threadfence();
+    const int n0 = s_parts[0], n1 = s_parts[1];
+    for (int item = n0 ? tid : tid + kItems; item < (n1 ? 2 * kItems : kItems); item += S::kThreads) {
+        const int x = item / kItems, row = item % kItems / kQuads, d = 4 * (item % kQuads);
         const Segment& s = x ? *cross[1] : *cross[0];
-        const int64_t c0 = cta_of(s.start + kSwitch), c1 = cta_of(s.start + kSwitch + s.keys.tiles - 1);
-        const int n = static_cast<int>(c1 - c0 + 1);
-        const auto part = [&](int i) { return slot(c0 + i, i == 0); };
-        float* const weights = reinterpret_cast<float*>(smem);  // [row][kMaxCtas]
-        static_assert(S::kRows * kMaxCtas * 4 <= S::kRing, "weights in the rings");
-        for (int row = warp; row < S::kRows; row += S::kWarps) {
-            float m = -INFINITY, l = 0.0f;
-            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(part(i) + kM + row));
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                float fl = 0.0f;
-                if (i0 + lane < n) {
-                    const float li = __ldcg(part(i0 + lane) + kL + row), f = join_weight(__ldcg(part(i0 + lane) + kM + row), li, m);
-                    weights[row * kMaxCtas + i0 + lane] = f;
-                    fl = li * f;
-                }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) fl += __shfl_xor_sync(0xFFFFFFFFu, fl, d);
-                l += fl;
-            }
-            if (lane == 0) s_m[0][row] = m, s_l[0][row] = l;
-        }
-        __syncthreads();
-        for (int item = tid; item < kItems; item += S::kThreads) {
-            const int row = item / kQuads, d = 4 * (item % kQuads);
-            if (s.row0 + row >= s.span.n * p.ratio) continue;
-            join_quad<T, D, G, NT, 10>(
-                p, s, row, d, n, s_m[0][row], s_l[0][row],
-                [&](int i) { return __ldcg(reinterpret_cast<const float4*>(part(i) + row * S::kPitch + d)); },
-                [&](int i) { return weights[row * kMaxCtas + i]; }, nullptr);
-        }
-        __syncthreads();  // the weights' place
-        if (tid == 0) arrived[c0] = 0;
+        if (s.row0 + row >= s.span.n * p.ratio) continue;
+        const int c0 = s_cta[x];
+        join_quad<T, D, G, NT, 10>(
+            p, s, row, d, x ? n1 : n0,
+            [&](int i, float& m, float& l, float4& v) {
+                const float* const q = slot(c0 + i, i == 0);
+                m = __ldcg(q + kM + row), l = __ldcg(q + kL + row), v = __ldcg(reinterpret_cast<const float4*>(q + row * S::kPitch + d));
+            },
+            nullptr);
     }
+    if (tid < 2 && s_parts[tid] > 0) arrived[s_cta[tid]] = 0;
 }
 
 }  // namespace sgemv
