@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         }
         return u;
     };
-    const int64_t cta0 = split(blockIdx.x), cta1 = split(blockIdx.x + 1);
+    const int64_t bound = split(blockIdx.x + (lane & 1));  // both ends at once
+    const int64_t cta0 = __shfl_sync(0xFFFFFFFFu, bound, 0), cta1 = __shfl_sync(0xFFFFFFFFu, bound, 1);
     if (cta0 == cta1) return;
     const int64_t begin = cta0 + ((warp * (cta1 - cta0)) / S::kWarps), end = cta0 + (((warp + 1) * (cta1 - cta0)) / S::kWarps);
 
