@@ -21,6 +21,12 @@
 // values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to 11 bits (in units of a power of two
 // that follows from the segment's largest scale), so that no scale need be kept a column. The softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
 //
+// Bound by the softmax's chain and by shared memory: a 64-key tile takes 2450 cycles, of which the two row tiles' products need
+// 1024 at the tensor cores' rate and 1500 as issued (64-column products read both operands from shared memory at more than
+// its 128 bytes a cycle), and a softmax thread is busy for 1850. Two threads a row (16 softmax warps that agree on a reference
+// tile by tile) took 3900 a tile: all roles contend for the same issue slots and shared memory. 3 requests of up to 2048 new tokens
+// behind up to 8192 cached ones, 32 query heads, 8 KV heads of 128 (259 GFLOP): 339 us; 8 such requests: 636 us, 766 TFLOP/s.
+//
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the last CTA to arrive joins.
 #pragma once
 
@@ -28,7 +34,8 @@
 
 namespace sgemv {
 
-constexpr int kChunkMinRows = 64;  // requests with more rows (new tokens x query heads of a KV head) come here
+// Requests with more rows (new tokens x query heads of a KV head) come here.
+constexpr int kChunkMinRows = 64;
 
 template <int D, int G>
 struct ChunkShape {
@@ -42,8 +49,9 @@ struct ChunkShape {
     static constexpr int kRawBytes = kRawSubs * kSubBytes;
     static constexpr int kAtoms = D / 64;                         // 128-byte columns of a row of x or K
     static constexpr int kQBytes = kTile * D * 2, kKBytes = kKeys * D * 2, kVBytes = D * kKeys * 2;
-    static constexpr int kWarps = 20, kThreads = 32 * kWarps;
-    // Registers a thread at launch, and after the split: 8 warps each, and 4. 8 kSoftmax + 8 kUnpack + 4 kOther = 20 kLaunch.
+    static constexpr int kWarps = 20, kThreads = 32 * kWarps, kSoftmaxThreads = 256;
+    // Registers a thread at launch, and after the split: 8 warps each, and 4. 8 kSoftmax + 8 kUnpack + 4 kOther = 20 kRegs. A warp
+    // asks once: a second time is allowed only after its warpgroup has met, which the roles do not, so only softmax warps join.
     static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsUnpack = 80, kRegsOther = 64;
     static constexpr int kSmem = 1024 + 2 * kQBytes + kBufs * (kKBytes + kVBytes) + kRawStages * kRawBytes;
     static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
@@ -102,7 +110,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// By every warp of a warpgroup: more registers a thread (once others have given theirs), or fewer.
+// By every warp of a warpgroup, once: more registers a thread (when others have given theirs), or fewer.
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -470,10 +478,36 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         } else if (live) {
             write_lse(p, tok, a, m, l);
         }
-        tc_before_sync();
         __syncwarp();
-        regs_dec<S::kRegs>();  // every warp has the launch's number again
-    } else if (warp < 16) {
+        tc_before_sync();
+        __syncthreads();  // (the other roles' at their ends)
+        if (parts == 1) return;
+
+        // Join the splits of the segment: the last CTA to arrive, 4 dims of a row a thread, in the order of the keys.
+        int* const arrived = static_cast<int*>(p.q.workspace_dev);
+        const int64_t seg = blockIdx.x / splits;
+        if (tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(&arrived[seg], 1) == parts - 1;
+            __threadfence();
+        }
+        named_bar_sync(1, S::kSoftmaxThreads);
+        if (!s_last) return;
+        const float* const slots = reinterpret_cast<const float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) + seg * splits * S::kPartial;
+        constexpr int kQuads = D / 4;
+        for (int item = tid; item < min(S::kRows, rows - row0) * kQuads; item += S::kSoftmaxThreads) {
+            const int rr = item / kQuads, d = 4 * (item % kQuads), at = row0 + rr, t = sp.first + at / p.ratio, ah = head * p.ratio + at % p.ratio;
+            float mj, lj;
+            const float4 o = join<8>(parts, [&](int n, float& mi, float& li, float4& v) {
+                const float* const q = slots + n * S::kPartial;
+                mi = __ldcg(q + S::kRows * D + rr), li = __ldcg(q + S::kRows * (D + 1) + rr), v = __ldcg(reinterpret_cast<const float4*>(q + rr * D + d));
+            }, mj, lj);
+            write_quad(p, static_cast<T*>(p.q.out_dev) + t * p.q.out_token_stride + ah * p.q.out_head_stride, d, o, mj, lj, t, ah);
+        }
+        if (tid == 0) arrived[seg] = 0;
+        return;
+    }
+    if (warp < 16) {
         regs_dec<S::kRegsUnpack>();
         // ---------------------------------------------------------------------------------------- unpack
         const bool keys_not_values = warp < 12;
@@ -571,8 +605,6 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             }
             mbar_arrive(&raw_free[stage]);
         }
-        __syncwarp();
-        regs_inc<S::kRegs>();
     } else {
         regs_dec<S::kRegsOther>();
         if (warp < 18) {
@@ -657,52 +689,11 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             if (bytes) bulk_g2s(s_raw + stage * S::kRawBytes + lane * (per / kSub) * S::kSubBytes, src, bytes, &raw_full[stage]);
         }
         }
-        __syncwarp();
-        regs_inc<S::kRegs>();
     }
     __syncwarp();
-    tc_before_sync();
     __syncthreads();
     tc_after_sync();
     if (warp == 16) tc_dealloc(tmem, S::kCols);
-    if (parts == 1) return;
-
-    // Join the splits of the segment: the last CTA to arrive, a row a warp, in the order of the keys.
-    int* const arrived = static_cast<int*>(p.q.workspace_dev);
-    const int64_t seg = blockIdx.x / splits;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&arrived[seg], 1) == parts - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const float* const slots = reinterpret_cast<const float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) + seg * splits * S::kPartial;
-    for (int r = warp; r < S::kRows && row0 + r < rows; r += S::kWarps) {
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(slots + i * S::kPartial + S::kRows * D + r));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        float o[D / 32], l = 0.0f;
-#pragma unroll
-        for (int v = 0; v < D / 32; ++v) o[v] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float* const q = slots + i * S::kPartial;
-            const float mi = __ldcg(q + S::kRows * D + r), li = __ldcg(q + S::kRows * (D + 1) + r);
-            if (mi == -INFINITY && li == 0.0f) continue;
-            const float f = mi == -INFINITY ? 1.0f : exp2_approx(mi - m);
-            l = fmaf(li, f, l);
-#pragma unroll
-            for (int v = 0; v < D / 32; ++v) o[v] = fmaf(__ldcg(q + r * D + 32 * v + lane), f, o[v]);
-        }
-        const int row = row0 + r, tok = sp.first + row / p.ratio, a = head * p.ratio + row % p.ratio;
-        T* const out = static_cast<T*>(p.q.out_dev) + tok * p.q.out_token_stride + a * p.q.out_head_stride;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int v = 0; v < D / 32; ++v) out[32 * v + lane] = from_f32<T>(o[v] * inv);
-        if (lane == 0) write_lse(p, tok, a, m, l);
-    }
-    if (tid == 0) arrived[seg] = 0;
 }
 
 }  // namespace sgemv

@@ -24,6 +24,13 @@
 // segments, and keeps the softmax's reference, sum and O in registers. Segments that cross warps are joined in shared
 // memory, those that cross CTAs through the workspace by the last CTA to arrive, always in the order of the keys: the
 // same inputs give the same bits.
+//
+// Measured: a longer context costs its bytes at 6.9 TB/s (8 KV heads of 128; a plain copy has 6.7), and a call that gives every SM
+// work 20 us besides: 7 us up to the first tile (lengths, the split, block tables, and then all SMs' rings fill at once, 20 MB),
+// 5 to 8 us after the last (joins, an arrival, joins across CTAs). These are short steps that wait for one another and run once,
+// so that their instructions come from L2 too: going through the join once beforehand, to have them near, cost more than it
+// saved (single 9.3 -> 10.3 us). 64 requests of up to 16384 tokens (571 MB): 97 us; one of 262144 (285 MB): 59 us; one
+// of 333 with 32 heads: 9.4 us; 24 trees of 12 tokens, 48 rows a head of 64: 23 us, half of it the products.
 #pragma once
 
 #include "kv_common.cuh"
@@ -179,13 +186,11 @@ __device__ __forceinline__ void write_lse(const AttnParams& p, int tok, int a, f
 __device__ __forceinline__ float join_weight(float mi, float li, float m) {
     return mi == -INFINITY ? (li == 0.0f ? 0.0f : 1.0f) : exp2_approx(mi - m);  // (1: li is not a number, and shows)
 }
-// get(i, m, l, x): partial i's reference, sum and 4 dims. Into the output (dst null) or a partial.
-template <typename T, int D, int G, int NT, int kFlight, typename Get>
-__device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s, int row, int d, int n, Get get, float* dst) {
-    using S = AttnShape<D, G, NT>;
-    constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
+// get(i, m, l, x): partial i's reference, sum and 4 dims.
+template <int kFlight, typename Get>
+__device__ __forceinline__ float4 join(int n, Get get, float& m, float& l) {
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float m = -INFINITY, l = 0.0f;
+    m = -INFINITY, l = 0.0f;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += kFlight) {
         float mi[kFlight], li[kFlight];
@@ -211,16 +216,30 @@ __device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s,
             o.w = fmaf(x[j].w, f, o.w);
         }
     }
+    return o;
+}
+// 4 dims of a finished row of the output; the first of them writes the row's lse.
+template <typename T>
+__device__ __forceinline__ void write_quad(const AttnParams& p, T* out, int d, float4 o, float m, float l, int tok, int a) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const T h[4] = {from_f32<T>(o.x * inv), from_f32<T>(o.y * inv), from_f32<T>(o.z * inv), from_f32<T>(o.w * inv)};
+    *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
+    if (d == 0) write_lse(p, tok, a, m, l);
+}
+// The join of a decode row, into the output (dst null) or a partial.
+template <typename T, int D, int G, int NT, int kFlight, typename Get>
+__device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s, int row, int d, int n, Get get, float* dst) {
+    using S = AttnShape<D, G, NT>;
+    constexpr int kM = S::kRows * S::kPitch, kL = kM + S::kRows;
+    float m, l;
+    const float4 o = join<kFlight>(n, get, m, l);
     if (dst != nullptr) {
         *reinterpret_cast<float4*>(dst + row * S::kPitch + d) = o;
         if (d == 0) dst[kM + row] = m, dst[kL + row] = l;
     } else {
         int tok, a;
         T* const out = out_row<T>(p, s, s.row0 + row, tok, a);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const T h[4] = {from_f32<T>(o.x * inv), from_f32<T>(o.y * inv), from_f32<T>(o.z * inv), from_f32<T>(o.w * inv)};
-        *reinterpret_cast<uint2*>(out + d) = *reinterpret_cast<const uint2*>(h);
-        if (d == 0) write_lse(p, tok, a, m, l);
+        write_quad(p, out, d, o, m, l, tok, a);
     }
 }
 
@@ -466,20 +485,28 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         float nx[kGr][NT][2], c;
         {
             float big = 0.0f;
+            const auto largest = [&](bool finite) {
+                big = 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int pn = 0; pn < S::kPanels; ++pn)
+                    for (int pn = 0; pn < S::kPanels; ++pn)
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
+                        for (int w = 0; w < kWords; ++w) {
+                            const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
-                    }
+                            for (int j = 0; j < 8; ++j) {
+                                const float x = fabsf(to_f32(h[j]));
+                                if (!finite || x < INFINITY) big = fmaxf(big, x);
+                            }
+                        }
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
-            const int be = static_cast<int>(__float_as_uint(big) >> 23);  // biased exponent; 0 and infinity are left alone
-            const int sh = be == 0 || be == 255 ? 0 : min(max(127 + 9 - be, -100), 100);
+                for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+            };
+            largest(false);
+            if (big == INFINITY) largest(true);  // an infinite query makes its own row not a number, and leaves the others' scale alone
+            const int be = static_cast<int>(__float_as_uint(big) >> 23);  // biased exponent; 0 is left alone
+            const int sh = be == 0 ? 0 : min(max(127 + 9 - be, -100), 100);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
             c = p.scale_log2 * kTwo24 / up;
 #pragma unroll

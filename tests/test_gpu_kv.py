@@ -541,6 +541,20 @@ def test_attention_rows_do_not_meet(env):
     assert np.array_equal(out[~bad], good[0][~bad]) and np.array_equal(lse[~bad], good[1][~bad])
 
 
+def test_attention_infinite_queries_stay_alone(env):
+    """Tiny queries beside an infinite one of the same tile keep their accuracy."""
+    c = Case(env, 128, 128, 32, 1, 8, "bfloat16", [(260, 1), (90, 20)])
+    c.q *= 1e-6
+    good = c.run()
+    c.check(*good)
+    c.q[0, 3, 70] = c.q[9, 1, 2] = float("inf")
+    out, lse = c.run()
+    bad = np.zeros(lse.shape, dtype=bool)
+    bad[0, 3] = bad[9, 1] = True
+    assert np.isnan(out[bad]).all()
+    assert np.array_equal(out[~bad], good[0][~bad]) and np.array_equal(lse[~bad], good[1][~bad])
+
+
 def test_attention_prompt_beyond_32_bit_offsets(env):
     sg, torch = env
     c = Case(env, 64, 64, 64, 8, 2, "float16", [(300, 90)])
