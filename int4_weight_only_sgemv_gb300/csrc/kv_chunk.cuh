@@ -34,14 +34,13 @@
 
 namespace sgemv {
 
-// Requests with more rows (new tokens x query heads of a KV head) come here.
-constexpr int kChunkMinRows = 64;
+constexpr int kChunkRows = 256;  // rows of a CTA
 
 template <int D, int G>
 struct ChunkShape {
     static constexpr int kGroups = D / G;
     static constexpr int kSubBytes = 16 * D + 128 * kGroups;
-    static constexpr int kRows = 256, kTile = 128;                // rows of a CTA and of a row tile
+    static constexpr int kRows = kChunkRows, kTile = 128;         // rows of a CTA and of a row tile
     static constexpr int kKeys = 64;                              // keys of a tile
     static constexpr int kSBufs = 2 / kGroups;                    // buffers of S
     static constexpr int kBufs = 4;                               // of K and V
@@ -135,7 +134,7 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n) {
 template <int kRows>
 __device__ __forceinline__ int64_t chunk_segments(const AttnParams& p, const Span& s) {
     const int rows = s.n * p.ratio;
-    return rows > kChunkMinRows ? static_cast<int64_t>((rows + kRows - 1) / kRows) * p.heads : 0;
+    return rows > p.max_rows ? static_cast<int64_t>((rows + kRows - 1) / kRows) * p.heads : 0;
 }
 
 template <typename T, int D, int G>

@@ -567,3 +567,96 @@ def test_attention_prompt_beyond_32_bit_offsets(env):
     c.cache, c.L = cache, big
     again = c.run()
     assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+# 131 tokens of 8 query heads a KV head are 1048 rows, 300 of 4 are 1200: with those the tensor-core form runs whatever the
+# number of segments (fewer rows go to it only where there is a segment for every SM).
+
+@pytest.mark.parametrize("dim,group,dtype", [(64, 64, "float16"), (128, 64, "bfloat16"), (128, 128, "float16"), (128, 128, "bfloat16")])
+@pytest.mark.parametrize("window", [0, 1, 37])
+def test_attention_large_chunks(env, dim, group, dtype, window):
+    """A whole prompt, a chunk behind a context, one that sees nothing at first, and decodes beside them."""
+    c = Case(env, dim, group, 32, 1, 8, dtype, [(131, 131), (400, 140), (100, 135), (50, 1), (0, 0), (333, 9)], window=window)
+    c.check(*c.run())
+
+
+def test_attention_many_short_chunks(env):
+    """Segments for every SM, 127 rows on average: requests of more than 64 go to the tensor-core form, the others do not."""
+    rng = np.random.default_rng(3)
+    reqs = [(int(o) + n, n) for o, n in zip(rng.integers(0, 90, 26), [33, 32, 1, 40, 65, 0, 34] * 3 + [64, 33, 50, 32, 36])]
+    c = Case(env, 128, 64, 16, 6, 4, "float16", reqs)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("vscale", [1e-6, 1e-3, 7e4])
+def test_attention_large_chunk_extreme_values(env, vscale):
+    c = Case(env, 128, 128, 16, 1, 8, "bfloat16", [(200, 1), (190, 131)], vscale=vscale)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("scale,factor", [(0.0, 1), (-0.11, 1), (0.09, 30)])
+def test_attention_large_chunk_scales(env, scale, factor):
+    c = Case(env, 128, 128, 32, 1, 8, "float16", [(330, 131), (260, 1)])
+    c.scale = scale
+    c.q *= factor
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_large_chunk_rows_do_not_meet(env, bad):
+    c = Case(env, 128, 64, 32, 1, 8, "bfloat16", [(300, 131), (260, 4)])
+    good = c.run()
+    c.q[17, 2, 5] = bad
+    c.q[133, 1, 70] = bad
+    out, lse = c.run()
+    poisoned = np.zeros(lse.shape, dtype=bool)
+    poisoned[17, 2] = poisoned[133, 1] = True
+    assert np.isnan(out[poisoned]).all()
+    assert np.array_equal(out[~poisoned], good[0][~poisoned]) and np.array_equal(lse[~poisoned], good[1][~poisoned])
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 64), (128, 128)])
+def test_attention_large_chunk_without_some_pages(env, dim, group):
+    """The keys of pages outside the cache are left out: the same as a context in which they never were."""
+    sg, torch = env
+    c = Case(env, dim, group, 16, 1, 8, "float16", [(160, 131)])
+    lost = 1  # positions 16 .. 31, seen by every query but the first ones
+    keep = c.table.copy()
+    c.table[0, lost] = c.L.n_pages
+    st = _status(torch)
+    out, lse = c.run(status=st)
+    assert int(st.item()) == sg.SGEMV_ERR_ARG
+    # the context without them: 144 positions, of which the queries from position 32 on see what they saw but the page
+    c.table = np.delete(keep, lost, axis=1)
+    c.reqs, c.starts = [(144, 128)], np.array([0, 128], np.int32)
+    c.q = c.q[3:]
+    c.check(out[3:], lse[3:])
+
+
+def test_attention_large_chunk_same_bits_and_far_offsets(env):
+    sg, torch = env
+    c = Case(env, 64, 64, 64, 8, 4, "float16", [(900, 300), (310, 270)])
+    ws = sg.kv_workspace()
+    first = c.run(ws)
+    for _ in range(3):
+        again = c.run(ws)
+        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+    far = (5 << 30) // c.L.page_bytes
+    big = sg.sgemv_kv_layout_query(8, 64, 64, 64, far + c.L.n_pages)
+    cache = torch.empty(big.total_bytes, dtype=torch.uint8, device="cuda")
+    cache[far * c.L.page_bytes:] = c.cache
+    c.table = np.where(c.table >= 0, c.table + far, -1)
+    c.cache, c.L = cache, big
+    again = c.run(ws)
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("n_req", [300, 700])
+def test_attention_many_requests_with_chunks(env, n_req):
+    rng = np.random.default_rng(n_req + 1)
+    reqs = []
+    for r in range(n_req):
+        old, n = int(rng.integers(0, 40)), int(rng.integers(0, 2))
+        reqs.append((old + 27, 27) if r % 60 == 50 else (old + n, n))
+    c = Case(env, 64, 64, 16, 1, 8, "float16", reqs)
+    c.check(*c.run())
