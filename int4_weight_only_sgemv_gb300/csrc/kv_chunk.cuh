@@ -16,8 +16,8 @@
 // when a softmax is done with one: with 128-key tiles and one buffer each softmax waited 2100 of 6100 cycles a tile for its
 // scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
 //
-// Roundings: scores have none but the sums' in 32 bits: x is fp16, scaled by a power of two a row (exact but for
-// elements 2^-23 of the row's largest and less), K's integers are exact, and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
+// Roundings: scores have none but the sums' in 32 bits: x is fp16, scaled by a power of two a segment (exact but
+// for elements 2^-23 of its largest and less), K's integers are exact, and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
 // values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to
 // 11 bits, in units of a power of two that follows from the segment's largest scale, so that no scale need be kept a column. The
 // softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
@@ -26,7 +26,7 @@
 // 1024 at the tensor cores' rate and 1500 as issued (64-column products read both operands from shared memory at more than
 // its 128 bytes a cycle), and a softmax thread is busy for 1850. Two threads a row (16 softmax warps that agree on a reference
 // tile by tile) took 3900 a tile: all roles contend for the same issue slots and shared memory. 3 requests of up to 2048 new tokens
-// behind up to 8192 cached ones, 32 query heads, 8 KV heads of 128 (259 GFLOP): 332 us; 8 such requests: 636 us, 766 TFLOP/s.
+// behind up to 8192 cached ones, 32 query heads, 8 KV heads of 128 (259 GFLOP): 331 us; 8 such requests: 620 us, 786 TFLOP/s.
 //
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the softmax warps of the
 // last CTA to arrive join.
@@ -37,6 +37,7 @@
 namespace sgemv {
 
 constexpr int kChunkRows = 256;  // rows of a CTA
+constexpr float kBig = 32768.0f; // 2^kLimit
 
 template <int D, int G>
 struct ChunkShape {
@@ -89,6 +90,11 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                  : SGEMV_R8(r, 0), SGEMV_R8(r, 8), SGEMV_R8(r, 16), SGEMV_R8(r, 24)
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : SGEMV_R8(r, 0), SGEMV_R8(r, 8)
                  : "r"(addr));
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -148,13 +154,13 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     uint8_t* const s_k = s_q + 2 * S::kQBytes;
     uint8_t* const s_v = s_k + S::kBufs * S::kKBytes;
     uint8_t* const s_raw = s_v + S::kBufs * S::kVBytes;
-    __shared__ __align__(16) float s_scale[S::kBufs][S::kGroups][S::kKeys];  // of K's groups
+    __shared__ __align__(16) float s_scale[S::kBufs][S::kGroups][S::kKeys];  // of K's groups, times c
     __shared__ __align__(8) uint64_t raw_full[S::kRawStages], raw_free[S::kRawStages];
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_free[S::kBufs];
-    __shared__ __align__(8) uint64_t q_full, s_full[2][2], p_full[2][2], o_full[2][2];
+    __shared__ __align__(8) uint64_t c_full, q_full, s_full[2][2], p_full[2][2], o_full[2][2];
     __shared__ uint32_t s_tmem;
     __shared__ int64_t s_sum[S::kWarps];
-    __shared__ int s_req, s_bad, s_last, s_vmax;
+    __shared__ int s_req, s_bad, s_last, s_vmax, s_xmax;
     __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -165,9 +171,9 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         }
         for (int i = 0; i < 4; ++i)
             mbar_init(&s_full[i >> 1][i & 1], 1), mbar_init(&p_full[i >> 1][i & 1], 128), mbar_init(&o_full[i >> 1][i & 1], 1);
-        mbar_init(&q_full, 256);
+        mbar_init(&c_full, 256), mbar_init(&q_full, 256);
         mbar_fence_init();
-        s_req = -1, s_bad = 0, s_vmax = 0;
+        s_req = -1, s_bad = 0, s_vmax = 0, s_xmax = 0;
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -286,6 +292,14 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         report(p.status, SGEMV_ERR_TIMEOUT);
     };
 
+    // The power of two that brings the segment's largest query element into [2^9, 2^10), with the sign of the scale, and what it
+    // leaves to the scores. Once every softmax thread has told its row's largest.
+    const auto x_unit = [&] {
+        const int be = s_xmax >> 23;  // biased exponent
+        const int sh = be == 0 ? 0 : min(max(127 + 9 - be, -100), 100);
+        return copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), p.scale_log2);
+    };
+
     if (warp < 8) {
         regs_inc<S::kRegsSoftmax>();
         // ---------------------------------------------------------------------------------------- softmax
@@ -295,7 +309,6 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         const uint32_t to = tmem + lanes + 256 + 128 * x;
         const int i = min(row, rows - 1) / p.ratio;
         // x: this thread's row, to shared memory; dims in the order 0 4 1 5 2 6 3 7 of each 8, as K's nibbles come out
-        float c;
         {
             const T* src = static_cast<const T*>(p.q.q_dev) + (sp.first + i) * p.q.q_token_stride +
                            (head * p.ratio + min(row, rows - 1) % p.ratio) * p.q.q_head_stride;
@@ -305,12 +318,17 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 const uint4 w = *reinterpret_cast<const uint4*>(src + d);
                 const T* h = reinterpret_cast<const T*>(&w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
+                for (int j = 0; j < 8; ++j) {
+                    const float f = fabsf(to_f32(h[j]));
+                    if (f < INFINITY) big = fmaxf(big, f);  // an infinite query leaves the others' unit alone
+                }
             }
-            const int be = static_cast<int>(__float_as_uint(big) >> 23);
-            const int sh = be == 0 || be == 255 ? 0 : min(max(127 + 9 - be, -100), 100);
-            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), p.scale_log2);
-            c = fmaxf(p.scale_log2 / up, 1e-30f);  // above 0, so that -inf stays -inf
+            const int most = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(big));
+            if (lane == 0) atomicMax(&s_xmax, most);
+            __syncwarp();
+            mbar_arrive(&c_full);
+            wait(&c_full, 0);
+            const float up = x_unit();
             uint8_t* const dst = s_q + x * S::kQBytes + r * 128;
 #pragma unroll 4
             for (int d = 0; d < D; d += 8) {
@@ -331,8 +349,9 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         const int ia = min(row0 + 128 * x, rows - 1) / p.ratio, ib = min(row0 + 128 * x + 127, rows - 1) / p.ratio;
         const int clear1 = any_bad ? 0 : (p.q.tree_dev != nullptr ? old : old + ia + 1);
         const int clear0 = p.q.window > 0 ? old + ib - p.q.window + 1 : 0;
-        float ref = 0.0f, lim = -INFINITY;  // lim = ref + kLimit, or -inf while nothing was seen
-        uint64_t l2 = 0;                    // two sums
+        float ref = 0.0f;   // the reference
+        bool seen = false;  // whether it was set
+        uint64_t l2 = 0;    // two sums
         for (int j = 0; j < tiles; ++j) {
             const int pos0 = key0 + j * S::kKeys, b = j % S::kSBufs;
             const uint32_t ts = tmem + lanes + 128 * x + 64 * b;
@@ -390,47 +409,56 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 for (int n = 0; n < 64; ++n)
                     if (!((see >> n) & 1u)) s[n] = -INFINITY;
             }
-            float top = fmaxf(s[0], s[63]), top1 = s[1];
+            // The weights. Whether a row's reference has to move shows in their sum, so that the largest score is looked for only in
+            // the rare tile that moves one (and until a row has one). What a row does depends on nothing in other rows.
+            uint32_t w[32];
+            uint64_t sum;
+            bool need = !seen;
+            for (int pass = 0;; ++pass) {
+                if (__any_sync(0xFFFFFFFFu, need)) {
+                    float top = fmaxf(s[0], s[63]), top1 = s[1];
 #pragma unroll
-            for (int n = 2; n < 62; n += 4) top = fmaxf(fmaxf(top, s[n]), s[n + 1]), top1 = fmaxf(fmaxf(top1, s[n + 2]), s[n + 3]);
-            top = fmaxf(fmaxf(top, top1), s[62]) * c;
-            if (__any_sync(0xFFFFFFFFu, top > lim)) {
-                float f = 1.0f;
-                if (top > lim) {
-                    if (lim != -INFINITY) f = exp2_approx(ref - (top - kTop));
-                    ref = top - kTop;
-                    lim = ref + kLimit;
-                }
-                l2 = mul2(l2, pair(f, f));
-                if (j > 0) {
-                    // O holds every tile before this one. (The tile before that is known to be in: this one's scores came after it.)
-                    wait(&o_full[x][(j - 1) % S::kSBufs], ((j - 1) / S::kSBufs) & 1);
-                    __syncwarp();
-                    tc_after_sync();
+                    for (int n = 2; n < 62; n += 4) top = fmaxf(fmaxf(top, s[n]), s[n + 1]), top1 = fmaxf(fmaxf(top1, s[n + 2]), s[n + 3]);
+                    top = fmaxf(fmaxf(top, top1), s[62]);
+                    float f = 1.0f;
+                    if (need && top > -INFINITY) {
+                        if (seen) f = exp2_approx(ref - (top - kTop));
+                        ref = top - kTop;
+                        seen = true;
+                    }
+                    l2 = mul2(l2, pair(f, f));
+                    if (j > 0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                        // O holds every tile before this one. (The tile before that is known to be in: this one's scores came after it.)
+                        wait(&o_full[x][(j - 1) % S::kSBufs], ((j - 1) / S::kSBufs) & 1);
+                        __syncwarp();
+                        tc_after_sync();
 #pragma unroll 1
-                    for (int d = 0; d < D / 32; ++d) {
-                        uint32_t o[32];
-                        tc_ld32(o, to + 32 * d);
-                        tc_wait_ld();
+                        for (int d = 0; d < D / 16; ++d) {
+                            uint32_t o[16];
+                            tc_ld16(o, to + 16 * d);
+                            tc_wait_ld();
 #pragma unroll
-                        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-                        tc_st32(to + 32 * d, o);
+                            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                            tc_st16(to + 16 * d, o);
+                        }
                     }
                 }
-            }
-            const uint64_t cc = pair(c, c), rr = pair(-ref, -ref);
+                // (the difference of two rounded numbers: a score far past 2^24 still has a weight of about 1 where it is the largest)
+                sum = 0;
+                const uint64_t rr = pair(-ref, -ref);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t w[16];
-#pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    const float2 t = parts_of(fma2(pair(s[32 * q + 2 * n], s[32 * q + 2 * n + 1]), cc, rr));
+                for (int n = 0; n < 32; ++n) {
+                    const float2 t = parts_of(add2(pair(s[2 * n], s[2 * n + 1]), rr));
                     const float a = exp2_approx(t.x), e = exp2_approx(t.y);
-                    l2 = add2(l2, pair(a, e));
+                    sum = add2(sum, pair(a, e));
                     w[n] = pack_half2(a, e);
                 }
-                tc_st16(ts + 16 * q, w);
+                const float2 both = parts_of(sum);
+                need = both.x + both.y > kBig;  // (not after the reference has moved)
+                if (pass == 2 || !__any_sync(0xFFFFFFFFu, need)) break;
             }
+            l2 = add2(l2, sum);
+            tc_st32(ts, w);
             tc_wait_st();
             tc_before_sync();
             mbar_arrive(&p_full[x][b]);
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         __syncwarp();
         tc_after_sync();
         const float2 lf = parts_of(l2);
-        const float m = lim == -INFINITY ? -INFINITY : ref, l = lf.x + lf.y;
+        const float m = seen ? ref : -INFINITY, l = lf.x + lf.y;
         float* const slot = parts > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(p.q.workspace_dev) + 4096) +
                                              static_cast<int64_t>(blockIdx.x) * S::kPartial : nullptr;
         int tok = 0, a = 0;
@@ -531,6 +559,11 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             const __half2 f = hi ? __hfma2(n, half2_16th, zero) : __hadd2(n, zero);
             return *reinterpret_cast<const uint32_t*>(&f);
         };
+        float c = 0.0f;
+        if (keys_not_values) {
+            wait(&c_full, 0);
+            c = p.scale_log2 / x_unit();  // not negative
+        }
         for (int j = 0; j < tiles; ++j) {
             const int stage = j % S::kRawStages, buf = j % S::kBufs;
             const int pos = key0 + S::kKeys * j + 16 * w;  // this warp's subtile
@@ -564,7 +597,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                     const int row = col + token;
                     *reinterpret_cast<uint4*>(dst + atom * (S::kKeys * 128) + row * 128 + ((wd ^ (row & 7)) * 16)) = o;
                     if (wd == 0 && 64 * atom % G == 0)
-                        s_scale[buf][64 * atom / G][row] = __half2float(__ushort_as_half(static_cast<unsigned short>(sz & 0xFFFFu)));
+                        s_scale[buf][64 * atom / G][row] = __half2float(__ushort_as_half(static_cast<unsigned short>(sz & 0xFFFFu))) * c;
                 }
                 fence_async();
                 mbar_arrive(&k_full[buf]);

@@ -660,3 +660,15 @@ def test_attention_many_requests_with_chunks(env, n_req):
         reqs.append((old + 27, 27) if r % 60 == 50 else (old + n, n))
     c = Case(env, 64, 64, 16, 1, 8, "float16", reqs)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("reqs", [[(300, 131), (40, 1)], [(300, 4)]])
+def test_attention_scores_past_24_bits(env, reqs):
+    """Scores so large that neighbouring ones differ by more than 1 in binary32: finite, and a weighted mean of the cached values."""
+    c = Case(env, 128, 128, 32, 1, 8, "float16", reqs)
+    c.q *= 4000
+    c.scale = 4000.0
+    out, lse = c.run()
+    v = okv.values(c.O, c.cache.cpu().numpy(), np.array([c.table[r][j // 32] * 32 + j % 32 for r, (n, _) in enumerate(reqs) for j in range(n)]), 0)[1]
+    assert np.isfinite(out).all() and np.isfinite(lse).all() and lse.max() > 2.0 ** 24
+    assert np.all(out <= v.max() * 1.001) and np.all(out >= v.min() * 1.001)
