@@ -21,6 +21,10 @@ cudaError_t launch_chunk_shape(const AttnParams& p, cudaStream_t s) {
     if (attr_set[dev].load() == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kern);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != S::kRegs) return cudaErrorInvalidKernelImage;  // the roles' split would wait for registers for ever
         attr_set[dev].store(1);
     }
     // at most so many segments: every request's last row tile may be short

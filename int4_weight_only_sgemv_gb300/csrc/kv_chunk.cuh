@@ -55,6 +55,7 @@ struct ChunkShape {
     // Registers a thread at launch, and after the split: 8 warps each, and 4. 8 kSoftmax + 8 kUnpack + 4 kOther = 20 kRegs. A warp
     // asks once: a second time is allowed only after its warpgroup has met, which the roles do not, so only softmax warps join.
     static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsUnpack = 80, kRegsOther = 64;
+    static_assert(8 * kRegsSoftmax + 8 * kRegsUnpack + 4 * kRegsOther == kWarps * kRegs, "the split of the launch's registers");
     static constexpr int kSmem = 1024 + 2 * kQBytes + kBufs * (kKBytes + kVBytes) + kRawStages * kRawBytes;
     static constexpr int kPartial = kRows * (D + 2);              // floats of a partial: O, m, l
     static constexpr int kCols = 512;                             // tensor memory: S0, S1, O0, O1
