@@ -248,6 +248,9 @@ def sgemv_logprobs(logits, out, tokens=None, status=None, stream=None) -> None:
     if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits: expected a CUDA tensor [rows, vocab] with a contiguous vocabulary")
     rows, vocab = logits.shape
+    stride = vocab if rows < 2 else logits.stride(0)
+    if stride < vocab:
+        raise ValueError("logits: rows overlap (a row stride below the vocabulary)")
     tok_logp, lse, entropy, top_tok, top_logp, logp = out
     f32, n_tok, top = torch.float32, 0, 0
     if (tokens is None) != (tok_logp is None) or (top_tok is None) != (top_logp is None):
@@ -265,9 +268,9 @@ def sgemv_logprobs(logits, out, tokens=None, status=None, stream=None) -> None:
             _flat(t, f32, n, what)
     if status is not None:
         _flat(status, torch.int32, None, "status")
-    code = _lib.sgemv_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), rows, vocab, max(logits.stride(0), vocab),
-                               _ptr(tokens), n_tok, top, _ptr(tok_logp), _ptr(lse), _ptr(entropy), _ptr(top_tok),
-                               _ptr(top_logp), _ptr(logp), _ptr(status), _on(stream, logits))
+    code = _lib.sgemv_logprobs(logits.data_ptr(), _DTYPE.get(logits.dtype, -1), rows, vocab, stride, _ptr(tokens), n_tok, top,
+                               _ptr(tok_logp), _ptr(lse), _ptr(entropy), _ptr(top_tok), _ptr(top_logp), _ptr(logp), _ptr(status),
+                               _on(stream, logits))
     if code:
         _check(code, "sgemv_logprobs")
 
