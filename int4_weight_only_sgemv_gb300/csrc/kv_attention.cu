@@ -43,6 +43,8 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     p.head_bytes = layout->head_bytes;
     p.page_bytes = layout->page_bytes;
     p.q = q;
+    // A window that no length reaches hides nothing, and without it positions minus the window stay in 32 bits.
+    if (q.window >= kMaxLen) p.q.window = 0;
     p.status = status_dev;
     p.heads = layout->heads;
     p.page = layout->page;
