@@ -16,8 +16,8 @@
 // when a softmax is done with one: with 128-key tiles and one buffer each softmax waited 2100 of 6100 cycles a tile for its
 // scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
 //
-// Roundings: scores have none but the sums' in 32 bits: x is fp16, scaled by a power of two a segment (exact but
-// for elements 2^-23 of its largest and less), K's integers are exact, and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
+// Roundings: scores have none but the sums' in 32 bits: x is fp16, each row scaled by a power of two of its own
+// (exact but for elements below 2^-29 of the row's largest), K's integers are exact, and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
 // values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to
 // 11 bits, in units of a power of two that follows from the segment's largest scale, so that no scale need be kept a column. The
 // softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
@@ -158,10 +158,10 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     __shared__ __align__(16) float s_scale[S::kBufs][S::kGroups][S::kKeys];  // of K's groups, times c
     __shared__ __align__(8) uint64_t raw_full[S::kRawStages], raw_free[S::kRawStages];
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_free[S::kBufs];
-    __shared__ __align__(8) uint64_t c_full, q_full, s_full[2][2], p_full[2][2], o_full[2][2];
+    __shared__ __align__(8) uint64_t q_full, s_full[2][2], p_full[2][2], o_full[2][2];
     __shared__ uint32_t s_tmem;
     __shared__ int64_t s_sum[S::kWarps];
-    __shared__ int s_req, s_bad, s_last, s_vmax, s_xmax;
+    __shared__ int s_req, s_bad, s_last, s_vmax;
     __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         }
         for (int i = 0; i < 4; ++i)
             mbar_init(&s_full[i >> 1][i & 1], 1), mbar_init(&p_full[i >> 1][i & 1], 128), mbar_init(&o_full[i >> 1][i & 1], 1);
-        mbar_init(&c_full, 256), mbar_init(&q_full, 256);
+        mbar_init(&q_full, 256);
         mbar_fence_init();
-        s_req = -1, s_bad = 0, s_vmax = 0, s_xmax = 0;
+        s_req = -1, s_bad = 0, s_vmax = 0;
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -293,14 +293,6 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         report(p.status, SGEMV_ERR_TIMEOUT);
     };
 
-    // The power of two that brings the segment's largest query element into [2^9, 2^10), with the sign of the scale, and what it
-    // leaves to the scores. Once every softmax thread has told its row's largest.
-    const auto x_unit = [&] {
-        const int be = s_xmax >> 23;  // biased exponent
-        const int sh = be == 0 ? 0 : min(max(127 + 9 - be, -100), 100);
-        return copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), p.scale_log2);
-    };
-
     if (warp < 8) {
         regs_inc<S::kRegsSoftmax>();
         // ---------------------------------------------------------------------------------------- softmax
@@ -309,7 +301,10 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + 256 + 128 * x;
         const int i = min(row, rows - 1) / p.ratio;
-        // x: this thread's row, to shared memory; dims in the order 0 4 1 5 2 6 3 7 of each 8, as K's nibbles come out
+        // x: this thread's row, to shared memory, times a power of two of its own (with the sign of the scale) that brings its largest
+        // element into [2^15, 2^16); what that leaves to the row's scores is `down`. Dims in the order 0 4 1 5 2 6 3 7 of each 8, as
+        // K's nibbles come out.
+        float down;
         {
             const T* src = static_cast<const T*>(p.q.q_dev) + (sp.first + i) * p.q.q_token_stride +
                            (head * p.ratio + min(row, rows - 1) % p.ratio) * p.q.q_head_stride;
@@ -319,17 +314,12 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                 const uint4 w = *reinterpret_cast<const uint4*>(src + d);
                 const T* h = reinterpret_cast<const T*>(&w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float f = fabsf(to_f32(h[j]));
-                    if (f < INFINITY) big = fmaxf(big, f);  // an infinite query leaves the others' unit alone
-                }
+                for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
             }
-            const int most = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(big));
-            if (lane == 0) atomicMax(&s_xmax, most);
-            __syncwarp();
-            mbar_arrive(&c_full);
-            wait(&c_full, 0);
-            const float up = x_unit();
+            const int sh = query_shift(big);
+            down = pow2(-sh);
+            // (a row with an infinite element has no number for a score)
+            const float up = big < INFINITY ? copysignf(pow2(sh), p.scale_log2) : __int_as_float(0x7FC00000);
             uint8_t* const dst = s_q + x * S::kQBytes + r * 128;
 #pragma unroll 4
             for (int d = 0; d < D; d += 8) {
@@ -360,7 +350,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             tc_after_sync();
             const bool plain = pos0 >= clear0 && pos0 + S::kKeys <= clear1;
-            // this row's scores: sums times scales, -inf where masked
+            // this row's scores but for `down`: sums times scales, -inf where masked
             float s[64];
             {
                 const float* const scale = &s_scale[j % S::kBufs][0][0];
@@ -423,8 +413,9 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                     top = fmaxf(fmaxf(top, top1), s[62]);
                     float f = 1.0f;
                     if (need && top > -INFINITY) {
-                        if (seen) f = exp2_approx(ref - (top - kTop));
-                        ref = top - kTop;
+                        const float at = fmaf(top, down, -kTop);
+                        if (seen) f = exp2_approx(ref - at);
+                        ref = at;
                         seen = true;
                     }
                     l2 = mul2(l2, pair(f, f));
@@ -444,12 +435,13 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
                         }
                     }
                 }
-                // (the difference of two rounded numbers: a score far past 2^24 still has a weight of about 1 where it is the largest)
+                // (`down` is a power of two, so this is the difference of two rounded numbers: a score far past 2^24 still has a weight of
+                // about 1 where it is the largest)
                 sum = 0;
-                const uint64_t rr = pair(-ref, -ref);
+                const uint64_t rr = pair(-ref, -ref), dd = pair(down, down);
 #pragma unroll
                 for (int n = 0; n < 32; ++n) {
-                    const float2 t = parts_of(add2(pair(s[2 * n], s[2 * n + 1]), rr));
+                    const float2 t = parts_of(fma2(pair(s[2 * n], s[2 * n + 1]), dd, rr));
                     const float a = exp2_approx(t.x), e = exp2_approx(t.y);
                     sum = add2(sum, pair(a, e));
                     w[n] = pack_half2(a, e);
@@ -560,11 +552,7 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             const __half2 f = hi ? __hfma2(n, half2_16th, zero) : __hadd2(n, zero);
             return *reinterpret_cast<const uint32_t*>(&f);
         };
-        float c = 0.0f;
-        if (keys_not_values) {
-            wait(&c_full, 0);
-            c = p.scale_log2 / x_unit();  // not negative
-        }
+        const float c = fabsf(p.scale_log2);
         for (int j = 0; j < tiles; ++j) {
             const int stage = j % S::kRawStages, buf = j % S::kBufs;
             const int pos = key0 + S::kKeys * j + 16 * w;  // this warp's subtile

@@ -8,8 +8,8 @@
 // once to 11 bits, by the integers of V; the zero points come off in 32 bits, from the same rounded weights.
 //
 // A nibble masked out of its word at bit 0 or 4 is the fp16 subnormal q 2^-24 or q 2^-20: one AND turns 4 bits into two
-// operands, no conversion. The powers of two are taken up by x (odd dims are divided by 16, each row is scaled into
-// fp16's middle by a power of two) and by the epilogue.
+// operands, no conversion. The powers of two are taken up by x (odd dims are divided by 16, each row is scaled into fp16's range by a
+// power of two of its own: exact but for elements below 2^-29 of the row's largest, 2^-25 in odd dims) and by the epilogue.
 //
 // Both products are computed transposed, S^T = K x^T and O^T = V^T P^T, so that the cache is the 16-row operand of
 // mma.m16n8k16 and 8 rows of queries (query heads of a KV head x new tokens) the narrow one: with few rows this is half the
@@ -167,6 +167,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 constexpr float kTwo24 = 16777216.0f, kTwo20 = 1048576.0f;
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // -126 <= e <= 127
+// The power of two that brings a row's largest element into [2^15, 2^16), fp16's last binade, or as near as a binary32 factor can.
+__device__ __forceinline__ int query_shift(float big) { return min(127 + 15 - static_cast<int>(__float_as_uint(big) >> 23), 126); }
 
 // Writes row R (of its request) of a finished segment: dims and logarithm of the sum.
 template <typename T>
@@ -479,38 +483,28 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
         const int old = seg.span.len - seg.span.n, rows = seg.span.n * p.ratio;
         load_queries();
 
-        // Queries: lane (g, t) holds dims 32 t .. 32 t + 31 of each panel of row g (16 t .. where a panel has 64), scaled by a
-        // power of two that brings the tile's largest into [2^9, 2^10); nx = - sums over a group's dims, per column.
+        // Queries: lane (g, t) holds dims 32 t .. 32 t + 31 of each panel of row g (16 t .. where a panel has 64), scaled by a power of
+        // two of the row's own that brings its largest into [2^15, 2^16): what a row gets depends on no other row. c: what that
+        // leaves to the scores, per column (in binary32 up to rows of 2^120 or so, whose scores come near its end); nx = - sums over
+        // a group's dims, per column.
         uint32_t qb[NT][S::kPanels][2 * kWords][2];
-        float nx[kGr][NT][2], c;
+        uint64_t nx[kGr][NT], c[NT];  // pairs
         {
-            float big = 0.0f;
-            const auto largest = [&](bool finite) {
-                big = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int pn = 0; pn < S::kPanels; ++pn)
-#pragma unroll
-                        for (int w = 0; w < kWords; ++w) {
-                            const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float x = fabsf(to_f32(h[j]));
-                                if (!finite || x < INFINITY) big = fmaxf(big, x);
-                            }
-                        }
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
-            };
-            largest(false);
-            if (big == INFINITY) largest(true);  // an infinite query makes its own row not a number, and leaves the others' scale alone
-            const int be = static_cast<int>(__float_as_uint(big) >> 23);  // biased exponent; 0 is left alone
-            const int sh = be == 0 ? 0 : min(max(127 + 9 - be, -100), 100);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-            c = p.scale_log2 * kTwo24 / up;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                float big = 0.0f;
+#pragma unroll
+                for (int pn = 0; pn < S::kPanels; ++pn)
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const T* h = reinterpret_cast<const T*>(&raw_q[nt][pn][w]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(to_f32(h[j])));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                const int sh = query_shift(big);
+                const float up = pow2(sh), down = pow2(-sh) * p.scale_log2;
                 float sum[S::kPanels];
 #pragma unroll
                 for (int pn = 0; pn < S::kPanels; ++pn) {
@@ -536,12 +530,14 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                     sum[pn] *= -1.0f / kTwo24;
                 }
                 // from rows (g) to the columns 2t, 2t + 1 of the products
+                const auto of_column = [&](float x, int j) { return __shfl_sync(0xFFFFFFFFu, x, 8 * t + j); };
+                c[nt] = pair(of_column(down, 0), of_column(down, 4));
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int gr = 0; gr < kGr; ++gr)
-                        nx[gr][nt][j] = __shfl_sync(0xFFFFFFFFu, sum[S::kSplit ? gr / 2 : gr],
-                                                    4 * (2 * t + j) + (S::kSplit ? 2 * (gr & 1) : 0));
+                for (int gr = 0; gr < kGr; ++gr) {
+                    const float x = sum[S::kSplit ? gr / 2 : gr];
+                    const int half = S::kSplit ? 2 * (gr & 1) : 0;
+                    nx[gr][nt] = pair(of_column(x, half), of_column(x, 4 + half));
+                }
             }
         }
 
@@ -670,12 +666,17 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float2 f = unpack_half2(kw[gr][e]);
-                            const float kc = f.x * c;
+                            const float ks = f.x * kTwo24;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    sc[u][nt][2 * e + j] = fmaf(kc, fmaf(f.y, nx[gr][nt][j], acc[h][nt][2 * e + j]), sc[u][nt][2 * e + j]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float* const to = &sc[u][nt][2 * e];
+                                // (the factor first: it need not wait for the product. With s_j (...) formed first and its factor last,
+                                // the batch of 64 requests took 99.3 us where it takes 97.5, the long context 61.2 for 60)
+                                const uint64_t kc = mul2(pair(ks, ks), c[nt]);
+                                const uint64_t in = fma2(pair(f.y, f.y), nx[gr][nt], pair(acc[h][nt][2 * e], acc[h][nt][2 * e + 1]));
+                                const float2 r = parts_of(fma2(kc, in, pair(to[0], to[1])));
+                                to[0] = r.x, to[1] = r.y;
+                            }
                         }
                     }
                 }

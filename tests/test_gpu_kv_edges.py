@@ -21,3 +21,66 @@ def test_attention_windows_wider_than_any_length(env, window, reqs):
     c.window = window
     out, lse = c.run()
     assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1])
+
+
+FACTORS = [1e-30, 1e-6, 1e8, 1e30, 2.0 ** 117, 2.0 ** -117]
+
+
+def _check_rows(c, out, lse):
+    """Case.check, and where a row's largest score stands out by more than what a score may be off: that key's values alone."""
+    c.check(out, lse)
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    q, cache = c.q.double().cpu().numpy(), c.cache.cpu().numpy()
+    page, ratio, sharp = c.L.page, c.q.shape[1] // c.L.heads, 0
+    for r, (n, new) in enumerate(c.reqs):
+        j = np.arange(n)
+        k, v, kmag, vmag = okv.values(c.O, cache, c.table[r][j // page].astype(np.int64) * page + j % page, 0)
+        for i in range(new):
+            for a in range(ratio):
+                tok, see = c.starts[r] + i, n - new + i + 1
+                s = k[:see] @ q[tok, a] * c.scale
+                off = 4 * c.L.dim * 2.0 ** -24 * (kmag[:see] @ np.abs(q[tok, a])).max() * c.scale
+                best = int(s.argmax())
+                if see > 1 and s[best] - np.partition(s, -2)[-2] <= off + 40:
+                    continue
+                sharp += 1
+                assert np.all(np.abs(out[tok, a] - v[best]) <= 2.0 ** -8 * np.abs(v[best]) + 2.0 ** -10 * vmag[best])
+    return sharp
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 32, 1, 8), (128, 64, 32, 1, 8), (128, 128, 16, 1, 8), (256, 64, 32, 1, 4), (256, 128, 16, 1, 4)])
+@pytest.mark.parametrize("reqs", [[(260, 1), (40, 1)], [(90, 20), (140, 3)]])
+def test_attention_rows_of_any_size(env, shape, reqs):
+    """Finite bf16 queries of very different sizes in one tile: each row as if it were alone."""
+    c = Case(env, *shape, "bfloat16", reqs)
+    good = c.run()
+    other = np.ones(good[1].shape, dtype=bool)
+    for n, f in enumerate(FACTORS):
+        at = n % len(c.q), n % c.q.shape[1]
+        c.q[at] *= f
+        other[at] = False
+    out, lse = c.run()
+    assert np.array_equal(out[other], good[0][other]) and np.array_equal(lse[other], good[1][other])
+    assert _check_rows(c, out, lse) > 0
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 32, 1, 8), (128, 64, 32, 1, 8), (128, 128, 16, 1, 8)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_large_chunk_rows_of_any_size(env, shape, sign):
+    """The same in a prompt chunk of 1048 rows, with scales of either sign."""
+    c = Case(env, *shape, "bfloat16", [(190, 131), (60, 1)])
+    good = c.run()
+    other = np.ones(good[1].shape, dtype=bool)
+    for n in range(24):
+        at = (7 * n) % 131, n % 8
+        c.q[at] *= FACTORS[n % 6]
+        other[at] = False
+    plain = c.run()
+    assert np.array_equal(plain[0][other], good[0][other]) and np.array_equal(plain[1][other], good[1][other])
+    if sign < 0:  # the signs of scale and queries cancel
+        c.q *= -1
+        c.scale = -c.scale
+        out, lse = c.run()
+        assert np.array_equal(out, plain[0]) and np.array_equal(lse, plain[1])
+        return
+    assert _check_rows(c, *plain) > 0
