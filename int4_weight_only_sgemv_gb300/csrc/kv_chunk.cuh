@@ -685,11 +685,18 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             if (next < n_tiles) scores(next);  // over the weights just used: the products run in the order of their issue
         }
+        // The last products arrive at barriers that nobody else waits for: none may be under way when the CTA leaves and its tensor
+        // memory goes, whether or not another role gave up.
+        for (int j = max(0, n_tiles - S::kBufs); j < n_tiles; ++j) {
+            mbar_wait(&k_free[j % S::kBufs], (j / S::kBufs) & 1);
+            mbar_wait(&v_free[j % S::kBufs], (j / S::kBufs) & 1);
+        }
         } else if (warp == 18) {
         // ---------------------------------------------------------------------------------------- copies
         const int per = min(p.page, 64);  // keys of a copy
         const uint8_t* const base = p.cache + head * p.head_bytes;
-        for (int j = 0; j < tiles; ++j) {
+        int j = 0;
+        for (; j < tiles; ++j) {
             const int stage = j % S::kRawStages;
             if (j >= S::kRawStages) wait(&raw_free[stage], (j / S::kRawStages - 1) & 1);
             const int pos = key0 + S::kKeys * j + lane * per;  // of this lane's copy
@@ -711,6 +718,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
             __syncwarp();
             if (bytes) bulk_g2s(s_raw + stage * S::kRawBytes + lane * (per / kSub) * S::kSubBytes, src, bytes, &raw_full[stage]);
         }
+        // (all have landed when the unpack warps are done, unless one of them gave up)
+        for (int i = max(0, j - S::kRawStages); i < j; ++i) mbar_wait(&raw_full[i % S::kRawStages], (i / S::kRawStages) & 1);
         }
     }
     __syncwarp();

@@ -574,6 +574,12 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                         report(p.status, SGEMV_ERR_TIMEOUT);
                         dead = true;
                         ahead.done = true;  // no more copies
+                        // those under way land in the rings, which the joins write and the CTA leaves behind: wait for them too
+#pragma unroll 1
+                        for (uint32_t i = 0; i < S::kStages; ++i) {
+                            const uint32_t next = stage + i;
+                            mbar_wait(&s_bar[warp][next % S::kStages], parity ^ (next >= S::kStages ? 1u : 0u));
+                        }
                     }
                 }
             }
