@@ -166,6 +166,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
+constexpr uint32_t kLeast = 1;  // scale 2^-24, zero point 0
 constexpr float kTwo24 = 16777216.0f, kTwo20 = 1048576.0f;
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // -126 <= e <= 127
@@ -366,6 +367,34 @@ struct Producer {
         ++k;
     }
 };
+
+// A V group of zeros is cached with s = 1, z = 0. The reference follows weight times scale, so that the weight of such a token would
+// push what far smaller values weigh out of fp16's range, for a product that is 0. Before the reference moves for a tile, those
+// of its tokens get s = 2^-24, which says the same, by a token a lane; whether one did.
+template <int D, int G>
+__device__ __forceinline__ bool drop_empty_groups(uint8_t* tile, int lane) {
+    uint8_t* const sub = tile + (lane >> 4) * (16 * D + 128 * (D / G));
+    uint32_t* const sz = reinterpret_cast<uint32_t*>(sub + 16 * D + 64 * (D / G)) + (lane & 15);
+    bool some = false;
+#pragma unroll
+    for (int gr = 0; gr < D / G; ++gr) some = some || sz[16 * gr] == 0x00003C00u;
+    if (!__any_sync(0xFFFFFFFFu, some)) return false;
+    some = false;
+    const uint8_t* const v = sub + 8 * D + ((lane & 15) >> 2) * 16 + (lane & 1) * 2;
+#pragma unroll 1
+    for (int gr = 0; gr < D / G; ++gr) {
+        uint32_t any = sz[16 * gr] ^ 0x00003C00u;
+#pragma unroll 1
+        for (int x = 0; x < G / 4; ++x) {  // 4 dims each
+            const int i = ((lane >> 1) & 1) * (D / 32) + gr * (G / 32) + (x >> 3);
+            any |= *reinterpret_cast<const uint16_t*>(v + (i >> 2) * 512 + (x & 7) * 64 + (i & 3) * 4);
+        }
+        if (any == 0) sz[16 * gr] = kLeast, some = true;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copy engine writes there next
+    __syncwarp();
+    return __any_sync(0xFFFFFFFFu, some);
+}
 
 template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kernel(const AttnParams p) {
@@ -588,11 +617,11 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
             const int pos0 = seg.keys.lo + k * kTileTok;
 
             if (!plain) {
-                // a token past the keys, or in a page outside the cache, may hold anything: s = 1, z = 0 for it
+                // a token past the keys, or in a page outside the cache, may hold anything: s = 2^-24, z = 0 for it
                 if (pos0 + lane >= seg.keys.hi || ((ahead.bad >> (2 * stage + (lane >> 4))) & 1u)) {
                     uint32_t* const w = reinterpret_cast<uint32_t*>(ahead.ring + stage * S::kStageBytes + (lane >> 4) * S::kSubBytes + 16 * D) + (lane & 15);
 #pragma unroll
-                    for (int gr = 0; gr < 2 * kGr; ++gr) w[16 * gr] = 0x00003C00u;
+                    for (int gr = 0; gr < 2 * kGr; ++gr) w[16 * gr] = kLeast;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copy engine writes there next
                 __syncwarp();
@@ -708,15 +737,39 @@ __global__ void __launch_bounds__(AttnShape<D, G, NT>::kThreads, 1) decode_kerne
                     }
             }
             float top[NT][2];
-            bool grow = false;
+            const auto largest = [&] {  // of the lane's scores; whether a weight would pass the limit
+                bool grow = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    top[nt][j] = fmaxf(fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][2 + j]), sc[1][nt][j]), sc[1][nt][2 + j]);
-                    grow = grow || top[nt][j] > lim[nt][j];
+                    for (int j = 0; j < 2; ++j) {
+                        top[nt][j] = fmaxf(fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][2 + j]), sc[1][nt][j]), sc[1][nt][2 + j]);
+                        grow = grow || top[nt][j] > lim[nt][j];
+                    }
+                return __any_sync(0xFFFFFFFFu, grow);
+            };
+            if (largest()) {
+                if (drop_empty_groups<D, G>(ahead.ring + stage * S::kStageBytes, lane)) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint8_t* const at = buf + u * S::kSubBytes + 16 * D + 64 * kGr + 4 * ta + 8 * e;
+                            float s[kGr], v = 0.0f;
+#pragma unroll
+                            for (int gr = 0; gr < kGr; ++gr) v = fmaxf(v, s[gr] = unpack_half2(*reinterpret_cast<const uint32_t*>(at + 64 * gr)).x);
+                            if (fabsf(iv[u][e] - 1.0f) > 1e-4f || v >= 1.0f) continue;  // the token's largest scale was not 1, or is still
+                            const float lv = log2_approx(v);
+                            iv[u][e] = exp2_approx(-lv);
+#pragma unroll
+                            for (int gr = 0; gr < kGr; ++gr) fr[u][gr][e] = s[gr] * iv[u][e];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) sc[u][nt][2 * e + j] += lv;
+                        }
+                    largest();
                 }
-            if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -84,3 +84,35 @@ def test_attention_large_chunk_rows_of_any_size(env, shape, sign):
         assert np.array_equal(out, plain[0]) and np.array_equal(lse, plain[1])
         return
     assert _check_rows(c, *plain) > 0
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 32, 1, 4), (128, 64, 16, 1, 4), (128, 128, 64, 1, 4), (256, 64, 32, 1, 4), (256, 128, 16, 1, 4)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_attention_keys_without_values(env, shape, new):
+    """Keys that take nearly all the weight and whose V is zero (its groups have scale 1) beside small values: what is left of those
+    is the output, as exact as ever."""
+    sg, torch = env
+    c = Case(env, *shape, "bfloat16", [(1000, new)], vscale=1e-3)
+    dim, page = c.L.dim, c.L.page
+    # a key so far along every query that its score is 17 above the others' usual ones
+    k = torch.linalg.lstsq(c.q.float().reshape(-1, dim).cpu(), torch.full((4 * new, 1), 17 / c.scale)).solution
+    j = np.arange(5, 1000 - new, 32)
+    slots = torch.tensor(c.table[0][j // page].astype(np.int64) * page + j % page, device="cuda")
+    k = k.view(1, 1, dim).bfloat16().cuda().expand(len(j), 1, dim)
+    sg.sgemv_kv_append(c.L, c.cache, k, torch.zeros_like(k), slots)
+    out, lse = c.run()
+    c.check(out, lse)
+    # and by the bound without its last term, which is larger than these outputs
+    ref, _, weight, size = okv.attention(c.O, c.cache.cpu().numpy(), c.q.float().cpu().numpy(), c.starts, [1000], c.table, c.scale)
+    score = 2 * dim * 2.0 ** -24 * size[..., None]
+    assert np.all(np.abs(out - ref) <= 2.0 ** -8 * np.abs(ref) + weight * (2.0 ** -11 + 2.0 ** -14 + score))
+
+
+def test_attention_whole_cache_without_values(env):
+    """V zero everywhere: zeros, and the softmax's sum as it should be."""
+    sg, torch = env
+    for shape in ((128, 128, 16, 1, 4), (256, 64, 16, 1, 4)):
+        c = Case(env, *shape, "float16", [(200, 1), (70, 5)], vscale=0.0)
+        out, lse = c.run()
+        c.check(out, lse)
+        assert not out.any()
