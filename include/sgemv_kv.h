@@ -133,6 +133,8 @@ typedef struct {
  * p = len[r] - n + i and sees positions j <= p, and j > p - window where window > 0. With tree_dev (window
  * must be 0, max_q <= 64) it sees every position before len - n, and new token m of its request where bit m of
  * tree_dev[q_start[r] + i] is set: the draft tokens of a token tree, each seeing its ancestors.
+ * Pages before the one that holds the first position that a request's new tokens see (len - n - window + 1) are
+ * not looked at: with a window they may be free, their table entries anything.
  * A token that sees nothing gets out = 0 and lse = -inf. lse is the natural logarithm of the softmax's sum.
  * Rows of out past q_start[n_req] are not written. What the cache holds past len is never used.
  * Results do not depend on the order in which the GPU runs the call's parts: the same inputs give the same bits.

@@ -241,9 +241,8 @@ __global__ void __launch_bounds__(ChunkShape<D, G>::kThreads, 1) chunk_kernel(co
     // within a request the last rows, which see the most keys, come first
     const int rows = sp.n * p.ratio, old = sp.len - sp.n;
     const int head = in_req % p.heads, row0 = ((rows + S::kRows - 1) / S::kRows - 1 - in_req / p.heads) * S::kRows;
-    Keys keys = keys_of(p, sp, row0, S::kRows);
-    keys.lo = keys.lo / S::kKeys * S::kKeys;
-    const int all_tiles = max(1, (keys.hi - keys.lo + S::kKeys - 1) / S::kKeys);
+    const Keys keys = keys_of<S::kKeys>(p, sp, row0, S::kRows);
+    const int all_tiles = keys.tiles;
     const int parts = min(splits, max(1, all_tiles / 4));  // a few tiles a split at least
     if (part >= parts) return;
     const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * part / parts);

@@ -116,18 +116,20 @@ __device__ __forceinline__ Span decode_span(const AttnParams& p, int r) {
     return s;
 }
 
-// The keys of rows [row0, row0 + rows) of a request: the first one (a multiple of the tile) and the end.
+// The keys of rows [row0, row0 + rows) of a request: where the first tile starts, in the page of the first key that a row sees (pages
+// before it may be free) and where a page's copies start, and the end.
 struct Keys {
     int lo, hi, tiles;
 };
 
+template <int kTile>
 __device__ __forceinline__ Keys keys_of(const AttnParams& p, const Span& s, int row0, int rows) {
     const int i0 = token_of_row(p, row0), i1 = token_of_row(p, min(row0 + rows - 1, s.n * p.ratio - 1));
     const int old = s.len - s.n;
     Keys k;
     k.hi = p.q.tree_dev != nullptr ? s.len : max(0, old + i1 + 1);
-    k.lo = p.q.window > 0 ? max(0, old + i0 - p.q.window + 1) / kTileTok * kTileTok : 0;
-    k.tiles = max(1, (k.hi - k.lo + kTileTok - 1) / kTileTok);  // rows that see nothing still have an owner
+    k.lo = p.q.window > 0 ? max(0, old + i0 - p.q.window + 1) & -min(p.page, kTile) : 0;
+    k.tiles = max(1, (k.hi - k.lo + kTile - 1) / kTile);  // rows that see nothing still have an owner
     return k;
 }
 
@@ -252,7 +254,7 @@ __device__ __forceinline__ void join_quad(const AttnParams& p, const Segment& s,
 template <int kRows>
 __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Span& s) {
     int64_t n = 0;
-    for (int row0 = 0; row0 < s.n * p.ratio; row0 += kRows) n += keys_of(p, s, row0, kRows).tiles + kSwitch;
+    for (int row0 = 0; row0 < s.n * p.ratio; row0 += kRows) n += keys_of<kTileTok>(p, s, row0, kRows).tiles + kSwitch;
     return n * p.heads;
 }
 
@@ -274,7 +276,7 @@ __device__ __forceinline__ void next_segment(const AttnParams& p, const Spans& s
         s.span = spans[++s.r];
         s.row0 = 0;
     }
-    s.keys = keys_of(p, s.span, s.row0, kRows);
+    s.keys = keys_of<kTileTok>(p, s.span, s.row0, kRows);
 }
 
 // The segment that holds a unit. before: units before each thread's run of requests.
@@ -295,7 +297,7 @@ __device__ __forceinline__ Segment locate(const AttnParams& p, const Spans& span
         s.start += n;
     }
     for (s.row0 = 0;; s.row0 += kRows) {
-        s.keys = keys_of(p, s.span, s.row0, kRows);
+        s.keys = keys_of<kTileTok>(p, s.span, s.row0, kRows);
         const int64_t n = static_cast<int64_t>(s.keys.tiles + kSwitch) * p.heads;
         if (unit < s.start + n) break;
         s.start += n;

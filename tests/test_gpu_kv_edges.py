@@ -116,3 +116,18 @@ def test_attention_whole_cache_without_values(env):
         out, lse = c.run()
         c.check(out, lse)
         assert not out.any()
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 16, 2, 4, "float16"), (128, 128, 16, 1, 8, "bfloat16"), (128, 64, 32, 1, 8, "float16"),
+                                   (256, 128, 16, 1, 2, "float16"), (128, 128, 128, 1, 8, "float16")])
+@pytest.mark.parametrize("window", [1, 20, 75])
+@pytest.mark.parametrize("new", [1, 5, 140])
+def test_attention_window_behind_freed_pages(env, shape, window, new):
+    """Pages that lie before everything that a row sees are free (-1 in the table): they are not looked at, and nothing is reported."""
+    c = Case(env, *shape, [(300 + a, new) for a in (0, 9, 17, 31)], window=window)
+    want = c.run()
+    c.check(*want)
+    for r, (n, _) in enumerate(c.reqs):
+        c.table[r, :max(0, n - new - window + 1) // c.L.page] = -1
+    out, lse = c.run()  # (asserts that the status stays 0)
+    assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1])
