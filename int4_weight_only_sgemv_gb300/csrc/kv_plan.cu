@@ -143,7 +143,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams 
         const int r = find(s_come, p.n_req, i);
         p.table[r * p.table_stride + pages_of(p, p.len[r]) + (i - s_come[padded(r)])] = handed(i);
     }
-    for (int i = come + first; i < gone; i += stride) p.free[n_free + i - come] = given(i);
+    for (int i = come + first; i < gone; i += stride) {
+        const int id = given(i);
+        if (id < 0 || id >= p.n_pages) report(p.status, SGEMV_ERR_ARG);  // (one that is handed on shows in its tokens' slots)
+        p.free[n_free + i - come] = id;
+    }
 #pragma unroll 2
     for (int i = first; i < p.n_slots; i += stride) {
         int64_t slot = -1;

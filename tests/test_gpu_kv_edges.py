@@ -131,3 +131,15 @@ def test_attention_window_behind_freed_pages(env, shape, window, new):
         c.table[r, :max(0, n - new - window + 1) // c.L.page] = -1
     out, lse = c.run()  # (asserts that the status stays 0)
     assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1])
+
+
+def test_plan_reports_bad_ids_of_released_pages(env):
+    """A page id outside the cache in a block that a request gives up is reported by the step that finds it."""
+    sg, _ = env
+    for bad in (-1, 4):
+        table = np.array([[2, bad, 1], [3, -1, -1]], dtype=np.int32)
+        got, status = _run_plan(env, [40, 3], [5, 3], [0, 1], table, [0, -9, -9, -9], 1, 16, 1)
+        assert status == sg.SGEMV_ERR_ARG
+        assert got[3].tolist() == [3 * 16 + 3] and got[1][0] == 3 and got[6][:3].tolist() == [0, bad, 1]
+    got, status = _run_plan(env, [40, 3], [5, 3], [0, 1], np.array([[2, 0, 1], [3, -1, -1]], dtype=np.int32), [-9] * 4, 0, 16, 1)
+    assert status == 0 and got[6][:2].tolist() == [0, 1]
