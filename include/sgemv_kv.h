@@ -79,7 +79,7 @@ int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* len_dev, cons
 /*
  * sgemv_kv_append -- quantise K and V rows into the cache.
  *   k_dev, v_dev : dtype (fp16 or bf16) [n_tokens][heads][dim]; dims are contiguous, a token's and a head's rows
- *                  start *_token_stride and *_head_stride elements apart (multiples of 8).
+ *                  start *_token_stride and *_head_stride elements apart (multiples of 8; that of an axis of length 1 is not used).
  *   slots_dev    : int64 [n_tokens], 8-byte aligned, as sgemv_kv_plan writes them. A negative slot is skipped;
  *                  one past the cache is skipped and reported (SGEMV_ERR_ARG). Slots are distinct.
  *   status_dev   : nullable; SGEMV_ERR_NONFINITE if a row holds inf or NaN, or a range too wide for an fp16 scale;
@@ -110,7 +110,7 @@ typedef struct {
     int32_t table_cols;
     float scale;        /* factor of q . k */
     int64_t table_stride;
-    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements, multiples of 8 */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements, multiples of 8 as in append */
     const void* q_dev;             /* [n_tokens][heads_q][dim] */
     const int32_t* q_start_dev;    /* [n_req + 1], as sgemv_kv_plan writes it */
     const int32_t* len_dev;        /* [n_req] tokens in the cache, the new ones included */

@@ -34,8 +34,8 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     const void* words[] = {q.q_start_dev, q.len_dev, q.table_dev, q.lse_dev, status_dev};
     for (const void* x : words)
         if (!is_aligned(x, 4)) return SGEMV_ERR_ALIGN;
-    if (!is_aligned(q.tree_dev, 8) || q.q_token_stride % 8 || q.q_head_stride % 8 || q.out_token_stride % 8 ||
-        q.out_head_stride % 8)
+    if (!is_aligned(q.tree_dev, 8) || !strides_aligned(q.n_tokens, q.q_token_stride, q.heads_q, q.q_head_stride) ||
+        !strides_aligned(q.n_tokens, q.out_token_stride, q.heads_q, q.out_head_stride))
         return SGEMV_ERR_ALIGN;
     AttnParams p;
     p.cache = static_cast<const uint8_t*>(cache_dev);

@@ -321,7 +321,8 @@ int sgemv_kv_append(const sgemv_kv_layout* layout, void* cache_dev, int dtype, c
     if (too_many(*layout, n_tokens)) return SGEMV_ERR_SHAPE;
     if (cache_dev == nullptr || k_dev == nullptr || v_dev == nullptr || slots_dev == nullptr) return SGEMV_ERR_ARG;
     if (!is_aligned(cache_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(slots_dev, 8) ||
-        !is_aligned(status_dev, 4) || k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8)
+        !is_aligned(status_dev, 4) || !strides_aligned(n_tokens, k_token_stride, layout->heads, k_head_stride) ||
+        !strides_aligned(n_tokens, v_token_stride, layout->heads, v_head_stride))
         return SGEMV_ERR_ALIGN;
     CacheParams p = params_of(*layout, cache_dev, slots_dev, n_tokens, status_dev);
     p.k = k_dev;

@@ -16,6 +16,10 @@ constexpr int kSub = 16;  // tokens of a subtile
 int check_kv_layout(const sgemv_kv_layout* layout);
 
 inline bool is_aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Strides of [tokens][heads][dim] that keep rows 16-byte aligned; that of an axis of length 1 is never used.
+inline bool strides_aligned(int tokens, int64_t token_stride, int heads, int64_t head_stride) {
+    return (tokens < 2 || token_stride % 8 == 0) && (heads < 2 || head_stride % 8 == 0);
+}
 
 // Host: launch with programmatic dependent launch (the kernels call pdl_wait before their first read).
 template <typename... P, typename... A>

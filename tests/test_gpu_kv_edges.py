@@ -143,3 +143,29 @@ def test_plan_reports_bad_ids_of_released_pages(env):
         assert got[3].tolist() == [3 * 16 + 3] and got[1][0] == 3 and got[6][:3].tolist() == [0, bad, 1]
     got, status = _run_plan(env, [40, 3], [5, 3], [0, 1], np.array([[2, 0, 1], [3, -1, -1]], dtype=np.int32), [-9] * 4, 0, 16, 1)
     assert status == 0 and got[6][:2].tolist() == [0, 1]
+
+
+def test_strides_of_single_tokens_and_heads_are_not_used(env):
+    """An axis of length 1 may have any stride."""
+    sg, torch = env
+    L = sg.sgemv_kv_layout_query(1, 128, 128, 16, 4)
+    st = _status(torch)
+    base = torch.randn(4000, device="cuda").half()
+    for shape, strides in (((1, 1, 128), (129, 131, 1)), ((5, 1, 128), (136, 3, 1))):
+        n = shape[0]
+        k, v = base.as_strided(shape, strides), base[1600:].as_strided(shape, strides)
+        slots = torch.arange(n, device="cuda")
+        got = []
+        for a, b in ((k, v), (k.contiguous(), v.contiguous())):
+            cache = torch.zeros(L.total_bytes, dtype=torch.uint8, device="cuda")
+            sg.sgemv_kv_append(L, cache, a, b, slots, status=st)
+            got.append(cache)
+        assert torch.equal(*got)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        outs = []
+        for q in (k, k.contiguous()):
+            out = torch.empty(n * 300, dtype=torch.float16, device="cuda").as_strided(shape, strides)
+            sg.sgemv_kv_attention(L, cache, q, torch.tensor([0, n], **i32), torch.tensor([n], **i32), torch.zeros((1, 1), **i32), out, n, 0.1,
+                                  sg.kv_workspace(), status=st)
+            outs.append(out.contiguous())
+        assert torch.equal(*outs) and int(st.item()) == 0
