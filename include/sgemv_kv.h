@@ -5,7 +5,9 @@
  *
  * The conventions of sgemv.h hold: status codes, no allocation, no synchronisation, argument errors found
  * on the host before anything is launched, `stream` and `status_dev` as described there. Device pointers
- * are 16-byte aligned unless a function says otherwise.
+ * are 16-byte aligned unless a function says otherwise. What a call writes overlaps neither its inputs nor what else it
+ * writes, but where a function says so: SGEMV_ERR_ARG. (Rows may lie between other rows, as in a fused projection's
+ * output; whether such rows share bytes is not looked into.)
  *
  * Cache bytes. The cache is n_pages pages; a page holds `page` tokens of every KV head; head h of page p
  * starts at p * page_bytes + h * head_bytes and is page / 16 subtiles of 16 tokens, sub_bytes each. Token
@@ -60,8 +62,7 @@ int sgemv_kv_layout_query(int heads, int dim, int group, int page, int n_pages, 
  *   pos_dev          : int32 [n_slots]: its position in its request; -1 for t >= q_start[n_req].
  * Pages that requests give up are handed out first, in request order and ascending blocks, to the requests
  * that grow, in the same order; then pages are popped from the stack. What is left of the given-up pages is
- * pushed, in order. The inputs len and free_count are not written (no output may overlap an input): a
- * caller swaps two buffers from step to step.
+ * pushed, in order. The inputs len and free_count are not written: a caller swaps two buffers from step to step.
  * Device-reported, and then nothing is taken or released (len_out = len, free_count_out = free_count, q_start all
  * 0, every slot and position -1): SGEMV_ERR_ARG (negative counts, keep > len, more new tokens than n_slots, a
  * stack height outside 0..n_pages), SGEMV_ERR_SHAPE (a row needs more than table_cols pages, or the free pages
@@ -136,7 +137,7 @@ typedef struct {
  * Pages before the one that holds the first position that a request's new tokens see (len - n - window + 1) are
  * not looked at: with a window they may be free, their table entries anything.
  * A token that sees nothing gets out = 0 and lse = -inf. lse is the natural logarithm of the softmax's sum.
- * Rows of out past q_start[n_req] are not written. What the cache holds past len is never used.
+ * out may be q itself (the same address and strides). Rows of out past q_start[n_req] are not written. What the cache holds past len is never used.
  * Results do not depend on the order in which the GPU runs the call's parts: the same inputs give the same bits.
  * Device-reported: SGEMV_ERR_ARG (a request with q_start out of order or out of range, n > max_q, a negative
  * length; a page id outside the cache), SGEMV_ERR_SHAPE (len needs more than table_cols pages, or passes 2^30): such a request's
@@ -159,7 +160,8 @@ int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cache_dev, con
  *   logp_dev   : nullable fp32 [rows][vocab], contiguous: every lp, the rows that sgemv_beam_step reads.
  * -inf logits (banned tokens) have probability 0 and lp -inf. A row of nothing else has lse -inf, every lp -inf
  * and entropy 0. A row with NaN or +inf has NaN in every output and -1 in top_tok, and status_dev gets
- * SGEMV_ERR_NONFINITE. Pointers are aligned to their element. rows 0 is allowed.
+ * SGEMV_ERR_NONFINITE. Pointers are aligned to their element. logp_dev may be logits_dev (fp32, stride vocab). rows 0 is
+ * allowed.
  * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (vocab outside 1..2^24), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_logprobs(const void* logits_dev, int dtype, int rows, int vocab, int64_t stride, const int32_t* tokens_dev,

@@ -37,6 +37,17 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     if (!is_aligned(q.tree_dev, 8) || !strides_aligned(q.n_tokens, q.q_token_stride, q.heads_q, q.q_head_stride) ||
         !strides_aligned(q.n_tokens, q.out_token_stride, q.heads_q, q.out_head_stride))
         return SGEMV_ERR_ALIGN;
+    // (rows between others, as those of a fused projection, may be out's: what lies from its first to its last byte is looked at
+    // only where nothing else has a place there)
+    const Bytes out = span_bytes(q.out_dev, q.n_tokens, q.out_token_stride, q.heads_q, q.out_head_stride, layout->dim);
+    const Bytes qs = span_bytes(q.q_dev, q.n_tokens, q.q_token_stride, q.heads_q, q.q_head_stride, layout->dim);
+    const Bytes cache(cache_dev, layout->total_bytes), ws(q.workspace_dev, SGEMV_KV_WORKSPACE);
+    const Bytes lse(q.lse_dev, 4ull * q.n_tokens * q.heads_q);
+    const Bytes written[] = {ws, lse, {status_dev, 4}};
+    const Bytes read[] = {cache, {q.q_start_dev, 4ull * q.n_req + 4}, {q.len_dev, 4ull * q.n_req}, {q.tree_dev, 8ull * q.n_tokens}};
+    if (!apart(written, read) || meet(out, cache) || meet(out, ws) || meet(qs, ws)) return SGEMV_ERR_ARG;
+    const uint64_t all = 2ull * q.n_tokens * q.heads_q * layout->dim;
+    if (q.out_dev != q.q_dev && out.size == all && qs.size == all && meet(out, qs)) return SGEMV_ERR_ARG;
     AttnParams p;
     p.cache = static_cast<const uint8_t*>(cache_dev);
     p.sub_bytes = layout->sub_bytes;

@@ -324,6 +324,11 @@ int sgemv_kv_append(const sgemv_kv_layout* layout, void* cache_dev, int dtype, c
         !is_aligned(status_dev, 4) || !strides_aligned(n_tokens, k_token_stride, layout->heads, k_head_stride) ||
         !strides_aligned(n_tokens, v_token_stride, layout->heads, v_head_stride))
         return SGEMV_ERR_ALIGN;
+    const Bytes written[] = {{cache_dev, layout->total_bytes}, {status_dev, 4}};
+    const Bytes read[] = {span_bytes(k_dev, n_tokens, k_token_stride, layout->heads, k_head_stride, layout->dim),
+                          span_bytes(v_dev, n_tokens, v_token_stride, layout->heads, v_head_stride, layout->dim),
+                          {slots_dev, 8ull * n_tokens}};
+    if (!apart(written, read)) return SGEMV_ERR_ARG;
     CacheParams p = params_of(*layout, cache_dev, slots_dev, n_tokens, status_dev);
     p.k = k_dev;
     p.v = v_dev;
@@ -348,6 +353,10 @@ int sgemv_kv_read(const sgemv_kv_layout* layout, const void* cache_dev, const in
     if (!is_aligned(cache_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(slots_dev, 8) ||
         !is_aligned(status_dev, 4))
         return SGEMV_ERR_ALIGN;
+    const uint64_t out_bytes = (dtype == SGEMV_F32 ? 4ull : 2ull) * n_tokens * layout->heads * layout->dim;
+    const Bytes written[] = {{k_dev, out_bytes}, {v_dev, out_bytes}, {status_dev, 4}};
+    const Bytes read[] = {{cache_dev, layout->total_bytes}, {slots_dev, 8ull * n_tokens}};
+    if (!apart(written, read)) return SGEMV_ERR_ARG;
     CacheParams p = params_of(*layout, cache_dev, slots_dev, n_tokens, status_dev);
     p.k_out = k_dev;
     p.v_out = v_dev;

@@ -16,6 +16,39 @@ constexpr int kSub = 16;  // tokens of a subtile
 int check_kv_layout(const sgemv_kv_layout* layout);
 
 inline bool is_aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Host: bytes that a call reads or writes.
+struct Bytes {
+    uintptr_t at;
+    uint64_t size;  // 0: nothing
+    Bytes(const void* p, uint64_t n) : at(reinterpret_cast<uintptr_t>(p)), size(p != nullptr ? n : 0) {}
+};
+inline bool meet(const Bytes& a, const Bytes& b) { return a.size != 0 && b.size != 0 && a.at < b.at + b.size && b.at < a.at + a.size; }
+// Whether one of `rows` rows of row.size bytes, `stride` bytes apart (row.size at least), has some of b's.
+inline bool rows_meet(const Bytes& row, uint64_t rows, uint64_t stride, const Bytes& b) {
+    if (row.size == 0 || rows == 0 || !meet({reinterpret_cast<const void*>(row.at), (rows - 1) * stride + row.size}, b)) return false;
+    const uint64_t i = b.at < row.at + row.size ? 0 : (b.at - row.at - row.size) / stride + 1;  // the first row that ends after b starts
+    return i < rows && row.at + i * stride < b.at + b.size;
+}
+// Everything from the first to the last row of [tokens][heads][dim] elements of 2 bytes.
+inline Bytes span_bytes(const void* p, int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t dim) {
+    const int64_t t = (tokens - 1) * token_stride, h = (heads - 1) * head_stride;
+    const int64_t lo = (t < 0 ? t : 0) + (h < 0 ? h : 0), hi = (t > 0 ? t : 0) + (h > 0 ? h : 0) + dim;
+    Bytes b(p, 2 * (hi - lo));
+    b.at += 2 * lo;
+    return b;
+}
+// What a call writes meets neither what else it writes nor what it reads.
+template <int W, int R>
+bool apart(const Bytes (&written)[W], const Bytes (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        for (int j = i + 1; j < W; ++j)
+            if (meet(written[i], written[j])) return false;
+        for (int j = 0; j < R; ++j)
+            if (meet(written[i], read[j])) return false;
+    }
+    return true;
+}
+
 // Strides of [tokens][heads][dim] that keep rows 16-byte aligned; that of an axis of length 1 is never used.
 inline bool strides_aligned(int tokens, int64_t token_stride, int heads, int64_t head_stride) {
     return (tokens < 2 || token_stride % 8 == 0) && (heads < 2 || head_stride % 8 == 0);

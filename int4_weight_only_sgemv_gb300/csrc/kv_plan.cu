@@ -210,9 +210,16 @@ extern "C" int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* le
     for (const void* q : ptrs)
         if (!is_aligned(q, 4)) return SGEMV_ERR_ALIGN;
     if (!is_aligned(slots_dev, 8)) return SGEMV_ERR_ALIGN;
-    if (free_count_dev == free_count_out_dev || (n_req > 0 && (len_dev == len_out_dev || keep_dev == len_out_dev ||
-                                                               add_dev == len_out_dev)))
-        return SGEMV_ERR_ARG;
+    const uint64_t per_req = 4ull * n_req;
+    const Bytes written[] = {{len_out_dev, per_req}, {free_count_out_dev, 4}, {q_start_dev, per_req + 4}, {slots_dev, 8ull * n_slots},
+                             {pos_dev, 4ull * n_slots}, {free_dev, 4ull * n_pages}, {status_dev, 4}};
+    const Bytes read[] = {{len_dev, per_req}, {keep_dev, per_req}, {add_dev, per_req}, {free_count_dev, 4}};
+    if (!apart(written, read)) return SGEMV_ERR_ARG;
+    const Bytes row(table_dev, 4ull * table_cols);  // the table's rows are written too
+    for (const Bytes& b : written)
+        if (rows_meet(row, n_req, 4ull * table_stride, b)) return SGEMV_ERR_ARG;
+    for (const Bytes& b : read)
+        if (rows_meet(row, n_req, 4ull * table_stride, b)) return SGEMV_ERR_ARG;
     DeviceInfo di;
     const int rc = device_info(&di);
     if (rc != SGEMV_OK) return rc;

@@ -456,6 +456,15 @@ extern "C" int sgemv_logprobs(const void* logits_dev, int dtype, int rows, int v
     for (const void* q : words)
         if (!is_aligned(q, 4)) return SGEMV_ERR_ALIGN;
     if (!is_aligned(logits_dev, dtype == SGEMV_F32 ? 4 : 2)) return SGEMV_ERR_ALIGN;
+    const uint64_t size = dtype == SGEMV_F32 ? 4 : 2, n = rows;
+    const Bytes full(logp_dev, 4 * n * vocab), row(logits_dev, size * vocab);
+    const Bytes written[] = {full, {tok_logp_dev, 4 * n * n_tok}, {lse_dev, 4 * n}, {entropy_dev, 4 * n}, {top_tok_dev, 4 * n * top},
+                             {top_logp_dev, 4 * n * top}, {status_dev, 4}};
+    const Bytes read[] = {{tokens_dev, 4 * n * n_tok}};
+    if (!apart(written, read)) return SGEMV_ERR_ARG;
+    for (int i = 0; i < 7; ++i)  // (a thread that writes a full row's element is the last to read it: logp may be logits)
+        if (rows_meet(row, n, size * stride, written[i]) && (i > 0 || logp_dev != logits_dev || size != 4 || stride != vocab))
+            return SGEMV_ERR_ARG;
     LogprobParams p = {};
     p.logits = logits_dev;
     p.stride = stride;

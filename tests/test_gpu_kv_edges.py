@@ -169,3 +169,38 @@ def test_strides_of_single_tokens_and_heads_are_not_used(env):
                                   sg.kv_workspace(), status=st)
             outs.append(out.contiguous())
         assert torch.equal(*outs) and int(st.item()) == 0
+
+
+def test_attention_out_in_place_of_q(env):
+    """out may be q itself: the same bits."""
+    sg, torch = env
+    for reqs in ([(700, 1), (90, 7), (40, 1)], [(300, 131), (50, 1)]):
+        c = Case(env, 128, 64, 32, 1, 8, "float16", reqs)
+        out, _ = c.run()
+        starts, lens, table, _ = c.tensors()
+        q = c.q.clone()
+        sg.sgemv_kv_attention(c.L, c.cache, q, starts, lens, table, q, c.max_q, c.scale, sg.kv_workspace())
+        assert np.array_equal(q.float().cpu().numpy(), out)
+
+
+def test_logprobs_in_place(env):
+    """Full rows may take the place of fp32 logits."""
+    sg, torch = env
+    for rows, vocab in ((3, 70001), (300, 517)):
+        x = torch.randn(rows, vocab, device="cuda")
+        want = sg.logprobs(x, top=5, full=True)
+        top = torch.empty(rows, 5, dtype=torch.int32, device="cuda"), torch.empty(rows, 5, device="cuda")
+        sg.sgemv_logprobs(x, (None, None, None, *top, x))
+        assert torch.equal(x, want["logp"]) and torch.equal(top[0], want["top_tok"]) and torch.equal(top[1], want["top_logp"])
+
+
+def test_plan_arrays_between_the_rows_of_a_table(env):
+    """A table of some columns of wider rows: what lies between its rows may be another array."""
+    sg, torch = env
+    i32 = dict(dtype=torch.int32, device="cuda")
+    wide = torch.full((2, 40), -1, **i32)
+    table, start = wide[:, :4], wide[0, 20:23]
+    length, add = torch.zeros(2, **i32), torch.tensor([20, 5], **i32)
+    out = (torch.empty(2, **i32), torch.empty(1, **i32), start, torch.empty(25, dtype=torch.int64, device="cuda"), torch.empty(25, **i32))
+    sg.sgemv_kv_plan(length, None, add, table, torch.arange(8, **i32), torch.tensor([8], **i32), 16, out)
+    assert start.tolist() == [0, 20, 25] and table.tolist() == [[7, 6, -1, -1], [5, -1, -1, -1]]
