@@ -305,10 +305,10 @@ def kv_workspace(device="cuda"):
 
 
 def kv_attention(layout: KvLayout, cache, q, q_start, length, table, max_q: int, scale: float, workspace, window: int = 0,
-                 tree=None, status=None, stream=None):
-    """sgemv_kv_attention into a new contiguous tensor, which it returns."""
+                 tree=None, status=None, stream=None, lse=None):
+    """sgemv_kv_attention into a new contiguous tensor, which it returns; lse: fp32 [tokens, heads_q] to write, or None."""
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    sgemv_kv_attention(layout, cache, q, q_start, length, table, out, max_q, scale, workspace, None, window, tree, status,
+    sgemv_kv_attention(layout, cache, q, q_start, length, table, out, max_q, scale, workspace, lse, window, tree, status,
                        stream)
     return out
 

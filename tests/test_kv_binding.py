@@ -90,3 +90,16 @@ def test_tensors_of_another_device_are_refused(env):
         with pytest.raises(ValueError):
             call(moved)
         assert len(calls) == done
+
+
+def test_attention_helper_passes_lse_on(env, monkeypatch):
+    sg, torch, cuda, calls = env
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: cuda(*shape, dtype=dtype))
+    tensors, _ = _calls(sg, torch, cuda)[3]
+    t = {k: v for k, v in tensors.items() if k not in ("out", "lse")}
+    layout = sg.sgemv_kv_layout_query(2, 128, 128, 16, 4)
+    out = sg.kv_attention(layout, max_q=1, scale=0.1, lse=tensors["lse"], **t)
+    query = calls[-1][1][2]._obj
+    assert query.lse_dev == tensors["lse"].data_ptr() and query.out_dev == out.data_ptr() and query.tree_dev == t["tree"].data_ptr()
+    sg.kv_attention(layout, max_q=1, scale=0.1, **t)
+    assert calls[-1][1][2]._obj.lse_dev is None
