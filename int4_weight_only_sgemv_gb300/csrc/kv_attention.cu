@@ -71,20 +71,9 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
     rc = device_info(&di);
     if (rc != SGEMV_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Requests with many rows (new tokens x query heads of a KV head) go to the chunk kernel, whose tensor memory holds dims up
-    // to 128. It takes the same time for 1 row as for the 256 of a CTA, the decode kernel a time in proportion: 16 requests of up
-    // to 4096 keys, 8 KV heads of 128, 77 rows on average: decode 64 us, chunk 91; 154: 109, 93; heads of 64, 154: 65, 78; 308: 112, 80.
-    // So the average decides, and half of a batch does not go either way (154 rows, divided at 128: 124 us). Where there are
-    // fewer segments than SMs, so that the chunk kernel splits them over the keys and joins large partials, it wins later: one
-    // request of 4096 keys with 614 rows: 60, 70; with 1228: 103, 81.
-    const int64_t all_rows = static_cast<int64_t>(q.n_tokens) * p.ratio;
-    const bool few = (all_rows / kChunkRows + q.n_req) * p.heads < di.sm_count;
-    const bool dense = all_rows > static_cast<int64_t>(q.n_req) * (layout->dim == 64 ? 224 : 112);
-    const int min_rows = few ? 1024 : dense ? 64 : 512;
-    const bool chunks = layout->dim <= 128 && static_cast<int64_t>(q.max_q) * p.ratio > min_rows;
-    p.max_rows = chunks ? min_rows : INT_MAX;
+    p.max_rows = chunk_threshold(layout->dim, layout->heads, p.ratio, q.n_req, q.n_tokens, q.max_q, di.sm_count);
     cudaError_t e = q.dtype == SGEMV_F16 ? launch_decode_f16(layout->dim, layout->group, p, di.sm_count, s)
                                          : launch_decode_bf16(layout->dim, layout->group, p, di.sm_count, s);
-    if (e == cudaSuccess && chunks) e = launch_chunk(q.dtype, layout->dim, layout->group, p, s);
+    if (e == cudaSuccess && p.max_rows < INT_MAX) e = launch_chunk(q.dtype, layout->dim, layout->group, p, s);
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }

@@ -36,7 +36,6 @@
 
 namespace sgemv {
 
-constexpr int kChunkRows = 256;  // rows of a CTA
 constexpr float kBig = 32768.0f; // 2^kLimit
 
 template <int D, int G>

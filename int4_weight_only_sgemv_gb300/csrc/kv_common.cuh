@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <climits>
 
 #include "common.cuh"
 #include "sgemv_kv.h"
@@ -68,6 +69,22 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, uint32_t smem,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+constexpr int kChunkRows = 256;  // rows of a CTA of the chunk kernel
+
+// Host: requests with more rows (new tokens x query heads of a KV head) than this go to the chunk kernel; INT_MAX where none does.
+// Its tensor memory holds dims up to 128. It takes the same time for 1 row as for the 256 of a CTA, the decode kernel a time in
+// proportion: 16 requests of up to 4096 keys, 8 KV heads of 128, 77 rows on average: decode 64 us, chunk 91; 154: 109, 93; heads of
+// 64, 154: 65, 78; 308: 112, 80. So the average decides, and half of a batch does not go either way (154 rows, divided at 128: 124
+// us). Where there are fewer segments than SMs, so that the chunk kernel splits them over the keys and joins large partials, it
+// wins later: one request of 4096 keys with 614 rows: 60, 70; with 1228: 103, 81.
+inline int chunk_threshold(int dim, int heads, int ratio, int n_req, int n_tokens, int max_q, int sms) {
+    const int64_t all_rows = static_cast<int64_t>(n_tokens) * ratio;
+    const bool few = (all_rows / kChunkRows + n_req) * heads < sms;
+    const bool dense = all_rows > static_cast<int64_t>(n_req) * (dim == 64 ? 224 : 112);
+    const int rows = few ? 1024 : dense ? 64 : 512;
+    return dim <= 128 && static_cast<int64_t>(max_q) * ratio > rows ? rows : INT_MAX;
 }
 
 __device__ __forceinline__ void report(int32_t* status, int code) {

@@ -204,3 +204,39 @@ def test_plan_arrays_between_the_rows_of_a_table(env):
     out = (torch.empty(2, **i32), torch.empty(1, **i32), start, torch.empty(25, dtype=torch.int64, device="cuda"), torch.empty(25, **i32))
     sg.sgemv_kv_plan(length, None, add, table, torch.arange(8, **i32), torch.tensor([8], **i32), 16, out)
     assert start.tolist() == [0, 20, 25] and table.tolist() == [[7, 6, -1, -1], [5, -1, -1, -1]]
+
+
+def many_requests(n_req):
+    """Mostly decodes and idle requests, and prompt chunks of 560 rows (8 query heads a KV head), three of them neighbours."""
+    rng = np.random.default_rng(n_req + 2)
+    reqs = []
+    for r in range(n_req):
+        old, n = int(rng.integers(0, 40)), int(rng.integers(0, 2))
+        reqs.append((old + 70, 70) if r % 97 in (50, 51, 52) else (old + n, n))
+    return reqs
+
+
+@pytest.mark.parametrize("n_req", [300, 700, 1400])
+def test_attention_many_requests_and_prompt_chunks(env, n_req):
+    """More requests than the tensor-core form has threads (640), so that a thread looks after several, with prompt chunks among them."""
+    c = Case(env, 64, 64, 16, 1, 8, "float16", many_requests(n_req))
+    c.check(*c.run())
+
+
+MANY_ROWS = [(300, 300), (371, 260), (64, 1)]  # (tokens, new ones): 2400 and 2080 rows a KV head, and a decode
+
+
+@pytest.mark.parametrize("dim,group,heads,dtype", [(128, 128, 2, "float16"), (64, 64, 1, "bfloat16"), (128, 64, 1, "float16"),
+                                                   (256, 128, 1, "float16"), (256, 64, 1, "bfloat16")])
+def test_attention_prompts_of_many_rows(env, dim, group, heads, dtype):
+    """More than 2000 rows a KV head: many row tiles a request, a whole prompt and one behind a context."""
+    c = Case(env, dim, group, 64, heads, 8, dtype, MANY_ROWS)
+    c.check(*c.run())
+
+
+def test_attention_shared_pages(env):
+    """Two requests whose tables list the same pages for a common prefix."""
+    c = Case(env, 128, 128, 16, 2, 4, "float16", [(90, 2), (75, 1), (200, 140)])
+    c.table[1, :3] = c.table[0, :3]
+    c.table[2, :4] = c.table[0, :4]
+    c.check(*c.run())
