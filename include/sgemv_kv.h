@@ -65,11 +65,11 @@ int sgemv_kv_layout_query(int heads, int dim, int group, int page, int n_pages, 
  * pushed, in order. The inputs len and free_count are not written: a caller swaps two buffers from step to step.
  * Device-reported, and then nothing is taken or released (len_out = len, free_count_out = free_count, q_start all
  * 0, every slot and position -1): SGEMV_ERR_ARG (negative counts, keep > len, more new tokens than n_slots, a
- * stack height outside 0..n_pages), SGEMV_ERR_SHAPE (a row needs more than table_cols pages, or the free pages
- * run out). A page id outside 0..n_pages-1 in a block that is given up (it goes where the page would) or that a new
+ * stack height outside 0..n_pages), SGEMV_ERR_SHAPE (a row needs more than table_cols pages, the free pages run out, or
+ * more pages than there are are given up or needed). A page id outside 0..n_pages-1 in a block that is given up (it goes where the page would) or that a new
  * token falls into: SGEMV_ERR_ARG, and -1 in that token's slot.
  * Pointers are 4-byte aligned (slots: 8-byte). n_req 0 and n_slots 0 are allowed.
- * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page; n_req above 16384), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
+ * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page; n_req above 16384, n_slots or n_pages above 2^30), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* len_dev, const int32_t* keep_dev,
                   const int32_t* add_dev, int32_t* table_dev, int table_cols, int64_t table_stride, int32_t* free_dev,

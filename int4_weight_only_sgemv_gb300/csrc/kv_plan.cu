@@ -17,6 +17,7 @@ namespace sgemv {
 namespace {
 
 constexpr int kPlanMaxReq = 16384;  // three prefix sums of so many requests fit in shared memory
+constexpr int kPlanMax = 1 << 30;   // slots and pages: an index and a grid's stride past it stay in 32 bits
 
 // Place of request r in shared memory: one word more every 32, so that threads with 8 (or 4, 16) requests each hit all banks.
 __host__ __device__ constexpr int padded(int r) { return r + (r >> 5); }
@@ -116,6 +117,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams 
     __syncthreads();
     int err = s_err;
     if (err == 0 && (all[0] > p.n_slots || n_free < 0 || n_free > p.n_pages)) err = SGEMV_ERR_ARG;
+    // (no more pages can change hands than there are: counts and indexes stay in 32 bits)
+    if (err == 0 && (all[1] > p.n_pages || all[2] > p.n_pages)) err = SGEMV_ERR_SHAPE;
     if (err == 0 && (all[2] - all[1] > n_free || all[1] - all[2] > p.n_pages - n_free)) err = SGEMV_ERR_SHAPE;
     const bool ok = err == 0;
     const int tokens = ok ? static_cast<int>(all[0]) : 0, gone = ok ? static_cast<int>(all[1]) : 0, come = ok ? static_cast<int>(all[2]) : 0;
@@ -198,7 +201,7 @@ extern "C" int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* le
                              int n_slots, int32_t* status_dev, void* stream) {
     if (n_req < 0 || n_slots < 0 || table_cols < 1 || table_stride < table_cols || n_pages < 1) return SGEMV_ERR_ARG;
     if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return SGEMV_ERR_SHAPE;
-    if (n_req > kPlanMaxReq) return SGEMV_ERR_SHAPE;
+    if (n_req > kPlanMaxReq || n_slots > kPlanMax || n_pages > kPlanMax) return SGEMV_ERR_SHAPE;
     const void* must[] = {free_dev, free_count_dev, free_count_out_dev, q_start_dev};
     for (const void* q : must)
         if (q == nullptr) return SGEMV_ERR_ARG;

@@ -240,3 +240,14 @@ def test_attention_shared_pages(env):
     c.table[1, :3] = c.table[0, :3]
     c.table[2, :4] = c.table[0, :4]
     c.check(*c.run())
+
+
+def test_plan_with_more_pages_than_there_are(env):
+    """Lengths that cannot be: requests give up and need more pages than the cache has, though as many as they give up. Nothing moves."""
+    sg, _ = env
+    table = np.array([[1, 2, 3, 0, 1, 2], [3, -1, -1, -1, -1, -1]], dtype=np.int32)
+    length, keep, add = [96, 16], [16, 16], [0, 80]
+    got, status = _run_plan(env, length, keep, add, table, [-9] * 4, 0, 16, 80)
+    assert status == sg.SGEMV_ERR_SHAPE
+    assert got[0].tolist() == length and got[1][0] == 0 and not got[2].any() and np.all(got[3] == -1) and np.all(got[4] == -1)
+    assert np.array_equal(got[5], table) and np.all(got[6] == -9)

@@ -97,3 +97,13 @@ def test_logprobs(sg):
     for kw in (dict(lse=A + 400), dict(ent=A + 4 * rows * vocab - 4), dict(full=A + 4), dict(full=A, dtype=0), dict(full=A, stride=vocab + 1),
                dict(tl=at["tok"]), dict(tt=at["tv"] + 8), dict(st=at["lse"] + 8), dict(ent=at["lse"]), dict(full=at["tl"] - 8), dict(tv=A)):
         assert lp(**kw) == sg.SGEMV_ERR_ARG, kw
+
+
+def test_plan_sizes_that_leave_32_bits(sg):
+    """(the addresses are apart, and refused for the sizes)"""
+    def plan(pages=9, n_slots=5):
+        return sg._lib.sgemv_kv_plan(4, 16, pages, A, None, A + 64, 2 * A, 3, 3, 3 * A, A + 128, A + 192, A + 256, A + 320, 1 << 40, 1 << 41,
+                                     n_slots, None, None)
+
+    assert plan(pages=(1 << 30) + 1) == sg.SGEMV_ERR_SHAPE
+    assert plan(n_slots=(1 << 30) + 1) == sg.SGEMV_ERR_SHAPE and plan(n_slots=(1 << 31) - 1) == sg.SGEMV_ERR_SHAPE
