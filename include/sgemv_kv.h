@@ -144,7 +144,7 @@ typedef struct {
  * rows are not written, keys of a page outside the cache are left out; SGEMV_ERR_TIMEOUT (a bounded wait for a
  * copy gave up: out is invalid).
  * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_FORMAT (layout fields), SGEMV_ERR_SHAPE (heads_q; n_tokens times query
- * heads a KV head above 2^30), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
+ * heads a KV head, or n_req, above 2^30), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cache_dev, const sgemv_kv_query* query,
                        int32_t* status_dev, void* stream);

@@ -22,6 +22,7 @@ extern "C" int sgemv_kv_attention(const sgemv_kv_layout* layout, const void* cac
         return SGEMV_ERR_ARG;
     if (q.heads_q < 1 || q.heads_q % layout->heads != 0 || q.heads_q > 16384) return SGEMV_ERR_SHAPE;
     if (static_cast<int64_t>(q.n_tokens) * (q.heads_q / layout->heads) > (1 << 30)) return SGEMV_ERR_SHAPE;  // rows in 32 bits
+    if (q.n_req > (1 << 30)) return SGEMV_ERR_SHAPE;  // and the runs of requests that threads look after
     if (q.tree_dev != nullptr && (q.window != 0 || q.max_q > 64)) return SGEMV_ERR_ARG;
     if (q.n_req == 0 || q.n_tokens == 0 || q.max_q == 0) return SGEMV_OK;
     const void* must[] = {cache_dev, q.q_dev, q.q_start_dev, q.len_dev, q.table_dev, q.out_dev, q.workspace_dev};

@@ -82,6 +82,7 @@ def test_attention(sg):
                dict(lse_dev=ok["tree_dev"] + 8 * n - 4), dict(st=ok["len_dev"]), dict(st=ok["lse_dev"] + 4),
                dict(out_dev=ok["q_dev"] + 16), dict(out_dev=ok["q_dev"] - dense + 16)):
         assert attn(**kw) == sg.SGEMV_ERR_ARG, kw
+    assert attn(n_req=(1 << 30) + 1, out_dev=A) == sg.SGEMV_ERR_SHAPE  # (before the overlap is looked at)
 
 
 def test_logprobs(sg):
