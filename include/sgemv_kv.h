@@ -63,13 +63,17 @@ int sgemv_kv_layout_query(int heads, int dim, int group, int page, int n_pages, 
  * Pages that requests give up are handed out first, in request order and ascending blocks, to the requests
  * that grow, in the same order; then pages are popped from the stack. What is left of the given-up pages is
  * pushed, in order. The inputs len and free_count are not written: a caller swaps two buffers from step to step.
+ * A page has one owner here: if two rows list one (a shared prefix), it goes back when the first of them gives it up,
+ * while the other still reads it. Attention does not mind shared pages; who shares them keeps count of the users and
+ * hands this call only what is to go.
  * Device-reported, and then nothing is taken or released (len_out = len, free_count_out = free_count, q_start all
  * 0, every slot and position -1): SGEMV_ERR_ARG (negative counts, keep > len, more new tokens than n_slots, a
  * stack height outside 0..n_pages), SGEMV_ERR_SHAPE (a row needs more than table_cols pages, the free pages run out, or
- * more pages than there are are given up or needed). A page id outside 0..n_pages-1 in a block that is given up (it goes where the page would) or that a new
- * token falls into: SGEMV_ERR_ARG, and -1 in that token's slot.
+ * more pages than there are are given up or needed). A page id outside 0..n_pages-1 in a block that is given up (it
+ * goes where the page would) or that a new token falls into: SGEMV_ERR_ARG, and -1 in that token's slot.
  * Pointers are 4-byte aligned (slots: 8-byte). n_req 0 and n_slots 0 are allowed.
- * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page; n_req above 16384, n_slots or n_pages above 2^30), SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
+ * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (page; n_req above 16384, n_slots or n_pages above 2^30),
+ * SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_kv_plan(int n_req, int page, int n_pages, const int32_t* len_dev, const int32_t* keep_dev,
                   const int32_t* add_dev, int32_t* table_dev, int table_cols, int64_t table_stride, int32_t* free_dev,
@@ -129,7 +133,11 @@ typedef struct {
 
 /*
  * sgemv_kv_attention -- out = softmax(scale * q K^T) V over the cache, with the values (q - z) * s the cache
- * stands for; scores, the softmax's maximum and sum, and out's sums are held in 32 bits.
+ * stands for; scores, the softmax's maximum and sum, and out's sums are held in 32 bits. What is rounded to fp16 on the
+ * way: a query row in units of a power of two of its own (exact above 2^-25 of its largest element); the softmax's
+ * weights before they meet V (11 bits); and, for requests with many rows, V's values (11 bits). So out is off by 2^-11
+ * (2^-10 there) of the weighted sum of V's magnitudes s (q + z) and its own rounding, lse by 2^-19 beside what 32-bit
+ * scores are.
  * New token i of request r (n = q_start[r+1] - q_start[r] of them, already in the cache) is at position
  * p = len[r] - n + i and sees positions j <= p, and j > p - window where window > 0. With tree_dev (window
  * must be 0, max_q <= 64) it sees every position before len - n, and new token m of its request where bit m of

@@ -17,16 +17,17 @@
 // scores. (Where a key has two groups, each has sums of its own, and the two take the place of the two buffers.)
 //
 // Roundings: scores have none but the sums' in 32 bits: x is fp16, each row scaled by a power of two of its own
-// (exact but for elements below 2^-29 of the row's largest), K's integers are exact, and the softmax multiplies a column by its scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's
-// values (q - z) s have up to 15 bits: they are formed as ((q - z) / 2) s, exact but for one rounding to
-// 11 bits, in units of a power of two that follows from the segment's largest scale, so that no scale need be kept a column. The
+// (exact but for elements below 2^-29 of the row's largest), K's integers are exact, and the softmax multiplies a column by its
+// scale. The weights are rounded to fp16, 11 bits, as in the decode kernel. V's values (q - z) s have up to 15 bits: they are formed
+// as ((q - z) / 2) s, exact but for one rounding to 11 bits, in units of a power of two that follows from the segment's largest scale, so that no scale need be kept a column. The
 // softmax's reference m moves only when a weight would pass 2^kLimit, so O is rarely rescaled.
 //
 // Bound by the softmax's chain and by shared memory: a 64-key tile takes 2450 cycles, of which the two row tiles' products need
 // 1024 at the tensor cores' rate and 1500 as issued (64-column products read both operands from shared memory at more than
 // its 128 bytes a cycle), and a softmax thread is busy for 1850. Two threads a row (16 softmax warps that agree on a reference
 // tile by tile) took 3900 a tile: all roles contend for the same issue slots and shared memory. 3 requests of up to 2048 new tokens
-// behind up to 8192 cached ones, 32 query heads, 8 KV heads of 128 (259 GFLOP): 331 us; 8 such requests: 620 us, 786 TFLOP/s.
+// behind up to 8192 cached ones, 32 query heads, 8 KV heads of 128 (259 GFLOP): 337 us a call; 8 such requests:
+// 624 us, 781 TFLOP/s (replayed from a graph over one set of inputs, the cache in L2: 331 and 620).
 //
 // Where there are fewer (row tile pair, head) segments than SMs, each is split over the keys; the softmax warps of the
 // last CTA to arrive join.

@@ -15,8 +15,8 @@
 // mma.m16n8k16 and 8 rows of queries (query heads of a KV head x new tokens) the narrow one: with few rows this is half the
 // tensor work of the usual orientation, and the weights become the second product's operand with one movmatrix per 8 x 8.
 //
-// out = 0 and lse = -inf where a row sees nothing; a masked key's weight is set to 0, so what the cache holds there (a
-// scale that is not a number included) never enters a sum.
+// out = 0 and lse = -inf where a row sees nothing; a masked key's weight is set to 0. What lies past the keys or in a page outside
+// the cache may hold scales that are not numbers: they are replaced before a tile that reaches there is read.
 //
 // Work: the 32-token tiles of all (request, row tile, head) segments form one list, split evenly over the CTAs and
 // again over their warps, whatever the lengths (a segment counts kSwitch tiles more than it has). A warp copies its
@@ -26,11 +26,12 @@
 // same inputs give the same bits.
 //
 // Measured: a longer context costs its bytes at 6.9 TB/s (8 KV heads of 128; a plain copy has 6.7), and a call that gives every SM
-// work 20 us besides: 7 us up to the first tile (lengths, the split, block tables, and then all SMs' rings fill at once, 20 MB),
+// work 15 to 19 us besides: 7 us up to the first tile (lengths, the split, block tables, and then all SMs' rings fill at once, 20 MB),
 // 5 to 8 us after the last (joins, an arrival, joins across CTAs). These are short steps that wait for one another and run once,
 // so that their instructions come from L2 too: going through the join once beforehand, to have them near, cost more than it
-// saved (single 9.3 -> 10.3 us). 64 requests of up to 16384 tokens (571 MB): 97 us; one of 262144 (285 MB): 59 us; one
-// of 333 with 32 heads: 9.4 us; 24 trees of 12 tokens, 48 rows a head of 64: 23 us, half of it the products.
+// saved (single 9.3 -> 10.3 us). 64 requests of up to 16384 tokens (571 MB): 98 us; one of 262144 (285 MB): 60 us; one
+// of 333 with 32 heads: 9.5 us; 24 trees of 12 tokens, 48 rows a head of 64: 23 us, half of it the products; the first of them
+// with a window of 4096 (251 MB): 52 us.
 #pragma once
 
 #include "kv_common.cuh"
@@ -372,7 +373,8 @@ struct Producer {
 
 // A V group of zeros is cached with s = 1, z = 0. The reference follows weight times scale, so that the weight of such a token would
 // push what far smaller values weigh out of fp16's range, for a product that is 0. Before the reference moves for a tile, those
-// of its tokens get s = 2^-24, which says the same, by a token a lane; whether one did.
+// of its tokens get s = 2^-24, which says the same, by a token a lane; whether one did. (Looked at in every tile: 102 us for the
+// batch of 64 requests that takes 98.)
 template <int D, int G>
 __device__ __forceinline__ bool drop_empty_groups(uint8_t* tile, int lane) {
     uint8_t* const sub = tile + (lane >> 4) * (16 * D + 128 * (D / G));

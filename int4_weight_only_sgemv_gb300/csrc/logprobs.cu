@@ -4,9 +4,9 @@
 // The work is one read of the logits. A row is a CTA's, or a cluster's of up to 8 that share it where rows are few or long. A
 // thread goes over its vectors of 16 bytes once, four loads under way, with sums about a reference of its own that follows the
 // largest value only when that is more than kLag above (binary32 has room for far more), and keeps its maximum and where it
-// is. At the end the sums are moved to the row's maximum. An element costs about 8 instructions, and what a warp does once a row
-// about 500, so CTAs are small where rows are many, and six of 256 threads share an SM (four: 106 us, five: 98, six: 94.5 for
-// 4096 rows of 50001 bf16 logits, 65% of the measured HBM rate; the instructions bound it).
+// is. At the end the sums are moved to the row's maximum. An element costs about 10 instructions, and what a warp does once a row
+// about 500 (counted at two vocabularies), so CTAs are small where rows are many, and six of 256 threads share an SM (four: 106 us,
+// five: 98, six: 94.5 for 4096 rows of 50001 bf16 logits, 64% of the measured HBM rate; the instructions bound it).
 //
 // The best tokens: each warp gives the ceil(top / warps)-th of its threads' maxima; the lowest of these is a bound that at least
 // `top` elements reach. The vectors of the threads whose maximum reaches it, spread over all threads, are read again (from L2)
