@@ -328,18 +328,27 @@ def sgemv_beam_traceback(parent, tok, count, seq, status=None, stream=None) -> N
                                      _addr(status), _stream(stream)), "sgemv_beam_traceback")
 
 
-# ---------------------------------------------------------------------------------------------- decode path
+# ---------------------------------------------------------------------------------------------- decode and prompt path
 
 _KV_NAMES = ("SGEMV_F16", "SGEMV_BF16", "SGEMV_F32", "KV_WORKSPACE", "EXPORTED_KV", "KvLayout", "KvQuery",
              "sgemv_kv_layout_query", "sgemv_kv_plan", "sgemv_kv_append", "sgemv_kv_read", "sgemv_kv_attention",
              "sgemv_logprobs", "kv_cache", "kv_workspace", "kv_attention", "logprobs")
 
+_PROMPT_NAMES = ("EXPORTED_PROMPT", "Fp4Layout", "PromptQuery", "sgemv_fp4_layout_query", "sgemv_fp4_quantize", "sgemv_fp4_read",
+                 "sgemv_fp4_product", "sgemv_prompt_attention", "fp4_quantize", "fp4_product", "prompt_attention")
+
 
 def __getattr__(name):
-    """The decode-path operators live in the module `kv`, which needs torch; it is imported on first use."""
+    """The decode-path operators live in the module `kv`, those of the prompt path in `prompt`, which need torch; they are imported on
+    first use."""
     if name in _KV_NAMES:
         from . import kv
         for n in _KV_NAMES:
             globals()[n] = getattr(kv, n)
+        return globals()[name]
+    if name in _PROMPT_NAMES:
+        from . import prompt
+        for n in _PROMPT_NAMES:
+            globals()[n] = getattr(prompt, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
