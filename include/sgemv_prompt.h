@@ -87,8 +87,8 @@ typedef struct {
     int32_t window;             /* 0, or (causal only) each token sees only the last `window` tokens, itself among them */
     float scale;                /* factor of q . k */
     int32_t reserved;
-    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride; /* elements, multiples of 8, those of k and v positive; that */
-    int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride; /* of an axis of length 1 is not used */
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride; /* elements, positive multiples of 8 (below 2^38); that of */
+    int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride; /* an axis of length 1 is not used */
     const void* q_dev;          /* [n_tokens][heads_q][dim] */
     const void* k_dev;          /* [n_tokens][heads][dim] */
     const void* v_dev;

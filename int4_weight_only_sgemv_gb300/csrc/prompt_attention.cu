@@ -1,4 +1,5 @@
 // Causal attention over packed prompts: the entry point (argument checks, tensor maps, launch).
+#include <algorithm>
 #include <climits>
 #include <type_traits>
 
@@ -23,21 +24,23 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// Tiles of 128 tokens of one head, 64 dims of a row at a time, swizzled for the tensor cores. (A stride of an axis of length 1 is not used.)
-bool map_rows(CUtensorMap* map, const void* base, const sgemv_prompt_query& q, int64_t token_stride, int64_t head_stride) {
+// Tiles of `tokens` tokens of `heads` neighbouring heads, 64 dims of a row at a time, swizzled for the tensor cores. (A stride of an axis of
+// length 1 is not used.)
+bool map_rows(CUtensorMap* map, const void* base, const sgemv_prompt_query& q, int all_heads, int64_t token_stride, int64_t head_stride, int tokens,
+              int heads) {
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(q.dim), static_cast<cuuint64_t>(q.heads), static_cast<cuuint64_t>(q.n_tokens)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(q.heads > 1 ? head_stride : q.dim) * 2,
-                                   static_cast<cuuint64_t>(q.n_tokens > 1 ? token_stride : static_cast<int64_t>(q.heads) * q.dim) * 2};
-    const cuuint32_t box[3] = {64, 1, 128}, step[3] = {1, 1, 1};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(q.dim), static_cast<cuuint64_t>(all_heads), static_cast<cuuint64_t>(q.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(all_heads > 1 ? head_stride : q.dim) * 2,
+                                   static_cast<cuuint64_t>(q.n_tokens > 1 ? token_stride : static_cast<int64_t>(all_heads) * q.dim) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)}, step[3] = {1, 1, 1};
     return encode(map, q.dtype == SGEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
                   dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D>
-cudaError_t launch_prompt(const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p, unsigned grid, cudaStream_t s) {
+cudaError_t launch_prompt(const CUtensorMap& qm, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p, unsigned grid, cudaStream_t s) {
     using S = PromptShape<D>;
     auto kern = prompt_kernel<T, D>;
     static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
@@ -48,9 +51,13 @@ cudaError_t launch_prompt(const CUtensorMap& k, const CUtensorMap& v, const Prom
     if (attr_set[dev].load() == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kern);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != S::kRegs) return cudaErrorInvalidKernelImage;  // the roles' split would wait for registers for ever
         attr_set[dev].store(1);
     }
-    return launch_pdl(kern, dim3(grid), dim3(S::kThreads), S::kSmem, s, k, v, p);
+    return launch_pdl(kern, dim3(grid), dim3(S::kThreads), S::kSmem, s, qm, k, v, p);
 }
 
 }  // namespace
@@ -84,12 +91,11 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
         !strides_aligned(q.n_tokens, q.v_token_stride, q.heads, q.v_head_stride))
         return SGEMV_ERR_ALIGN;
     constexpr int64_t kFar = 1ll << 38;  // a tensor map's strides are below 2^40 bytes
-    const int64_t kv_strides[][2] = {{q.n_tokens, q.k_token_stride}, {q.heads, q.k_head_stride}, {q.n_tokens, q.v_token_stride}, {q.heads, q.v_head_stride}};
-    for (const auto& s : kv_strides)
+    const int64_t strides[][2] = {{q.n_tokens, q.q_token_stride}, {q.heads_q, q.q_head_stride}, {q.n_tokens, q.k_token_stride}, {q.heads, q.k_head_stride},
+                                  {q.n_tokens, q.v_token_stride}, {q.heads, q.v_head_stride}, {q.n_tokens, q.out_token_stride},
+                                  {q.heads_q, q.out_head_stride}};
+    for (const auto& s : strides)
         if (s[0] > 1 && (s[1] < 1 || s[1] > kFar)) return SGEMV_ERR_SHAPE;
-    const int64_t q_strides[][2] = {{q.n_tokens, q.q_token_stride}, {q.heads_q, q.q_head_stride}, {q.n_tokens, q.out_token_stride}, {q.heads_q, q.out_head_stride}};
-    for (const auto& s : q_strides)
-        if (s[0] > 1 && (s[1] < -kFar || s[1] > kFar)) return SGEMV_ERR_SHAPE;
     // (rows between others, as those of a fused projection, may be out's: what lies from its first to its last byte is looked at only where
     // nothing else has a place there)
     const uint64_t all = 2ull * q.n_tokens * q.heads_q * q.dim;
@@ -119,16 +125,25 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
     p.status = status_dev;
     p.ratio = q.heads_q / q.heads;
     p.scale_log2 = q.scale * 1.44269504088896340736f;
-    CUtensorMap k_map, v_map;
-    if (!map_rows(&k_map, q.k_dev, q, q.k_token_stride, q.k_head_stride) || !map_rows(&v_map, q.v_dev, q, q.v_token_stride, q.v_head_stride))
-        return SGEMV_ERR_CUDA;
+    p.sub = std::min(p.ratio, 128);
+    while (p.ratio % p.sub != 0) --p.sub;
+    p.tokens = 128 / p.sub;
+    p.groups = q.heads_q / p.sub;
     // at most so many segments: every request's last may be short
-    const int64_t most = (static_cast<int64_t>(q.n_tokens) * p.ratio / PromptShape<128>::kRows + q.n_req) * q.heads;
+    const int64_t most = (static_cast<int64_t>(q.n_tokens) / (2 * p.tokens) + q.n_req) * p.groups;
     if (most > INT_MAX) return SGEMV_ERR_SHAPE;
-    const unsigned grid = static_cast<unsigned>(most);
+    CUtensorMap q_map, k_map, v_map;
+    if (!map_rows(&q_map, q.q_dev, q, q.heads_q, q.q_token_stride, q.q_head_stride, p.tokens, p.sub) ||
+        !map_rows(&k_map, q.k_dev, q, q.heads, q.k_token_stride, q.k_head_stride, 128, 1) ||
+        !map_rows(&v_map, q.v_dev, q, q.heads, q.v_token_stride, q.v_head_stride, 128, 1))
+        return SGEMV_ERR_CUDA;
+    DeviceInfo di;
+    const int rc = device_info(&di);
+    if (rc != SGEMV_OK) return rc;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most, di.sm_count));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = q.dtype == SGEMV_F16;
-    const cudaError_t e = q.dim == 64 ? (half ? launch_prompt<__half, 64>(k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 64>(k_map, v_map, p, grid, s))
-                                      : (half ? launch_prompt<__half, 128>(k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 128>(k_map, v_map, p, grid, s));
+    const cudaError_t e = q.dim == 64 ? (half ? launch_prompt<__half, 64>(q_map, k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 64>(q_map, k_map, v_map, p, grid, s))
+                                      : (half ? launch_prompt<__half, 128>(q_map, k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 128>(q_map, k_map, v_map, p, grid, s));
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }

@@ -2,11 +2,13 @@
 //
 // Bound by the products, 4 D operations a (row, key), where prompts are long. Both go to the 5th-generation tensor cores with 128 x 128 x 16 and 128
 // x D x 16 instructions. A row is a (token, query head) of one KV head, token after token, so that grouped heads share the keys they read and
-// a tile's rows see about the same keys. A CTA has two 128-row tiles against the same 128-key tiles: while one is in its softmax the other's
-// products run. Roles, by warp:
-//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, scores from tensor memory, weights back over them
-//   8, 9      issue the products, a row tile each      10  issues the copies of K and V tiles (two buffers each)
-//   11        looks through V tiles that are masked for some row (below)
+// a tile's rows see about the same keys. A segment is two 128-row tiles against the same 128-key tiles: while one is in its softmax the
+// other's products run. Each SM has one CTA, which goes through segments, the longest first; its roles run ahead of one another from one segment into
+// the next, so that the start of a segment (queries, first keys, first scores) hides under the end of the one before. Roles, by warp:
+//   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, scores from tensor memory, weights back over them; the outputs
+//   8         issues the products
+//   9         finds the segments and issues the copies of their K and V tiles (two buffers each)
+//   10, 11    bring the queries of a row tile each, and look through V tiles that are masked for some row (below)
 // The softmax's reference m moves only when a tile's sum of weights passes 2^15 (and in a row's first tile), so that the largest score is
 // looked for in few tiles and the output's sums are rarely rescaled.
 //
@@ -28,22 +30,31 @@ namespace sgemv {
 struct PromptParams {
     sgemv_prompt_query q;
     int32_t* status;
-    int ratio;
+    int ratio;      // query heads a KV head
+    int sub;        // of them, in a row tile: the largest divisor of ratio up to 128
+    int tokens;     // of a row tile: 128 / sub
+    int groups;     // heads * ratio / sub: KV heads, each as often as it has groups of `sub` query heads
     float scale_log2;
 };
 
 template <int D>
 struct PromptShape {
-    static constexpr int kRows = 256, kTile = 128, kKeys = 128;
+    static constexpr int kTile = 128, kKeys = 128;
     static constexpr int kAtoms = D / 64;  // 128-byte columns of a row
     static constexpr int kBufs = 2;        // of K and of V
+    static constexpr int kSegs = 4;        // segments known ahead
     static constexpr int kQBytes = kTile * D * 2, kKvBytes = kKeys * D * 2;
+    static constexpr int kOutBytes = 32 * 64;  // a warp's staging: 32 dims of 32 rows
     static constexpr int kWarps = 12, kThreads = 32 * kWarps;
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kBufs * kKvBytes;
+    // Registers a thread at launch, and after the split: the softmax's 8 warps, whose rows' 128 scores stay in them, and 4.
+    static constexpr int kRegs = 168, kRegsSoftmax = 200, kRegsOther = 104;
+    static_assert(8 * kRegsSoftmax + 4 * kRegsOther == kWarps * kRegs, "the split of the launch's registers");
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kBufs * kKvBytes + 8 * kOutBytes;
     static constexpr int kCols = 512;  // tensor memory: S of both row tiles (128 columns each), O of both
 };
 
-constexpr float kPromptTop = 6.0f, kPromptBig = 32768.0f;  // log2 of the largest weight when the reference is set; the limit of a tile's sum
+// log2 of the largest weight when the reference is set; the limits of a tile's sum and, as log2, of a weight: 128 of those are that sum
+constexpr float kPromptTop = 6.0f, kPromptBig = 32768.0f, kPromptFar = 8.0f;
 
 // A request's tokens.
 struct PromptSpan {
@@ -58,9 +69,7 @@ __device__ __forceinline__ PromptSpan prompt_span(const PromptParams& p, int r) 
     }
     return {a, n};
 }
-__device__ __forceinline__ int64_t prompt_segments(const PromptParams& p, const PromptSpan& s, int rows) {
-    return static_cast<int64_t>((static_cast<int64_t>(s.n) * p.ratio + rows - 1) / rows) * p.q.heads;
-}
+__device__ __forceinline__ int prompt_blocks(const PromptParams& p, int n) { return (n + 2 * p.tokens - 1) / (2 * p.tokens); }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -78,62 +87,97 @@ __host__ __device__ constexpr uint32_t tc_idesc_type() {
     return std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
 }
 
+// A segment: a request's tokens from t0 on, as many as two row tiles hold, and `sub` query heads of one KV head.
+struct PromptSegment {
+    int first, n;   // the request's tokens; n < 0: no more segments
+    int group, t0;
+};
+// Key tiles [from, to) that row tile x of a segment has; tiles in positions [clear0, clear1) are seen in full by all its rows.
+struct PromptRange {
+    int from, to, clear0, clear1;
+};
+__device__ __forceinline__ PromptRange prompt_range(const PromptParams& p, const PromptSegment& s, int x) {
+    const int ia = s.t0 + p.tokens * x;
+    if (ia >= s.n) return {INT_MAX, 0, INT_MIN, INT_MAX};
+    const int ib = min(ia + p.tokens, s.n) - 1;
+    const int lo = p.q.window > 0 ? max(0, ia - p.q.window + 1) : 0, hi = p.q.causal ? ib + 1 : s.n;
+    return {lo / 128, (hi + 127) / 128, p.q.window > 0 ? max(0, ib - p.q.window + 1) : 0, p.q.causal ? ia + 1 : s.n};
+}
+struct PromptTiles {
+    PromptRange r[2];
+    __device__ __forceinline__ int first() const { return r[0].from; }
+    __device__ __forceinline__ int last() const { return max(r[0].to, r[1].to); }
+    __device__ __forceinline__ bool has(int x, int j) const { return j >= r[x].from && j < r[x].to; }
+    __device__ __forceinline__ bool masked(int j) const {  // for some row that has it
+        const int pos0 = j * 128, pos1 = pos0 + 128;
+        return (has(0, j) && (pos0 < r[0].clear0 || pos1 > r[0].clear1)) || (has(1, j) && (pos0 < r[1].clear0 || pos1 > r[1].clear1));
+    }
+};
+__device__ __forceinline__ PromptTiles prompt_tiles(const PromptParams& p, const PromptSegment& s) {
+    return {{prompt_range(p, s, 0), prompt_range(p, s, 1)}};
+}
 template <typename T, int D>
 __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
-    prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
+    prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
     using S = PromptShape<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* const s_q = smem;
     uint8_t* const s_k = s_q + 2 * S::kQBytes;
     uint8_t* const s_v = s_k + S::kBufs * S::kKvBytes;
+    uint8_t* const s_out = s_v + S::kBufs * S::kKvBytes;
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_ok[S::kBufs], v_free[S::kBufs];
-    __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], seg_full[S::kSegs], seg_free[S::kSegs];
+    __shared__ PromptSegment s_seg[S::kSegs];
+    __shared__ int s_odd[S::kSegs];                                             // a segment's V has elements that are no numbers
+    __shared__ int t_before[S::kThreads], t_blocks[S::kThreads];  // where segments are, below
+    __shared__ PromptSpan t_span[S::kThreads];
     __shared__ uint32_t s_tmem;
     __shared__ int64_t s_sum[S::kWarps];
-    __shared__ int s_req, s_odd;
-    __shared__ int64_t s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 2);
-            mbar_init(&v_full[i], 1), mbar_init(&v_ok[i], 32), mbar_init(&v_free[i], 2);
+            mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 1);
+            mbar_init(&v_full[i], 1), mbar_init(&v_ok[i], 64), mbar_init(&v_free[i], 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
-        mbar_init(&q_full, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1), mbar_init(&q_free[i], 1);
+            mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < S::kSegs; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_free[i], 11);
         mbar_fence_init();
-        s_req = -1, s_odd = 0;
     }
+    if (warp == 8) tc_alloc(&s_tmem, S::kCols);
     pdl_launch_dependents();
     pdl_wait();
 
-    // The request whose segment (two row tiles of a KV head) this CTA has. Thread x has requests [x * run, (x + 1) * run); where that is one
-    // each, they are taken by descending length, so that the longest segments do not come last.
+    // The list of segments. Thread x has requests [x * run, (x + 1) * run). Where that is one each, they are sorted by descending length, and
+    // t_blocks, t_span have their blocks (two row tiles of tokens) and tokens; t_before is where what thread x adds to the list starts:
+    //   causal: by descending block, whose number says how many keys it sees, over all requests that have it: thread x adds the blocks that
+    //           requests 0..x have and x + 1.. have not
+    //   else:   request after request
     const int run = (p.q.n_req + S::kThreads - 1) / S::kThreads;
+    const bool by_block = run == 1 && p.q.causal != 0;
     int64_t mine = 0;
-    int* const t_len = reinterpret_cast<int*>(s_q);  // until the queries come
-    int* const t_order = t_len + S::kThreads;
-    int* const t_count = t_order + S::kThreads;
     if (run == 1) {
-        int count = 0;
-        if (tid < p.q.n_req) {
-            const PromptSpan s = prompt_span(p, tid);
-            count = static_cast<int>(prompt_segments(p, s, S::kRows));
-            t_len[tid] = s.n;
-        }
+        int* const t_len = t_before;
+        PromptSpan s = {0, 0};
+        if (tid < p.q.n_req) s = prompt_span(p, tid), t_len[tid] = s.n;
         __syncthreads();
         if (tid < p.q.n_req) {
-            const int len = t_len[tid];
             int rank = 0;
-            for (int r = 0; r < p.q.n_req; ++r) rank += t_len[r] > len || (t_len[r] == len && r < tid);
-            t_order[rank] = tid;
-            t_count[rank] = count;
+            for (int r = 0; r < p.q.n_req; ++r) rank += t_len[r] > s.n || (t_len[r] == s.n && r < tid);
+            t_span[rank] = s;
+            t_blocks[rank] = prompt_blocks(p, s.n);
         }
         __syncthreads();
-        if (tid < p.q.n_req) mine = t_count[tid];
+        if (tid < p.q.n_req) {
+            const int b = t_blocks[tid], next = tid + 1 < p.q.n_req ? t_blocks[tid + 1] : 0;
+            mine = (by_block ? static_cast<int64_t>(b - next) * (tid + 1) : b) * p.groups;
+        }
     } else {
         for (int64_t r = static_cast<int64_t>(tid) * run; r < min(static_cast<int64_t>(tid + 1) * run, static_cast<int64_t>(p.q.n_req)); ++r)
-            mine += prompt_segments(p, prompt_span(p, static_cast<int>(r)), S::kRows);
+            mine += static_cast<int64_t>(prompt_blocks(p, prompt_span(p, static_cast<int>(r)).n)) * p.groups;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -148,213 +192,220 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
     }
-    if (blockIdx.x >= total) return;
-    const int64_t want = blockIdx.x;
-    if (want >= before && want < before + mine) {
-        int r = run == 1 ? t_order[tid] : tid * run;
-        for (; run > 1; ++r) {
-            const int64_t n = prompt_segments(p, prompt_span(p, r), S::kRows);
-            if (want < before + n) break;
-            before += n;
-        }
-        s_req = r, s_before = before;
-    }
-    if (warp == 8) tc_alloc(&s_tmem, S::kCols);
+    t_before[tid] = static_cast<int>(before);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = s_tmem;
-    const PromptSpan sp = prompt_span(p, s_req);
-    // within a request the last rows, which see the most keys, come first
-    const int in_req = static_cast<int>(want - s_before), rows = sp.n * p.ratio;
-    const int head = in_req % p.q.heads, row0 = ((rows + S::kRows - 1) / S::kRows - 1 - in_req / p.q.heads) * S::kRows;
-    // Keys [lo, hi) that row tile x sees, in tiles [from, to); those with positions in [clear0, clear1) are seen in full by all its rows.
-    struct Range {
-        int from, to, clear0, clear1;
-    };
-    const auto range_of = [&](int x) {
-        const int a = row0 + 128 * x;
-        if (a >= rows) return Range{INT_MAX, 0, INT_MIN, INT_MAX};
-        const int ia = a / p.ratio, ib = min(a + 127, rows - 1) / p.ratio;
-        const int lo = p.q.window > 0 ? max(0, ia - p.q.window + 1) : 0, hi = p.q.causal ? ib + 1 : sp.n;
-        return Range{lo / S::kKeys, (hi + S::kKeys - 1) / S::kKeys, p.q.window > 0 ? max(0, ib - p.q.window + 1) : 0, p.q.causal ? ia + 1 : sp.n};
-    };
-    const Range r0 = range_of(0), r1 = range_of(1);
-    const int first = r0.from, last = max(r0.to, r1.to);  // tiles of the CTA
     bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (dead || mbar_wait(bar, parity)) return;
         dead = true;
         report(p.status, SGEMV_ERR_TIMEOUT);
     };
-    const auto masked = [&](int j) {  // for some row that has it
-        const int pos0 = j * S::kKeys, pos1 = pos0 + S::kKeys;
-        return (j >= r0.from && j < r0.to && (pos0 < r0.clear0 || pos1 > r0.clear1)) ||
-               (j >= r1.from && j < r1.to && (pos0 < r1.clear0 || pos1 > r1.clear1));
+    // Segment `it` of this CTA, by a whole warp; n < 0 where there is none (or a wait gave up).
+    const auto segment = [&](int it) {
+        wait(&seg_full[it % S::kSegs], (it / S::kSegs) & 1);
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        PromptSegment s = s_seg[it % S::kSegs];
+        if (dead) s.n = -1;
+        return s;
+    };
+    const auto release = [&](int it) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_free[it % S::kSegs]);
     };
 
     if (warp < 8) {
+        regs_inc<S::kRegsSoftmax>();
         // ---------------------------------------------------------------------------------------- softmax
-        const int x = warp >> 2, r = tid & 127, row = row0 + 128 * x + r;
-        const bool live = row < rows;
-        const Range rg = x == 0 ? r0 : r1;
+        const int x = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
-        const int i = min(row, rows - 1) / p.ratio, a = head * p.ratio + min(row, rows - 1) % p.ratio;
-        {
-            const T* const src = static_cast<const T*>(p.q.q_dev) + (sp.first + i) * p.q.q_token_stride + a * p.q.q_head_stride;
-            uint8_t* const dst = s_q + x * S::kQBytes + r * 128;
-#pragma unroll
-            for (int d = 0; d < D; d += 8) {
-                const uint4 w = live ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(dst + d / 64 * (128 * 128) + (((d / 8) & 7) ^ (r & 7)) * 16) = w;
-            }
-            fence_async();
-            mbar_arrive(&q_full);
-        }
-        // this row sees positions [see0, see0 + see)
-        const int see0 = p.q.window > 0 ? max(0, i - p.q.window + 1) : 0;
-        const uint32_t see = static_cast<uint32_t>((p.q.causal ? i + 1 : sp.n) - see0);
         const float c = p.scale_log2;
-        float ref = 0.0f;   // the reference
-        bool seen = false;  // whether it was set
-        uint64_t l2 = 0;    // two sums
-        for (int j = rg.from; j < rg.to; ++j) {
-            const int pos0 = j * S::kKeys;
-            wait(&s_full[x], (j - rg.from) & 1);  // (and all products issued before: O holds every tile before this one)
-            __syncwarp();
-            tc_after_sync();
-            const bool plain = pos0 >= rg.clear0 && pos0 + S::kKeys <= rg.clear1;
-            uint32_t w[64];
-            uint64_t sum;
-            // The weights of 32 keys. Past 2^26, scores are rounded before the reference comes off, so that the largest has a weight of about
-            // 2^kPromptTop; else one rounding for both.
-            const auto weights = [&](const uint32_t (&raw)[32], int q, bool select) {
-                if (!select) {
+        uint32_t tiles = 0, segs = 0;  // that this row tile has had
+        for (int it = 0;; ++it) {
+            const PromptSegment sg = segment(it);
+            if (sg.n < 0) break;
+            const PromptTiles all = prompt_tiles(p, sg);
+            const PromptRange rg = x == 0 ? all.r[0] : all.r[1];
+            if (rg.from >= rg.to) {
+                release(it);
+                continue;
+            }
+            // this thread's token and query head (rows that there are not: as the last token's)
+            const int i0 = sg.t0 + p.tokens * x, i = min(i0 + r / p.sub, min(i0 + p.tokens, sg.n) - 1), a = sg.group * p.sub + r % p.sub;
+            const bool live = i == i0 + r / p.sub;
+            // this row sees positions [see0, see0 + see)
+            const int see0 = p.q.window > 0 ? max(0, i - p.q.window + 1) : 0;
+            const uint32_t see = static_cast<uint32_t>((p.q.causal ? i + 1 : sg.n) - see0);
+            float ref = 0.0f;   // the reference
+            bool seen = false;  // whether it was set
+            uint64_t l2 = 0;    // two sums
+            for (int j = rg.from; j < rg.to; ++j, ++tiles) {
+                const int pos0 = j * S::kKeys;
+                wait(&s_full[x], tiles & 1);  // (and all products issued before: O holds every tile before this one)
+                __syncwarp();
+                tc_after_sync();
+                const bool plain = pos0 >= rg.clear0 && pos0 + S::kKeys <= rg.clear1;
+                // Seen in full, and the row has its reference: weights in one go. Whether the reference has to move shows in their sum, so that
+                // the largest score is looked for in few tiles. (Past 2^26 scores are rounded before the reference comes off: slow, below.)
+                bool done = false;
+                if (plain && __all_sync(0xFFFFFFFFu, seen && fabsf(ref) < 67108864.0f)) {
+                    uint32_t raw[4][32], w[64];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_ld32(raw[q], ts + 32 * q);
+                    tc_wait_ld();
+                    uint64_t sums[4] = {0, 0, 0, 0};
                     const uint64_t cc = pair(c, c), mm = pair(-ref, -ref);
 #pragma unroll
-                    for (int n = 0; n < 32; n += 2) {
-                        const float2 t = parts_of(fma2(pair(__uint_as_float(raw[n]), __uint_as_float(raw[n + 1])), cc, mm));
+                    for (int n = 0; n < 128; n += 2) {
+                        const float2 t = parts_of(fma2(pair(__uint_as_float(raw[n / 32][n % 32]), __uint_as_float(raw[n / 32][n % 32 + 1])), cc, mm));
                         const float e0 = exp2_approx(t.x), e1 = exp2_approx(t.y);
-                        sum = add2(sum, pair(e0, e1));
-                        w[16 * q + n / 2] = pack_two<T>(e0, e1);
+                        sums[n / 2 % 4] = add2(sums[n / 2 % 4], pair(e0, e1));
+                        w[n / 2] = pack_two<T>(e0, e1);
                     }
-                } else {
-                    const uint32_t at = static_cast<uint32_t>(pos0 + 32 * q - see0);
-#pragma unroll
-                    for (int n = 0; n < 32; n += 2) {
-                        const float t0 = __fadd_rn(__fmul_rn(__uint_as_float(raw[n]), c), -ref), t1 = __fadd_rn(__fmul_rn(__uint_as_float(raw[n + 1]), c), -ref);
-                        const float e0 = at + n < see ? exp2_approx(t0) : 0.0f, e1 = at + n + 1 < see ? exp2_approx(t1) : 0.0f;
-                        sum = add2(sum, pair(e0, e1));
-                        w[16 * q + n / 2] = pack_two<T>(e0, e1);
+                    sums[0] = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                    const float2 both = parts_of(sums[0]);
+                    done = !__any_sync(0xFFFFFFFFu, both.x + both.y > kPromptBig);
+                    if (done) {
+                        l2 = add2(l2, sums[0]);
+                        tc_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(w));
+                        tc_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(w + 32));
                     }
                 }
-            };
-            bool need = !seen;
-            for (int pass = 0;; ++pass) {
-                if (__any_sync(0xFFFFFFFFu, need)) {
-                    // the largest score that this row sees
-                    float top = -INFINITY;
-#pragma unroll
+                if (!done) {
+                    // 32 keys at a time, in little code: the largest score that each row sees, then the weights. (Those of 32 keys take the
+                    // columns of 16: they never reach scores that are still to be read.)
+                    const int rel0 = see0 - pos0, rel1 = rel0 + static_cast<int>(see);
+                    const auto seen_bits = [&](int q) {  // of keys 32 q .. 32 q + 31
+                        const int lo = min(32, max(0, rel0 - 32 * q)), hi = min(32, max(0, rel1 - 32 * q));
+                        return static_cast<uint32_t>((1ull << hi) - 1) & ~static_cast<uint32_t>((1ull << lo) - 1);
+                    };
+                    float most = -INFINITY;
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t raw[32];
                         tc_ld32(raw, ts + 32 * q);
                         tc_wait_ld();
-                        const uint32_t at = static_cast<uint32_t>(pos0 + 32 * q - see0);
+                        const uint32_t bits = seen_bits(q);
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            if (at + n < see) top = fmaxf(top, __fmul_rn(__uint_as_float(raw[n]), c));
+                        for (int n = 0; n < 32; ++n) top[n & 3] = fmaxf(top[n & 3], (bits >> n) & 1 ? __fmul_rn(__uint_as_float(raw[n]), c) : -INFINITY);
+                        most = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
                     }
                     float f = 1.0f;
-                    if (need && top > -INFINITY) {
-                        const float m = top - kPromptTop;
+                    if (most > -INFINITY && (!seen || most - ref > kPromptFar)) {
+                        const float m = most - kPromptTop;
                         if (seen) f = exp2_approx(ref - m);
                         ref = m;
                         seen = true;
                     }
-                    l2 = mul2(l2, pair(f, f));
-                    if (j > rg.from && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                    if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                        l2 = mul2(l2, pair(f, f));
+                        if (j > rg.from) {
 #pragma unroll 1
-                        for (int d = 0; d < D / 16; ++d) {
-                            uint32_t o[16];
-                            tc_ld16(o, to + 16 * d);
-                            tc_wait_ld();
+                            for (int d = 0; d < D / 16; ++d) {
+                                uint32_t o[16];
+                                tc_ld16(o, to + 16 * d);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
-                            tc_st16(to + 16 * d, o);
+                                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                                tc_st16(to + 16 * d, o);
+                            }
                         }
                     }
-                }
-                sum = 0;
-                const bool select = !plain || __any_sync(0xFFFFFFFFu, fabsf(ref) > 67108864.0f);
-                uint32_t raw[2][32];
-                tc_ld32(raw[0], ts);
-                tc_wait_ld();
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t raw[32], w[16];
+                        tc_ld32(raw, ts + 32 * q);
+                        tc_wait_ld();
+                        const uint32_t bits = seen_bits(q);
+                        uint64_t sums[2] = {0, 0};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q < 3) tc_ld32(raw[(q + 1) & 1], ts + 32 * (q + 1));
-                    weights(raw[q & 1], q, select);
-                    if (q < 3) tc_wait_ld();
+                        for (int n = 0; n < 32; n += 2) {
+                            const float t0 = __fadd_rn(__fmul_rn(__uint_as_float(raw[n]), c), -ref), t1 = __fadd_rn(__fmul_rn(__uint_as_float(raw[n + 1]), c), -ref);
+                            const float e0 = exp2_approx((bits >> n) & 1 ? t0 : -INFINITY), e1 = exp2_approx((bits >> (n + 1)) & 1 ? t1 : -INFINITY);
+                            sums[n / 2 % 2] = add2(sums[n / 2 % 2], pair(e0, e1));
+                            w[n / 2] = pack_two<T>(e0, e1);
+                        }
+                        l2 = add2(l2, add2(sums[0], sums[1]));
+                        tc_st16(ts + 16 * q, w);
+                    }
                 }
-                const float2 both = parts_of(sum);
-                need = both.x + both.y > kPromptBig;  // (not after the reference has moved)
-                if (pass == 2 || !__any_sync(0xFFFFFFFFu, need)) break;
+                tc_wait_st();
+                tc_before_sync();
+                mbar_arrive(&p_full[x]);
             }
-            l2 = add2(l2, sum);
-            tc_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(w));
-            tc_st32(ts + 32, *reinterpret_cast<const uint32_t(*)[32]>(w + 32));
-            tc_wait_st();
-            tc_before_sync();
-            mbar_arrive(&p_full[x]);
-        }
-        if (rg.from < rg.to) {
-            wait(&o_full[x], 0);
-            __syncwarp();
-            tc_after_sync();
             const float2 lf = parts_of(l2);
             const float l = lf.x + lf.y;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            T* const out = static_cast<T*>(p.q.out_dev) + (sp.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
-            const bool odd = *static_cast<volatile int*>(&s_odd) != 0;
+            if (live && p.q.lse_dev != nullptr)
+                p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            wait(&o_full[x], segs & 1);
+            ++segs;
+            __syncwarp();
+            tc_after_sync();
+            const bool odd = *static_cast<volatile int*>(&s_odd[it % S::kSegs]) != 0;
+            // 32 dims at a time through shared memory, so that 4 lanes write 64 bytes of a row
+            uint8_t* const stage = s_out + warp * S::kOutBytes;
+            T* out[4];
 #pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int rr = 32 * (warp & 3) + 8 * n + (lane >> 2), token = i0 + rr / p.sub;
+                out[n] = rr < p.tokens * p.sub && token < sg.n
+                             ? static_cast<T*>(p.q.out_dev) + (sg.first + token) * p.q.out_token_stride +
+                                   (sg.group * p.sub + rr % p.sub) * p.q.out_head_stride + 8 * (lane & 3)
+                             : nullptr;
+            }
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tc_ld32(o, to + 32 * q);
                 tc_wait_ld();
-                if (!live) continue;
-                if (odd) {
-                    // what was taken out of V, for the rows that see it
-                    for (int j = rg.from; j < rg.to; ++j) {
-                        if (!masked(j)) continue;
-                        for (int pos = max(see0, j * S::kKeys); pos < min(see0 + static_cast<int>(see), (j + 1) * S::kKeys); ++pos) {
-                            const T* const v = static_cast<const T*>(p.q.v_dev) + (sp.first + pos) * p.q.v_token_stride + head * p.q.v_head_stride + 32 * q;
 #pragma unroll
-                            for (int n = 0; n < 32; ++n) {
-                                const float f = to_f32(v[n]);
-                                if (!(fabsf(f) < INFINITY)) o[n] = __float_as_uint(__uint_as_float(o[n]) + f);
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < 32; n += 8) {
+                for (int n = 0; n < 4; ++n) {
                     uint32_t h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        h[e] = pack_two<T>(__uint_as_float(o[n + 2 * e]) * inv, __uint_as_float(o[n + 2 * e + 1]) * inv);
-                    *reinterpret_cast<uint4*>(out + 32 * q + n) = make_uint4(h[0], h[1], h[2], h[3]);
+                        h[e] = pack_two<T>(__uint_as_float(o[8 * n + 2 * e]) * inv, __uint_as_float(o[8 * n + 2 * e + 1]) * inv);
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((n ^ (lane >> 1)) & 3) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int rr = 8 * n + (lane >> 2);
+                    const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+                    if (out[n] != nullptr) *reinterpret_cast<uint4*>(out[n] + 32 * q) = h;
+                }
+                __syncwarp();
+            }
+            if (odd && live) {
+                // what was taken out of V, for the rows that see it
+                T* const mine = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
+                const T* const v_rows = static_cast<const T*>(p.q.v_dev) + sg.group * p.sub / p.ratio * p.q.v_head_stride;
+#pragma unroll 1
+                for (int pos = max(see0, rg.from * S::kKeys); pos < see0 + static_cast<int>(see); ++pos) {
+                    if (!all.masked(pos / S::kKeys)) continue;
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d) {
+                        const float f = to_f32(v_rows[(sg.first + pos) * p.q.v_token_stride + d]);
+                        if (!(fabsf(f) < INFINITY)) mine[d] = from_f32<T>(to_f32(mine[d]) + f);
+                    }
                 }
             }
-            if (live && p.q.lse_dev != nullptr)
-                p.q.lse_dev[static_cast<int64_t>(sp.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            tc_before_sync();  // (the next segment's first weights, which these threads hand over, come after this O)
+            release(it);
         }
-    } else if (warp < 10) {
+    } else {
+        regs_dec<S::kRegsOther>();
+        if (warp == 8) {
         // ---------------------------------------------------------------------------------------- products
-        // A warp a row tile. The whole warp goes through the loop, with values that are the same in its lanes; one lane issues.
-        const int x = warp - 8;
-        const int from = x == 0 ? r0.from : r1.from, end = x == 0 ? r0.to : r1.to;
-        const uint32_t ts = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128 * x, to = ts + 256;
-        const uint64_t q_desc = tc_desc(smem_addr(s_q) + x * S::kQBytes), k_desc = tc_desc(smem_addr(s_k));
+        // The whole warp goes through the loop, with values that are the same in its lanes; one lane issues. A row tile's products of a key tile,
+        // O += P V and the next scores (of the next segment, at the end of one), are issued together, so that the two row tiles stay half a
+        // period apart: with a warp for each, both were in their softmax and then both in their products (3740 cycles a key tile against 3225).
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t q_desc = tc_desc(smem_addr(s_q)), k_desc = tc_desc(smem_addr(s_k));
         const uint64_t v_desc = tc_desc_v(smem_addr(s_v), S::kKeys * 128);
         constexpr uint32_t kScores = tc_idesc(S::kKeys) | tc_idesc_type<T>(), kOut = tc_idesc(D) | tc_idesc_type<T>() | (1u << 16);
         const auto hold = [&](uint64_t* bar, uint32_t parity) {
@@ -362,111 +413,207 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             dead = __any_sync(0xFFFFFFFFu, dead);
             tc_after_sync();
         };
-        const auto scores = [&](int j) {
-            const int at = j - first, buf = at % S::kBufs;
-            hold(&k_full[buf], (at / S::kBufs) & 1);
+        const auto last_user = [](const PromptTiles& t, int x, int j) { return x == 1 || !t.has(1, j); };  // of a key tile's buffers
+        uint32_t q_had[2] = {0, 0}, p_had[2] = {0, 0};
+        int g = 0;  // key tiles so far
+        const auto scores = [&](const PromptTiles& t, int x, int j, int gk) {
+            const int buf = gk % S::kBufs;
+            if (j == t.r[x].from) hold(&q_full[x], q_had[x]++ & 1);
+            hold(&k_full[buf], (gk / S::kBufs) & 1);
             if (elect_one()) {
-                const uint64_t kd = k_desc + buf * (S::kKvBytes >> 4);
+                const uint64_t kd = k_desc + buf * (S::kKvBytes >> 4), qd = q_desc + x * (S::kQBytes >> 4);
                 if (!dead) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk / 4 * (128 * 128) + kk % 4 * 32) >> 4;
-                        tc_mma_ss(ts, q_desc + off, kd + off, kScores, kk > 0);
+                        tc_mma_ss(tm + 128 * x, qd + off, kd + off, kScores, kk > 0);
                     }
                 }
                 tc_commit(&s_full[x]);
-                tc_commit(&k_free[buf]);
+                if (last_user(t, x, j)) tc_commit(&k_free[buf]);
+                if (j == t.r[x].to - 1) tc_commit(&q_free[x]);
             }
             __syncwarp();
         };
-        const auto pass_by = [&](int j) {  // a tile of the other row tile only
-            const int at = j - first, buf = at % S::kBufs;
-            hold(&k_full[buf], (at / S::kBufs) & 1);
-            if (lane == 0) mbar_arrive(&k_free[buf]);
-            hold(&v_ok[buf], (at / S::kBufs) & 1);
-            if (lane == 0) mbar_arrive(&v_free[buf]);
-            __syncwarp();
-        };
-        hold(&q_full, 0);
-        for (int j = first; j < min(from, last); ++j) pass_by(j);
-        if (from < end) scores(from);
-        for (int j = from; j < end; ++j) {
-            const int at = j - first, buf = at % S::kBufs;
-            hold(&v_ok[buf], (at / S::kBufs) & 1);
-            hold(&p_full[x], (j - from) & 1);
-            if (elect_one()) {
-                const uint64_t vd = v_desc + buf * (S::kKvBytes >> 4);
-                if (!dead) {
+        PromptSegment sg = segment(0);
+        PromptTiles t = prompt_tiles(p, sg);
+        if (sg.n >= 0) {
 #pragma unroll
-                    for (int kk = 0; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, ts + 8 * kk, vd + kk * (2048 >> 4), kOut, j > from || kk > 0);
+            for (int x = 0; x < 2; ++x)
+                if (t.has(x, t.first())) scores(t, x, t.first(), 0);
+        }
+        for (int it = 0; sg.n >= 0; ++it) {
+            const int first = t.first(), last = t.last();
+            PromptSegment next_sg;
+            PromptTiles next = t;
+            for (int j = first; j < last; ++j, ++g) {
+                if (j == last - 1) {
+                    next_sg = segment(it + 1);
+                    next = prompt_tiles(p, next_sg);
                 }
-                tc_commit(&v_free[buf]);
-                if (j == end - 1) tc_commit(&o_full[x]);
+                const int buf = g % S::kBufs;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (t.has(x, j)) {
+                        hold(&v_ok[buf], (g / S::kBufs) & 1);
+                        hold(&p_full[x], p_had[x]++ & 1);
+                        if (elect_one()) {
+                            const uint64_t vd = v_desc + buf * (S::kKvBytes >> 4);
+                            if (!dead) {
+#pragma unroll
+                                for (int kk = 0; kk < S::kKeys / 16; ++kk)
+                                    tc_mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * kk, vd + kk * (2048 >> 4), kOut, j > t.r[x].from || kk > 0);
+                            }
+                            if (last_user(t, x, j)) tc_commit(&v_free[buf]);
+                            if (j == t.r[x].to - 1) tc_commit(&o_full[x]);
+                        }
+                        __syncwarp();
+                    }
+                    // (over the weights just used: the products run in the order of their issue)
+                    if (j + 1 < last) {
+                        if (t.has(x, j + 1)) scores(t, x, j + 1, g + 1);
+                    } else if (next_sg.n >= 0 && next.has(x, next.first())) {
+                        scores(next, x, next.first(), g + 1);
+                    }
+                }
+            }
+            release(it);
+            sg = next_sg;
+            t = next;
+        }
+        // The last products arrive at barriers that nobody else waits for: none may be under way when the CTA's memory goes.
+        for (int i = max(0, g - S::kBufs); i < g; ++i) {
+            mbar_wait(&k_free[i % S::kBufs], (i / S::kBufs) & 1);
+            mbar_wait(&v_free[i % S::kBufs], (i / S::kBufs) & 1);
+        }
+        } else if (warp == 9) {
+        // ---------------------------------------------------------------------------------------- segments and copies
+        int g = 0;
+        for (int it = 0;; ++it) {
+            if (it >= S::kSegs) wait(&seg_free[it % S::kSegs], (it / S::kSegs - 1) & 1);
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            // Every other round of the list is dealt backwards, so that who has the longest of one has the shortest of the next.
+            const int64_t want = static_cast<int64_t>(it) * gridDim.x + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            PromptSegment sg = {0, -1, 0, 0};
+            if (want < total && !dead) {
+                int x = -1;  // the last thread that starts at or before `want`
+                for (int i = lane; i < min(p.q.n_req, S::kThreads); i += 32)
+                    if (t_before[i] <= want) x = i;
+                x = __reduce_max_sync(0xFFFFFFFFu, x);
+                unsigned o = static_cast<unsigned>(want) - t_before[x];
+                const unsigned groups = p.groups;
+                PromptSpan s;
+                unsigned block;
+                if (run == 1) {
+                    const unsigned width = by_block ? (x + 1) * groups : groups;
+                    block = t_blocks[x] - 1 - o / width;
+                    o %= width;
+                    s = t_span[by_block ? o / groups : x];
+                } else {
+                    for (int req = x * run;; ++req) {
+                        s = prompt_span(p, req);
+                        const unsigned n = prompt_blocks(p, s.n) * groups;
+                        if (o < n) {
+                            block = n / groups - 1 - o / groups;
+                            break;
+                        }
+                        o -= n;
+                    }
+                }
+                sg = {s.first, s.n, static_cast<int>(o % groups), static_cast<int>(block) * 2 * p.tokens};
+            }
+            if (lane == 0) {
+                s_seg[it % S::kSegs] = sg;
+                s_odd[it % S::kSegs] = 0;
+                mbar_arrive(&seg_full[it % S::kSegs]);
             }
             __syncwarp();
-            if (j + 1 < end) scores(j + 1);  // over the weights just used: the products run in the order of their issue
-        }
-        for (int j = max(end, min(from, last)); j < last; ++j) pass_by(j);
-        // The last products arrive at barriers that nobody else waits for: none may be under way when the CTA's memory goes.
-        for (int at = max(0, last - first - S::kBufs); at < last - first; ++at) {
-            mbar_wait(&k_free[at % S::kBufs], (at / S::kBufs) & 1);
-            mbar_wait(&v_free[at % S::kBufs], (at / S::kBufs) & 1);
-        }
-    } else if (warp == 10) {
-        // ---------------------------------------------------------------------------------------- copies
-        if (lane == 0) {
-            int at = 0;
-            for (; at < last - first; ++at) {
-                const int buf = at % S::kBufs, key = sp.first + (first + at) * S::kKeys;
+            if (sg.n < 0) break;
+            const PromptTiles t = prompt_tiles(p, sg);
+            const int head = sg.group * p.sub / p.ratio;
+            for (int j = t.first(); j < t.last() && !dead; ++j, ++g) {
+                const int buf = g % S::kBufs, key = sg.first + j * S::kKeys;
+#pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     uint64_t* const bar = v ? &v_full[buf] : &k_full[buf];
-                    if (at >= S::kBufs) wait(v ? &v_free[buf] : &k_free[buf], (at / S::kBufs - 1) & 1);
-                    if (dead) break;
-                    mbar_arrive_expect_tx(bar, S::kKvBytes);
-                    uint8_t* const dst = (v ? s_v : s_k) + buf * S::kKvBytes;
+                    if (g >= S::kBufs) wait(v ? &v_free[buf] : &k_free[buf], (g / S::kBufs - 1) & 1);
+                    dead = __any_sync(0xFFFFFFFFu, dead);
+                    if (dead) {  // (what was asked for is waited for below)
+                        if (v) mbar_wait(&k_full[buf], (g / S::kBufs) & 1);
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, S::kKvBytes);
+                        uint8_t* const dst = (v ? s_v : s_k) + buf * S::kKvBytes;
 #pragma unroll
-                    for (int d = 0; d < S::kAtoms; ++d) tma_load(dst + d * (S::kKeys * 128), v ? &v_map : &k_map, 64 * d, head, key, bar);
+                        for (int d = 0; d < S::kAtoms; ++d) tma_load(dst + d * (S::kKeys * 128), v ? &v_map : &k_map, 64 * d, head, key, bar);
+                    }
+                    __syncwarp();
                 }
                 if (dead) break;
             }
-            for (int i = max(0, at - S::kBufs); i < min(at + 1, last - first); ++i) {  // (all have landed, unless someone gave up)
-                mbar_wait(&k_full[i % S::kBufs], (i / S::kBufs) & 1);
-                if (i < at) mbar_wait(&v_full[i % S::kBufs], (i / S::kBufs) & 1);
-            }
         }
-        __syncwarp();
-    } else {
-        // ---------------------------------------------------------------------------------------- V that is not seen
-        for (int at = 0; at < last - first; ++at) {
-            const int buf = at % S::kBufs, j = first + at;
-            wait(&v_full[buf], (at / S::kBufs) & 1);
-            __syncwarp();
-            if (masked(j)) {
-                uint8_t* const tile = s_v + buf * S::kKvBytes;
-                const int keys = sp.n - j * S::kKeys;  // of the request
-                constexpr uint32_t kNot = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
-                bool odd = false;
-#pragma unroll 4
-                for (int n = lane; n < S::kKvBytes / 16; n += 32) {
-                    uint4* const at16 = reinterpret_cast<uint4*>(tile) + n;
-                    uint4 w = *at16;
-                    if (n / 8 % S::kKeys >= keys) {
-                        *at16 = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    const uint32_t bx = __vcmpeq2(w.x & kNot, kNot), by = __vcmpeq2(w.y & kNot, kNot), bz = __vcmpeq2(w.z & kNot, kNot),
-                                   bw = __vcmpeq2(w.w & kNot, kNot);
-                    if (bx | by | bz | bw) {
-                        w.x &= ~bx, w.y &= ~by, w.z &= ~bz, w.w &= ~bw;
-                        *at16 = w;
-                        odd = true;
-                    }
+        // (all have landed, unless someone gave up)
+        for (int i = max(0, g - S::kBufs); i < g; ++i) {
+            mbar_wait(&k_full[i % S::kBufs], (i / S::kBufs) & 1);
+            mbar_wait(&v_full[i % S::kBufs], (i / S::kBufs) & 1);
+        }
+        } else {
+        // ---------------------------------------------------------------------------------------- queries; V that is not seen
+        const int x = warp - 10;
+        uint32_t had = 0;
+        int g = 0;
+        for (int it = 0;; ++it) {
+            const PromptSegment sg = segment(it);
+            if (sg.n < 0) break;
+            const PromptTiles t = prompt_tiles(p, sg);
+            if ((x == 0 ? t.r[0] : t.r[1]).to > 0) {
+                if (had > 0) wait(&q_free[x], (had - 1) & 1);
+                ++had;
+                __syncwarp();
+                if (lane == 0 && !dead) {
+                    mbar_arrive_expect_tx(&q_full[x], p.tokens * p.sub * D * 2);
+#pragma unroll
+                    for (int d = 0; d < S::kAtoms; ++d)
+                        tma_load(s_q + x * S::kQBytes + d * (128 * 128), &q_map, 64 * d, sg.group * p.sub, sg.first + sg.t0 + p.tokens * x, &q_full[x]);
                 }
-                if (odd) *static_cast<volatile int*>(&s_odd) = 1;
-                __threadfence_block();
-                fence_async();
+                __syncwarp();
             }
-            mbar_arrive(&v_ok[buf]);
+            const int last = t.last();
+            for (int j = t.first(); j < last; ++j, ++g) {
+                const int buf = g % S::kBufs;
+                wait(&v_full[buf], (g / S::kBufs) & 1);
+                __syncwarp();
+                if (t.masked(j)) {
+                    uint8_t* const tile = s_v + buf * S::kKvBytes;
+                    const int keys = sg.n - j * S::kKeys;  // of the request
+                    constexpr uint32_t kNot = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+                    bool odd = false;
+#pragma unroll 4
+                    for (int n = tid - 320; n < S::kKvBytes / 16; n += 64) {
+                        uint4* const at16 = reinterpret_cast<uint4*>(tile) + n;
+                        uint4 w = *at16;
+                        if (n / 8 % S::kKeys >= keys) {
+                            *at16 = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint32_t bx = __vcmpeq2(w.x & kNot, kNot), by = __vcmpeq2(w.y & kNot, kNot), bz = __vcmpeq2(w.z & kNot, kNot),
+                                       bw = __vcmpeq2(w.w & kNot, kNot);
+                        if (bx | by | bz | bw) {
+                            w.x &= ~bx, w.y &= ~by, w.z &= ~bz, w.w &= ~bw;
+                            *at16 = w;
+                            odd = true;
+                        }
+                    }
+                    if (odd) *static_cast<volatile int*>(&s_odd[it % S::kSegs]) = 1;
+                    __threadfence_block();
+                    fence_async();
+                }
+                mbar_arrive(&v_ok[buf]);
+            }
+            release(it);
+        }
+        if (had > 0 && !dead) mbar_wait(&q_full[x], (had - 1) & 1);  // (landed, unless someone gave up)
         }
     }
     __syncwarp();

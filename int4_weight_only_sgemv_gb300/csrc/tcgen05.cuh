@@ -51,6 +51,9 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
                  SGEMV_I8(r, 0), SGEMV_I8(r, 8), SGEMV_I8(r, 16), SGEMV_I8(r, 24)
                  : "memory");
 }
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), SGEMV_I8(r, 0) : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
                  SGEMV_I8(r, 0), SGEMV_I8(r, 8)

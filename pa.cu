@@ -1,0 +1,136 @@
+// Causal attention over packed prompts: the entry point (argument checks, tensor maps, launch).
+#include <climits>
+#include <type_traits>
+
+#include "prompt_attention.cuh"
+
+namespace sgemv {
+
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Tiles of 128 tokens of one head, 64 dims of a row at a time, swizzled for the tensor cores. (A stride of an axis of length 1 is not used.)
+bool map_rows(CUtensorMap* map, const void* base, const sgemv_prompt_query& q, int64_t token_stride, int64_t head_stride) {
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(q.dim), static_cast<cuuint64_t>(q.heads), static_cast<cuuint64_t>(q.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(q.heads > 1 ? head_stride : q.dim) * 2,
+                                   static_cast<cuuint64_t>(q.n_tokens > 1 ? token_stride : static_cast<int64_t>(q.heads) * q.dim) * 2};
+    const cuuint32_t box[3] = {64, 1, 128}, step[3] = {1, 1, 1};
+    return encode(map, q.dtype == SGEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_prompt(const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p, unsigned grid, cudaStream_t s) {
+    using S = PromptShape<D>;
+    auto kern = prompt_kernel<T, D>;
+    static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (attr_set[dev].load() == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(1);
+    }
+    return launch_pdl(kern, dim3(grid), dim3(S::kThreads), S::kSmem, s, k, v, p);
+}
+
+}  // namespace
+
+}  // namespace sgemv
+
+using namespace sgemv;
+
+extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* status_dev, void* stream) {
+    if (query == nullptr) return SGEMV_ERR_ARG;
+    const sgemv_prompt_query& q = *query;
+    if ((q.dtype != SGEMV_F16 && q.dtype != SGEMV_BF16) || q.n_req < 0 || q.n_tokens < 0 || q.window < 0 || (q.causal != 0 && q.causal != 1) ||
+        (q.window > 0 && q.causal == 0) || !(q.scale == q.scale))
+        return SGEMV_ERR_ARG;
+    if (q.dim != 64 && q.dim != 128) return SGEMV_ERR_SHAPE;
+    if (q.heads < 1 || q.heads_q < q.heads || q.heads_q % q.heads != 0 || q.heads_q > 16384) return SGEMV_ERR_SHAPE;
+    if (static_cast<int64_t>(q.n_tokens) * q.heads_q > (1 << 30) || q.n_req > (1 << 30)) return SGEMV_ERR_SHAPE;
+    if (q.n_req == 0 || q.n_tokens == 0) return SGEMV_OK;
+    const void* must[] = {q.q_dev, q.k_dev, q.v_dev, q.start_dev, q.out_dev};
+    for (const void* x : must)
+        if (x == nullptr) return SGEMV_ERR_ARG;
+    const void* lines[] = {q.q_dev, q.k_dev, q.v_dev, q.out_dev};
+    for (const void* x : lines)
+        if (!is_aligned(x, 16)) return SGEMV_ERR_ALIGN;
+    const void* words[] = {q.start_dev, q.length_dev, q.lse_dev, status_dev};
+    for (const void* x : words)
+        if (!is_aligned(x, 4)) return SGEMV_ERR_ALIGN;
+    if (!strides_aligned(q.n_tokens, q.q_token_stride, q.heads_q, q.q_head_stride) ||
+        !strides_aligned(q.n_tokens, q.out_token_stride, q.heads_q, q.out_head_stride) ||
+        !strides_aligned(q.n_tokens, q.k_token_stride, q.heads, q.k_head_stride) ||
+        !strides_aligned(q.n_tokens, q.v_token_stride, q.heads, q.v_head_stride))
+        return SGEMV_ERR_ALIGN;
+    constexpr int64_t kFar = 1ll << 38;  // a tensor map's strides are below 2^40 bytes
+    const int64_t kv_strides[][2] = {{q.n_tokens, q.k_token_stride}, {q.heads, q.k_head_stride}, {q.n_tokens, q.v_token_stride}, {q.heads, q.v_head_stride}};
+    for (const auto& s : kv_strides)
+        if (s[0] > 1 && (s[1] < 1 || s[1] > kFar)) return SGEMV_ERR_SHAPE;
+    const int64_t q_strides[][2] = {{q.n_tokens, q.q_token_stride}, {q.heads_q, q.q_head_stride}, {q.n_tokens, q.out_token_stride}, {q.heads_q, q.out_head_stride}};
+    for (const auto& s : q_strides)
+        if (s[0] > 1 && (s[1] < -kFar || s[1] > kFar)) return SGEMV_ERR_SHAPE;
+    // (rows between others, as those of a fused projection, may be out's: what lies from its first to its last byte is looked at only where
+    // nothing else has a place there)
+    const uint64_t all = 2ull * q.n_tokens * q.heads_q * q.dim;
+    const auto span = [&](const void* p, int64_t ts, int heads, int64_t hs) {
+        return span_bytes(p, q.n_tokens, q.n_tokens > 1 ? ts : 0, heads, heads > 1 ? hs : 0, q.dim);
+    };
+    const Bytes out = span(q.out_dev, q.out_token_stride, q.heads_q, q.out_head_stride), qs = span(q.q_dev, q.q_token_stride, q.heads_q, q.q_head_stride);
+    const Bytes ks = span(q.k_dev, q.k_token_stride, q.heads, q.k_head_stride), vs = span(q.v_dev, q.v_token_stride, q.heads, q.v_head_stride);
+    const uint64_t kv_all = 2ull * q.n_tokens * q.heads * q.dim;
+    const Bytes lse(q.lse_dev, 4ull * q.n_tokens * q.heads_q), status(status_dev, 4);
+    const Bytes start(q.start_dev, 4ull * q.n_req + 4), length(q.length_dev, 4ull * q.n_req);
+    const Bytes written[] = {lse, status}, read[] = {start, length};
+    if (!apart(written, read)) return SGEMV_ERR_ARG;
+    for (const Bytes& b : {lse, status, start, length}) {
+        if (out.size == all && meet(out, b)) return SGEMV_ERR_ARG;
+        if ((b.at == lse.at || b.at == status.at) && ((qs.size == all && meet(qs, b)) || (ks.size == kv_all && meet(ks, b)) || (vs.size == kv_all && meet(vs, b))))
+            return SGEMV_ERR_ARG;
+    }
+    if (q.out_dev != q.q_dev && out.size == all && qs.size == all && meet(out, qs)) return SGEMV_ERR_ARG;
+    if (q.out_dev == q.q_dev && ((q.n_tokens > 1 && q.q_token_stride != q.out_token_stride) || (q.heads_q > 1 && q.q_head_stride != q.out_head_stride)))
+        return SGEMV_ERR_ARG;
+    if (out.size == all && ((ks.size == kv_all && meet(out, ks)) || (vs.size == kv_all && meet(out, vs)))) return SGEMV_ERR_ARG;
+    PromptParams p;
+    p.q = q;
+    // A window that no request reaches hides nothing, and without it positions minus the window stay in 32 bits.
+    if (q.window >= q.n_tokens) p.q.window = 0;
+    p.status = status_dev;
+    p.ratio = q.heads_q / q.heads;
+    p.scale_log2 = q.scale * 1.44269504088896340736f;
+    CUtensorMap k_map, v_map;
+    if (!map_rows(&k_map, q.k_dev, q, q.k_token_stride, q.k_head_stride) || !map_rows(&v_map, q.v_dev, q, q.v_token_stride, q.v_head_stride))
+        return SGEMV_ERR_CUDA;
+    // at most so many segments: every request's last may be short
+    const int64_t most = (static_cast<int64_t>(q.n_tokens) * p.ratio / PromptShape<128>::kRows + q.n_req) * q.heads;
+    if (most > INT_MAX) return SGEMV_ERR_SHAPE;
+    const unsigned grid = static_cast<unsigned>(most);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool half = q.dtype == SGEMV_F16;
+    const cudaError_t e = q.dim == 64 ? (half ? launch_prompt<__half, 64>(k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 64>(k_map, v_map, p, grid, s))
+                                      : (half ? launch_prompt<__half, 128>(k_map, v_map, p, grid, s) : launch_prompt<__nv_bfloat16, 128>(k_map, v_map, p, grid, s));
+    return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
+}
+
+extern "C" int get_stamps(long long* out) { return cudaMemcpyFromSymbol(out, sgemv::g_stamp, sizeof(sgemv::g_stamp)); }
