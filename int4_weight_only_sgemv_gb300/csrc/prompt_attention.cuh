@@ -6,9 +6,9 @@
 // other's products run. Each SM has one CTA, which goes through segments, the longest first; its roles run ahead of one another from one segment into
 // the next, so that the start of a segment (queries, first keys, first scores) hides under the end of the one before. Roles, by warp:
 //   0-3, 4-7  softmax of the first and of the second row tile: a thread a row, scores from tensor memory, weights back over them; the outputs
-//   8         issues the products
-//   9         finds the segments and issues the copies of their K and V tiles (two buffers each)
-//   10, 11    bring the queries of a row tile each, and look through V tiles that are masked for some row (below)
+//   8, 9      issue the products, a row tile each
+//   10        finds the segments and issues the copies of their queries and K and V tiles (two buffers each)
+//   11        looks through V tiles that are masked for some row (below)
 // The softmax's reference m moves only when a tile's sum of weights passes 2^15 (and in a row's first tile), so that the largest score is
 // looked for in few tiles and the output's sums are rarely rescaled.
 //
@@ -41,7 +41,7 @@ template <int D>
 struct PromptShape {
     static constexpr int kTile = 128, kKeys = 128;
     static constexpr int kAtoms = D / 64;  // 128-byte columns of a row
-    static constexpr int kBufs = 2;        // of K and of V
+    static constexpr int kBufs = 2;        // of K and of V (the product warps count on two)
     static constexpr int kSegs = 4;        // segments known ahead
     static constexpr int kQBytes = kTile * D * 2, kKvBytes = kKeys * D * 2;
     static constexpr int kOutBytes = 32 * 64;  // a warp's staging: 32 dims of 32 rows
@@ -54,7 +54,7 @@ struct PromptShape {
 };
 
 // log2 of the largest weight when the reference is set; the limits of a tile's sum and, as log2, of a weight: 128 of those are that sum
-constexpr float kPromptTop = 6.0f, kPromptBig = 32768.0f, kPromptFar = 8.0f;
+constexpr float kPromptTop = 6.0f, kPromptBig = 32768.0f, kPromptFar = 8.0f, kPromptRound = 67108864.0f;
 
 // A request's tokens.
 struct PromptSpan {
@@ -104,18 +104,46 @@ __device__ __forceinline__ PromptRange prompt_range(const PromptParams& p, const
     return {lo / 128, (hi + 127) / 128, p.q.window > 0 ? max(0, ib - p.q.window + 1) : 0, p.q.causal ? ia + 1 : s.n};
 }
 struct PromptTiles {
-    PromptRange r[2];
-    __device__ __forceinline__ int first() const { return r[0].from; }
-    __device__ __forceinline__ int last() const { return max(r[0].to, r[1].to); }
-    __device__ __forceinline__ bool has(int x, int j) const { return j >= r[x].from && j < r[x].to; }
+    PromptRange r0, r1;  // of the two row tiles
+    __device__ __forceinline__ int from(int x) const { return x == 0 ? r0.from : r1.from; }
+    __device__ __forceinline__ int to(int x) const { return x == 0 ? r0.to : r1.to; }
+    __device__ __forceinline__ int first() const { return r0.from; }
+    __device__ __forceinline__ int last() const { return max(r0.to, r1.to); }
+    __device__ __forceinline__ bool has(int x, int j) const { return j >= from(x) && j < to(x); }
     __device__ __forceinline__ bool masked(int j) const {  // for some row that has it
         const int pos0 = j * 128, pos1 = pos0 + 128;
-        return (has(0, j) && (pos0 < r[0].clear0 || pos1 > r[0].clear1)) || (has(1, j) && (pos0 < r[1].clear0 || pos1 > r[1].clear1));
+        return (has(0, j) && (pos0 < r0.clear0 || pos1 > r0.clear1)) || (has(1, j) && (pos0 < r1.clear0 || pos1 > r1.clear1));
     }
 };
 __device__ __forceinline__ PromptTiles prompt_tiles(const PromptParams& p, const PromptSegment& s) {
-    return {{prompt_range(p, s, 0), prompt_range(p, s, 1)}};
+    return {prompt_range(p, s, 0), prompt_range(p, s, 1)};
 }
+// Whether `bytes` bytes (a multiple of 4096) of shared memory hold elements that are no numbers; by a whole warp.
+template <typename T>
+__device__ __forceinline__ bool no_numbers(const uint8_t* at, int bytes, int lane) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(&sum[i]) = 0;
+    const T2 zero = sum[0];
+#pragma unroll 1
+    for (int n = 0; n < bytes; n += 4096) {
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(at + n + 512 * i + 16 * lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const T2* const h = reinterpret_cast<const T2*>(&w[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __hfma2(h[e], zero, sum[e]);
+        }
+    }
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) odd |= (*reinterpret_cast<const uint32_t*>(&sum[e]) & 0x7FFF7FFFu) != 0;
+    return __any_sync(0xFFFFFFFFu, odd);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
@@ -127,7 +155,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     uint8_t* const s_v = s_k + S::kBufs * S::kKvBytes;
     uint8_t* const s_out = s_v + S::kBufs * S::kKvBytes;
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_ok[S::kBufs], v_free[S::kBufs];
-    __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], seg_full[S::kSegs], seg_free[S::kSegs];
+    __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], seg_full[S::kSegs], seg_free[S::kSegs], turn[2];
     __shared__ PromptSegment s_seg[S::kSegs];
     __shared__ int s_odd[S::kSegs];                                             // a segment's V has elements that are no numbers
     __shared__ int t_before[S::kThreads], t_blocks[S::kThreads];  // where segments are, below
@@ -137,15 +165,16 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 1);
-            mbar_init(&v_full[i], 1), mbar_init(&v_ok[i], 64), mbar_init(&v_free[i], 1);
+            mbar_init(&k_full[i], 1), mbar_init(&k_free[i], 2);
+            mbar_init(&v_full[i], 1), mbar_init(&v_ok[i], 32), mbar_init(&v_free[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1), mbar_init(&q_free[i], 1);
-            mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
+            mbar_init(&turn[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
         }
         for (int i = 0; i < S::kSegs; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_free[i], 11);
         mbar_fence_init();
+        mbar_arrive(&turn[0]);
     }
     if (warp == 8) tc_alloc(&s_tmem, S::kCols);
     pdl_launch_dependents();
@@ -166,6 +195,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         __syncthreads();
         if (tid < p.q.n_req) {
             int rank = 0;
+#pragma unroll 1
             for (int r = 0; r < p.q.n_req; ++r) rank += t_len[r] > s.n || (t_len[r] == s.n && r < tid);
             t_span[rank] = s;
             t_blocks[rank] = prompt_blocks(p, s.n);
@@ -176,6 +206,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             mine = (by_block ? static_cast<int64_t>(b - next) * (tid + 1) : b) * p.groups;
         }
     } else {
+#pragma unroll 1
         for (int64_t r = static_cast<int64_t>(tid) * run; r < min(static_cast<int64_t>(tid + 1) * run, static_cast<int64_t>(p.q.n_req)); ++r)
             mine += static_cast<int64_t>(prompt_blocks(p, prompt_span(p, static_cast<int>(r)).n)) * p.groups;
     }
@@ -188,6 +219,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     int64_t total = 0, before = incl - mine;
+#pragma unroll 1
     for (int w = 0; w < S::kWarps; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
@@ -224,11 +256,12 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
         const float c = p.scale_log2;
         uint32_t tiles = 0, segs = 0;  // that this row tile has had
+#pragma unroll 1
         for (int it = 0;; ++it) {
             const PromptSegment sg = segment(it);
             if (sg.n < 0) break;
             const PromptTiles all = prompt_tiles(p, sg);
-            const PromptRange rg = x == 0 ? all.r[0] : all.r[1];
+            const PromptRange rg = x == 0 ? all.r0 : all.r1;
             if (rg.from >= rg.to) {
                 release(it);
                 continue;
@@ -242,20 +275,43 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             float ref = 0.0f;   // the reference
             bool seen = false;  // whether it was set
             uint64_t l2 = 0;    // two sums
+#pragma unroll 1
             for (int j = rg.from; j < rg.to; ++j, ++tiles) {
                 const int pos0 = j * S::kKeys;
                 wait(&s_full[x], tiles & 1);  // (and all products issued before: O holds every tile before this one)
                 __syncwarp();
                 tc_after_sync();
                 const bool plain = pos0 >= rg.clear0 && pos0 + S::kKeys <= rg.clear1;
-                // Seen in full, and the row has its reference: weights in one go. Whether the reference has to move shows in their sum, so that
-                // the largest score is looked for in few tiles. (Past 2^26 scores are rounded before the reference comes off: slow, below.)
+                // Weights in one go. Whether the reference has to move shows in their sum, so that the largest score is looked for in few tiles.
+                // (Past 2^26 scores are rounded before the reference comes off: slow, below, as is a scale of 0, which cannot carry the mask.)
+                const int rel0 = see0 - pos0, rel1 = rel0 + static_cast<int>(see);
+                const auto seen_bits = [&](int q) {  // of keys 32 q .. 32 q + 31
+                    const int lo = min(32, max(0, rel0 - 32 * q)), hi = min(32, max(0, rel1 - 32 * q));
+                    return static_cast<uint32_t>((1ull << hi) - 1) & ~static_cast<uint32_t>((1ull << lo) - 1);
+                };
                 bool done = false;
-                if (plain && __all_sync(0xFFFFFFFFu, seen && fabsf(ref) < 67108864.0f)) {
+                if (c != 0.0f) {
                     uint32_t raw[4][32], w[64];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tc_ld32(raw[q], ts + 32 * q);
                     tc_wait_ld();
+                    if (!plain) {
+                        const uint32_t none = c > 0.0f ? 0xFF800000u : 0x7F800000u;  // a score of -inf
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t bits = seen_bits(q);
+#pragma unroll
+                            for (int n = 0; n < 32; ++n)
+                                if (!((bits >> n) & 1)) raw[q][n] = none;
+                        }
+                    }
+                    if (__any_sync(0xFFFFFFFFu, !seen)) {
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int n = 0; n < 128; ++n) top[n & 3] = fmaxf(top[n & 3], __uint_as_float(raw[n / 32][n % 32]) * c);
+                        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        if (!seen && most > -INFINITY) ref = most - kPromptTop, seen = true;
+                    }
                     uint64_t sums[4] = {0, 0, 0, 0};
                     const uint64_t cc = pair(c, c), mm = pair(-ref, -ref);
 #pragma unroll
@@ -267,7 +323,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                     }
                     sums[0] = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                     const float2 both = parts_of(sums[0]);
-                    done = !__any_sync(0xFFFFFFFFu, both.x + both.y > kPromptBig);
+                    done = !__any_sync(0xFFFFFFFFu, both.x + both.y > kPromptBig || fabsf(ref) > kPromptRound);
                     if (done) {
                         l2 = add2(l2, sums[0]);
                         tc_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(w));
@@ -277,11 +333,6 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                 if (!done) {
                     // 32 keys at a time, in little code: the largest score that each row sees, then the weights. (Those of 32 keys take the
                     // columns of 16: they never reach scores that are still to be read.)
-                    const int rel0 = see0 - pos0, rel1 = rel0 + static_cast<int>(see);
-                    const auto seen_bits = [&](int q) {  // of keys 32 q .. 32 q + 31
-                        const int lo = min(32, max(0, rel0 - 32 * q)), hi = min(32, max(0, rel1 - 32 * q));
-                        return static_cast<uint32_t>((1ull << hi) - 1) & ~static_cast<uint32_t>((1ull << lo) - 1);
-                    };
                     float most = -INFINITY;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
@@ -342,12 +393,6 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (live && p.q.lse_dev != nullptr)
                 p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
-            wait(&o_full[x], segs & 1);
-            ++segs;
-            __syncwarp();
-            tc_after_sync();
-            const bool odd = *static_cast<volatile int*>(&s_odd[it % S::kSegs]) != 0;
-            // 32 dims at a time through shared memory, so that 4 lanes write 64 bytes of a row
             uint8_t* const stage = s_out + warp * S::kOutBytes;
             T* out[4];
 #pragma unroll
@@ -358,17 +403,24 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                                    (sg.group * p.sub + rr % p.sub) * p.q.out_head_stride + 8 * (lane & 3)
                              : nullptr;
             }
-#pragma unroll 1
+            wait(&o_full[x], segs & 1);
+            ++segs;
+            __syncwarp();
+            tc_after_sync();
+            const bool odd = *static_cast<volatile int*>(&s_odd[it % S::kSegs]) != 0;
+            // 32 dims at a time through shared memory, so that 4 lanes write 64 bytes of a row
+            uint32_t o[D / 32][32];
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) tc_ld32(o[q], to + 32 * q);
+            tc_wait_ld();
+#pragma unroll
             for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tc_ld32(o, to + 32 * q);
-                tc_wait_ld();
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     uint32_t h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        h[e] = pack_two<T>(__uint_as_float(o[8 * n + 2 * e]) * inv, __uint_as_float(o[8 * n + 2 * e + 1]) * inv);
+                        h[e] = pack_two<T>(__uint_as_float(o[q][8 * n + 2 * e]) * inv, __uint_as_float(o[q][8 * n + 2 * e + 1]) * inv);
                     *reinterpret_cast<uint4*>(stage + lane * 64 + ((n ^ (lane >> 1)) & 3) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 __syncwarp();
@@ -399,96 +451,99 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         }
     } else {
         regs_dec<S::kRegsOther>();
-        if (warp == 8) {
+        if (warp < 10) {
         // ---------------------------------------------------------------------------------------- products
-        // The whole warp goes through the loop, with values that are the same in its lanes; one lane issues. A row tile's products of a key tile,
-        // O += P V and the next scores (of the next segment, at the end of one), are issued together, so that the two row tiles stay half a
-        // period apart: with a warp for each, both were in their softmax and then both in their products (3740 cycles a key tile against 3225).
-        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const uint64_t q_desc = tc_desc(smem_addr(s_q)), k_desc = tc_desc(smem_addr(s_k));
+        // A warp a row tile, which goes through the loop as a whole, with values that are the same in its lanes; one lane issues. They take turns: a
+        // row tile's products of a key tile, O += P V and the next scores (of the next segment, at the end of one), are issued together, so that
+        // the two row tiles stay half a period apart (without turns both were in their softmax and then both in their products: 3740 cycles a
+        // key tile); and as one waits for what its turn needs while the other issues, the tensor cores get one's after the other's (with
+        // one warp for both they stood still for 450 cycles a turn: 3370 cycles).
+        const int x = warp - 8;
+        const uint32_t ts = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128 * x, to = ts + 256;
+        const uint64_t q_desc = tc_desc(smem_addr(s_q) + x * S::kQBytes), k_desc = tc_desc(smem_addr(s_k));
         const uint64_t v_desc = tc_desc_v(smem_addr(s_v), S::kKeys * 128);
         constexpr uint32_t kScores = tc_idesc(S::kKeys) | tc_idesc_type<T>(), kOut = tc_idesc(D) | tc_idesc_type<T>() | (1u << 16);
         const auto hold = [&](uint64_t* bar, uint32_t parity) {
             wait(bar, parity);
             dead = __any_sync(0xFFFFFFFFu, dead);
-            tc_after_sync();
         };
-        const auto last_user = [](const PromptTiles& t, int x, int j) { return x == 1 || !t.has(1, j); };  // of a key tile's buffers
-        uint32_t q_had[2] = {0, 0}, p_had[2] = {0, 0};
-        int g = 0;  // key tiles so far
-        const auto scores = [&](const PromptTiles& t, int x, int j, int gk) {
-            const int buf = gk % S::kBufs;
-            if (j == t.r[x].from) hold(&q_full[x], q_had[x]++ & 1);
-            hold(&k_full[buf], (gk / S::kBufs) & 1);
-            if (elect_one()) {
-                const uint64_t kd = k_desc + buf * (S::kKvBytes >> 4), qd = q_desc + x * (S::kQBytes >> 4);
-                if (!dead) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4 * (128 * 128) + kk % 4 * 32) >> 4;
-                        tc_mma_ss(tm + 128 * x, qd + off, kd + off, kScores, kk > 0);
-                    }
-                }
-                tc_commit(&s_full[x]);
-                if (last_user(t, x, j)) tc_commit(&k_free[buf]);
-                if (j == t.r[x].to - 1) tc_commit(&q_free[x]);
-            }
-            __syncwarp();
-        };
+        uint32_t q_had = 0, p_had = 0;
         PromptSegment sg = segment(0);
         PromptTiles t = prompt_tiles(p, sg);
-        if (sg.n >= 0) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (t.has(x, t.first())) scores(t, x, t.first(), 0);
-        }
-        for (int it = 0; sg.n >= 0; ++it) {
-            const int first = t.first(), last = t.last();
-            PromptSegment next_sg;
+        int it = 0, g = -1;  // segment; key tiles so far
+#pragma unroll 1
+        for (int j = t.first() - 1; sg.n >= 0; ++g) {
+            // O += P V of key tile j (but before the first of all), and scores of the tile after it, of this segment or the next
+            PromptSegment next_sg = sg;
             PromptTiles next = t;
-            for (int j = first; j < last; ++j, ++g) {
-                if (j == last - 1) {
-                    next_sg = segment(it + 1);
-                    next = prompt_tiles(p, next_sg);
-                }
-                const int buf = g % S::kBufs;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (t.has(x, j)) {
-                        hold(&v_ok[buf], (g / S::kBufs) & 1);
-                        hold(&p_full[x], p_had[x]++ & 1);
-                        if (elect_one()) {
-                            const uint64_t vd = v_desc + buf * (S::kKvBytes >> 4);
-                            if (!dead) {
-#pragma unroll
-                                for (int kk = 0; kk < S::kKeys / 16; ++kk)
-                                    tc_mma_ts(tm + 256 + 128 * x, tm + 128 * x + 8 * kk, vd + kk * (2048 >> 4), kOut, j > t.r[x].from || kk > 0);
-                            }
-                            if (last_user(t, x, j)) tc_commit(&v_free[buf]);
-                            if (j == t.r[x].to - 1) tc_commit(&o_full[x]);
-                        }
-                        __syncwarp();
-                    }
-                    // (over the weights just used: the products run in the order of their issue)
-                    if (j + 1 < last) {
-                        if (t.has(x, j + 1)) scores(t, x, j + 1, g + 1);
-                    } else if (next_sg.n >= 0 && next.has(x, next.first())) {
-                        scores(next, x, next.first(), g + 1);
-                    }
-                }
+            int next_j = j + 1;
+            const bool cross = next_j == t.last();
+            if (cross) {
+                next_sg = segment(it + 1);
+                next = prompt_tiles(p, next_sg);
+                next_j = next.first();
             }
-            release(it);
-            sg = next_sg;
-            t = next;
+            const bool old_keys = t.has(x, j), new_keys = next_sg.n >= 0 && next.has(x, next_j);
+            const int buf = g & 1, next_buf = buf ^ 1;
+            const uint32_t parity = (g >> 1) & 1, next_parity = ((g + 1) >> 1) & 1;
+            const uint64_t vd = v_desc + buf * (S::kKvBytes >> 4), kd = k_desc + next_buf * (S::kKvBytes >> 4);
+            const bool add = j > t.from(x);
+            // (who does not have a tile lets it go all the same, once it is there: its buffers wait for both)
+            if (g >= 0) hold(&v_ok[buf], parity);
+            if (!cross) hold(&k_full[next_buf], next_parity);
+            if (!old_keys && g >= 0 && lane == 0) mbar_arrive(&v_free[buf]);
+            hold(&turn[x], (g + 1) & 1);
+            if (old_keys) hold(&p_full[x], p_had++ & 1);
+            tc_after_sync();
+            if (old_keys) {
+                if (elect_one()) {
+                    if (!dead) {
+#pragma unroll
+                        for (int kk = 0; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, ts + 8 * kk, vd + kk * (2048 >> 4), kOut, kk > 0 || add);
+                    }
+                    tc_commit(&v_free[buf]);
+                    if (j == t.to(x) - 1) tc_commit(&o_full[x]);
+                }
+                __syncwarp();
+            }
+            if (cross && next_sg.n >= 0) hold(&k_full[next_buf], next_parity);
+            if (new_keys) {
+                if (next_j == next.from(x)) {
+                    hold(&q_full[x], q_had++ & 1);
+                    tc_after_sync();
+                }
+                if (elect_one()) {
+                    if (!dead) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk / 4 * (128 * 128) + kk % 4 * 32) >> 4;
+                            tc_mma_ss(ts, q_desc + off, kd + off, kScores, kk > 0);  // (over the weights just used: products run in the order of their issue)
+                        }
+                    }
+                    mbar_arrive(&turn[x ^ 1]);
+                    tc_commit(&s_full[x]);
+                    tc_commit(&k_free[next_buf]);
+                    if (next_j == next.to(x) - 1) tc_commit(&q_free[x]);
+                }
+                __syncwarp();
+            } else if (lane == 0) {
+                mbar_arrive(&turn[x ^ 1]);
+                if (next_sg.n >= 0) mbar_arrive(&k_free[next_buf]);
+            }
+            if (cross) release(it++);
+            sg = next_sg, t = next, j = next_j;
         }
         // The last products arrive at barriers that nobody else waits for: none may be under way when the CTA's memory goes.
+#pragma unroll 1
         for (int i = max(0, g - S::kBufs); i < g; ++i) {
             mbar_wait(&k_free[i % S::kBufs], (i / S::kBufs) & 1);
             mbar_wait(&v_free[i % S::kBufs], (i / S::kBufs) & 1);
         }
-        } else if (warp == 9) {
+        } else if (warp == 10) {
         // ---------------------------------------------------------------------------------------- segments and copies
         int g = 0;
+        uint32_t q_had[2] = {0, 0};
+#pragma unroll 1
         for (int it = 0;; ++it) {
             if (it >= S::kSegs) wait(&seg_free[it % S::kSegs], (it / S::kSegs - 1) & 1);
             dead = __any_sync(0xFFFFFFFFu, dead);
@@ -497,6 +552,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             PromptSegment sg = {0, -1, 0, 0};
             if (want < total && !dead) {
                 int x = -1;  // the last thread that starts at or before `want`
+#pragma unroll 1
                 for (int i = lane; i < min(p.q.n_req, S::kThreads); i += 32)
                     if (t_before[i] <= want) x = i;
                 x = __reduce_max_sync(0xFFFFFFFFu, x);
@@ -510,6 +566,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                     o %= width;
                     s = t_span[by_block ? o / groups : x];
                 } else {
+#pragma unroll 1
                     for (int req = x * run;; ++req) {
                         s = prompt_span(p, req);
                         const unsigned n = prompt_blocks(p, s.n) * groups;
@@ -531,9 +588,10 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             if (sg.n < 0) break;
             const PromptTiles t = prompt_tiles(p, sg);
             const int head = sg.group * p.sub / p.ratio;
+#pragma unroll 1
             for (int j = t.first(); j < t.last() && !dead; ++j, ++g) {
                 const int buf = g % S::kBufs, key = sg.first + j * S::kKeys;
-#pragma unroll
+#pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     uint64_t* const bar = v ? &v_full[buf] : &k_full[buf];
                     if (g >= S::kBufs) wait(v ? &v_free[buf] : &k_free[buf], (g / S::kBufs - 1) & 1);
@@ -549,48 +607,59 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                         for (int d = 0; d < S::kAtoms; ++d) tma_load(dst + d * (S::kKeys * 128), v ? &v_map : &k_map, 64 * d, head, key, bar);
                     }
                     __syncwarp();
+                    if (v == 0 && j == t.first()) {
+                        // the segment's queries, once the products are done with those of the one before
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (t.to(x) == 0) continue;
+                            if (q_had[x] > 0) wait(&q_free[x], (q_had[x] - 1) & 1);
+                            dead = __any_sync(0xFFFFFFFFu, dead);
+                            if (dead) break;
+                            ++q_had[x];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&q_full[x], p.tokens * p.sub * D * 2);
+#pragma unroll
+                                for (int d = 0; d < S::kAtoms; ++d)
+                                    tma_load(s_q + x * S::kQBytes + d * (128 * 128), &q_map, 64 * d, sg.group * p.sub, sg.first + sg.t0 + p.tokens * x, &q_full[x]);
+                            }
+                            __syncwarp();
+                        }
+                    }
                 }
                 if (dead) break;
             }
         }
         // (all have landed, unless someone gave up)
+#pragma unroll 1
         for (int i = max(0, g - S::kBufs); i < g; ++i) {
             mbar_wait(&k_full[i % S::kBufs], (i / S::kBufs) & 1);
             mbar_wait(&v_full[i % S::kBufs], (i / S::kBufs) & 1);
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (q_had[x] > 0) mbar_wait(&q_full[x], (q_had[x] - 1) & 1);
         } else {
-        // ---------------------------------------------------------------------------------------- queries; V that is not seen
-        const int x = warp - 10;
-        uint32_t had = 0;
+        // ---------------------------------------------------------------------------------------- V that is not seen
         int g = 0;
+#pragma unroll 1
         for (int it = 0;; ++it) {
             const PromptSegment sg = segment(it);
             if (sg.n < 0) break;
             const PromptTiles t = prompt_tiles(p, sg);
-            if ((x == 0 ? t.r[0] : t.r[1]).to > 0) {
-                if (had > 0) wait(&q_free[x], (had - 1) & 1);
-                ++had;
-                __syncwarp();
-                if (lane == 0 && !dead) {
-                    mbar_arrive_expect_tx(&q_full[x], p.tokens * p.sub * D * 2);
-#pragma unroll
-                    for (int d = 0; d < S::kAtoms; ++d)
-                        tma_load(s_q + x * S::kQBytes + d * (128 * 128), &q_map, 64 * d, sg.group * p.sub, sg.first + sg.t0 + p.tokens * x, &q_full[x]);
-                }
-                __syncwarp();
-            }
             const int last = t.last();
+#pragma unroll 1
             for (int j = t.first(); j < last; ++j, ++g) {
                 const int buf = g % S::kBufs;
                 wait(&v_full[buf], (g / S::kBufs) & 1);
                 __syncwarp();
-                if (t.masked(j)) {
+                // 0 times a number is 0: a look at the whole tile takes one instruction a word
+                if (t.masked(j) && no_numbers<T>(s_v + buf * S::kKvBytes, S::kKvBytes, lane)) {
                     uint8_t* const tile = s_v + buf * S::kKvBytes;
                     const int keys = sg.n - j * S::kKeys;  // of the request
                     constexpr uint32_t kNot = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
                     bool odd = false;
-#pragma unroll 4
-                    for (int n = tid - 320; n < S::kKvBytes / 16; n += 64) {
+#pragma unroll 1
+                    for (int n = lane; n < S::kKvBytes / 16; n += 32) {
                         uint4* const at16 = reinterpret_cast<uint4*>(tile) + n;
                         uint4 w = *at16;
                         if (n / 8 % S::kKeys >= keys) {
@@ -613,7 +682,6 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             }
             release(it);
         }
-        if (had > 0 && !dead) mbar_wait(&q_full[x], (had - 1) & 1);  // (landed, unless someone gave up)
         }
     }
     __syncwarp();
