@@ -9,11 +9,11 @@
 //   8, 9      issue the products, a row tile each
 //   10        finds the segments and issues the copies of their queries and K and V tiles (two buffers each)
 //   11        looks through V tiles that are masked for some row (below)
-// The softmax's reference m moves only when a tile's sum of weights passes 2^15 (and in a row's first tile), so that the largest score is
+// The softmax's reference m moves only when a tile's sum of weights passes a limit (and in a row's first tile), so that the largest score is
 // looked for in few tiles and the output's sums are rarely rescaled.
 //
 // Roundings: scores are sums of exact products in 32 bits, scaled in 32 bits. Weights 2^(t - m) are rounded to the type of V, since the
-// instruction takes one type for both (11 bits for fp16, whose end 2^16 the limit on m keeps away from; 8 for bf16).
+// instruction takes one type for both (11 bits for fp16, 8 for bf16).
 //
 // What a row does not see must not enter its sums whatever it holds, but 0 * NaN is NaN in the tensor cores. Scores are selected, so K needs
 // nothing. In V tiles that some row does not see in full, rows past the request's end are cleared, and elements that are no numbers are
@@ -53,8 +53,20 @@ struct PromptShape {
     static constexpr int kCols = 512;  // tensor memory: S of both row tiles (128 columns each), O of both
 };
 
-// log2 of the largest weight when the reference is set; the limits of a tile's sum and, as log2, of a weight: 128 of those are that sum
-constexpr float kPromptTop = 6.0f, kPromptBig = 32768.0f, kPromptFar = 8.0f, kPromptRound = 67108864.0f;
+// Weights 2^(t - m): the largest is 2^kTop when the reference m is set, which happens anew when a tile's sum passes kBig (or, where the largest score
+// is looked for, when a weight would pass 2^kFar: 128 of those are that sum). fp16's weights end at 2^16 and lose bits below 2^-14, nothing at all
+// being left below 2^(kTop - 27) of the largest, so kTop is low enough that a window's first few keys rarely set a reference that is left behind
+// (kTop 6: 162 us for 5 requests of up to 4096 tokens with a window of 1000; 2: 113) and high enough for 2^16 keys below that end to add up to
+// no more than a rounding. bf16 has 8 bits of exponent: there the reference hardly ever moves, and sums stay below V's own size.
+template <typename T>
+struct PromptWeights {
+    static constexpr float kTop = 2.0f, kBig = 32768.0f, kFar = 8.0f;
+};
+template <>
+struct PromptWeights<__nv_bfloat16> {
+    static constexpr float kTop = -40.0f, kBig = 1.0f, kFar = -7.0f;
+};
+constexpr float kPromptRound = 67108864.0f;  // past this, scores are rounded before the reference comes off
 
 // A request's tokens.
 struct PromptSpan {
@@ -148,6 +160,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptParams p) {
     using S = PromptShape<D>;
+    using W = PromptWeights<T>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* const s_q = smem;
@@ -273,7 +286,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             const int see0 = p.q.window > 0 ? max(0, i - p.q.window + 1) : 0;
             const uint32_t see = static_cast<uint32_t>((p.q.causal ? i + 1 : sg.n) - see0);
             float ref = 0.0f;   // the reference
-            bool seen = false;  // whether it was set
+            bool seen = !live;  // whether it was set (rows that there are not hold anything, and nothing waits for them)
             uint64_t l2 = 0;    // two sums
 #pragma unroll 1
             for (int j = rg.from; j < rg.to; ++j, ++tiles) {
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                 tc_after_sync();
                 const bool plain = pos0 >= rg.clear0 && pos0 + S::kKeys <= rg.clear1;
                 // Weights in one go. Whether the reference has to move shows in their sum, so that the largest score is looked for in few tiles.
-                // (Past 2^26 scores are rounded before the reference comes off: slow, below, as is a scale of 0, which cannot carry the mask.)
+                // (Past kPromptRound: slow, below, as is a scale of 0, which cannot carry the mask.)
                 const int rel0 = see0 - pos0, rel1 = rel0 + static_cast<int>(see);
                 const auto seen_bits = [&](int q) {  // of keys 32 q .. 32 q + 31
                     const int lo = min(32, max(0, rel0 - 32 * q)), hi = min(32, max(0, rel1 - 32 * q));
@@ -310,7 +323,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
 #pragma unroll
                         for (int n = 0; n < 128; ++n) top[n & 3] = fmaxf(top[n & 3], __uint_as_float(raw[n / 32][n % 32]) * c);
                         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        if (!seen && most > -INFINITY) ref = most - kPromptTop, seen = true;
+                        if (!seen && most > -INFINITY) ref = most - W::kTop, seen = true;
                     }
                     uint64_t sums[4] = {0, 0, 0, 0};
                     const uint64_t cc = pair(c, c), mm = pair(-ref, -ref);
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                     }
                     sums[0] = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                     const float2 both = parts_of(sums[0]);
-                    done = !__any_sync(0xFFFFFFFFu, both.x + both.y > kPromptBig || fabsf(ref) > kPromptRound);
+                    done = !__any_sync(0xFFFFFFFFu, live && (both.x + both.y > W::kBig || fabsf(ref) > kPromptRound));
                     if (done) {
                         l2 = add2(l2, sums[0]);
                         tc_st32(ts, *reinterpret_cast<const uint32_t(*)[32]>(w));
@@ -346,8 +359,8 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                         most = fmaxf(most, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
                     }
                     float f = 1.0f;
-                    if (most > -INFINITY && (!seen || most - ref > kPromptFar)) {
-                        const float m = most - kPromptTop;
+                    if (live && most > -INFINITY && (!seen || most - ref > W::kFar)) {
+                        const float m = most - W::kTop;
                         if (seen) f = exp2_approx(ref - m);
                         ref = m;
                         seen = true;
