@@ -3,9 +3,12 @@
 // With few tokens the weights' bytes bound the work (0.56 bytes a weight against 2 operations a token), and with the tensor cores' block-
 // scaled instruction nothing has to be unpacked: copies of contiguous bytes go from HBM to shared memory and are multiplied as they are.
 // The weights are the instruction's 128 rows and the tokens its narrow side (8 to 128), so that one token costs no more than eight. A
-// CTA has one tile of 128 weight rows, and where there are fewer tiles than places (two CTAs an SM), a cluster of up to 8 CTAs shares it: each
-// sums a run of the columns, and they join their sums over distributed shared memory, in the order of the columns.
-// Roles: warp 0 issues the copies, warp 1 the products, warps 2-5 take the sums out; all warps join and write.
+// CTA has one tile of 128 weight rows, and where there are fewer tiles than places, a cluster of up to 8 CTAs shares it: each sums a run of the
+// columns, and sends every other one its share of the outputs' sums over distributed shared memory, where they are joined in the order of
+// the columns. (With sums read by their users between two barriers of the cluster, a call of one token took 1 us more.) What is sent has a
+// place of its own where tiles are narrow; with 64 or 128 tokens it comes where the ring was, so that two CTAs fit an SM, after a barrier of the cluster.
+// Roles: warp 0 issues the copies, a lane each (by one lane, 90 ns a copy bound everything), warp 1 the products, warps 2-5 take the sums
+// out, send, join and write.
 #pragma once
 
 #include "fp4_tc.cuh"
@@ -13,33 +16,46 @@
 namespace sgemv {
 
 constexpr int kFewThreads = 192;
-constexpr int kFewSmem = 108 * 1024;  // of the ring: two CTAs an SM, and never three (their tensor memory, 256 columns each, is full)
+constexpr int kFewSmem = 108 * 1024;   // of the ring: two CTAs an SM
+constexpr int kFewLeast = 80 * 1024;   // and never three, whose tensor memory (256 columns each) would not fit
+constexpr int kFewMost = 216 * 1024;
 constexpr int kFewCols = 256;
 constexpr int kFewMaxRing = 8;
 
+// Columns of a stage. A stage costs its copies (60 to 90 ns each), its barriers and commits (170 ns) whatever its size: one token, 4096 x 11008: 9.4 us a
+// call with 256 columns, XXX with 512. With 64 or 128 tokens a tile, two stages of 512 would not fit.
+__host__ __device__ constexpr int few_stage_k(int x_tile) { return x_tile <= 32 ? 512 : 256; }
 // Bytes of a stage: codes of 128 weight rows and of the tokens, scales of both.
-__host__ __device__ inline int few_stage_bytes(int block, int x_tile) {
-    return 128 * kStageK / 2 + x_tile * kStageK / 2 + 2 * (kStageK / (4 * block)) * 512;
+__host__ __device__ constexpr int few_stage_bytes(int block, int x_tile) {
+    const int k = few_stage_k(x_tile);
+    return 128 * k / 2 + x_tile * k / 2 + 2 * (k / (4 * block)) * 512;
 }
+// Float4s of sums that a CTA of a cluster joins, and bytes of what the others send it.
+__host__ __device__ inline int few_share(int x_tile, int split) { return (x_tile * 32 + split - 1) / split; }
+__host__ __device__ inline int few_sent(int x_tile, int split) { return (split - 1) * few_share(x_tile, split) * 16; }
 
-__device__ __forceinline__ void cluster_arrive_wait() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {  // the same place in another CTA's shared memory
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
 }
-__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {  // of the same place in another CTA's shared memory
-    float4 v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr), "r"(rank)
+// 16 bytes into a peer's shared memory, counted on its barrier.
+__device__ __forceinline__ void send16(uint32_t to, float4 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
-    return v;
 }
 
-template <typename T, int kBlock>
+template <typename T, int kBlock, int kStageK>
 __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[kFewMaxRing], free_[kFewMaxRing], done;
+    __shared__ __align__(8) uint64_t full[kFewMaxRing], free_[kFewMaxRing], done, sent;
     __shared__ uint32_t s_tmem;
+    __shared__ float s_x_scale[128];
     constexpr int kGroups = kStageK / (4 * kBlock);  // of 4 scales, a stage
+    constexpr int kChunks = kStageK / 32;            // of 16 bytes of codes
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
     const int wt = tile / p.x_tiles, xt = tile % p.x_tiles;
@@ -47,26 +63,34 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     const int n = static_cast<int>(static_cast<int64_t>(p.k_stages) * (rank + 1) / p.split) - st0;
     const uint32_t stage_bytes = few_stage_bytes(kBlock, p.x.tile);
     const int chunks = p.w.kp / 32;
-    const uint8_t* const w_codes = p.w.codes + (static_cast<int64_t>(wt) * chunks + 8 * st0) * p.w.tile * 16;
+    const uint8_t* const w_codes = p.w.codes + (static_cast<int64_t>(wt) * chunks + kChunks * st0) * p.w.tile * 16;
     const uint8_t* const w_scales = p.w.scales + (static_cast<int64_t>(wt) * p.w.groups + kGroups * st0) * 512;
     const int cols = min(p.x.tile, p.x.rows - xt * 128);  // tokens of this tile
     const int rows = min(128, p.w.rows - wt * 128);
+    // Sums go by four weight rows of a token (32 a token); this CTA joins [item0, item1) of them, at most `share`, and gets the others' behind its own.
+    const int share = few_share(p.x.tile, p.split), items = cols * 32;
+    const int item0 = min(items, share * rank), item1 = min(items, share * (rank + 1));
+    constexpr bool kEarly = kStageK == 512;  // what is sent has a place of its own
+    float4* const got = reinterpret_cast<float4*>(smem + max(kEarly ? p.ring * stage_bytes : 0u, p.x.tile * 512u));
 
     if (tid == 0) {
         for (int i = 0; i < p.ring; ++i) mbar_init(&full[i], 1), mbar_init(&free_[i], 1);
-        mbar_init(&done, 1);
+        mbar_init(&done, 1), mbar_init(&sent, 1);
         mbar_fence_init();
         // into L2 while the kernel before this one ends (nothing is read before it has)
         const int early = min(n, p.ring);
-        const int many = min(8 * early, chunks - 8 * st0), groups = min(kGroups * early, p.w.groups - kGroups * st0);
+        const int many = min(kChunks * early, chunks - kChunks * st0), groups = min(kGroups * early, p.w.groups - kGroups * st0);
         for (int b = 0; b < many * p.w.tile * 16; b += kPrefetchPiece) prefetch_l2(w_codes + b, min(static_cast<int>(kPrefetchPiece), many * p.w.tile * 16 - b));
         prefetch_l2(w_scales, groups * 512);
+        if (p.split > 1) mbar_arrive_expect_tx(&sent, (p.split - 1) * (item1 - item0) * 16);
     }
+    __syncwarp();
     pdl_launch_dependents();
     if (warp == 1) tc_alloc(&s_tmem, kFewCols);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
+    if (kEarly && p.split > 1) cluster_arrive();  // (barriers are there; waited for before anything is sent)
     const uint32_t tmem = s_tmem, t_sa = tmem + 128, t_sb = tmem + 128 + 4 * kGroups;
     pdl_wait();
 
@@ -79,26 +103,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     // a stage: weights' codes, tokens' codes, weights' scales, tokens' scales
     const uint32_t at_x = 128 * kStageK / 2, at_sw = at_x + p.x.tile * kStageK / 2, at_sx = at_sw + kGroups * 512;
     if (warp == 0) {
-        if (lane == 0) {
-            const uint8_t* const x_codes = p.x.codes + (static_cast<int64_t>(xt) * chunks + 8 * st0) * p.x.tile * 16;
-            const uint8_t* const x_scales = p.x.scales + (static_cast<int64_t>(xt) * p.x.groups + kGroups * st0) * 512;
-            int i = 0;
-            for (; i < n; ++i) {
-                const int b = i % p.ring;
-                if (i >= p.ring) wait(&free_[b], (i / p.ring - 1) & 1);
-                if (dead) break;
-                const int c = min(8, chunks - 8 * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
-                uint8_t* const to = smem + b * stage_bytes;
-                mbar_arrive_expect_tx(&full[b], c * (p.w.tile + p.x.tile) * 16 + 2 * g * 512);
-                bulk_g2s(to, w_codes + static_cast<int64_t>(i) * 8 * p.w.tile * 16, c * p.w.tile * 16, &full[b]);
-                bulk_g2s(to + at_x, x_codes + static_cast<int64_t>(i) * 8 * p.x.tile * 16, c * p.x.tile * 16, &full[b]);
-                bulk_g2s(to + at_sw, w_scales + static_cast<int64_t>(i) * kGroups * 512, g * 512, &full[b]);
-                bulk_g2s(to + at_sx, x_scales + static_cast<int64_t>(i) * kGroups * 512, g * 512, &full[b]);
-            }
-            // (none may be under way when the CTA leaves; all have landed when the products are done, unless someone gave up)
-            for (int j = max(0, i - p.ring); j < i; ++j) mbar_wait(&full[j % p.ring], (j / p.ring) & 1);
+        // copy `kind` of stage i
+        const uint8_t* const x_codes = p.x.codes + (static_cast<int64_t>(xt) * chunks + kChunks * st0) * p.x.tile * 16;
+        const uint8_t* const x_scales = p.x.scales + (static_cast<int64_t>(xt) * p.x.groups + kGroups * st0) * 512;
+        const auto copy = [&](int i, int kind) {
+            const int b = i % p.ring, c = min(kChunks, chunks - kChunks * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
+            uint8_t* const to = smem + b * stage_bytes;
+            if (kind == 0) mbar_arrive_expect_tx(&full[b], c * (p.w.tile + p.x.tile) * 16 + 2 * g * 512);
+            const uint8_t* const from = kind == 0   ? w_codes + static_cast<int64_t>(i) * kChunks * p.w.tile * 16
+                                        : kind == 1 ? x_codes + static_cast<int64_t>(i) * kChunks * p.x.tile * 16
+                                        : kind == 2 ? w_scales + static_cast<int64_t>(i) * kGroups * 512
+                                                    : x_scales + static_cast<int64_t>(i) * kGroups * 512;
+            bulk_g2s(to + (kind == 0 ? 0 : kind == 1 ? at_x : kind == 2 ? at_sw : at_sx), from,
+                     kind == 0 ? c * p.w.tile * 16 : kind == 1 ? c * p.x.tile * 16 : g * 512, &full[b]);
+        };
+        int i = min(n, p.ring);
+        if (lane < 4 * i) copy(lane >> 2, lane & 3);
+        for (; i < n; ++i) {
+            wait(&free_[i % p.ring], (i / p.ring - 1) & 1);
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            if (dead) break;
+            if (lane < 4) copy(i, lane);
         }
+        // (none may be under way when the CTA leaves; all have landed when the products are done, unless someone gave up)
+        for (int j = max(0, i - p.ring); j < i; ++j) mbar_wait(&full[j % p.ring], (j / p.ring) & 1);
         __syncwarp();
+        if (p.split > 1) {
+            if (!kEarly) cluster_arrive();
+            cluster_wait();
+        }
     } else if (warp == 1) {
         const uint32_t base = smem_addr(smem);
         const uint32_t idesc = tc_idesc_fp4<kBlock>(128, (cols + 7) / 8 * 8, 0);
@@ -109,7 +142,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
             dead = __any_sync(0xFFFFFFFFu, dead);
             if (dead) break;
             tc_after_sync();
-            const int steps = min(4, chunks / 2 - 4 * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
+            const int steps = min(kStageK / 64, chunks / 2 - kStageK / 64 * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
             const uint32_t at = base + b * stage_bytes;
             if (elect_one()) {
                 for (int j = 0; j < g; ++j) {
@@ -129,10 +162,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         }
         // the last products: none may be under way when the CTA's tensor memory goes
         for (int j = max(0, i - p.ring); j < i; ++j) mbar_wait(&free_[j % p.ring], (j / p.ring) & 1);
+        __syncwarp();
+        if (p.split > 1) {
+            if (!kEarly) cluster_arrive();
+            cluster_wait();
+        }
     } else {
+        const int me = tid - 64;  // of 128
+        // the scales of rows and tokens, while the products run
+        const int item_first = item0 + me, q = item_first & 31;  // (the same four rows for all of them)
+        const float4 ws = *reinterpret_cast<const float4*>(p.w.row_scale + wt * 128 + 4 * q);
+        if (me < cols) s_x_scale[me] = p.x.row_scale[xt * 128 + me];
         wait(&done, 0);
         __syncwarp();
         tc_after_sync();
+        if (!kEarly && p.split > 1) cluster_arrive();
         // sums [token][weight row] over the ring, which nobody needs any more
         float* const part = reinterpret_cast<float*>(smem);
         const int row = 32 * (warp & 3) + lane;
@@ -144,44 +188,46 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
             for (int j = 0; j < 8; ++j)
                 if (c + j < cols) part[(c + j) * 128 + row] = __uint_as_float(r[j]);
         }
+        __syncwarp();
+        named_bar_sync(1, 128);
+        const float4* const sums = reinterpret_cast<const float4*>(smem);
+        if (p.split > 1) {
+            cluster_wait();
+            for (int d = 1; d < p.split; ++d) {
+                const int to = rank + d < p.split ? rank + d : rank + d - p.split;  // (not all to the same one at a time)
+                const int from0 = min(items, share * to), from1 = min(items, share * (to + 1));
+                const uint32_t place = peer_addr(got + share * (rank < to ? rank : rank - 1), to), bar = peer_addr(&sent, to);
+                for (int item = from0 + me; item < from1; item += 128) send16(place + (item - from0) * 16, sums[item], bar);
+            }
+            wait(&sent, 0);
+        }
+        // four weight rows of a token a thread
+        const int quads = (rows + 3) / 4;
+        T* const y = static_cast<T*>(p.y) + static_cast<int64_t>(xt) * 128 * p.stride + wt * 128;
+        const bool vec = p.stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
+        for (int item = item_first; item < item1; item += 128) {
+            const int t = item >> 5;
+            if (q >= quads) break;
+            const float xs = s_x_scale[t];
+            float4 v = rank == 0 ? sums[item] : got[item - item0];
+            for (int r = 1; r < p.split; ++r) {
+                const float4 o = r == rank ? sums[item] : got[share * (r < rank ? r : r - 1) + item - item0];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            const float f[4] = {row_scaled(v.x, xs, ws.x), row_scaled(v.y, xs, ws.y), row_scaled(v.z, xs, ws.z), row_scaled(v.w, xs, ws.w)};
+            T* const to = y + t * p.stride + 4 * q;
+            if (vec && 4 * q + 4 <= rows) {
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_two<T>(f[0], f[1]), pack_two<T>(f[2], f[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * q + j < rows) to[j] = from_f32<T>(f[j]);
+            }
+        }
     }
     __syncwarp();
     tc_before_sync();
-    if (p.split > 1) cluster_arrive_wait();
-    else __syncthreads();
-    tc_after_sync();
-    // four weight rows of a token a thread
-    const uint32_t part = smem_addr(smem);
-    const int quads = (rows + 3) / 4, items = cols * 32;
-    T* const y = static_cast<T*>(p.y) + static_cast<int64_t>(xt) * 128 * p.stride + wt * 128;
-    const bool vec = p.stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
-    for (int item = items * rank / p.split + tid; item < items * (rank + 1) / p.split; item += kFewThreads) {
-        const int t = item >> 5, q = item & 31;
-        if (q >= quads) continue;
-        float4 v;
-        if (p.split == 1) {
-            v = *reinterpret_cast<const float4*>(smem + item * 16);
-        } else {
-            v = ld_peer(part + item * 16, 0);
-            for (int r = 1; r < p.split; ++r) {
-                const float4 o = ld_peer(part + item * 16, r);
-                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-        }
-        const float xs = p.x.row_scale[xt * 128 + t];
-        const float4 ws = *reinterpret_cast<const float4*>(p.w.row_scale + wt * 128 + 4 * q);
-        const float f[4] = {row_scaled(v.x, xs, ws.x), row_scaled(v.y, xs, ws.y), row_scaled(v.z, xs, ws.z), row_scaled(v.w, xs, ws.w)};
-        T* const to = y + t * p.stride + 4 * q;
-        if (vec && 4 * q + 4 <= rows) {
-            *reinterpret_cast<uint2*>(to) = make_uint2(pack_two<T>(f[0], f[1]), pack_two<T>(f[2], f[3]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * q + j < rows) to[j] = from_f32<T>(f[j]);
-        }
-    }
-    __syncwarp();
-    if (p.split > 1) cluster_arrive_wait();  // (the others may still read this one's sums)
+    __syncthreads();
     if (warp == 1) tc_dealloc(tmem, kFewCols);
 }
 

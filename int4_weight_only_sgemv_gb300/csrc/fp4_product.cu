@@ -8,23 +8,23 @@ namespace sgemv {
 
 namespace {
 
-template <typename T, int kBlock>
-cudaError_t launch_few(const ProductParams& p, int64_t tiles, cudaStream_t s) {
-    auto kern = fp4_few_kernel<T, kBlock>;
+template <typename T, int kBlock, int kStageK>
+cudaError_t launch_few_stage(const ProductParams& p, int64_t tiles, int smem, cudaStream_t s) {
+    auto kern = fp4_few_kernel<T, kBlock, kStageK>;
     static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (attr_set[dev].load() == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMost);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.dynamicSmemBytes = static_cast<unsigned>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -36,6 +36,10 @@ cudaError_t launch_few(const ProductParams& p, int64_t tiles, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+template <typename T, int kBlock>
+cudaError_t launch_few(const ProductParams& p, int64_t tiles, int smem, cudaStream_t s) {
+    return few_stage_k(p.x.tile) == 512 ? launch_few_stage<T, kBlock, 512>(p, tiles, smem, s) : launch_few_stage<T, kBlock, 256>(p, tiles, smem, s);
 }
 
 }  // namespace
@@ -65,16 +69,22 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     ProductParams p;
     p.w = Fp4Matrix(w, w_dev), p.x = Fp4Matrix(x, x_dev);
     p.y = y_dev, p.stride = st, p.status = status_dev;
-    p.k_stages = (w.kp + kStageK - 1) / kStageK;
+    p.k_stages = (w.kp + few_stage_k(x.tile) - 1) / few_stage_k(x.tile);
     p.x_tiles = (x.rows + 127) / 128;
     const int64_t tiles = static_cast<int64_t>((w.rows + 127) / 128) * p.x_tiles;
-    // CTAs a tile: as many as fill two places an SM, each with a stage at least
-    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * di.sm_count / tiles, p.k_stages})));
-    p.ring = std::min(kFewMaxRing, kFewSmem / few_stage_bytes(w.block, x.tile));
+    // CTAs a tile: as many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
+    // tiles of 128 tokens are sent leaves one place an SM.
+    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * di.sm_count / tiles, p.k_stages / 2})));
+    if (x.tile == 128 && p.split > 4) p.split = std::min(p.split, std::max(4, static_cast<int>(di.sm_count / tiles)));
+    const int stage = few_stage_bytes(w.block, x.tile), sent = p.split > 1 ? few_sent(x.tile, p.split) : 0;
+    const bool early = few_stage_k(x.tile) == 512;
+    p.ring = std::min({kFewMaxRing, (kFewSmem - (early ? sent : 0)) / stage, (p.k_stages + p.split - 1) / p.split});
+    // (the sums of a tile take the ring's place, and in wide tiles what is sent too)
+    const int smem = std::max(early ? std::max(p.ring * stage, x.tile * 512) + sent : std::max(p.ring * stage, x.tile * 512 + sent), kFewLeast);
     if (tiles * p.split > INT_MAX) return SGEMV_ERR_SHAPE;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = dtype == SGEMV_F16;
-    const cudaError_t e = w.block == 16 ? (half ? launch_few<__half, 16>(p, tiles, s) : launch_few<__nv_bfloat16, 16>(p, tiles, s))
-                                        : (half ? launch_few<__half, 32>(p, tiles, s) : launch_few<__nv_bfloat16, 32>(p, tiles, s));
+    const cudaError_t e = w.block == 16 ? (half ? launch_few<__half, 16>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 16>(p, tiles, smem, s))
+                                        : (half ? launch_few<__half, 32>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 32>(p, tiles, smem, s));
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }

@@ -50,8 +50,6 @@ __device__ __forceinline__ float row_scaled(float sum, float a, float b) {
     return ldexpf(sum, static_cast<int>(__float_as_uint(a) >> 23) + static_cast<int>(__float_as_uint(b) >> 23) - 254);
 }
 
-constexpr int kStageK = 256;  // columns of a stage of the products' rings
-
 struct ProductParams {
     Fp4Matrix w, x;
     void* y;
