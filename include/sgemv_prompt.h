@@ -72,7 +72,7 @@ int sgemv_fp4_read(const sgemv_fp4_layout* layout, const void* packed_dev, void*
  *   status_dev : nullable; SGEMV_ERR_TIMEOUT if a bounded wait for a copy gave up (y is then invalid).
  * The same inputs give the same bits: sums are split by sizes alone and joined in a fixed order.
  * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_FORMAT (layout fields; different k or block), SGEMV_ERR_ALIGN, SGEMV_ERR_SHAPE (more than
- * 2^31 - 1 tiles of 128 x 128), SGEMV_ERR_CUDA.
+ * 2^28 - 1 tiles of 128 x 128), SGEMV_ERR_CUDA.
  */
 int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w_dev, const sgemv_fp4_layout* x_layout, const void* x_dev,
                       void* y_dev, int dtype, int64_t stride, int32_t* status_dev, void* stream);

@@ -34,13 +34,6 @@ __host__ __device__ constexpr int few_stage_bytes(int block, int x_tile) {
 __host__ __device__ inline int few_share(int x_tile, int split) { return (x_tile * 32 + split - 1) / split; }
 __host__ __device__ inline int few_sent(int x_tile, int split) { return (split - 1) * few_share(x_tile, split) * 16; }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {  // the same place in another CTA's shared memory
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    return a;
-}
 // 16 bytes into a peer's shared memory, counted on its barrier.
 __device__ __forceinline__ void send16(uint32_t to, float4 v, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "f"(v.x), "f"(v.y),

@@ -1,0 +1,288 @@
+// The product of two 4-bit matrices: the kernel of calls with many tiles.
+//
+// Bound by the products' rate, and by what feeds them: a CTA that computes 128 x 128 outputs reads 36 KB for 256 columns, 256 cycles of the tensor
+// cores, and an SM takes in about 50 bytes a cycle. So two SMs share a tile of 256 tokens x 256 weight rows (cta_group::2): each holds the
+// codes of 128 tokens and of 128 weight rows, and its tensor memory the sums of its 128 tokens; 38 KB for 512 cycles.
+// One CTA an SM goes through tiles, tokens fastest within groups of 8 token tiles, so that what the SMs read at a time stays in L2. Roles:
+//   warp 0      issues the copies of its SM's half, a lane each
+//   warp 1      of the first CTA issues the products of both; of the second, tells the first what has landed
+//   warps 2-5   take the sums out, a thread a token, and write them
+// Tensor memory: two sets of sums, columns 0..255 and 208..463, and the scales in the last 48. The columns that the sets share are taken out
+// first, and then the next tile's products start while the rest is written.
+#pragma once
+
+#include "fp4_tc.cuh"
+
+namespace sgemv {
+
+template <int kBlock>
+struct ManyShape {
+    static constexpr int kStageK = 256, kChunks = kStageK / 32, kGroups = kStageK / (4 * kBlock);
+    static constexpr int kCodes = 128 * kStageK / 2, kScales = kGroups * 512;
+    static constexpr int kStage = 2 * kCodes + 3 * kScales;  // codes of tokens and weights; scales of 128 tokens and 256 weight rows
+    static constexpr int kRing = 5, kThreads = 192;
+    static constexpr int kSmem = kRing * kStage + 4 * 4096;  // and 32 rows of 64 outputs a warp
+    static constexpr int kSecond = 208, kShared = 256 - kSecond;  // columns
+    static constexpr int kScaleCols = kSecond + 256;
+    static_assert(kScaleCols + 12 * kGroups <= 512, "tensor memory");
+};
+constexpr int kManyGroup = 8;  // token tiles
+
+__device__ __forceinline__ void tc_alloc_pair(uint32_t* smem_slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_slot)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// On the barrier at this place in both CTAs, once the products issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "h"(static_cast<unsigned short>(3))
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {  // in any CTA of the cluster
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for arrivals from the other CTA too.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((i & 63u) == 0 && global_ns() - t0 > kMbarWaitNs) return false;
+    }
+}
+
+template <typename T, int kBlock>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::kThreads, 1) fp4_many_kernel(const ProductParams p) {
+    using S = ManyShape<kBlock>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[S::kRing], other_full[S::kRing], free_[S::kRing], sums_full, sums_free;
+    __shared__ uint32_t s_tmem;
+    __shared__ __align__(16) float s_w_scale[256];
+    __shared__ float s_least[4], s_most[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+    const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int chunks = p.w.kp / 32, tiles = p.tiles_x * p.tiles_w;
+    if (tid == 0) {
+        for (int i = 0; i < S::kRing; ++i) mbar_init(&full[i], 1), mbar_init(&other_full[i], 1), mbar_init(&free_[i], 1);
+        mbar_init(&sums_full, 1), mbar_init(&sums_free, 8);
+        mbar_fence_init();
+    }
+    pdl_launch_dependents();
+    __syncthreads();
+    if (warp == 1) tc_alloc_pair(&s_tmem, 512);
+    tc_before_sync();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    tc_after_sync();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (dead || mbar_wait_cluster(bar, parity)) return;
+        dead = true;
+        report(p.status, SGEMV_ERR_TIMEOUT);
+    };
+    const auto tile_at = [&](int tile, int& xt, int& wt) {
+        const int per = kManyGroup * p.tiles_w, group = tile / per, in = tile % per;
+        const int width = min(kManyGroup, p.tiles_x - group * kManyGroup);
+        xt = group * kManyGroup + in % width, wt = in / width;
+    };
+    const int have_x = (p.x.rows + 127) / 128, have_w = (p.w.rows + 127) / 128;  // tiles of 128 that there are
+
+    if (warp == 0) {
+        int g = 0;
+#pragma unroll 1
+        for (int tile = pair; tile < tiles && !dead; tile += pairs) {
+            int xt, wt;
+            tile_at(tile, xt, wt);
+            // lane: 0 tokens' codes, 1 weights' codes, 2 tokens' scales, 3 and 4 weights' scales (of both halves)
+            const int x_tile = 2 * xt + rank, w_tile = 2 * wt + (lane == 1 ? rank : lane - 3);
+            const bool of_x = lane == 0 || lane == 2;
+            const bool there = lane < 5 && (of_x ? x_tile < have_x : w_tile < have_w);
+            const Fp4Matrix& m = of_x ? p.x : p.w;
+            const int t = of_x ? x_tile : w_tile;
+            const uint8_t* const from = lane < 2 ? m.codes + static_cast<int64_t>(t) * chunks * 2048 : m.scales + static_cast<int64_t>(t) * m.groups * 512;
+            const uint32_t to = lane < 2 ? lane * S::kCodes : 2 * S::kCodes + (lane - 2) * S::kScales;
+#pragma unroll 1
+            for (int i = 0; i < p.k_stages; ++i, ++g) {
+                const int b = g % S::kRing;
+                if (g >= S::kRing) wait(&free_[b], (g / S::kRing - 1) & 1);
+                dead = __any_sync(0xFFFFFFFFu, dead);
+                if (dead) break;
+                const int c = min(S::kChunks, chunks - S::kChunks * i), n = min(S::kGroups, p.w.groups - S::kGroups * i);
+                const uint32_t bytes = !there ? 0 : lane < 2 ? c * 2048 : n * 512;
+                const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&full[b], all);
+                __syncwarp();
+                if (bytes) bulk_g2s(smem + b * S::kStage + to, from + static_cast<int64_t>(i) * (lane < 2 ? S::kChunks * 2048 : S::kScales), bytes, &full[b]);
+            }
+        }
+        // (all have landed, unless someone gave up)
+        for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
+    } else if (warp == 1) {
+        int g = 0, turn = 0;
+        if (rank == 0) {
+            const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0), t_sa = tmem + S::kScaleCols, t_sb = t_sa + 4 * S::kGroups;
+            constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, 256, 0);
+#pragma unroll 1
+            for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+                if (turn > 0) wait(&sums_free, (turn - 1) & 1);
+                const uint32_t d = tmem + ((turn & 1) ? S::kSecond : 0);
+#pragma unroll 1
+                for (int i = 0; i < p.k_stages; ++i, ++g) {
+                    const int b = g % S::kRing;
+                    wait(&full[b], (g / S::kRing) & 1);
+                    wait(&other_full[b], (g / S::kRing) & 1);
+                    dead = __any_sync(0xFFFFFFFFu, dead);
+                    tc_after_sync();
+                    const int steps = min(S::kStageK / 64, chunks / 2 - S::kStageK / 64 * i), n = min(S::kGroups, p.w.groups - S::kGroups * i);
+                    const uint32_t at = base + b * S::kStage;
+                    if (elect_one()) {
+                        if (!dead) {
+                            const uint64_t sd = tc_desc_plain(at + 2 * S::kCodes, 0);
+#pragma unroll
+                            for (int j = 0; j < S::kGroups; ++j) {
+                                if (j < n) {
+                                    tc_copy_scales<2>(t_sa + 4 * j, sd + 32 * j);
+                                    tc_copy_scales<2>(t_sb + 8 * j, sd + 32 * (j + S::kGroups));
+                                    tc_copy_scales<2>(t_sb + 8 * j + 4, sd + 32 * (j + 2 * S::kGroups));
+                                }
+                            }
+                            const uint64_t xd = tc_desc_plain(at, 2048), wd = tc_desc_plain(at + S::kCodes, 2048);
+#pragma unroll
+                            for (int j = 0; j < S::kStageK / 64; ++j) {
+                                const uint32_t col = kBlock == 16 ? j : j / 2, id = kBlock == 16 ? 0 : 2 * (j & 1);
+                                if (j < steps)
+                                    tc_mma_fp4<kBlock, 2>(d, xd + j * 256, wd + j * 256, idesc | (id << 4) | (id << 29), t_sa + 4 * col, t_sb + 8 * col,
+                                                          i > 0 || j > 0);
+                            }
+                        }
+                        tc_commit_pair(&free_[b]);
+                        if (i == p.k_stages - 1) tc_commit_pair(&sums_full);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else {
+            const uint32_t first = peer_addr(other_full, 0);
+#pragma unroll 1
+            for (int tile = pair; tile < tiles; tile += pairs)
+#pragma unroll 1
+                for (int i = 0; i < p.k_stages; ++i, ++g) {
+                    const int b = g % S::kRing;
+                    wait(&full[b], (g / S::kRing) & 1);
+                    if (lane == 0) arrive_at(first + 8 * b);
+                    __syncwarp();
+                }
+        }
+        // the last products: none may be under way when the CTA's memory goes
+        for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait_cluster(&free_[i % S::kRing], (i / S::kRing) & 1);
+    } else {
+        const int me = tid - 64, row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16, told = peer_addr(&sums_free, 0);
+        const bool vec = p.stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+        int turn = 0;
+#pragma unroll 1
+        for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+            int xt, wt;
+            tile_at(tile, xt, wt);
+            const int token = xt * 256 + rank * 128 + row, n0 = wt * 256;
+            // the scales of the rows, and whether any product of two leaves binary32's normal range
+            const float xs = token < p.x.rows ? p.x.row_scale[token] : 1.0f;
+            float least = INFINITY, most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = 2 * me + i;
+                const float f = n0 + n < p.w.rows ? p.w.row_scale[n0 + n] : 1.0f;
+                s_w_scale[n] = f;
+                least = fminf(least, f == f ? f : 0.0f), most = fmaxf(most, f);
+            }
+            const unsigned lo = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(least)), hi = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+            if (lane == 0) s_least[warp & 3] = __uint_as_float(lo), s_most[warp & 3] = __uint_as_float(hi);
+            named_bar_sync(1, 128);
+            least = fminf(fminf(s_least[0], s_least[1]), fminf(s_least[2], s_least[3]));
+            most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+            const bool plain = __all_sync(0xFFFFFFFFu, xs * least >= 1.17549435e-38f && xs * most < INFINITY);
+            wait(&sums_full, turn & 1);
+            __syncwarp();
+            tc_after_sync();
+            const uint32_t from = tmem + lanes + ((turn & 1) ? S::kSecond : 0);
+            const int token0 = token - lane, rows = min(32, p.x.rows - token0);
+            // 64 columns at a time, first those that the other set of sums shares, through shared memory, so that whole lines of rows are written
+            uint8_t* const stage = smem + S::kRing * S::kStage + (warp & 3) * 4096;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int part = ((turn & 1) ? k : k + 3) & 3, col = n0 + 64 * part;
+                uint32_t r[2][32];
+                tc_ld32(r[0], from + 64 * part);
+                tc_ld32(r[1], from + 64 * part + 32);
+                tc_wait_ld();
+                if (k == 0) {
+                    tc_before_sync();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(told);
+                }
+                if (col >= p.w.rows) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int n = 8 * i + 2 * e;
+                        const float2 ws = *reinterpret_cast<const float2*>(&s_w_scale[64 * part + n]);
+                        const float v0 = __uint_as_float(r[n / 32][n % 32]), v1 = __uint_as_float(r[n / 32][n % 32 + 1]);
+                        h[e] = plain ? pack_two<T>(v0 * (xs * ws.x), v1 * (xs * ws.y)) : pack_two<T>(row_scaled(v0, xs, ws.x), row_scaled(v1, xs, ws.y));
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ lane) & 7) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                __syncwarp();
+                T* const y = static_cast<T*>(p.y) + token0 * p.stride + col;
+                const int cols = min(64, p.w.rows - col);
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3), piece = lane & 7;
+                        const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((piece ^ rr) & 7) * 16);
+                        T* const to = y + rr * p.stride + 8 * piece;
+                        if (rr < rows && 8 * piece + 8 <= cols) {
+                            *reinterpret_cast<uint4*>(to) = h;
+                        } else if (rr < rows) {
+                            const T* const e = reinterpret_cast<const T*>(&h);
+                            for (int n = 0; n < cols - 8 * piece; ++n) to[n] = e[n];
+                        }
+                    }
+                } else {
+#pragma unroll 4
+                    for (int rr = 0; rr < rows; ++rr) {
+                        const uint8_t* const line = stage + rr * 128;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int n = 32 * i + lane;
+                            if (n < cols) y[rr * p.stride + n] = *reinterpret_cast<const T*>(line + ((n / 8 ^ rr) & 7) * 16 + n % 8 * 2);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            named_bar_sync(1, 128);  // (the scales' place)
+        }
+    }
+    __syncwarp();
+    tc_before_sync();
+    cluster_arrive();
+    cluster_wait();
+    tc_after_sync();
+    if (warp == 1) tc_dealloc_pair(tmem, 512);
+}
+
+}  // namespace sgemv

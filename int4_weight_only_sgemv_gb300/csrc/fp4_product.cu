@@ -3,10 +3,16 @@
 #include <climits>
 
 #include "fp4_few.cuh"
+#include "fp4_many.cuh"
 
 namespace sgemv {
 
 namespace {
+
+// Whether a call goes to the kernel of many tiles.
+bool many_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x, int sms) {
+    return x.rows > 128 && w.rows > 128;
+}
 
 template <typename T, int kBlock, int kStageK>
 cudaError_t launch_few_stage(const ProductParams& p, int64_t tiles, int smem, cudaStream_t s) {
@@ -42,6 +48,24 @@ cudaError_t launch_few(const ProductParams& p, int64_t tiles, int smem, cudaStre
     return few_stage_k(p.x.tile) == 512 ? launch_few_stage<T, kBlock, 512>(p, tiles, smem, s) : launch_few_stage<T, kBlock, 256>(p, tiles, smem, s);
 }
 
+template <typename T, int kBlock>
+cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
+    using S = ManyShape<kBlock>;
+    auto kern = fp4_many_kernel<T, kBlock>;
+    static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (attr_set[dev].load() == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(1);
+    }
+    const int pairs = std::min(p.tiles_x * p.tiles_w, sms / 2);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(S::kThreads), S::kSmem, s, p);
+}
+
 }  // namespace
 
 }  // namespace sgemv
@@ -72,6 +96,17 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     p.k_stages = (w.kp + few_stage_k(x.tile) - 1) / few_stage_k(x.tile);
     p.x_tiles = (x.rows + 127) / 128;
     const int64_t tiles = static_cast<int64_t>((w.rows + 127) / 128) * p.x_tiles;
+    if (tiles * 8 > INT_MAX) return SGEMV_ERR_SHAPE;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool half = dtype == SGEMV_F16;
+    if (many_tiles(w, x, di.sm_count)) {
+        p.tiles_x = (x.rows + 255) / 256, p.tiles_w = (w.rows + 255) / 256;
+        p.k_stages = (w.kp + ManyShape<16>::kStageK - 1) / ManyShape<16>::kStageK;
+        const int sms = di.sm_count;
+        const cudaError_t e = w.block == 16 ? (half ? launch_many<__half, 16>(p, sms, s) : launch_many<__nv_bfloat16, 16>(p, sms, s))
+                                            : (half ? launch_many<__half, 32>(p, sms, s) : launch_many<__nv_bfloat16, 32>(p, sms, s));
+        return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
+    }
     // CTAs a tile: as many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
     // tiles of 128 tokens are sent leaves one place an SM.
     p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * di.sm_count / tiles, p.k_stages / 2})));
@@ -81,9 +116,6 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     p.ring = std::min({kFewMaxRing, (kFewSmem - (early ? sent : 0)) / stage, (p.k_stages + p.split - 1) / p.split});
     // (the sums of a tile take the ring's place, and in wide tiles what is sent too)
     const int smem = std::max(early ? std::max(p.ring * stage, x.tile * 512) + sent : std::max(p.ring * stage, x.tile * 512 + sent), kFewLeast);
-    if (tiles * p.split > INT_MAX) return SGEMV_ERR_SHAPE;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool half = dtype == SGEMV_F16;
     const cudaError_t e = w.block == 16 ? (half ? launch_few<__half, 16>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 16>(p, tiles, smem, s))
                                         : (half ? launch_few<__half, 32>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 32>(p, tiles, smem, s));
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
