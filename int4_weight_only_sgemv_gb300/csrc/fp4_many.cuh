@@ -4,12 +4,14 @@
 // cores, and an SM takes in about 50 bytes a cycle. So two SMs share a tile of 256 tokens x 256 weight rows (cta_group::2): each holds the
 // codes of 128 tokens and of 128 weight rows, and its tensor memory the sums of its 128 tokens; 38 KB for 512 cycles.
 // One CTA an SM goes through tiles, tokens fastest within groups of 8 token tiles, so that what the SMs read at a time stays in L2. Roles:
-//   warp 0      issues the copies of its SM's half, a lane each
-//   warp 1      of the first CTA issues the products of both; of the second, tells the first what has landed
+//   warp 0      issues the copies of its SM's half, a lane each; what lands in either is counted on the first one's barriers
+//   warp 1      of the first CTA issues the products of both
 //   warps 2-5   take the sums out, a thread a token, and write them
 // Tensor memory: two sets of sums, columns 0..255 and 208..463, and the scales in the last 48. The columns that the sets share are taken out
 // first, and then the next tile's products start while the rest is written.
 #pragma once
+
+#include <cuda.h>
 
 #include "fp4_tc.cuh"
 
@@ -28,6 +30,17 @@ struct ManyShape {
 };
 constexpr int kManyGroup = 8;  // token tiles
 
+// A 4-bit matrix as tensors of 8-byte elements: codes [tile][chunk of 32 columns][2048 bytes], scales [tile][group][512 bytes].
+struct Fp4Maps {
+    CUtensorMap codes, scales;
+};
+// A box of a tensor into this CTA's shared memory, counted on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void tc_alloc_pair(uint32_t* smem_slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_slot)), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -61,10 +74,10 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 }
 
 template <typename T, int kBlock>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::kThreads, 1) fp4_many_kernel(const ProductParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::kThreads, 1) fp4_many_kernel(const __grid_constant__ Fp4Maps x_maps, const __grid_constant__ Fp4Maps w_maps, const __grid_constant__ ProductParams p) {
     using S = ManyShape<kBlock>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S::kRing], other_full[S::kRing], free_[S::kRing], sums_full, sums_free;
+    __shared__ __align__(8) uint64_t full[S::kRing], free_[S::kRing], sums_full, sums_free;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_w_scale[256];
     __shared__ float s_least[4], s_most[4];
@@ -72,7 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int chunks = p.w.kp / 32, tiles = p.tiles_x * p.tiles_w;
     if (tid == 0) {
-        for (int i = 0; i < S::kRing; ++i) mbar_init(&full[i], 1), mbar_init(&other_full[i], 1), mbar_init(&free_[i], 1);
+        for (int i = 0; i < S::kRing; ++i) mbar_init(&full[i], 1), mbar_init(&free_[i], 1);
         mbar_init(&sums_full, 1), mbar_init(&sums_free, 8);
         mbar_fence_init();
     }
@@ -88,7 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     pdl_wait();
     bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (dead || mbar_wait_cluster(bar, parity)) return;
+        if (dead || mbar_wait(bar, parity)) return;
         dead = true;
         report(p.status, SGEMV_ERR_TIMEOUT);
     };
@@ -97,38 +110,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         const int width = min(kManyGroup, p.tiles_x - group * kManyGroup);
         xt = group * kManyGroup + in % width, wt = in / width;
     };
-    const int have_x = (p.x.rows + 127) / 128, have_w = (p.w.rows + 127) / 128;  // tiles of 128 that there are
 
     if (warp == 0) {
+        const uint32_t first_full = peer_addr(full, 0);
         int g = 0;
 #pragma unroll 1
         for (int tile = pair; tile < tiles && !dead; tile += pairs) {
             int xt, wt;
             tile_at(tile, xt, wt);
-            // lane: 0 tokens' codes, 1 weights' codes, 2 tokens' scales, 3 and 4 weights' scales (of both halves)
-            const int x_tile = 2 * xt + rank, w_tile = 2 * wt + (lane == 1 ? rank : lane - 3);
-            const bool of_x = lane == 0 || lane == 2;
-            const bool there = lane < 5 && (of_x ? x_tile < have_x : w_tile < have_w);
-            const Fp4Matrix& m = of_x ? p.x : p.w;
-            const int t = of_x ? x_tile : w_tile;
-            const uint8_t* const from = lane < 2 ? m.codes + static_cast<int64_t>(t) * chunks * 2048 : m.scales + static_cast<int64_t>(t) * m.groups * 512;
-            const uint32_t to = lane < 2 ? lane * S::kCodes : 2 * S::kCodes + (lane - 2) * S::kScales;
 #pragma unroll 1
             for (int i = 0; i < p.k_stages; ++i, ++g) {
                 const int b = g % S::kRing;
                 if (g >= S::kRing) wait(&free_[b], (g / S::kRing - 1) & 1);
                 dead = __any_sync(0xFFFFFFFFu, dead);
                 if (dead) break;
-                const int c = min(S::kChunks, chunks - S::kChunks * i), n = min(S::kGroups, p.w.groups - S::kGroups * i);
-                const uint32_t bytes = !there ? 0 : lane < 2 ? c * 2048 : n * 512;
-                const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
-                if (lane == 0) mbar_arrive_expect_tx(&full[b], all);
+                // (whole boxes, zeros where the matrices end)
+                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[b], 2 * S::kStage);
                 __syncwarp();
-                if (bytes) bulk_g2s(smem + b * S::kStage + to, from + static_cast<int64_t>(i) * (lane < 2 ? S::kChunks * 2048 : S::kScales), bytes, &full[b]);
+                uint8_t* const to = smem + b * S::kStage;
+                const uint32_t bar = first_full + 8 * b;
+                if (lane == 0) tma_load_pair(to, &x_maps.codes, 0, S::kChunks * i, 2 * xt + rank, bar);
+                if (lane == 1) tma_load_pair(to + S::kCodes, &w_maps.codes, 0, S::kChunks * i, 2 * wt + rank, bar);
+                if (lane == 2) tma_load_pair(to + 2 * S::kCodes, &x_maps.scales, 0, S::kGroups * i, 2 * xt + rank, bar);
+                if (lane == 3) tma_load_pair(to + 2 * S::kCodes + S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt, bar);
+                if (lane == 4) tma_load_pair(to + 2 * S::kCodes + 2 * S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt + 1, bar);
             }
         }
-        // (all have landed, unless someone gave up)
-        for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
+        // (all have landed, unless someone gave up: the first CTA sees it, and the second leaves after it)
+        if (rank == 0)
+            for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
     } else if (warp == 1) {
         int g = 0, turn = 0;
         if (rank == 0) {
@@ -136,13 +146,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
             constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, 256, 0);
 #pragma unroll 1
             for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
-                if (turn > 0) wait(&sums_free, (turn - 1) & 1);
+                if (turn > 0 && !dead && !mbar_wait_cluster(&sums_free, (turn - 1) & 1)) {
+                    dead = true;
+                    report(p.status, SGEMV_ERR_TIMEOUT);
+                }
                 const uint32_t d = tmem + ((turn & 1) ? S::kSecond : 0);
 #pragma unroll 1
                 for (int i = 0; i < p.k_stages; ++i, ++g) {
                     const int b = g % S::kRing;
                     wait(&full[b], (g / S::kRing) & 1);
-                    wait(&other_full[b], (g / S::kRing) & 1);
                     dead = __any_sync(0xFFFFFFFFu, dead);
                     tc_after_sync();
                     const int steps = min(S::kStageK / 64, chunks / 2 - S::kStageK / 64 * i), n = min(S::kGroups, p.w.groups - S::kGroups * i);
@@ -173,20 +185,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
                     __syncwarp();
                 }
             }
-        } else {
-            const uint32_t first = peer_addr(other_full, 0);
-#pragma unroll 1
-            for (int tile = pair; tile < tiles; tile += pairs)
-#pragma unroll 1
-                for (int i = 0; i < p.k_stages; ++i, ++g) {
-                    const int b = g % S::kRing;
-                    wait(&full[b], (g / S::kRing) & 1);
-                    if (lane == 0) arrive_at(first + 8 * b);
-                    __syncwarp();
-                }
         }
         // the last products: none may be under way when the CTA's memory goes
-        for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait_cluster(&free_[i % S::kRing], (i / S::kRing) & 1);
+        for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&free_[i % S::kRing], (i / S::kRing) & 1);
     } else {
         const int me = tid - 64, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16, told = peer_addr(&sums_free, 0);

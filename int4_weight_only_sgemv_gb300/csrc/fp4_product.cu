@@ -4,6 +4,7 @@
 
 #include "fp4_few.cuh"
 #include "fp4_many.cuh"
+#include "tensor_map.cuh"
 
 namespace sgemv {
 
@@ -48,6 +49,15 @@ cudaError_t launch_few(const ProductParams& p, int64_t tiles, int smem, cudaStre
     return few_stage_k(p.x.tile) == 512 ? launch_few_stage<T, kBlock, 512>(p, tiles, smem, s) : launch_few_stage<T, kBlock, 256>(p, tiles, smem, s);
 }
 
+template <int kBlock>
+bool map_fp4(Fp4Maps* maps, const Fp4Matrix& m) {
+    using S = ManyShape<kBlock>;
+    const cuuint64_t tiles = static_cast<cuuint64_t>((m.rows + 127) / 128), chunks = static_cast<cuuint64_t>(m.kp / 32), groups = static_cast<cuuint64_t>(m.groups);
+    return encode_map(&maps->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.codes, {256, chunks, tiles}, {2048, chunks * 2048}, {256, S::kChunks, 1},
+                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
+           encode_map(&maps->scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scales, {64, groups, tiles}, {512, groups * 512}, {64, S::kGroups, 1},
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+}
 template <typename T, int kBlock>
 cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
     using S = ManyShape<kBlock>;
@@ -62,8 +72,10 @@ cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr_set[dev].store(1);
     }
+    Fp4Maps x_maps, w_maps;
+    if (!map_fp4<kBlock>(&x_maps, p.x) || !map_fp4<kBlock>(&w_maps, p.w)) return cudaErrorInvalidValue;
     const int pairs = std::min(p.tiles_x * p.tiles_w, sms / 2);
-    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(S::kThreads), S::kSmem, s, p);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(S::kThreads), S::kSmem, s, x_maps, w_maps, p);
 }
 
 }  // namespace

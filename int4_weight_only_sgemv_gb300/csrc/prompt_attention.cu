@@ -4,39 +4,22 @@
 #include <type_traits>
 
 #include "prompt_attention.cuh"
+#include "tensor_map.cuh"
 
 namespace sgemv {
 
 namespace {
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // Tiles of `tokens` tokens of `heads` neighbouring heads, 64 dims of a row at a time, swizzled for the tensor cores. (A stride of an axis of
 // length 1 is not used.)
 bool map_rows(CUtensorMap* map, const void* base, const sgemv_prompt_query& q, int all_heads, int64_t token_stride, int64_t head_stride, int tokens,
               int heads) {
-    const EncodeTiled encode = encode_tiled();
-    if (encode == nullptr) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(q.dim), static_cast<cuuint64_t>(all_heads), static_cast<cuuint64_t>(q.n_tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(all_heads > 1 ? head_stride : q.dim) * 2,
                                    static_cast<cuuint64_t>(q.n_tokens > 1 ? token_stride : static_cast<int64_t>(all_heads) * q.dim) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)}, step[3] = {1, 1, 1};
-    return encode(map, q.dtype == SGEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+    return encode_map(map, q.dtype == SGEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <typename T, int D>
