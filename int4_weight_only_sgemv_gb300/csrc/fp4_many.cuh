@@ -4,9 +4,10 @@
 // cores, and an SM takes in about 50 bytes a cycle. So two SMs share a tile of 256 tokens x 256 weight rows (cta_group::2): each holds the
 // codes of 128 tokens and of 128 weight rows, and its tensor memory the sums of its 128 tokens; 38 KB for 512 cycles.
 // One CTA an SM goes through tiles, tokens fastest within groups of 8 token tiles, so that what the SMs read at a time stays in L2. Roles:
-//   warp 0      issues the copies of its SM's half, a lane each; what lands in either is counted on the first one's barriers
-//   warp 1      of the first CTA issues the products of both
-//   warps 2-5   take the sums out, a thread a token, and write them
+//   warps 0-3   issue the copies of its SM's half, one each a stage (a copy takes 200 cycles to issue: five by one warp took 1270 a stage); what
+//               lands in either is counted on the first one's barriers
+//   warps 4-7   take the sums out, a thread a token, and write them
+//   warp 8      of the first CTA issues the products of both
 // Tensor memory: two sets of sums, columns 0..255 and 208..463, and the scales in the last 48. The columns that the sets share are taken out
 // first, and then the next tile's products start while the rest is written.
 #pragma once
@@ -22,7 +23,7 @@ struct ManyShape {
     static constexpr int kStageK = 256, kChunks = kStageK / 32, kGroups = kStageK / (4 * kBlock);
     static constexpr int kCodes = 128 * kStageK / 2, kScales = kGroups * 512;
     static constexpr int kStage = 2 * kCodes + 3 * kScales;  // codes of tokens and weights; scales of 128 tokens and 256 weight rows
-    static constexpr int kRing = 5, kThreads = 192;
+    static constexpr int kRing = 5, kThreads = 288;
     static constexpr int kSmem = kRing * kStage + 4 * 4096;  // and 32 rows of 64 outputs a warp
     static constexpr int kSecond = 208, kShared = 256 - kSecond;  // columns
     static constexpr int kScaleCols = kSecond + 256;
@@ -30,7 +31,8 @@ struct ManyShape {
 };
 constexpr int kManyGroup = 8;  // token tiles
 
-// A 4-bit matrix as tensors of 8-byte elements: codes [tile][chunk of 32 columns][2048 bytes], scales [tile][group][512 bytes].
+// A 4-bit matrix as tensors of 8-byte elements: codes [tile][chunk of 32 columns][2048 bytes], scales [tile][group][512 bytes] (the tokens' in boxes of
+// one tile, the weights' of two).
 struct Fp4Maps {
     CUtensorMap codes, scales;
 };
@@ -91,7 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     }
     pdl_launch_dependents();
     __syncthreads();
-    if (warp == 1) tc_alloc_pair(&s_tmem, 512);
+    if (warp == 8) tc_alloc_pair(&s_tmem, 512);
     tc_before_sync();
     __syncwarp();
     cluster_arrive();
@@ -111,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         xt = group * kManyGroup + in % width, wt = in / width;
     };
 
-    if (warp == 0) {
+    if (warp < 4) {
         const uint32_t first_full = peer_addr(full, 0);
         int g = 0;
 #pragma unroll 1
@@ -125,21 +127,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
                 dead = __any_sync(0xFFFFFFFFu, dead);
                 if (dead) break;
                 // (whole boxes, zeros where the matrices end)
-                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[b], 2 * S::kStage);
+                if (elect_one()) {
+                    uint8_t* const to = smem + b * S::kStage;
+                    const uint32_t bar = first_full + 8 * b;
+                    if (warp == 0) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[b], 2 * S::kStage);
+                        tma_load_pair(to, &x_maps.codes, 0, S::kChunks * i, 2 * xt + rank, bar);
+                    } else if (warp == 1) {
+                        tma_load_pair(to + S::kCodes, &w_maps.codes, 0, S::kChunks * i, 2 * wt + rank, bar);
+                    } else if (warp == 2) {
+                        tma_load_pair(to + 2 * S::kCodes, &x_maps.scales, 0, S::kGroups * i, 2 * xt + rank, bar);
+                    } else {
+                        tma_load_pair(to + 2 * S::kCodes + S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt, bar);
+                    }
+                }
                 __syncwarp();
-                uint8_t* const to = smem + b * S::kStage;
-                const uint32_t bar = first_full + 8 * b;
-                if (lane == 0) tma_load_pair(to, &x_maps.codes, 0, S::kChunks * i, 2 * xt + rank, bar);
-                if (lane == 1) tma_load_pair(to + S::kCodes, &w_maps.codes, 0, S::kChunks * i, 2 * wt + rank, bar);
-                if (lane == 2) tma_load_pair(to + 2 * S::kCodes, &x_maps.scales, 0, S::kGroups * i, 2 * xt + rank, bar);
-                if (lane == 3) tma_load_pair(to + 2 * S::kCodes + S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt, bar);
-                if (lane == 4) tma_load_pair(to + 2 * S::kCodes + 2 * S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt + 1, bar);
             }
         }
         // (all have landed, unless someone gave up: the first CTA sees it, and the second leaves after it)
-        if (rank == 0)
+        if (warp == 0 && rank == 0)
             for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
-    } else if (warp == 1) {
+    } else if (warp == 8) {
         int g = 0, turn = 0;
         if (rank == 0) {
             const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0), t_sa = tmem + S::kScaleCols, t_sb = t_sa + 4 * S::kGroups;
@@ -189,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         // the last products: none may be under way when the CTA's memory goes
         for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&free_[i % S::kRing], (i / S::kRing) & 1);
     } else {
-        const int me = tid - 64, row = 32 * (warp & 3) + lane;
+        const int me = tid - 128, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16, told = peer_addr(&sums_free, 0);
         const bool vec = p.stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
         int turn = 0;
@@ -283,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     cluster_arrive();
     cluster_wait();
     tc_after_sync();
-    if (warp == 1) tc_dealloc_pair(tmem, 512);
+    if (warp == 8) tc_dealloc_pair(tmem, 512);
 }
 
 }  // namespace sgemv

@@ -50,12 +50,12 @@ cudaError_t launch_few(const ProductParams& p, int64_t tiles, int smem, cudaStre
 }
 
 template <int kBlock>
-bool map_fp4(Fp4Maps* maps, const Fp4Matrix& m) {
+bool map_fp4(Fp4Maps* maps, const Fp4Matrix& m, unsigned scale_tiles) {
     using S = ManyShape<kBlock>;
     const cuuint64_t tiles = static_cast<cuuint64_t>((m.rows + 127) / 128), chunks = static_cast<cuuint64_t>(m.kp / 32), groups = static_cast<cuuint64_t>(m.groups);
     return encode_map(&maps->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.codes, {256, chunks, tiles}, {2048, chunks * 2048}, {256, S::kChunks, 1},
                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
-           encode_map(&maps->scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scales, {64, groups, tiles}, {512, groups * 512}, {64, S::kGroups, 1},
+           encode_map(&maps->scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scales, {64, groups, tiles}, {512, groups * 512}, {64, S::kGroups, scale_tiles},
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 template <typename T, int kBlock>
@@ -73,7 +73,7 @@ cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
         attr_set[dev].store(1);
     }
     Fp4Maps x_maps, w_maps;
-    if (!map_fp4<kBlock>(&x_maps, p.x) || !map_fp4<kBlock>(&w_maps, p.w)) return cudaErrorInvalidValue;
+    if (!map_fp4<kBlock>(&x_maps, p.x, 1) || !map_fp4<kBlock>(&w_maps, p.w, 2)) return cudaErrorInvalidValue;
     const int pairs = std::min(p.tiles_x * p.tiles_w, sms / 2);
     return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(S::kThreads), S::kSmem, s, x_maps, w_maps, p);
 }
