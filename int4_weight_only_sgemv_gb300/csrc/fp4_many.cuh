@@ -6,8 +6,8 @@
 // One CTA an SM goes through tiles, tokens fastest within groups of 8 token tiles, so that what the SMs read at a time stays in L2. Roles:
 //   warps 0-3   issue the copies of its SM's half, one each a stage (a copy takes 200 cycles to issue: five by one warp took 1270 a stage); what
 //               lands in either is counted on the first one's barriers
-//   warps 4-7   take the sums out, a thread a token, and write them
-//   warp 8      of the first CTA issues the products of both
+//   warps 4-11  take the sums out, two threads a token, and write them
+//   warp 12     of the first CTA issues the products of both
 // Tensor memory: two sets of sums, columns 0..255 and 208..463, and the scales in the last 48. The columns that the sets share are taken out
 // first, and then the next tile's products start while the rest is written.
 #pragma once
@@ -23,8 +23,8 @@ struct ManyShape {
     static constexpr int kStageK = 256, kChunks = kStageK / 32, kGroups = kStageK / (4 * kBlock);
     static constexpr int kCodes = 128 * kStageK / 2, kScales = kGroups * 512;
     static constexpr int kStage = 2 * kCodes + 3 * kScales;  // codes of tokens and weights; scales of 128 tokens and 256 weight rows
-    static constexpr int kRing = 5, kThreads = 288;
-    static constexpr int kSmem = kRing * kStage + 4 * 4096;  // and 32 rows of 64 outputs a warp
+    static constexpr int kRing = 5, kThreads = 416;
+    static constexpr int kSmem = kRing * kStage + 8 * 4096;  // and 32 rows of 64 outputs a warp
     static constexpr int kSecond = 208, kShared = 256 - kSecond;  // columns
     static constexpr int kScaleCols = kSecond + 256;
     static_assert(kScaleCols + 12 * kGroups <= 512, "tensor memory");
@@ -82,9 +82,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     __shared__ __align__(8) uint64_t full[S::kRing], free_[S::kRing], sums_full, sums_free;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_w_scale[256];
-    __shared__ float s_least[4], s_most[4];
+    __shared__ float s_least[8], s_most[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-    const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = blockIdx.x & 1, me_pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int chunks = p.w.kp / 32, tiles = p.tiles_x * p.tiles_w;
     if (tid == 0) {
         for (int i = 0; i < S::kRing; ++i) mbar_init(&full[i], 1), mbar_init(&free_[i], 1);
@@ -93,7 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     }
     pdl_launch_dependents();
     __syncthreads();
-    if (warp == 8) tc_alloc_pair(&s_tmem, 512);
+    if (warp == 12) tc_alloc_pair(&s_tmem, 512);
     tc_before_sync();
     __syncwarp();
     cluster_arrive();
@@ -117,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         const uint32_t first_full = peer_addr(full, 0);
         int g = 0;
 #pragma unroll 1
-        for (int tile = pair; tile < tiles && !dead; tile += pairs) {
+        for (int tile = me_pair; tile < tiles && !dead; tile += pairs) {
             int xt, wt;
             tile_at(tile, xt, wt);
 #pragma unroll 1
@@ -147,13 +147,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         // (all have landed, unless someone gave up: the first CTA sees it, and the second leaves after it)
         if (warp == 0 && rank == 0)
             for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
-    } else if (warp == 8) {
+    } else if (warp == 12) {
         int g = 0, turn = 0;
         if (rank == 0) {
             const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0), t_sa = tmem + S::kScaleCols, t_sb = t_sa + 4 * S::kGroups;
             constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, 256, 0);
 #pragma unroll 1
-            for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+            for (int tile = me_pair; tile < tiles; tile += pairs, ++turn) {
                 if (turn > 0 && !dead && !mbar_wait_cluster(&sums_free, (turn - 1) & 1)) {
                     dead = true;
                     report(p.status, SGEMV_ERR_TIMEOUT);
@@ -197,30 +197,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         // the last products: none may be under way when the CTA's memory goes
         for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&free_[i % S::kRing], (i / S::kRing) & 1);
     } else {
-        const int me = tid - 128, row = 32 * (warp & 3) + lane;
+        const int me = tid - 128, row = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16, told = peer_addr(&sums_free, 0);
         const bool vec = p.stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
         int turn = 0;
 #pragma unroll 1
-        for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+        for (int tile = me_pair; tile < tiles; tile += pairs, ++turn) {
             int xt, wt;
             tile_at(tile, xt, wt);
             const int token = xt * 256 + rank * 128 + row, n0 = wt * 256;
             // the scales of the rows, and whether any product of two leaves binary32's normal range
             const float xs = token < p.x.rows ? p.x.row_scale[token] : 1.0f;
-            float least = INFINITY, most = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = 2 * me + i;
-                const float f = n0 + n < p.w.rows ? p.w.row_scale[n0 + n] : 1.0f;
-                s_w_scale[n] = f;
-                least = fminf(least, f == f ? f : 0.0f), most = fmaxf(most, f);
+            float least, most;
+            {
+                const float f = n0 + me < p.w.rows ? p.w.row_scale[n0 + me] : 1.0f;
+                s_w_scale[me] = f;
+                least = f == f ? f : 0.0f, most = f;
             }
             const unsigned lo = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(least)), hi = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-            if (lane == 0) s_least[warp & 3] = __uint_as_float(lo), s_most[warp & 3] = __uint_as_float(hi);
-            named_bar_sync(1, 128);
-            least = fminf(fminf(s_least[0], s_least[1]), fminf(s_least[2], s_least[3]));
-            most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+            if (lane == 0) s_least[warp - 4] = __uint_as_float(lo), s_most[warp - 4] = __uint_as_float(hi);
+            named_bar_sync(1, 256);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) least = fminf(least, s_least[i]), most = fmaxf(most, s_most[i]);
             const bool plain = __all_sync(0xFFFFFFFFu, xs * least >= 1.17549435e-38f && xs * most < INFINITY);
             wait(&sums_full, turn & 1);
             __syncwarp();
@@ -228,47 +226,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
             const uint32_t from = tmem + lanes + ((turn & 1) ? S::kSecond : 0);
             const int token0 = token - lane, rows = min(32, p.x.rows - token0);
             // 64 columns at a time, first those that the other set of sums shares, through shared memory, so that whole lines of rows are written
-            uint8_t* const stage = smem + S::kRing * S::kStage + (warp & 3) * 4096;
+            uint8_t* const stage = smem + S::kRing * S::kStage + (warp - 4) * 4096;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int part = ((turn & 1) ? k : k + 3) & 3, col = n0 + 64 * part;
+            for (int k = 0; k < 2; ++k) {
+                const int part = ((turn & 1) ? k : k + 3) + 2 * half & 3, col = n0 + 64 * part;
                 uint32_t r[2][32];
                 tc_ld32(r[0], from + 64 * part);
                 tc_ld32(r[1], from + 64 * part + 32);
                 tc_wait_ld();
-                if (k == 0) {
+                if (k == 0 && half == 0) {
                     tc_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_at(told);
                 }
                 if (col >= p.w.rows) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int n = 8 * i + 2 * e;
-                        const float2 ws = *reinterpret_cast<const float2*>(&s_w_scale[64 * part + n]);
-                        const float v0 = __uint_as_float(r[n / 32][n % 32]), v1 = __uint_as_float(r[n / 32][n % 32 + 1]);
-                        h[e] = plain ? pack_two<T>(v0 * (xs * ws.x), v1 * (xs * ws.y)) : pack_two<T>(row_scaled(v0, xs, ws.x), row_scaled(v1, xs, ws.y));
-                    }
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ lane) & 7) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                __syncwarp();
-                T* const y = static_cast<T*>(p.y) + token0 * p.stride + col;
-                const int cols = min(64, p.w.rows - col);
-                if (vec) {
+                if (plain) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int rr = 4 * i + (lane >> 3), piece = lane & 7;
-                        const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((piece ^ rr) & 7) * 16);
-                        T* const to = y + rr * p.stride + 8 * piece;
-                        if (rr < rows && 8 * piece + 8 <= cols) {
-                            *reinterpret_cast<uint4*>(to) = h;
-                        } else if (rr < rows) {
-                            const T* const e = reinterpret_cast<const T*>(&h);
-                            for (int n = 0; n < cols - 8 * piece; ++n) to[n] = e[n];
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int n = 8 * i + 4 * e;
+                            const float4 ws = *reinterpret_cast<const float4*>(&s_w_scale[64 * part + n]);
+                            const uint32_t* const v = &r[n / 32][n % 32];
+                            const float2 a = parts_of(mul2(pair(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2(pair(xs, xs), pair(ws.x, ws.y))));
+                            const float2 b = parts_of(mul2(pair(__uint_as_float(v[2]), __uint_as_float(v[3])), mul2(pair(xs, xs), pair(ws.z, ws.w))));
+                            h[2 * e] = pack_two<T>(a.x, a.y), h[2 * e + 1] = pack_two<T>(b.x, b.y);
                         }
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ lane) & 7) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 64; ++n)
+                        *reinterpret_cast<T*>(stage + lane * 128 + ((n / 8 ^ lane) & 7) * 16 + n % 8 * 2) =
+                            from_f32<T>(row_scaled(__uint_as_float(r[n / 32][n % 32]), xs, s_w_scale[64 * part + n]));
+                }
+                __syncwarp();
+                T* y = static_cast<T*>(p.y) + token0 * p.stride + col;
+                const int cols = min(64, p.w.rows - col);
+                if (vec && col + 64 <= p.w.rows) {
+                    T* to = y + (lane >> 3) * p.stride + 8 * (lane & 7);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3);
+                        const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((lane ^ rr) & 7) * 16);
+                        if (rr < rows) *reinterpret_cast<uint4*>(to) = h;
+                        to += 4 * p.stride;
                     }
                 } else {
 #pragma unroll 4
@@ -283,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
                 }
                 __syncwarp();
             }
-            named_bar_sync(1, 128);  // (the scales' place)
+            named_bar_sync(1, 256);  // (the scales' place; and nobody is a tile behind)
         }
     }
     __syncwarp();
@@ -291,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
     cluster_arrive();
     cluster_wait();
     tc_after_sync();
-    if (warp == 8) tc_dealloc_pair(tmem, 512);
+    if (warp == 12) tc_dealloc_pair(tmem, 512);
 }
 
 }  // namespace sgemv
