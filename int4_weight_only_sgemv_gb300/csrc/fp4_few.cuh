@@ -7,15 +7,15 @@
 // columns, and sends every other one its share of the outputs' sums over distributed shared memory, where they are joined in the order of
 // the columns. (With sums read by their users between two barriers of the cluster, a call of one token took 1 us more.) What is sent has a
 // place of its own where tiles are narrow; with 64 or 128 tokens it comes where the ring was, so that two CTAs fit an SM, after a barrier of the cluster.
-// Roles: warp 0 issues the copies, a lane each (by one lane, 90 ns a copy bound everything), warp 1 the products, warps 2-5 take the sums
-// out, send, join and write.
+// Roles: warps 0-3 issue the copies, one each a stage (90 ns a copy to issue, whoever's lane does, bound everything with one warp for all four);
+// warps 4-7 take the sums out, send, join and write; warp 8 issues the products.
 #pragma once
 
 #include "fp4_tc.cuh"
 
 namespace sgemv {
 
-constexpr int kFewThreads = 192;
+constexpr int kFewThreads = 288;
 constexpr int kFewSmem = 108 * 1024;   // of the ring: two CTAs an SM
 constexpr int kFewLeast = 80 * 1024;   // and never three, whose tensor memory (256 columns each) would not fit
 constexpr int kFewMost = 216 * 1024;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     }
     __syncwarp();
     pdl_launch_dependents();
-    if (warp == 1) tc_alloc(&s_tmem, kFewCols);
+    if (warp == 8) tc_alloc(&s_tmem, kFewCols);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -95,28 +95,24 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     };
     // a stage: weights' codes, tokens' codes, weights' scales, tokens' scales
     const uint32_t at_x = 128 * kStageK / 2, at_sw = at_x + p.x.tile * kStageK / 2, at_sx = at_sw + kGroups * 512;
-    if (warp == 0) {
-        // copy `kind` of stage i
-        const uint8_t* const x_codes = p.x.codes + (static_cast<int64_t>(xt) * chunks + kChunks * st0) * p.x.tile * 16;
-        const uint8_t* const x_scales = p.x.scales + (static_cast<int64_t>(xt) * p.x.groups + kGroups * st0) * 512;
-        const auto copy = [&](int i, int kind) {
-            const int b = i % p.ring, c = min(kChunks, chunks - kChunks * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
-            uint8_t* const to = smem + b * stage_bytes;
-            if (kind == 0) mbar_arrive_expect_tx(&full[b], c * (p.w.tile + p.x.tile) * 16 + 2 * g * 512);
-            const uint8_t* const from = kind == 0   ? w_codes + static_cast<int64_t>(i) * kChunks * p.w.tile * 16
-                                        : kind == 1 ? x_codes + static_cast<int64_t>(i) * kChunks * p.x.tile * 16
-                                        : kind == 2 ? w_scales + static_cast<int64_t>(i) * kGroups * 512
-                                                    : x_scales + static_cast<int64_t>(i) * kGroups * 512;
-            bulk_g2s(to + (kind == 0 ? 0 : kind == 1 ? at_x : kind == 2 ? at_sw : at_sx), from,
-                     kind == 0 ? c * p.w.tile * 16 : kind == 1 ? c * p.x.tile * 16 : g * 512, &full[b]);
-        };
-        int i = min(n, p.ring);
-        if (lane < 4 * i) copy(lane >> 2, lane & 3);
+    if (warp < 4) {
+        // this warp's copy of a stage: weights' codes, tokens' codes, weights' scales, tokens' scales
+        const int64_t x_chunk = static_cast<int64_t>(xt) * chunks + kChunks * st0, x_group = static_cast<int64_t>(xt) * p.x.groups + kGroups * st0;
+        const uint8_t* const from = warp == 0 ? w_codes : warp == 1 ? p.x.codes + x_chunk * p.x.tile * 16 : warp == 2 ? w_scales : p.x.scales + x_group * 512;
+        const uint32_t unit = warp == 0 ? p.w.tile * 16 : warp == 1 ? p.x.tile * 16 : 512;  // bytes of a chunk or group
+        const uint32_t to = warp == 0 ? 0 : warp == 1 ? at_x : warp == 2 ? at_sw : at_sx;
+        int i = 0;
         for (; i < n; ++i) {
-            wait(&free_[i % p.ring], (i / p.ring - 1) & 1);
+            const int b = i % p.ring;
+            if (i >= p.ring) wait(&free_[b], (i / p.ring - 1) & 1);
             dead = __any_sync(0xFFFFFFFFu, dead);
             if (dead) break;
-            if (lane < 4) copy(i, lane);
+            const int c = min(kChunks, chunks - kChunks * (st0 + i)), g = min(kGroups, p.w.groups - kGroups * (st0 + i));
+            if (lane == 0) {
+                if (warp == 0) mbar_arrive_expect_tx(&full[b], c * (p.w.tile + p.x.tile) * 16 + 2 * g * 512);
+                bulk_g2s(smem + b * stage_bytes + to, from + static_cast<int64_t>(i) * (warp < 2 ? kChunks : kGroups) * unit, (warp < 2 ? c : g) * unit, &full[b]);
+            }
+            __syncwarp();
         }
         // (none may be under way when the CTA leaves; all have landed when the products are done, unless someone gave up)
         for (int j = max(0, i - p.ring); j < i; ++j) mbar_wait(&full[j % p.ring], (j / p.ring) & 1);
@@ -125,7 +121,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
             if (!kEarly) cluster_arrive();
             cluster_wait();
         }
-    } else if (warp == 1) {
+    } else if (warp == 8) {
         const uint32_t base = smem_addr(smem);
         const uint32_t idesc = tc_idesc_fp4<kBlock>(128, (cols + 7) / 8 * 8, 0);
         int i = 0;
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
             cluster_wait();
         }
     } else {
-        const int me = tid - 64;  // of 128
+        const int me = tid - 128;  // of 128
         // the scales of rows and tokens, while the products run
         const int item_first = item0 + me, q = item_first & 31;  // (the same four rows for all of them)
         const float4 ws = *reinterpret_cast<const float4*>(p.w.row_scale + wt * 128 + 4 * q);
@@ -221,7 +217,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     __syncwarp();
     tc_before_sync();
     __syncthreads();
-    if (warp == 1) tc_dealloc(tmem, kFewCols);
+    if (warp == 8) tc_dealloc(tmem, kFewCols);
 }
 
 }  // namespace sgemv

@@ -10,9 +10,12 @@ namespace sgemv {
 
 namespace {
 
-// Whether a call goes to the kernel of many tiles.
-bool many_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x, int sms) {
-    return x.rows > 128 && w.rows > 128;
+// Whether a call goes to the kernel of many tiles: with more than 64 tokens, but where few tiles meet a long sum, which the other splits. us a call,
+// many and few: 65 x 4096 x 4096 9.1, 10.6; 128 x 11008 x 4096 10.4, 14.2; 129 x 1024 x 4096 8.7, 8.4; 129 x 1024 x 8192 13.3, 10.3; 512 x 512 x 8192 13.2, 10.5;
+// 100 x 200 x 16384 22.3, 9.8; 256 x 300 x 16384 23.2, 10.7.
+bool many_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x) {
+    const int64_t tiles = static_cast<int64_t>((x.rows + 255) / 256) * ((w.rows + 255) / 256);
+    return x.rows > 64 && w.rows > 64 && (tiles >= 8 || w.kp <= 4096);
 }
 
 template <typename T, int kBlock, int kStageK>
@@ -111,7 +114,7 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     if (tiles * 8 > INT_MAX) return SGEMV_ERR_SHAPE;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = dtype == SGEMV_F16;
-    if (many_tiles(w, x, di.sm_count)) {
+    if (many_tiles(w, x)) {
         p.tiles_x = (x.rows + 255) / 256, p.tiles_w = (w.rows + 255) / 256;
         p.k_stages = (w.kp + ManyShape<16>::kStageK - 1) / ManyShape<16>::kStageK;
         const int sms = di.sm_count;
@@ -120,9 +123,9 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
         return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
     }
     // CTAs a tile: as many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
-    // tiles of 128 tokens are sent leaves one place an SM.
+    // tiles of 128 tokens are sent leaves one place an SM, and not every SM is in a cluster (512 x 512 x 8192: 6 CTAs 10.5 us, 8 16.9).
     p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * di.sm_count / tiles, p.k_stages / 2})));
-    if (x.tile == 128 && p.split > 4) p.split = std::min(p.split, std::max(4, static_cast<int>(di.sm_count / tiles)));
+    if (x.tile == 128 && p.split > 4) p.split = std::min(p.split, std::max(4, static_cast<int>(2 * di.sm_count / 3 / tiles)));
     const int stage = few_stage_bytes(w.block, x.tile), sent = p.split > 1 ? few_sent(x.tile, p.split) : 0;
     const bool early = few_stage_k(x.tile) == 512;
     p.ring = std::min({kFewMaxRing, (kFewSmem - (early ? sent : 0)) / stage, (p.k_stages + p.split - 1) / p.split});
