@@ -26,8 +26,14 @@ struct QuantParams {
     int64_t stride;
     int32_t* status;
     int wpr;         // warps a row
-    int align;       // of the rows' pieces: 32 bytes, 16, or 0 (elements)
+    int align;       // of the rows' pieces: 32 bytes, 16, or 0 (an element)
 };
+
+__device__ __forceinline__ float reciprocal(float x) {  // to a unit in the last place or so
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // The row of a CTA's slot.
 __device__ __forceinline__ int row_of_slot(const Fp4Matrix& m, int64_t slot) {
@@ -43,22 +49,48 @@ __device__ __forceinline__ void load16(const T* row, int c, int k, int align, ui
         asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                      : "l"(row + 16 * c));
-    } else if (align > 0) {
+    } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (16 * c + 8 * i < k) v = *reinterpret_cast<const uint4*>(row + 16 * c + 8 * i);
             w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
-    } else {
-        const unsigned short* h = reinterpret_cast<const unsigned short*>(row);
+    }
+}
+// Rows that start anywhere go through shared memory, so that a warp reads and writes whole words next to one another: the 512 values from column
+// 16 * base on as 257 words, a word of two halves of which one lies outside of the row by halves.
+struct Line {
+    const unsigned short* at;  // the first value
+    int n;                     // values
+    bool odd;                  // it is the upper half of a word
+    template <typename T>
+    __device__ __forceinline__ Line(const T* row, int base, int k)
+        : at(reinterpret_cast<const unsigned short*>(row) + 16ll * base), n(min(512, k - 16 * base)), odd((reinterpret_cast<uintptr_t>(row) & 2) != 0) {}
+};
+__device__ __forceinline__ void load_line(const Line& l, int lane, uint32_t (&v)[9]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = 16 * c + 2 * i;
-            const uint32_t lo = at < k ? h[at] : 0, hi = at + 1 < k ? h[at + 1] : 0;
-            w[i] = lo | (hi << 16);
+    for (int i = 0; i < 9; ++i) {
+        const int first = 2 * (lane + 32 * i) - l.odd;  // of the word's two values
+        v[i] = 0;
+        if (first >= 0 && first + 1 < l.n) {
+            v[i] = *reinterpret_cast<const uint32_t*>(l.at + first);
+        } else {
+            if (first >= 0 && first < l.n) v[i] = l.at[first];
+            if (first + 1 >= 0 && first + 1 < l.n) v[i] |= static_cast<uint32_t>(l.at[first + 1]) << 16;
         }
     }
+}
+__device__ __forceinline__ void spread_line(const Line& l, int lane, const uint32_t (&v)[9], uint32_t* buf, uint32_t (&w)[8]) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 9; ++i)
+        if (i < 8 || lane == 0) buf[lane + 32 * i] = v[i];
+    __syncwarp();
+    const uint4 a = *reinterpret_cast<const uint4*>(buf + 8 * lane), b = *reinterpret_cast<const uint4*>(buf + 8 * lane + 4);
+    const uint32_t u[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, buf[8 * lane + 8]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = l.odd ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
 }
 // The largest magnitude of 8 words' elements, as 16 bits (infinities and NaN above all numbers).
 __device__ __forceinline__ uint32_t most16(const uint32_t (&w)[8]) {
@@ -79,6 +111,7 @@ constexpr uint32_t kInfBits<__nv_bfloat16> = 0x7F80u;
 template <typename T, int kBlock>
 __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParams p) {
     __shared__ uint32_t s_most[kWarpsQ];
+    __shared__ __align__(16) uint32_t s_line[kWarpsQ][260];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slot = warp / p.wpr, part = warp % p.wpr;
     if (threadIdx.x < kWarpsQ) s_most[threadIdx.x] = 0;
@@ -91,26 +124,46 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
     pdl_wait();
     uint32_t held[kHeld][8];
     uint32_t held_most[kHeld];
+    const auto some = [&](int i) { return 32 * part + i * step < pieces; };  // whether any lane of the warp has its piece i
+    if (p.align > 0) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int c = first + i * step;
-        if (c < pieces) {
-            load16(x, c, p.m.k, p.align, held[i]);
-        } else {
+        for (int i = 0; i < kHeld; ++i) {
+            const int c = first + i * step;
 #pragma unroll
             for (int e = 0; e < 8; ++e) held[i][e] = 0;
+            if (c < pieces) load16(x, c, p.m.k, p.align, held[i]);
         }
+    } else {
+        uint32_t v[kHeld][9];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (some(i)) load_line(Line(x, 32 * part + i * step, p.m.k), lane, v[i]);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (some(i)) spread_line(Line(x, 32 * part + i * step, p.m.k), lane, v[i], s_line[warp], held[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held_most[i] = most16(held[i]);
+    for (int i = 0; i < kHeld; ++i) held_most[i] = some(i) ? most16(held[i]) : 0;
+    const auto load = [&](int base, uint32_t (&w)[8]) {  // piece base + lane of a long row
+        if (p.align > 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 0;
+            if (base + lane < pieces) load16(x, base + lane, p.m.k, p.align, w);
+        } else {
+            const Line l(x, base, p.m.k);
+            uint32_t v[9];
+            load_line(l, lane, v);
+            spread_line(l, lane, v, s_line[warp], w);
+        }
+    };
     float unit = 1.0f, down = 1.0f;
     bool bad = false;
     if constexpr (kBlock == 16) {
         // the row's largest magnitude, and from it the row's power of two
         uint32_t most = max(max(held_most[0], held_most[1]), max(held_most[2], held_most[3]));
-        for (int c = first + kHeld * step; c < pieces; c += step) {
+        for (int base = 32 * part + kHeld * step; base < pieces; base += step) {
             uint32_t w[8];
-            load16(x, c, p.m.k, p.align, w);
+            load(base, w);
             most = max(most, most16(w));
         }
         most = __reduce_max_sync(0xFFFFFFFFu, most);
@@ -125,6 +178,9 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
         unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
     uint32_t seen = 0;
+    uint8_t* const row_codes = codes_at(p.m, live ? row : 0, 0) + 8 * (lane & 1);
+    uint8_t* const row_scales = scales_at(p.m, live ? row : 0, 0);
+    const int chunk_bytes = p.m.tile * 16;
     // Piece c of the row, by the whole warp (lanes past the row's end have zeros).
     const auto quantize = [&](int c, const uint32_t (&w)[8], uint32_t most) {
         uint32_t scale;
@@ -135,9 +191,10 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
             scale = max(0, static_cast<int>(__float_as_uint(as_f32<T>(most)) >> 23) - 2);
             inv = __uint_as_float((254u - scale) << 23), s = 0.0f;
         } else {
-            scale = to_e4m3(__fdiv_rn(as_f32<T>(most) * down, 6.0f));
+            const float m = as_f32<T>(most) * down, sixth = m * (1.0f / 6.0f);
+            scale = to_e4m3(fmaf(fmaf(-6.0f, sixth, m), 1.0f / 6.0f, sixth));
             s = from_e4m3(scale) * unit;
-            inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            inv = s > 0.0f ? reciprocal(s) : 0.0f;
         }
         uint32_t codes[2];
         const uint64_t r = pair(inv, inv), d = pair(-s, -s);
@@ -161,16 +218,16 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
         scale |= __shfl_down_sync(0xFFFFFFFFu, scale, kApart) << 8;
         scale |= __shfl_down_sync(0xFFFFFFFFu, scale, 2 * kApart) << 16;
         if (c < pieces) {
-            *reinterpret_cast<uint2*>(codes_at(p.m, row, c / 2) + 8 * (c & 1)) = make_uint2(codes[0], codes[1]);
-            if (lane % (4 * kApart) == 0) *reinterpret_cast<uint32_t*>(scales_at(p.m, row, c / (4 * kApart))) = scale;
+            *reinterpret_cast<uint2*>(row_codes + static_cast<int64_t>(c / 2) * chunk_bytes) = make_uint2(codes[0], codes[1]);
+            if (lane % (4 * kApart) == 0) *reinterpret_cast<uint32_t*>(row_scales + static_cast<int64_t>(c / (4 * kApart)) * 512) = scale;
         }
     };
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-        if (32 * part + i * step < pieces) quantize(first + i * step, held[i], held_most[i]);
+        if (some(i)) quantize(first + i * step, held[i], held_most[i]);
     for (int base = 32 * part + kHeld * step; base < pieces; base += step) {
-        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (base + lane < pieces) load16(x, base + lane, p.m.k, p.align, w);
+        uint32_t w[8];
+        load(base, w);
         quantize(base + lane, w, most16(w));
     }
     if constexpr (kBlock == 32) {
@@ -188,6 +245,38 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
     }
 }
 
+// The warp's 512 values from column 16 * base on, 16 a lane, as words next to one another.
+template <typename T>
+__device__ __forceinline__ void store_line(T* row, int base, int k, int lane, const uint32_t (&w)[8 * sizeof(T) / 2], uint32_t* buf) {
+    constexpr int kWords = 8 * sizeof(T) / 2;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(buf + kWords * lane + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    __syncwarp();
+    const int n = min(512, k - 16 * base);
+    T* const at = row + 16ll * base;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) reinterpret_cast<uint32_t*>(at)[i] = buf[i];
+    } else {
+        const bool odd = (reinterpret_cast<uintptr_t>(row) & 2) != 0;
+        unsigned short* const h = reinterpret_cast<unsigned short*>(at);
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+            const int word = lane + 32 * i, first = 2 * word - odd;
+            if (first >= n) break;
+            const uint32_t here = word < 256 ? buf[word] : 0, before = odd && word > 0 ? buf[word - 1] : 0;
+            const uint32_t v = odd ? __funnelshift_r(before, here, 16) : here;
+            if (first >= 0 && first + 1 < n) {
+                *reinterpret_cast<uint32_t*>(h + first) = v;
+            } else {
+                if (first >= 0) h[first] = static_cast<unsigned short>(v);
+                if (first + 1 < n) h[first + 1] = static_cast<unsigned short>(v >> 16);
+            }
+        }
+    }
+}
+
 template <typename T, int kBlock>
 __global__ void __launch_bounds__(32 * kWarpsQ) read_kernel(const QuantParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -198,9 +287,14 @@ __global__ void __launch_bounds__(32 * kWarpsQ) read_kernel(const QuantParams p)
     if (row >= p.m.rows) return;
     T* const out = const_cast<T*>(static_cast<const T*>(p.x)) + row * p.stride;
     const float unit = p.m.row_scale[row];
-    for (int c = 32 * part + lane; 16 * c < p.m.k; c += 32 * p.wpr) {
-        const uint2 codes = *reinterpret_cast<const uint2*>(codes_at(p.m, row, c / 2) + 8 * (c & 1));
-        const uint32_t sb = scales_at(p.m, row, c * 16 / kBlock / 4)[c * 16 / kBlock % 4];
+    const uint8_t *const row_codes = codes_at(p.m, row, 0), *const row_scales = scales_at(p.m, row, 0);
+    const int chunk_bytes = p.m.tile * 16;
+    __shared__ __align__(16) uint32_t s_line[kWarpsQ][32 * 8 * sizeof(T) / 2];
+    for (int base = 32 * part; 16 * base < p.m.k; base += 32 * p.wpr) {
+        const int c = base + lane;
+        const int at = min(c, p.m.kp / 16 - 1);  // (a lane without a piece among others that have one: any)
+        const uint2 codes = *reinterpret_cast<const uint2*>(row_codes + static_cast<int64_t>(at / 2) * chunk_bytes + 8 * (at & 1));
+        const uint32_t sb = row_scales[static_cast<int64_t>(at * 16 / kBlock / 4) * 512 + at * 16 / kBlock % 4];
         const float s = (kBlock == 16 ? from_e4m3(sb) : from_e8m0(sb)) * unit;
         float f[16];
 #pragma unroll
@@ -221,7 +315,9 @@ __global__ void __launch_bounds__(32 * kWarpsQ) read_kernel(const QuantParams p)
             else w[i] = pack_two<T>(f[2 * i], f[2 * i + 1]);
         }
         T* const to = out + 16 * c;
-        if (p.align == 32 || (p.align == 16 && 16 * c + 16 <= p.m.k)) {
+        if (p.align == 0) {
+            store_line(out, base, p.m.k, lane, w, s_line[warp]);
+        } else if (16 * c + 16 <= p.m.k) {
 #pragma unroll
             for (int i = 0; i < kWords; i += 8) {
                 if (p.align == 32) {
