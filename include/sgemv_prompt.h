@@ -42,7 +42,7 @@ typedef struct {
 } sgemv_fp4_layout;
 
 /*
- * sgemv_fp4_layout_query -- host only, pure. rows 1..2^24, k 1..2^20, block 16 or 32.
+ * sgemv_fp4_layout_query -- host only, pure. rows 0..2^24 (calls with a matrix of no rows do nothing), k 1..2^20, block 16 or 32.
  * Errors: SGEMV_ERR_ARG (out is NULL), SGEMV_ERR_SHAPE.
  */
 int sgemv_fp4_layout_query(int rows, int k, int block, sgemv_fp4_layout* out);
@@ -105,7 +105,7 @@ typedef struct {
  * Keys and values that a token does not see do not enter its outputs, whatever they hold. A NaN or infinite element of v that it sees
  * makes that dim of its output NaN or infinite; one of q or k the whole output NaN.
  * Rows that belong to no request (past start[n_req], or past a request's length) are neither used nor written. Requests of no tokens are
- * allowed. out may be q itself (the same address and strides).
+ * allowed. out may be q itself (the same address and strides); out's rows do not overlap one another.
  * The same inputs give the same bits.
  * Device-reported: SGEMV_ERR_ARG (a request with start out of order or out of range, or a length outside 0..start[r + 1] - start[r]: its
  * rows are not written); SGEMV_ERR_TIMEOUT (a bounded wait for a copy gave up: out is invalid).

@@ -94,7 +94,9 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     if (rc != SGEMV_OK) return rc;
     const sgemv_fp4_layout &w = *w_layout, &x = *x_layout;
     if (w.k != x.k || w.block != x.block) return SGEMV_ERR_FORMAT;
-    if ((dtype != SGEMV_F16 && dtype != SGEMV_BF16) || w_dev == nullptr || x_dev == nullptr || y_dev == nullptr) return SGEMV_ERR_ARG;
+    if (dtype != SGEMV_F16 && dtype != SGEMV_BF16) return SGEMV_ERR_ARG;
+    if (w.rows == 0 || x.rows == 0) return SGEMV_OK;
+    if (w_dev == nullptr || x_dev == nullptr || y_dev == nullptr) return SGEMV_ERR_ARG;
     if (x.rows > 1 && (stride < w.rows || stride > (1ll << 40))) return SGEMV_ERR_ARG;
     if (!is_aligned(w_dev, 16) || !is_aligned(x_dev, 16) || !is_aligned(y_dev, 2) || !is_aligned(status_dev, 4)) return SGEMV_ERR_ALIGN;
     const int64_t st = x.rows > 1 ? stride : w.rows;

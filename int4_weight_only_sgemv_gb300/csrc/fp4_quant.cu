@@ -381,7 +381,7 @@ using namespace sgemv;
 
 extern "C" int sgemv_fp4_layout_query(int rows, int k, int block, sgemv_fp4_layout* out) {
     if (out == nullptr) return SGEMV_ERR_ARG;
-    if (rows < 1 || rows > (1 << 24) || k < 1 || k > (1 << 20) || (block != 16 && block != 32)) return SGEMV_ERR_SHAPE;
+    if (rows < 0 || rows > (1 << 24) || k < 1 || k > (1 << 20) || (block != 16 && block != 32)) return SGEMV_ERR_SHAPE;
     sgemv_fp4_layout l = {};
     l.rows = rows, l.k = k, l.block = block;
     l.tile = 8;
@@ -399,7 +399,9 @@ extern "C" int sgemv_fp4_quantize(const sgemv_fp4_layout* layout, const void* x_
                                   int32_t* status_dev, void* stream) {
     const int rc = check_fp4_layout(layout);
     if (rc != SGEMV_OK) return rc;
-    if ((dtype != SGEMV_F16 && dtype != SGEMV_BF16) || x_dev == nullptr || packed_dev == nullptr) return SGEMV_ERR_ARG;
+    if (dtype != SGEMV_F16 && dtype != SGEMV_BF16) return SGEMV_ERR_ARG;
+    if (layout->rows == 0) return SGEMV_OK;
+    if (x_dev == nullptr || packed_dev == nullptr) return SGEMV_ERR_ARG;
     if (layout->rows > 1 && (stride < layout->k || stride > (1ll << 40))) return SGEMV_ERR_ARG;
     if (!is_aligned(packed_dev, 16) || !is_aligned(x_dev, 2) || !is_aligned(status_dev, 4)) return SGEMV_ERR_ALIGN;
     const int64_t st = layout->rows > 1 ? stride : layout->k;
@@ -421,7 +423,9 @@ extern "C" int sgemv_fp4_read(const sgemv_fp4_layout* layout, const void* packed
                               void* stream) {
     const int rc = check_fp4_layout(layout);
     if (rc != SGEMV_OK) return rc;
-    if (dtype < SGEMV_F16 || dtype > SGEMV_F32 || out_dev == nullptr || packed_dev == nullptr) return SGEMV_ERR_ARG;
+    if (dtype < SGEMV_F16 || dtype > SGEMV_F32) return SGEMV_ERR_ARG;
+    if (layout->rows == 0) return SGEMV_OK;
+    if (out_dev == nullptr || packed_dev == nullptr) return SGEMV_ERR_ARG;
     if (layout->rows > 1 && (stride < layout->k || stride > (1ll << 40))) return SGEMV_ERR_ARG;
     const unsigned size = dtype == SGEMV_F32 ? 4 : 2;
     if (!is_aligned(packed_dev, 16) || !is_aligned(out_dev, size)) return SGEMV_ERR_ALIGN;

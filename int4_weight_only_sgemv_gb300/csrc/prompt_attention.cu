@@ -79,6 +79,13 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
                                   {q.heads_q, q.out_head_stride}};
     for (const auto& s : strides)
         if (s[0] > 1 && (s[1] < 1 || s[1] > kFar)) return SGEMV_ERR_SHAPE;
+    // out's rows do not overlap
+    if (q.n_tokens > 1 || q.heads_q > 1) {
+        const bool heads_inside = q.heads_q > 1 && (q.n_tokens < 2 || q.out_head_stride <= q.out_token_stride);
+        const int64_t inner = heads_inside ? q.out_head_stride : q.out_token_stride, n_inner = heads_inside ? q.heads_q : q.n_tokens;
+        const int64_t outer = heads_inside ? q.out_token_stride : q.out_head_stride, n_outer = heads_inside ? q.n_tokens : q.heads_q;
+        if (inner < q.dim || (n_outer > 1 && outer < (n_inner - 1) * inner + q.dim)) return SGEMV_ERR_ARG;
+    }
     // (rows between others, as those of a fused projection, may be out's: what lies from its first to its last byte is looked at only where
     // nothing else has a place there)
     const uint64_t all = 2ull * q.n_tokens * q.heads_q * q.dim;

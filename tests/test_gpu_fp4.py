@@ -172,3 +172,131 @@ def _check_product(env, x, w, block, dtype, y=None):
 def test_product(env, tokens, n, k, block, dtype):
     sg, torch = env
     _check_product(env, _x(torch, tokens, k, dtype, tokens + k), _x(torch, n, k, "float16", n + k, 0.3), block, dtype)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("rows,k,offset,stride", [(3, 64, 8, 80), (3, 64, 1, 65), (5, 513, 3, 517), (70, 1030, 7, 1040), (2, 4099, 1, 5001), (9, 17, 0, 17),
+                                                  (4, 16, 2, 31), (1, 20000, 1, 20001), (3, 2, 1, 3), (2, 511, 5, 512)])
+def test_rows_that_start_anywhere(env, rows, k, offset, stride, dtype, block):
+    """The same bytes whatever the rows' alignment; what lies around them is not read into them (it holds NaN) and not written."""
+    sg, torch = env
+    x = _x(torch, rows, k, dtype, rows + k)
+    wide = torch.full((rows * stride + offset + 8,), float("nan"), dtype=x.dtype, device="cuda")
+    y = wide.as_strided((rows, k), (stride, 1), offset)
+    y.copy_(x)
+    L, a, s1 = _quantise(env, x, block)
+    _, b, s2 = _quantise(env, y, block)
+    assert s1 == 0 and s2 == 0 and torch.equal(a, b)
+    for out in (torch.float16, torch.bfloat16, torch.float32):
+        want = torch.empty((rows, k), dtype=out, device="cuda")
+        sg.sgemv_fp4_read(L, a, want)
+        base = torch.full((rows * stride + offset + 8,), 77.0, dtype=out, device="cuda")
+        got = base.as_strided((rows, k), (stride, 1), offset)
+        sg.sgemv_fp4_read(L, a, got)
+        assert torch.equal(got, want)
+        got.fill_(77.0)
+        assert torch.all(base == 77.0)
+
+
+@pytest.mark.parametrize("tokens,n,stride,offset", [(3, 130, 133, 1), (20, 131, 131, 0), (70, 300, 301, 3), (300, 257, 1000, 5), (300, 264, 272, 8), (200, 5, 9, 1),
+                                                    (64, 200, 204, 4)])
+def test_product_into_rows_of_a_wider_tensor(env, tokens, n, stride, offset):
+    sg, torch = env
+    base = torch.full((tokens * stride + offset + 8,), 77.0, device="cuda").half()
+    y = base.as_strided((tokens, n), (stride, 1), offset)
+    _check_product(env, _x(torch, tokens, 200, "float16", 1), _x(torch, n, 200, "float16", 2, 0.3), 16, "float16", y)
+    y.fill_(77.0)
+    assert torch.all(base == 77.0)
+
+
+@pytest.mark.parametrize("tokens,n,k", [(1, 256, 16384), (5, 100, 30000), (40, 128, 16384), (100, 200, 16384), (256, 300, 16384), (130, 130, 16384)])
+@pytest.mark.parametrize("block", [16, 32])
+def test_long_sums(env, tokens, n, k, block):
+    """Few tiles and a long k: clusters of up to 8 CTAs share a tile."""
+    sg, torch = env
+    _check_product(env, _x(torch, tokens, k, "bfloat16", 5), _x(torch, n, k, "float16", 6, 0.3), block, "bfloat16")
+
+
+@pytest.mark.parametrize("tokens,n", [(7, 300), (50, 300), (150, 200), (700, 4000)])
+@pytest.mark.parametrize("block", [16, 32])
+def test_exact_products(env, tokens, n, block):
+    """Values that the format holds, whole numbers whose sums binary32 and the output hold exactly: the product is exact."""
+    sg, torch = env
+    k, rng = 128, np.random.default_rng(tokens)
+    grid = np.array([0, 1, 2, 3, 4, 6]) * 1.0
+    x, w = (rng.choice(grid, (m, k)) * rng.choice([-1, 1], (m, k)) * (rng.random((m, k)) < 0.2) for m in (tokens, n))
+    x[:, ::16], w[:, ::16] = 6, 6  # every block's scale is then 1
+    if block == 16:
+        x[:, 0], w[:, 0] = 6, 6
+    tx, tw = (torch.tensor(t, device="cuda").half() for t in (x, w))
+    xl, xd = sg.fp4_quantize(tx, block)
+    wl, wd = sg.fp4_quantize(tw, block)
+    got = sg.fp4_product(wl, wd, xl, xd, torch.float16)
+    want = x @ w.T
+    assert np.abs(want).max() <= 2048
+    assert np.array_equal(got.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("tokens,n", [(3, 140), (100, 140), (300, 200)])
+def test_row_scales_of_any_size(env, tokens, n):
+    """Row scales whose product leaves binary32's normal range, where the result does not, and where it does."""
+    sg, torch = env
+    k, rng = 64, np.random.default_rng(1)
+    x, w = rng.standard_normal((tokens, k)), rng.standard_normal((n, k))
+    ex, ew = rng.integers(-100, 100, tokens), rng.integers(-100, 100, n)
+    tx = torch.tensor(x * 2.0 ** ex[:, None], device="cuda").bfloat16()
+    tw = torch.tensor(w * 2.0 ** ew[:, None], device="cuda").bfloat16()
+    xl, xd = sg.fp4_quantize(tx, 16)
+    wl, wd = sg.fp4_quantize(tw, 16)
+    got = sg.fp4_product(wl, wd, xl, xd, torch.bfloat16).double()
+    xv, wv = torch.empty((tokens, k), device="cuda"), torch.empty((n, k), device="cuda")
+    sg.sgemv_fp4_read(xl, xd, xv)
+    sg.sgemv_fp4_read(wl, wd, wv)
+    ref, size = xv.double() @ wv.double().t(), xv.double().abs() @ wv.double().abs().t()
+    past = ref.to(torch.bfloat16).double()
+    err = (got - ref).abs()
+    ok = (err <= 2.0 ** -8 * ref.abs() + 16 * 2.0 ** -22 * size + 2.0 ** -134) | (got.isinf() & (got == past)) | (ref.abs() < 2.0 ** -126) & (got.abs() < 2.0 ** -125)
+    assert ok.all(), ((~ok).nonzero()[:5].tolist(), got[~ok][:5], ref[~ok][:5])
+
+
+def test_no_rows(env):
+    sg, torch = env
+    x = torch.randn((3, 64), device="cuda").half()
+    xl, xd = sg.fp4_quantize(x)
+    nl, nd = sg.fp4_quantize(x[:0])
+    assert nd.numel() == 0 and sg.fp4_product(xl, xd, nl, nd).shape == (0, 3) and sg.fp4_product(nl, nd, xl, xd).shape == (3, 0)
+    sg.sgemv_fp4_read(nl, nd, torch.empty((0, 64), device="cuda"))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens,n,k", [(1, 4096, 2048), (30, 1000, 5000), (100, 300, 8192), (400, 1500, 1000)])
+def test_product_same_bits_streams_and_graphs(env, tokens, n, k):
+    sg, torch = env
+    w = _x(torch, n, k, "float16", 1, 0.3)
+    xs = [_x(torch, tokens, k, "float16", s) for s in (2, 3)]
+    wl, wd = sg.fp4_quantize(w)
+    xq = [sg.fp4_quantize(x) for x in xs]
+    want = [sg.fp4_product(wl, wd, *q) for q in xq]
+    for _ in range(3):
+        for q, y in zip(xq, want):
+            assert torch.equal(sg.fp4_product(wl, wd, *q), y)
+    outs = [torch.empty_like(want[0]) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, q, o in zip(streams, xq, outs):
+            with torch.cuda.stream(s):
+                sg.sgemv_fp4_product(wl, wd, *q, o)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    x, (xl, xd), y = xs[0].clone(), xq[0], torch.empty_like(want[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sg.sgemv_fp4_quantize(xl, xd, x)
+        sg.sgemv_fp4_product(wl, wd, xl, xd, y)
+    for i in (1, 0):
+        x.copy_(xs[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
