@@ -9,7 +9,7 @@
 //   warps 4-11  take the sums out, two threads a token, and write them
 //   warp 12     of the first CTA issues the products of both
 // Tensor memory: two sets of sums, columns 0..255 and 208..463, and the scales in the last 48. The columns that the sets share are taken out
-// first, and then the next tile's products start while the rest is written.
+// first, and then the next tile's products start while the rest is written. Where tiles are fewer than pairs of SMs they are half as wide (kN = 128).
 #pragma once
 
 #include <cuda.h>
@@ -18,16 +18,18 @@
 
 namespace sgemv {
 
-template <int kBlock>
+template <int kBlock, int kN>
 struct ManyShape {
     static constexpr int kStageK = 256, kChunks = kStageK / 32, kGroups = kStageK / (4 * kBlock);
-    static constexpr int kCodes = 128 * kStageK / 2, kScales = kGroups * 512;
-    static constexpr int kStage = 2 * kCodes + 3 * kScales;  // codes of tokens and weights; scales of 128 tokens and 256 weight rows
-    static constexpr int kRing = 5, kThreads = 416;
+    static constexpr int kCodes = 128 * kStageK / 2, kScales = kGroups * 512;      // of 128 tokens
+    static constexpr int kWCodes = kN / 2 * kStageK / 2, kWScales = kN / 128 * kScales;  // of kN / 2 weight rows; of kN
+    static constexpr int kStage = kCodes + kWCodes + kScales + kWScales;
+    static constexpr int kRing = kN == 256 ? 5 : 6, kThreads = 416;
     static constexpr int kSmem = kRing * kStage + 8 * 4096;  // and 32 rows of 64 outputs a warp
-    static constexpr int kSecond = 208, kShared = 256 - kSecond;  // columns
-    static constexpr int kScaleCols = kSecond + 256;
-    static_assert(kScaleCols + 12 * kGroups <= 512, "tensor memory");
+    static constexpr int kSecond = kN == 256 ? 208 : 128;    // columns
+    static constexpr int kScaleCols = kSecond + kN;
+    static constexpr int kParts = kN / 64;
+    static_assert(kScaleCols + (4 + kN / 32) * kGroups <= 512 && kSmem <= 227 * 1024, "tensor memory and shared memory");
 };
 constexpr int kManyGroup = 8;  // token tiles
 
@@ -75,13 +77,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
-template <typename T, int kBlock>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::kThreads, 1) fp4_many_kernel(const __grid_constant__ Fp4Maps x_maps, const __grid_constant__ Fp4Maps w_maps, const __grid_constant__ ProductParams p) {
-    using S = ManyShape<kBlock>;
+template <typename T, int kBlock, int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN>::kThreads, 1) fp4_many_kernel(const __grid_constant__ Fp4Maps x_maps, const __grid_constant__ Fp4Maps w_maps, const __grid_constant__ ProductParams p) {
+    using S = ManyShape<kBlock, kN>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[S::kRing], free_[S::kRing], sums_full, sums_free;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_w_scale[256];
+    __shared__ __align__(16) float s_w_scale[kN];
     __shared__ float s_least[8], s_most[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int rank = blockIdx.x & 1, me_pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -134,11 +136,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
                         if (rank == 0) mbar_arrive_expect_tx(&full[b], 2 * S::kStage);
                         tma_load_pair(to, &x_maps.codes, 0, S::kChunks * i, 2 * xt + rank, bar);
                     } else if (warp == 1) {
-                        tma_load_pair(to + S::kCodes, &w_maps.codes, 0, S::kChunks * i, 2 * wt + rank, bar);
+                        if constexpr (kN == 256) tma_load_pair(to + S::kCodes, &w_maps.codes, 0, S::kChunks * i, 2 * wt + rank, bar);
+                        else tma_load_pair(to + S::kCodes, &w_maps.codes, 128 * rank, S::kChunks * i, wt, bar);
                     } else if (warp == 2) {
-                        tma_load_pair(to + 2 * S::kCodes, &x_maps.scales, 0, S::kGroups * i, 2 * xt + rank, bar);
+                        tma_load_pair(to + S::kCodes + S::kWCodes, &x_maps.scales, 0, S::kGroups * i, 2 * xt + rank, bar);
                     } else {
-                        tma_load_pair(to + 2 * S::kCodes + S::kScales, &w_maps.scales, 0, S::kGroups * i, 2 * wt, bar);
+                        tma_load_pair(to + S::kCodes + S::kWCodes + S::kScales, &w_maps.scales, 0, S::kGroups * i, kN / 128 * wt, bar);
                     }
                 }
                 __syncwarp();
@@ -151,7 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         int g = 0, turn = 0;
         if (rank == 0) {
             const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0), t_sa = tmem + S::kScaleCols, t_sb = t_sa + 4 * S::kGroups;
-            constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, 256, 0);
+            constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, kN, 0);
+            constexpr int kWCols = kN / 32;  // of scales, 64 or 128 columns of k
 #pragma unroll 1
             for (int tile = me_pair; tile < tiles; tile += pairs, ++turn) {
                 if (turn > 0 && !dead && !mbar_wait_cluster(&sums_free, (turn - 1) & 1)) {
@@ -169,21 +173,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
                     const uint32_t at = base + b * S::kStage;
                     if (elect_one()) {
                         if (!dead) {
-                            const uint64_t sd = tc_desc_plain(at + 2 * S::kCodes, 0);
+                            const uint64_t sd = tc_desc_plain(at + S::kCodes + S::kWCodes, 0);
 #pragma unroll
                             for (int j = 0; j < S::kGroups; ++j) {
                                 if (j < n) {
                                     tc_copy_scales<2>(t_sa + 4 * j, sd + 32 * j);
-                                    tc_copy_scales<2>(t_sb + 8 * j, sd + 32 * (j + S::kGroups));
-                                    tc_copy_scales<2>(t_sb + 8 * j + 4, sd + 32 * (j + 2 * S::kGroups));
+#pragma unroll
+                                    for (int h = 0; h < kN / 128; ++h) tc_copy_scales<2>(t_sb + kWCols * j + 4 * h, sd + 32 * (j + (1 + h) * S::kGroups));
                                 }
                             }
-                            const uint64_t xd = tc_desc_plain(at, 2048), wd = tc_desc_plain(at + S::kCodes, 2048);
+                            const uint64_t xd = tc_desc_plain(at, 2048), wd = tc_desc_plain(at + S::kCodes, kN / 2 * 16);
 #pragma unroll
                             for (int j = 0; j < S::kStageK / 64; ++j) {
                                 const uint32_t col = kBlock == 16 ? j : j / 2, id = kBlock == 16 ? 0 : 2 * (j & 1);
                                 if (j < steps)
-                                    tc_mma_fp4<kBlock, 2>(d, xd + j * 256, wd + j * 256, idesc | (id << 4) | (id << 29), t_sa + 4 * col, t_sb + 8 * col,
+                                    tc_mma_fp4<kBlock, 2>(d, xd + j * 256, wd + j * kN, idesc | (id << 4) | (id << 29), t_sa + 4 * col, t_sb + kWCols * col,
                                                           i > 0 || j > 0);
                             }
                         }
@@ -205,13 +209,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
         for (int tile = me_pair; tile < tiles; tile += pairs, ++turn) {
             int xt, wt;
             tile_at(tile, xt, wt);
-            const int token = xt * 256 + rank * 128 + row, n0 = wt * 256;
+            const int token = xt * 256 + rank * 128 + row, n0 = wt * kN;
             // the scales of the rows, and whether any product of two leaves binary32's normal range
             const float xs = token < p.x.rows ? p.x.row_scale[token] : 1.0f;
             float least, most;
             {
-                const float f = n0 + me < p.w.rows ? p.w.row_scale[n0 + me] : 1.0f;
-                s_w_scale[me] = f;
+                const float f = me < kN && n0 + me < p.w.rows ? p.w.row_scale[n0 + me] : 1.0f;
+                if (me < kN) s_w_scale[me] = f;
                 least = f == f ? f : 0.0f, most = f;
             }
             const unsigned lo = __reduce_min_sync(0xFFFFFFFFu, __float_as_uint(least)), hi = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
@@ -228,8 +232,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock>::k
             // 64 columns at a time, first those that the other set of sums shares, through shared memory, so that whole lines of rows are written
             uint8_t* const stage = smem + S::kRing * S::kStage + (warp - 4) * 4096;
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const int part = ((turn & 1) ? k : k + 3) + 2 * half & 3, col = n0 + 64 * part;
+            for (int k = 0; k < S::kParts / 2; ++k) {
+                const int part = kN == 256 ? ((turn & 1) ? k : k + 3) + 2 * half & 3 : half, col = n0 + 64 * part;
                 uint32_t r[2][32];
                 tc_ld32(r[0], from + 64 * part);
                 tc_ld32(r[1], from + 64 * part + 32);

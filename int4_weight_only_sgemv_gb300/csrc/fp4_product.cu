@@ -18,6 +18,12 @@ bool many_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x) {
     return x.rows > 64 && w.rows > 64 && (tiles >= 8 || w.kp <= 4096);
 }
 
+// Whether its tiles are 256 weight rows wide, or 128.
+bool wide_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x, int sms) {
+    const int64_t tiles = static_cast<int64_t>((x.rows + 255) / 256) * ((w.rows + 255) / 256);
+    return tiles > sms / 4;
+}
+
 template <typename T, int kBlock, int kStageK>
 cudaError_t launch_few_stage(const ProductParams& p, int64_t tiles, int smem, cudaStream_t s) {
     auto kern = fp4_few_kernel<T, kBlock, kStageK>;
@@ -52,19 +58,18 @@ cudaError_t launch_few(const ProductParams& p, int64_t tiles, int smem, cudaStre
     return few_stage_k(p.x.tile) == 512 ? launch_few_stage<T, kBlock, 512>(p, tiles, smem, s) : launch_few_stage<T, kBlock, 256>(p, tiles, smem, s);
 }
 
-template <int kBlock>
-bool map_fp4(Fp4Maps* maps, const Fp4Matrix& m, unsigned scale_tiles) {
-    using S = ManyShape<kBlock>;
+// `rows` rows of a tile's codes (128 or 64) and the scales of `tiles` tiles at a time.
+bool map_fp4(Fp4Maps* maps, const Fp4Matrix& m, unsigned chunks_a_box, unsigned groups_a_box, unsigned rows, unsigned scale_tiles) {
     const cuuint64_t tiles = static_cast<cuuint64_t>((m.rows + 127) / 128), chunks = static_cast<cuuint64_t>(m.kp / 32), groups = static_cast<cuuint64_t>(m.groups);
-    return encode_map(&maps->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.codes, {256, chunks, tiles}, {2048, chunks * 2048}, {256, S::kChunks, 1},
+    return encode_map(&maps->codes, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.codes, {256, chunks, tiles}, {2048, chunks * 2048}, {2 * rows, chunks_a_box, 1},
                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
-           encode_map(&maps->scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scales, {64, groups, tiles}, {512, groups * 512}, {64, S::kGroups, scale_tiles},
+           encode_map(&maps->scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scales, {64, groups, tiles}, {512, groups * 512}, {64, groups_a_box, scale_tiles},
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
-template <typename T, int kBlock>
-cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
-    using S = ManyShape<kBlock>;
-    auto kern = fp4_many_kernel<T, kBlock>;
+template <typename T, int kBlock, int kN>
+cudaError_t launch_many_wide(ProductParams p, int sms, cudaStream_t s) {
+    using S = ManyShape<kBlock, kN>;
+    auto kern = fp4_many_kernel<T, kBlock, kN>;
     static std::atomic<int> attr_set[64];  // per device: dynamic shared memory already enabled
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -76,9 +81,15 @@ cudaError_t launch_many(const ProductParams& p, int sms, cudaStream_t s) {
         attr_set[dev].store(1);
     }
     Fp4Maps x_maps, w_maps;
-    if (!map_fp4<kBlock>(&x_maps, p.x, 1) || !map_fp4<kBlock>(&w_maps, p.w, 2)) return cudaErrorInvalidValue;
+    if (!map_fp4(&x_maps, p.x, S::kChunks, S::kGroups, 128, 1) || !map_fp4(&w_maps, p.w, S::kChunks, S::kGroups, kN / 2, kN / 128)) return cudaErrorInvalidValue;
+    p.tiles_x = (p.x.rows + 255) / 256, p.tiles_w = (p.w.rows + kN - 1) / kN;
+    p.k_stages = (p.w.kp + S::kStageK - 1) / S::kStageK;
     const int pairs = std::min(p.tiles_x * p.tiles_w, sms / 2);
     return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(S::kThreads), S::kSmem, s, x_maps, w_maps, p);
+}
+template <typename T, int kBlock>
+cudaError_t launch_many(const ProductParams& p, bool wide, int sms, cudaStream_t s) {
+    return wide ? launch_many_wide<T, kBlock, 256>(p, sms, s) : launch_many_wide<T, kBlock, 128>(p, sms, s);
 }
 
 }  // namespace
@@ -117,11 +128,10 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool half = dtype == SGEMV_F16;
     if (many_tiles(w, x)) {
-        p.tiles_x = (x.rows + 255) / 256, p.tiles_w = (w.rows + 255) / 256;
-        p.k_stages = (w.kp + ManyShape<16>::kStageK - 1) / ManyShape<16>::kStageK;
         const int sms = di.sm_count;
-        const cudaError_t e = w.block == 16 ? (half ? launch_many<__half, 16>(p, sms, s) : launch_many<__nv_bfloat16, 16>(p, sms, s))
-                                            : (half ? launch_many<__half, 32>(p, sms, s) : launch_many<__nv_bfloat16, 32>(p, sms, s));
+        const bool wide = wide_tiles(w, x, sms);
+        const cudaError_t e = w.block == 16 ? (half ? launch_many<__half, 16>(p, wide, sms, s) : launch_many<__nv_bfloat16, 16>(p, wide, sms, s))
+                                            : (half ? launch_many<__half, 32>(p, wide, sms, s) : launch_many<__nv_bfloat16, 32>(p, wide, sms, s));
         return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
     }
     // CTAs a tile: as many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
