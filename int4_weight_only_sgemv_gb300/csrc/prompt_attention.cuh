@@ -33,6 +33,7 @@ struct PromptParams {
     int ratio;      // query heads a KV head
     int sub;        // of them, in a row tile: the largest divisor of ratio up to 128
     int tokens;     // of a row tile: 128 / sub
+    int out32;      // rows of out start at multiples of 32 bytes
     int groups;     // heads * ratio / sub: KV heads, each as often as it has groups of `sub` query heads
     float scale_log2;
 };
@@ -44,12 +45,11 @@ struct PromptShape {
     static constexpr int kBufs = 2;        // of K and of V (the product warps count on two)
     static constexpr int kSegs = 4;        // segments known ahead
     static constexpr int kQBytes = kTile * D * 2, kKvBytes = kKeys * D * 2;
-    static constexpr int kOutBytes = 32 * 64;  // a warp's staging: 32 dims of 32 rows
     static constexpr int kWarps = 12, kThreads = 32 * kWarps;
     // Registers a thread at launch, and after the split: the softmax's 8 warps, whose rows' 128 scores stay in them, and 4.
     static constexpr int kRegs = 168, kRegsSoftmax = 200, kRegsOther = 104;
     static_assert(8 * kRegsSoftmax + 4 * kRegsOther == kWarps * kRegs, "the split of the launch's registers");
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kBufs * kKvBytes + 8 * kOutBytes;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kBufs * kKvBytes;
     static constexpr int kCols = 512;  // tensor memory: S of both row tiles (128 columns each), O of both
 };
 
@@ -88,6 +88,9 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
                      smem_addr(dst)),
                  "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
                  : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int x, int y, int z) {  // into L2
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
 }
 // Operand descriptor of V [key][64 dims] tiles as the instruction's transposed side: 128-byte swizzle, 8 keys every 1024 bytes, `next`
 // bytes from 64 dims to the next 64.
@@ -166,7 +169,6 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     uint8_t* const s_q = smem;
     uint8_t* const s_k = s_q + 2 * S::kQBytes;
     uint8_t* const s_v = s_k + S::kBufs * S::kKvBytes;
-    uint8_t* const s_out = s_v + S::kBufs * S::kKvBytes;
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_ok[S::kBufs], v_free[S::kBufs];
     __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], seg_full[S::kSegs], seg_free[S::kSegs], turn[2];
     __shared__ PromptSegment s_seg[S::kSegs];
@@ -406,48 +408,36 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (live && p.q.lse_dev != nullptr)
                 p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
-            uint8_t* const stage = s_out + warp * S::kOutBytes;
-            T* out[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int rr = 32 * (warp & 3) + 8 * n + (lane >> 2), token = i0 + rr / p.sub;
-                out[n] = rr < p.tokens * p.sub && token < sg.n
-                             ? static_cast<T*>(p.q.out_dev) + (sg.first + token) * p.q.out_token_stride +
-                                   (sg.group * p.sub + rr % p.sub) * p.q.out_head_stride + 8 * (lane & 3)
-                             : nullptr;
-            }
+            T* const out = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
             wait(&o_full[x], segs & 1);
             ++segs;
             __syncwarp();
             tc_after_sync();
             const bool odd = *static_cast<volatile int*>(&s_odd[it % S::kSegs]) != 0;
-            // 32 dims at a time through shared memory, so that 4 lanes write 64 bytes of a row
             uint32_t o[D / 32][32];
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) tc_ld32(o[q], to + 32 * q);
             tc_wait_ld();
+            if (live) {
+                // (32 bytes at a time are whole sectors; through shared memory, into whole lines, a tile's outputs took XXX cycles)
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
+                for (int n = 0; n < D; n += 16) {
+                    uint32_t h[8];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        h[e] = pack_two<T>(__uint_as_float(o[q][8 * n + 2 * e]) * inv, __uint_as_float(o[q][8 * n + 2 * e + 1]) * inv);
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((n ^ (lane >> 1)) & 3) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int e = 0; e < 8; ++e)
+                        h[e] = pack_two<T>(__uint_as_float(o[n / 32][n % 32 + 2 * e]) * inv, __uint_as_float(o[n / 32][n % 32 + 2 * e + 1]) * inv);
+                    if (p.out32) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + n), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]),
+                                     "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                                     : "memory");
+                    } else {
+                        *reinterpret_cast<uint4*>(out + n) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(out + n + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
                 }
-                __syncwarp();
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int rr = 8 * n + (lane >> 2);
-                    const uint4 h = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
-                    if (out[n] != nullptr) *reinterpret_cast<uint4*>(out[n] + 32 * q) = h;
-                }
-                __syncwarp();
             }
             if (odd && live) {
                 // what was taken out of V, for the rows that see it
-                T* const mine = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
                 const T* const v_rows = static_cast<const T*>(p.q.v_dev) + sg.group * p.sub / p.ratio * p.q.v_head_stride;
 #pragma unroll 1
                 for (int pos = max(see0, rg.from * S::kKeys); pos < see0 + static_cast<int>(see); ++pos) {
@@ -455,7 +445,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
 #pragma unroll 1
                     for (int d = 0; d < D; ++d) {
                         const float f = to_f32(v_rows[(sg.first + pos) * p.q.v_token_stride + d]);
-                        if (!(fabsf(f) < INFINITY)) mine[d] = from_f32<T>(to_f32(mine[d]) + f);
+                        if (!(fabsf(f) < INFINITY)) out[d] = from_f32<T>(to_f32(out[d]) + f);
                     }
                 }
             }
@@ -601,6 +591,9 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             if (sg.n < 0) break;
             const PromptTiles t = prompt_tiles(p, sg);
             const int head = sg.group * p.sub / p.ratio;
+            if (it > 0 && lane < 2 * S::kAtoms && t.to(lane & 1) > 0)  // (their place is not free for a while)
+                tma_prefetch(&q_map, 64 * (lane >> 1), sg.group * p.sub, sg.first + sg.t0 + p.tokens * (lane & 1));
+            __syncwarp();
 #pragma unroll 1
             for (int j = t.first(); j < t.last() && !dead; ++j, ++g) {
                 const int buf = g % S::kBufs, key = sg.first + j * S::kKeys;
