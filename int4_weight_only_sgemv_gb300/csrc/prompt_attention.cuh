@@ -50,7 +50,12 @@ struct PromptShape {
     static constexpr int kRegs = 168, kRegsSoftmax = 200, kRegsOther = 104;
     static_assert(8 * kRegsSoftmax + 4 * kRegsOther == kWarps * kRegs, "the split of the launch's registers");
     static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kBufs * kKvBytes;
-    static constexpr int kCols = 512;  // tensor memory: S of both row tiles (128 columns each), O of both
+    // Tensor memory: O of both row tiles, and S, 128 columns a tile. With heads of 64 there is room for a third S: a row tile's next scores are then
+    // formed before its weights are taken, so that they are there when its softmax is done with the last ones.
+    static constexpr bool kAhead = D == 64;
+    static constexpr int kCols = 512, kOCols = kAhead ? 384 : 256;
+    // Columns of the scores of row tile x and the CTA's g-th key tile: the places go round in the order of the turns.
+    static __device__ __forceinline__ uint32_t scores_at(int g, int x) { return 128u * (kAhead ? static_cast<uint32_t>(2 * g + x) % 3u : static_cast<uint32_t>(x)); }
 };
 
 // Weights 2^(t - m): the largest is 2^kTop when the reference m is set, which happens anew when a tile's sum passes kBig (or, where the largest score
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     uint8_t* const s_k = s_q + 2 * S::kQBytes;
     uint8_t* const s_v = s_k + S::kBufs * S::kKvBytes;
     __shared__ __align__(8) uint64_t k_full[S::kBufs], k_free[S::kBufs], v_full[S::kBufs], v_ok[S::kBufs], v_free[S::kBufs];
-    __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], seg_full[S::kSegs], seg_free[S::kSegs], turn[2];
+    __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2][2], o_full[2][2], seg_full[S::kSegs], seg_free[S::kSegs], turn[2];
     __shared__ PromptSegment s_seg[S::kSegs];
     __shared__ int s_odd[S::kSegs];                                             // a segment's V has elements that are no numbers
     __shared__ int t_before[S::kThreads], t_blocks[S::kThreads];  // where segments are, below
@@ -185,7 +190,8 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1), mbar_init(&q_free[i], 1);
-            mbar_init(&turn[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
+            mbar_init(&turn[i], 1);
+            for (int e = 0; e < 2; ++e) mbar_init(&s_full[i][e], 1), mbar_init(&p_full[i][e], 128), mbar_init(&o_full[i][e], 1);
         }
         for (int i = 0; i < S::kSegs; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_free[i], 11);
         mbar_fence_init();
@@ -268,15 +274,18 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         // ---------------------------------------------------------------------------------------- softmax
         const int x = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + 128 * x;
+        const uint32_t to = tmem + lanes + S::kOCols + (S::kAhead ? 64 : 128) * x;
         const float c = p.scale_log2;
-        uint32_t tiles = 0, segs = 0;  // that this row tile has had
+        uint32_t tiles = 0;  // that this row tile has had
+        int before_segment = 0;  // key tiles of the CTA before the segment
 #pragma unroll 1
         for (int it = 0;; ++it) {
             const PromptSegment sg = segment(it);
             if (sg.n < 0) break;
             const PromptTiles all = prompt_tiles(p, sg);
             const PromptRange rg = x == 0 ? all.r0 : all.r1;
+            const int g0 = before_segment - all.first();  // key tile j is the CTA's g0 + j th
+            before_segment += all.last() - all.first();
             if (rg.from >= rg.to) {
                 release(it);
                 continue;
@@ -293,7 +302,8 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
 #pragma unroll 1
             for (int j = rg.from; j < rg.to; ++j, ++tiles) {
                 const int pos0 = j * S::kKeys;
-                wait(&s_full[x], tiles & 1);  // (and all products issued before: O holds every tile before this one)
+                const uint32_t ts = tmem + lanes + S::scores_at(g0 + j, x);
+                wait(&s_full[x][tiles & 1], (tiles >> 1) & 1);
                 __syncwarp();
                 tc_after_sync();
                 const bool plain = pos0 >= rg.clear0 && pos0 + S::kKeys <= rg.clear1;
@@ -370,6 +380,9 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                     if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
                         l2 = mul2(l2, pair(f, f));
                         if (j > rg.from) {
+                            wait(&o_full[x][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);  // (O holds every tile before this one)
+                            __syncwarp();
+                            tc_after_sync();
 #pragma unroll 1
                             for (int d = 0; d < D / 16; ++d) {
                                 uint32_t o[16];
@@ -401,7 +414,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                 }
                 tc_wait_st();
                 tc_before_sync();
-                mbar_arrive(&p_full[x]);
+                mbar_arrive(&p_full[x][tiles & 1]);
             }
             const float2 lf = parts_of(l2);
             const float l = lf.x + lf.y;
@@ -409,8 +422,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             if (live && p.q.lse_dev != nullptr)
                 p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
             T* const out = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
-            wait(&o_full[x], segs & 1);
-            ++segs;
+            wait(&o_full[x][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
             __syncwarp();
             tc_after_sync();
             const bool odd = *static_cast<volatile int*>(&s_odd[it % S::kSegs]) != 0;
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         // key tile); and as one waits for what its turn needs while the other issues, the tensor cores get one's after the other's (with
         // one warp for both they stood still for 450 cycles a turn: 3370 cycles).
         const int x = warp - 8;
-        const uint32_t ts = __shfl_sync(0xFFFFFFFFu, tmem, 0) + 128 * x, to = ts + 256;
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), to = tm + S::kOCols + (S::kAhead ? 64 : 128) * x;
         const uint64_t q_desc = tc_desc(smem_addr(s_q) + x * S::kQBytes), k_desc = tc_desc(smem_addr(s_k));
         const uint64_t v_desc = tc_desc_v(smem_addr(s_v), S::kKeys * 128);
         constexpr uint32_t kScores = tc_idesc(S::kKeys) | tc_idesc_type<T>(), kOut = tc_idesc(D) | tc_idesc_type<T>() | (1u << 16);
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             wait(bar, parity);
             dead = __any_sync(0xFFFFFFFFu, dead);
         };
-        uint32_t q_had = 0, p_had = 0;
+        uint32_t q_had = 0, s_had = 0, p_had = 0;
         PromptSegment sg = segment(0);
         PromptTiles t = prompt_tiles(p, sg);
         int it = 0, g = -1;  // segment; key tiles so far
@@ -491,26 +503,37 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             const uint32_t parity = (g >> 1) & 1, next_parity = ((g + 1) >> 1) & 1;
             const uint64_t vd = v_desc + buf * (S::kKvBytes >> 4), kd = k_desc + next_buf * (S::kKvBytes >> 4);
             const bool add = j > t.from(x);
-            // (who does not have a tile lets it go all the same, once it is there: its buffers wait for both)
-            if (g >= 0) hold(&v_ok[buf], parity);
-            if (!cross) hold(&k_full[next_buf], next_parity);
-            if (!old_keys && g >= 0 && lane == 0) mbar_arrive(&v_free[buf]);
-            hold(&turn[x], (g + 1) & 1);
-            if (old_keys) hold(&p_full[x], p_had++ & 1);
-            tc_after_sync();
-            if (old_keys) {
+            const uint32_t from = tm + S::scores_at(g, x), ts = tm + S::scores_at(g + 1, x);
+            const auto give_turn = [&]() {  // the other's products come after those issued so far
+                tc_before_sync();
+                mbar_arrive(&turn[x ^ 1]);
+            };
+            const auto outputs = [&]() {
+                if (!old_keys) {
+                    if (S::kAhead && lane == 0) give_turn();
+                    return;
+                }
+                hold(&p_full[x][p_had & 1], (p_had >> 1) & 1);
+                tc_after_sync();
                 if (elect_one()) {
                     if (!dead) {
 #pragma unroll
-                        for (int kk = 0; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, ts + 8 * kk, vd + kk * (2048 >> 4), kOut, kk > 0 || add);
+                        for (int kk = 0; kk < S::kKeys / 16; ++kk) tc_mma_ts(to, from + 8 * kk, vd + kk * (2048 >> 4), kOut, kk > 0 || add);
                     }
+                    if (S::kAhead) give_turn();
                     tc_commit(&v_free[buf]);
-                    if (j == t.to(x) - 1) tc_commit(&o_full[x]);
+                    tc_commit(&o_full[x][p_had & 1]);
                 }
+                ++p_had;
                 __syncwarp();
-            }
-            if (cross && next_sg.n >= 0) hold(&k_full[next_buf], next_parity);
-            if (new_keys) {
+            };
+            const auto scores = [&]() {
+                if (cross && next_sg.n >= 0) hold(&k_full[next_buf], next_parity);
+                if (!new_keys) {
+                    if (!S::kAhead && lane == 0) give_turn();
+                    if (next_sg.n >= 0 && lane == 0) mbar_arrive(&k_free[next_buf]);
+                    return;
+                }
                 if (next_j == next.from(x)) {
                     hold(&q_full[x], q_had++ & 1);
                     tc_after_sync();
@@ -520,18 +543,30 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = (kk / 4 * (128 * 128) + kk % 4 * 32) >> 4;
-                            tc_mma_ss(ts, q_desc + off, kd + off, kScores, kk > 0);  // (over the weights just used: products run in the order of their issue)
+                            tc_mma_ss(ts, q_desc + off, kd + off, kScores, kk > 0);
                         }
                     }
-                    mbar_arrive(&turn[x ^ 1]);
-                    tc_commit(&s_full[x]);
+                    if (!S::kAhead) give_turn();
+                    tc_commit(&s_full[x][s_had & 1]);
                     tc_commit(&k_free[next_buf]);
                     if (next_j == next.to(x) - 1) tc_commit(&q_free[x]);
                 }
+                ++s_had;
                 __syncwarp();
-            } else if (lane == 0) {
-                mbar_arrive(&turn[x ^ 1]);
-                if (next_sg.n >= 0) mbar_arrive(&k_free[next_buf]);
+            };
+            // (who does not have a tile lets it go all the same, once it is there: its buffers wait for both)
+            if (g >= 0) hold(&v_ok[buf], parity);
+            if (!cross) hold(&k_full[next_buf], next_parity);
+            if (!old_keys && g >= 0 && lane == 0) mbar_arrive(&v_free[buf]);
+            hold(&turn[x], (g + 1) & 1);
+            tc_after_sync();
+            // (products run in the order of their issue: the scores go over weights whose products come before)
+            if constexpr (S::kAhead) {
+                scores();
+                outputs();
+            } else {
+                outputs();
+                scores();
             }
             if (cross) release(it++);
             sg = next_sg, t = next, j = next_j;
