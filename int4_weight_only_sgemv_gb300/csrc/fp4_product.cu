@@ -11,14 +11,15 @@ namespace sgemv {
 namespace {
 
 // Whether a call goes to the kernel of many tiles: with more than 64 tokens, but where few tiles meet a long sum, which the other splits. us a call,
-// many and few: 65 x 4096 x 4096 9.1, 10.6; 128 x 11008 x 4096 10.4, 14.2; 129 x 1024 x 4096 8.7, 8.4; 129 x 1024 x 8192 13.3, 10.3; 512 x 512 x 8192 13.2, 10.5;
-// 100 x 200 x 16384 22.3, 9.8; 256 x 300 x 16384 23.2, 10.7.
+// many and few: 65 x 4096 x 4096 7.4, 10.6; 129 x 1024 x 4096 7.0, 8.2; 129 x 1024 x 6144 9.0, 9.3; 129 x 1024 x 8192 10.7, 10.3; 512 x 512 x 8192 11.0,
+// 10.5; 100 x 200 x 16384 17.8, 9.8; 256 x 300 x 16384 18.7, 10.6.
 bool many_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x) {
     const int64_t tiles = static_cast<int64_t>((x.rows + 255) / 256) * ((w.rows + 255) / 256);
-    return x.rows > 64 && w.rows > 64 && (tiles >= 8 || w.kp <= 4096);
+    return x.rows > 64 && w.rows > 64 && (tiles >= 8 || w.kp <= 6144);
 }
 
-// Whether its tiles are 256 weight rows wide, or 128.
+// Whether its tiles are 256 weight rows wide, or 128, of which there are twice as many. us a call, 256 and 128: 512 x 4096 x 4096 (32 tiles of 256) 10.0, 8.5;
+// 333 x 4096 x 11008 (32) 17.6, 14.6; 100 x 11008 x 4096 (43) 10.6, 13.3; 1024 x 4096 x 4096 (64) 10.7, 13.5.
 bool wide_tiles(const sgemv_fp4_layout& w, const sgemv_fp4_layout& x, int sms) {
     const int64_t tiles = static_cast<int64_t>((x.rows + 255) / 256) * ((w.rows + 255) / 256);
     return tiles > sms / 4;

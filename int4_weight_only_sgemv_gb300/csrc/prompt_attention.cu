@@ -123,6 +123,7 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
     // at most so many segments: every request's last may be short
     const int64_t most = (static_cast<int64_t>(q.n_tokens) / (2 * p.tokens) + q.n_req) * p.groups;
     if (most > INT_MAX) return SGEMV_ERR_SHAPE;
+    p.most = static_cast<int>(most);
     CUtensorMap q_map, k_map, v_map;
     if (!map_rows(&q_map, q.q_dev, q, q.heads_q, q.q_token_stride, q.q_head_stride, p.tokens, p.sub) ||
         !map_rows(&k_map, q.k_dev, q, q.heads, q.k_token_stride, q.k_head_stride, 128, 1) ||

@@ -41,6 +41,7 @@ struct PromptParams {
     int tokens;     // of a row tile: 128 / sub
     int out32;      // rows of out start at multiples of 32 bytes
     int groups;     // heads * ratio / sub: KV heads, each as often as it has groups of `sub` query heads
+    int most;       // segments that requests in order can have
     float scale_log2;
 };
 
@@ -250,6 +251,10 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
     for (int w = 0; w < S::kWarps; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
+    }
+    if (total > p.most) {  // (requests that overlap: their starts are not in order)
+        report(p.status, SGEMV_ERR_ARG);
+        total = 0;
     }
     t_before[tid] = static_cast<int>(before);
     tc_before_sync();
@@ -610,9 +615,10 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                     o %= width;
                     s = t_span[by_block ? o / groups : x];
                 } else {
+                    s = {0, 0}, block = 0;
 #pragma unroll 1
-                    for (int req = x * run;; ++req) {
-                        s = prompt_span(p, req);
+                    for (int64_t req = static_cast<int64_t>(x) * run; req < min(static_cast<int64_t>(x + 1) * run, static_cast<int64_t>(p.q.n_req)); ++req) {
+                        s = prompt_span(p, static_cast<int>(req));
                         const unsigned n = prompt_blocks(p, s.n) * groups;
                         if (o < n) {
                             block = n / groups - 1 - o / groups;
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                         o -= n;
                     }
                 }
-                sg = {s.first, s.n, static_cast<int>(o % groups), static_cast<int>(block) * 2 * p.tokens};
+                if (s.n > 0) sg = {s.first, s.n, static_cast<int>(o % groups), static_cast<int>(block) * 2 * p.tokens};
             }
             if (lane == 0) {
                 s_seg[it % S::kSegs] = sg;

@@ -9,6 +9,7 @@ shape and strides, and their addresses passed on. Nothing here allocates except 
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -42,29 +43,27 @@ class PromptQuery(ctypes.Structure):
         [(n, ctypes.c_void_p) for n in ("q_dev", "k_dev", "v_dev", "start_dev", "length_dev", "out_dev", "lse_dev")]
 
 
+# PromptQuery's bytes: filling them in at once takes 0.6 us, a Structure field by field 2.
+_QUERY = struct.Struct("=8ifi8q7Q")
+assert _QUERY.size == ctypes.sizeof(PromptQuery)
+
 _c, _p, _i, _l = ctypes, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 _lib.sgemv_fp4_layout_query.argtypes = [_i] * 3 + [_c.POINTER(Fp4Layout)]
 _lib.sgemv_fp4_quantize.argtypes = [_c.POINTER(Fp4Layout), _p, _i, _l, _p, _p, _p]
 _lib.sgemv_fp4_read.argtypes = [_c.POINTER(Fp4Layout), _p, _p, _i, _l, _p]
 _lib.sgemv_fp4_product.argtypes = [_c.POINTER(Fp4Layout), _p, _c.POINTER(Fp4Layout), _p, _p, _i, _l, _p, _p]
-_lib.sgemv_prompt_attention.argtypes = [_c.POINTER(PromptQuery), _p, _p]
+_lib.sgemv_prompt_attention.argtypes = [_p, _p, _p]
 for _name in EXPORTED_PROMPT:
     getattr(_lib, _name).restype = ctypes.c_int
 
 
-def _handle(stream, dev):
-    return _kv._raw_stream(dev) if stream is None else _stream(stream)
-
-
-def _matrix(t, rows, cols, what, dev):
+def _row_stride(t, rows, cols, what, dev):
     """t is a tensor [rows, cols] on the device with contiguous columns: its row stride."""
     try:
-        if t.get_device() == dev and t.dim() == 2:
-            n, k = t.shape
-            if n == rows and k == cols:
-                s0, s1 = t.stride()
-                if (k < 2 or s1 == 1) and (n < 2 or s0 >= k):
-                    return s0 if n > 1 else k
+        if t.get_device() == dev and t.shape == (rows, cols):
+            s0, s1 = t.stride()
+            if (s1 == 1 or cols < 2) and (s0 >= cols or rows < 2):
+                return s0 if rows > 1 else cols
     except AttributeError:
         raise TypeError(f"{what}: expected a torch.Tensor") from None
     raise ValueError(f"{what}: expected a tensor [{rows}, {cols}] on cuda:{dev} with contiguous columns and rows that do not overlap")
@@ -91,11 +90,11 @@ def sgemv_fp4_layout_query(rows: int, k: int, block: int) -> Fp4Layout:
 def sgemv_fp4_quantize(layout: Fp4Layout, packed, x, status=None, stream=None) -> None:
     """The 4-bit matrix of x (fp16 or bf16 [rows, k], any row stride) into packed (uint8, layout.total_bytes)."""
     dev = _packed(layout, packed, "packed")
-    stride = _matrix(x, layout.rows, layout.k, "x", dev)
+    row = _row_stride(x, layout.rows, layout.k, "x", dev)
     if status is not None:
         _flat(status, torch.int32, None, "status", dev)
-    code = _lib.sgemv_fp4_quantize(ctypes.byref(layout), x.data_ptr(), _DTYPE.get(x.dtype, -1), stride, packed.data_ptr(), _ptr(status),
-                                   _handle(stream, dev))
+    code = _lib.sgemv_fp4_quantize(ctypes.byref(layout), x.data_ptr(), _DTYPE.get(x.dtype, -1), row, packed.data_ptr(), _ptr(status),
+                                   _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_fp4_quantize")
 
@@ -103,9 +102,9 @@ def sgemv_fp4_quantize(layout: Fp4Layout, packed, x, status=None, stream=None) -
 def sgemv_fp4_read(layout: Fp4Layout, packed, out, stream=None) -> None:
     """The values that a 4-bit matrix stands for into out (fp16, bf16 or fp32 [rows, k], any row stride)."""
     dev = _packed(layout, packed, "packed")
-    stride = _matrix(out, layout.rows, layout.k, "out", dev)
+    stride = _row_stride(out, layout.rows, layout.k, "out", dev)
     code = _lib.sgemv_fp4_read(ctypes.byref(layout), packed.data_ptr(), out.data_ptr(), _DTYPE.get(out.dtype, -1), stride,
-                               _handle(stream, dev))
+                               _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_fp4_read")
 
@@ -114,11 +113,12 @@ def sgemv_fp4_product(w_layout: Fp4Layout, w, x_layout: Fp4Layout, x, y, status=
     """y[t][n] = sum over k of x[t][k] w[n][k] of two 4-bit matrices; y: fp16 or bf16 [x rows, w rows], any row stride."""
     dev = _packed(w_layout, w, "w")
     _packed(x_layout, x, "x")
-    stride = _matrix(y, x_layout.rows, w_layout.rows, "y", dev)
+    stride = _row_stride(y, x_layout.rows, w_layout.rows, "y", dev)
     if status is not None:
         _flat(status, torch.int32, None, "status", dev)
     code = _lib.sgemv_fp4_product(ctypes.byref(w_layout), w.data_ptr(), ctypes.byref(x_layout), x.data_ptr(), y.data_ptr(),
-                                  _DTYPE.get(y.dtype, -1), stride, _ptr(status), _handle(stream, dev))
+                                  _DTYPE.get(y.dtype, -1), stride, _ptr(status),
+                                  _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_fp4_product")
 
@@ -130,30 +130,47 @@ def sgemv_prompt_attention(q, k, v, start, out, scale: float, length=None, lse=N
     ends); lse: fp32 [tokens, heads_q] or None."""
     i32 = torch.int32
     try:
-        dev = _device(q, "q")
-        dtype = q.dtype
-        n, heads_q, dim = shape = q.shape
-        if k.dim() != 3:
-            raise ValueError("k: expected a tensor [tokens, heads, dim]")
-        heads = k.shape[1]
-        kv_shape = (n, heads, dim)
-        qs, os = _rows(q, shape, dtype, "q", dev), _rows(out, shape, dtype, "out", dev)
-        ks, vs = _rows(k, kv_shape, dtype, "k", dev), _rows(v, kv_shape, dtype, "v", dev)
+        dev, dtype, shape = q.get_device(), q.dtype, q.shape
+        if dev < 0 or dev != _kv._current():
+            _device(q, "q")
+        n, heads_q, dim = shape
+        kv_shape = k.shape
+        # (asked in one go: a call for each tensor costs as much as the questions)
+        if not (k.dtype is dtype and v.dtype is dtype and out.dtype is dtype and k.get_device() == dev and v.get_device() == dev and
+                out.get_device() == dev and out.shape == shape and v.shape == kv_shape and len(kv_shape) == 3 and kv_shape[0] == n and
+                kv_shape[2] == dim):
+            if k.dim() != 3:
+                raise ValueError("k: expected a tensor [tokens, heads, dim]")
+            _rows(out, shape, dtype, "out", dev)
+            kv_shape = (n, k.shape[1], dim)
+            _rows(k, kv_shape, dtype, "k", dev)
+            _rows(v, kv_shape, dtype, "v", dev)
+        q0, q1, q2 = q.stride()
+        k0, k1, k2 = k.stride()
+        v0, v1, v2 = v.stride()
+        o0, o1, o2 = out.stride()
+        if not q2 == k2 == v2 == o2 == 1:
+            raise ValueError("q, k, v, out: expected contiguous dims")
         if start.dtype is not i32 or start.get_device() != dev or not start.is_contiguous():
             _flat(start, i32, None, "start", dev)
         n_req = start.numel() - 1
         if length is not None:
             _flat(length, i32, n_req, "length", dev)
         if lse is not None:
-            _flat(lse, torch.float32, n * heads_q, "lse", dev)
+            if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.numel() != n * heads_q:
+                _flat(lse, torch.float32, n * heads_q, "lse", dev)
         if status is not None:
             _flat(status, i32, None, "status", dev)
     except AttributeError:
         raise TypeError("sgemv_prompt_attention: expected torch.Tensors") from None
-    args = PromptQuery(_DTYPE.get(dtype, -1), heads_q, heads, dim, n_req, n, 1 if causal else 0, window, scale, 0, qs[0], qs[1], ks[0],
-                       ks[1], vs[0], vs[1], os[0], os[1], q.data_ptr(), k.data_ptr(), v.data_ptr(), start.data_ptr(), _ptr(length),
-                       out.data_ptr(), _ptr(lse))
-    code = _lib.sgemv_prompt_attention(ctypes.byref(args), _ptr(status), _handle(stream, dev))
+    try:
+        query = _QUERY.pack(_DTYPE.get(dtype, -1), heads_q, kv_shape[1], dim, n_req, n, 1 if causal else 0, window, scale, 0, q0, q1, k0, k1, v0, v1,
+                            o0, o1, q.data_ptr(), k.data_ptr(), v.data_ptr(), start.data_ptr(), 0 if length is None else length.data_ptr(),
+                            out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"sgemv_prompt_attention: {e}") from None
+    code = _lib.sgemv_prompt_attention(query, None if status is None else status.data_ptr(),
+                                       _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_prompt_attention")
 

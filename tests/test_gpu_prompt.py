@@ -248,6 +248,18 @@ def test_requests_out_of_range_are_reported(env, start, length, bad):
             assert torch.equal(out[at], want), r
 
 
+@pytest.mark.parametrize("n_req", [301, 1001])
+def test_overlapping_requests_do_nothing(env, n_req):
+    """Starts that go back and forth: every second request is out of order, and the others are the same rows again and again."""
+    sg, torch = env
+    t = torch.randn((600, 4, 64), device="cuda").half()
+    out, status = torch.full((600, 2, 64), 9.0, device="cuda").half(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 600] * (n_req // 2 + 1), dtype=torch.int32, device="cuda")[:n_req + 1].contiguous()
+    sg.sgemv_prompt_attention(t[:, :2], t[:, 2:3], t[:, 3:], start, out, 0.125, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == sg.SGEMV_ERR_ARG and torch.all(out == 9.0)
+
+
 def test_no_requests_and_no_tokens(env):
     sg, torch = env
     t = torch.randn((10, 4, 64), device="cuda").half()

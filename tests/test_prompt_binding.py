@@ -104,7 +104,7 @@ def test_rows(env):
     t = cuda(9, 8, 64, dtype=torch.float16)
     q, k, v, out, start = t[:, :4], t[:, 4:6], t[:, 6:], cuda(9, 4, 64, dtype=torch.float16), cuda(2, dtype=torch.int32)
     sg.sgemv_prompt_attention(q, k, v, start, out, 0.125)
-    a = calls[-1][1][0]._obj
+    a = sg.PromptQuery.from_buffer_copy(calls[-1][1][0])
     assert (a.q_token_stride, a.k_token_stride, a.v_head_stride, a.out_token_stride, a.n_req, a.n_tokens, a.heads, a.heads_q) == (512, 512, 64, 256, 1, 9, 2, 4)
     n = len(calls)
     for bad in (dict(k=cuda(9, 2, 32, dtype=torch.float16)), dict(v=cuda(8, 2, 64, dtype=torch.float16)), dict(v=cuda(9, 1, 64, dtype=torch.float16)),
