@@ -77,14 +77,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         prefetch_l2(w_scales, groups * 512);
         if (p.split > 1) mbar_arrive_expect_tx(&sent, (p.split - 1) * (item1 - item0) * 16);
     }
-    __syncwarp();
-    pdl_launch_dependents();
-    if (warp == 8) tc_alloc(&s_tmem, kFewCols);
-    tc_before_sync();
     __syncthreads();
-    tc_after_sync();
-    if (kEarly && p.split > 1) cluster_arrive();  // (barriers are there; waited for before anything is sent)
-    const uint32_t tmem = s_tmem, t_sa = tmem + 128, t_sb = tmem + 128 + 4 * kGroups;
+    if (kEarly && p.split > 1 && warp != 8) cluster_arrive();  // (barriers are there; waited for before anything is sent)
+    pdl_launch_dependents();
     pdl_wait();
 
     bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
@@ -122,6 +117,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
             cluster_wait();
         }
     } else if (warp == 8) {
+        // Tensor memory only once the kernels before this one have ended: who held some while waiting for them could keep it from one of their CTAs.
+        tc_alloc(&s_tmem, kFewCols);
+        __syncwarp();
+        if (kEarly && p.split > 1) cluster_arrive();
+        tc_before_sync();
+        named_bar_sync(2, 160);
+        tc_after_sync();
+        const uint32_t tmem = s_tmem, t_sa = tmem + 128, t_sb = tmem + 128 + 4 * kGroups;
         const uint32_t base = smem_addr(smem);
         const uint32_t idesc = tc_idesc_fp4<kBlock>(128, (cols + 7) / 8 * 8, 0);
         int i = 0;
@@ -162,6 +165,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         const int item_first = item0 + me, q = item_first & 31;  // (the same four rows for all of them)
         const float4 ws = *reinterpret_cast<const float4*>(p.w.row_scale + wt * 128 + 4 * q);
         if (me < cols) s_x_scale[me] = p.x.row_scale[xt * 128 + me];
+        __syncwarp();
+        named_bar_sync(2, 160);
+        tc_after_sync();
+        const uint32_t tmem = s_tmem;
         wait(&done, 0);
         __syncwarp();
         tc_after_sync();
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
     __syncwarp();
     tc_before_sync();
     __syncthreads();
-    if (warp == 8) tc_dealloc(tmem, kFewCols);
+    if (warp == 8) tc_dealloc(s_tmem, kFewCols);
 }
 
 }  // namespace sgemv

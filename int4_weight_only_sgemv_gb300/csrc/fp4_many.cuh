@@ -81,7 +81,7 @@ template <typename T, int kBlock, int kN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN>::kThreads, 1) fp4_many_kernel(const __grid_constant__ Fp4Maps x_maps, const __grid_constant__ Fp4Maps w_maps, const __grid_constant__ ProductParams p) {
     using S = ManyShape<kBlock, kN>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S::kRing], free_[S::kRing], sums_full, sums_free;
+    __shared__ __align__(8) uint64_t full[S::kRing], free_[S::kRing], sums_full, sums_free, other_ready;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_w_scale[kN];
     __shared__ float s_least[8], s_most[8];
@@ -90,18 +90,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN
     const int chunks = p.w.kp / 32, tiles = p.tiles_x * p.tiles_w;
     if (tid == 0) {
         for (int i = 0; i < S::kRing; ++i) mbar_init(&full[i], 1), mbar_init(&free_[i], 1);
-        mbar_init(&sums_full, 1), mbar_init(&sums_free, 8);
+        mbar_init(&sums_full, 1), mbar_init(&sums_free, 8), mbar_init(&other_ready, 1);
         mbar_fence_init();
     }
     pdl_launch_dependents();
     __syncthreads();
-    if (warp == 12) tc_alloc_pair(&s_tmem, 512);
-    tc_before_sync();
-    __syncwarp();
     cluster_arrive();
     cluster_wait();
-    tc_after_sync();
-    const uint32_t tmem = s_tmem;
     pdl_wait();
     bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -151,8 +146,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN
         if (warp == 0 && rank == 0)
             for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&full[i % S::kRing], (i / S::kRing) & 1);
     } else if (warp == 12) {
+        // Tensor memory only once the kernels before this one have ended: who held some while waiting for them could keep it from one of their CTAs.
+        tc_alloc_pair(&s_tmem, 512);
+        tc_before_sync();
+        named_bar_sync(2, 288);
+        if (rank == 1 && lane == 0) arrive_at(peer_addr(&other_ready, 0));
+        const uint32_t tmem = s_tmem;
         int g = 0, turn = 0;
         if (rank == 0) {
+            if (!mbar_wait_cluster(&other_ready, 0)) {
+                dead = true;
+                report(p.status, SGEMV_ERR_TIMEOUT);
+            }
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            tc_after_sync();
             const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0), t_sa = tmem + S::kScaleCols, t_sb = t_sa + 4 * S::kGroups;
             constexpr uint32_t idesc = tc_idesc_fp4<kBlock>(256, kN, 0);
             constexpr int kWCols = kN / 32;  // of scales, 64 or 128 columns of k
@@ -202,6 +209,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN
         for (int i = max(0, g - S::kRing); i < g; ++i) mbar_wait(&free_[i % S::kRing], (i / S::kRing) & 1);
     } else {
         const int me = tid - 128, row = 32 * (warp & 3) + lane, half = (warp - 4) >> 2;
+        named_bar_sync(2, 288);
+        tc_after_sync();
+        const uint32_t tmem = s_tmem;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16, told = peer_addr(&sums_free, 0);
         const bool vec = p.stride % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
         int turn = 0;
@@ -298,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN
     cluster_arrive();
     cluster_wait();
     tc_after_sync();
-    if (warp == 12) tc_dealloc_pair(tmem, 512);
+    if (warp == 12) tc_dealloc_pair(s_tmem, 512);
 }
 
 }  // namespace sgemv

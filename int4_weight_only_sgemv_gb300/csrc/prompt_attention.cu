@@ -116,6 +116,7 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
     p.ratio = q.heads_q / q.heads;
     p.out32 = is_aligned(q.out_dev, 32) && (q.n_tokens < 2 || q.out_token_stride % 16 == 0) && (q.heads_q < 2 || q.out_head_stride % 16 == 0);
     p.scale_log2 = q.scale * 1.44269504088896340736f;
+    p.unscale = p.scale_log2 == 0.0f ? 0.693147180559945309f : static_cast<float>(static_cast<double>(q.scale) / p.scale_log2);
     p.sub = std::min(p.ratio, 128);
     while (p.ratio % p.sub != 0) --p.sub;
     p.tokens = 128 / p.sub;

@@ -43,6 +43,7 @@ struct PromptParams {
     int groups;     // heads * ratio / sub: KV heads, each as often as it has groups of `sub` query heads
     int most;       // segments that requests in order can have
     float scale_log2;
+    float unscale;  // scale / scale_log2: ln 2, and what scale_log2 was rounded by
 };
 
 template <int D>
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
         mbar_fence_init();
         mbar_arrive(&turn[0]);
     }
-    if (warp == 8) tc_alloc(&s_tmem, S::kCols);
     pdl_launch_dependents();
     pdl_wait();
+    // Tensor memory only once the kernels before this one have ended: who held some while waiting for them could keep it from one of their CTAs.
+    if (warp == 8) tc_alloc(&s_tmem, S::kCols);
 
     // The list of segments. Thread x has requests [x * run, (x + 1) * run). Where that is one each, they are sorted by descending length, and
     // t_blocks, t_span have their blocks (two row tiles of tokens) and tokens; t_before is where what thread x adds to the list starts:
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
             const float l = lf.x + lf.y;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (live && p.q.lse_dev != nullptr)
-                p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+                p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * p.unscale : -INFINITY;
             T* const out = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
             wait(&o_full[x][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
             __syncwarp();
