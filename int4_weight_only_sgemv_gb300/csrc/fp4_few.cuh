@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         if (p.split > 1) mbar_arrive_expect_tx(&sent, (p.split - 1) * (item1 - item0) * 16);
     }
     __syncthreads();
-    if (kEarly && p.split > 1 && warp != 8) cluster_arrive();  // (barriers are there; waited for before anything is sent)
+    if (kEarly && p.split > 1 && warp != 8) cluster_arrive_relaxed();  // (barriers are there; waited for before anything is sent)
     pdl_launch_dependents();
     pdl_wait();
 
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         // Tensor memory only once the kernels before this one have ended: who held some while waiting for them could keep it from one of their CTAs.
         tc_alloc(&s_tmem, kFewCols);
         __syncwarp();
-        if (kEarly && p.split > 1) cluster_arrive();
+        if (kEarly && p.split > 1) cluster_arrive_relaxed();
         tc_before_sync();
         named_bar_sync(2, 160);
         tc_after_sync();

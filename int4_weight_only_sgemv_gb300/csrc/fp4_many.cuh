@@ -95,7 +95,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ManyShape<kBlock, kN
     }
     pdl_launch_dependents();
     __syncthreads();
-    cluster_arrive();
+    cluster_arrive_relaxed();
     cluster_wait();
     pdl_wait();
     bool dead = false;  // a wait gave up: nothing is waited for any more, and what comes out is reported as invalid

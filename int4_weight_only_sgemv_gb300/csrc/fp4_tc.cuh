@@ -51,6 +51,8 @@ __device__ __forceinline__ float row_scaled(float sum, float a, float b) {
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// Without waiting for this thread's memory operations (prefetches among them): for barriers, whose initialisation has a fence of its own.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {  // the same place in another CTA's shared memory
     uint32_t a;
