@@ -15,7 +15,7 @@ import torch
 
 from . import _check, _lib, _stream
 from . import kv as _kv
-from .kv import _DTYPE, _device, _flat, _ptr, _rows
+from .kv import _DTYPE, _device, _flat, _rows
 
 EXPORTED_PROMPT = ("sgemv_fp4_layout_query", "sgemv_fp4_quantize", "sgemv_fp4_read", "sgemv_fp4_product", "sgemv_prompt_attention")
 
@@ -43,6 +43,7 @@ class PromptQuery(ctypes.Structure):
         [(n, ctypes.c_void_p) for n in ("q_dev", "k_dev", "v_dev", "start_dev", "length_dev", "out_dev", "lse_dev")]
 
 
+_U8 = torch.uint8
 # PromptQuery's bytes: filling them in at once takes 0.6 us, a Structure field by field 2.
 _QUERY = struct.Struct("=8ifi8q7Q")
 assert _QUERY.size == ctypes.sizeof(PromptQuery)
@@ -89,11 +90,22 @@ def sgemv_fp4_layout_query(rows: int, k: int, block: int) -> Fp4Layout:
 
 def sgemv_fp4_quantize(layout: Fp4Layout, packed, x, status=None, stream=None) -> None:
     """The 4-bit matrix of x (fp16 or bf16 [rows, k], any row stride) into packed (uint8, layout.total_bytes)."""
-    dev = _packed(layout, packed, "packed")
-    row = _row_stride(x, layout.rows, layout.k, "x", dev)
+    # (the usual case asked in place, as in sgemv_kv_plan: a call here costs as much as the questions)
+    try:
+        dev, shape, stride = packed.get_device(), x.shape, x.stride()
+        usual = packed.dtype is _U8 and packed.numel() >= layout.total_bytes and packed.is_contiguous() and x.get_device() == dev and \
+            dev == _kv._current() and shape == (layout.rows, layout.k) and stride[1] == 1 and stride[0] >= shape[1]
+    except (AttributeError, IndexError):
+        usual = False
+    if usual:
+        row = stride[0]
+    else:
+        dev = _packed(layout, packed, "packed")
+        row = _row_stride(x, layout.rows, layout.k, "x", dev)
     if status is not None:
         _flat(status, torch.int32, None, "status", dev)
-    code = _lib.sgemv_fp4_quantize(ctypes.byref(layout), x.data_ptr(), _DTYPE.get(x.dtype, -1), row, packed.data_ptr(), _ptr(status),
+    code = _lib.sgemv_fp4_quantize(ctypes.byref(layout), x.data_ptr(), _DTYPE.get(x.dtype, -1), row, packed.data_ptr(),
+                                   None if status is None else status.data_ptr(),
                                    _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_fp4_quantize")
@@ -111,13 +123,23 @@ def sgemv_fp4_read(layout: Fp4Layout, packed, out, stream=None) -> None:
 
 def sgemv_fp4_product(w_layout: Fp4Layout, w, x_layout: Fp4Layout, x, y, status=None, stream=None) -> None:
     """y[t][n] = sum over k of x[t][k] w[n][k] of two 4-bit matrices; y: fp16 or bf16 [x rows, w rows], any row stride."""
-    dev = _packed(w_layout, w, "w")
-    _packed(x_layout, x, "x")
-    stride = _row_stride(y, x_layout.rows, w_layout.rows, "y", dev)
+    try:
+        dev, shape, stride = w.get_device(), y.shape, y.stride()
+        usual = w.dtype is _U8 and x.dtype is _U8 and w.numel() >= w_layout.total_bytes and x.numel() >= x_layout.total_bytes and \
+            w.is_contiguous() and x.is_contiguous() and x.get_device() == dev and y.get_device() == dev and dev == _kv._current() and \
+            shape == (x_layout.rows, w_layout.rows) and stride[1] == 1 and stride[0] >= shape[1]
+    except (AttributeError, IndexError):
+        usual = False
+    if usual:
+        row = stride[0]
+    else:
+        dev = _packed(w_layout, w, "w")
+        _packed(x_layout, x, "x")
+        row = _row_stride(y, x_layout.rows, w_layout.rows, "y", dev)
     if status is not None:
         _flat(status, torch.int32, None, "status", dev)
     code = _lib.sgemv_fp4_product(ctypes.byref(w_layout), w.data_ptr(), ctypes.byref(x_layout), x.data_ptr(), y.data_ptr(),
-                                  _DTYPE.get(y.dtype, -1), stride, _ptr(status),
+                                  _DTYPE.get(y.dtype, -1), row, None if status is None else status.data_ptr(),
                                   _kv._raw_stream(dev) if stream is None else _stream(stream))
     if code:
         _check(code, "sgemv_fp4_product")
