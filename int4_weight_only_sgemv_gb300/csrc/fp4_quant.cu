@@ -26,6 +26,7 @@ struct QuantParams {
     int64_t stride;
     int32_t* status;
     int wpr;         // warps a row
+    int lanes;       // lanes a row, where rows are short
     int align;       // of the rows' pieces: 32 bytes, 16, or 0 (an element)
 };
 
@@ -108,6 +109,45 @@ constexpr uint32_t kInfBits = 0x7C00u;
 template <>
 constexpr uint32_t kInfBits<__nv_bfloat16> = 0x7F80u;
 
+// Codes of 16 values whose block's largest magnitude is `most` (as 16 bits), and the block's scale. unit and down: the row's power of two and its inverse.
+template <typename T, int kBlock>
+__device__ __forceinline__ uint2 encode16(const uint32_t (&w)[8], uint32_t most, float unit, float down, uint32_t& scale) {
+    float s, inv;
+    if constexpr (kBlock == 32) {
+        scale = max(0, static_cast<int>(__float_as_uint(as_f32<T>(most)) >> 23) - 2);
+        inv = __uint_as_float((254u - scale) << 23), s = 0.0f;
+    } else {
+        const float m = as_f32<T>(most) * down, sixth = m * (1.0f / 6.0f);
+        scale = to_e4m3(fmaf(fmaf(-6.0f, sixth, m), 1.0f / 6.0f, sixth));
+        s = from_e4m3(scale) * unit;
+        inv = s > 0.0f ? reciprocal(s) : 0.0f;
+    }
+    uint32_t codes[2];
+    const uint64_t r = pair(inv, inv), d = pair(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = two_f32<T>(w[4 * i + j]);
+            const uint64_t v = pair(f.x, f.y);
+            uint64_t q = mul2(v, r);
+            if constexpr (kBlock == 16) q = fma2(fma2(q, d, v), r, q);
+            const float2 g = parts_of(q);
+            t[2 * j] = g.x, t[2 * j + 1] = g.y;
+        }
+        codes[i] = to_e2m1x8(t);
+    }
+    return make_uint2(codes[0], codes[1]);
+}
+// The row's power of two for its largest magnitude (1 for a row with none, or with an element that is no number), and its inverse. 2688 = 1.3125 * 2^11
+template <typename T>
+__device__ __forceinline__ void row_unit(uint32_t most, float& unit, float& down) {
+    const uint32_t b = __float_as_uint(as_f32<T>(most));
+    const int e = most >= kInfBits<T> || b == 0 ? 0 : max(-100, static_cast<int>(b >> 23) - 138 + ((b & 0x7FFFFFu) > 0x280000u));
+    unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
 template <typename T, int kBlock>
 __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParams p) {
     __shared__ uint32_t s_most[kWarpsQ];
@@ -173,9 +213,7 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
             most = s_most[slot];
         }
         bad = most >= kInfBits<T>;
-        const uint32_t b = __float_as_uint(as_f32<T>(most));  // 2688 = 1.3125 * 2^11
-        const int e = bad || b == 0 ? 0 : max(-100, static_cast<int>(b >> 23) - 138 + ((b & 0x7FFFFFu) > 0x280000u));
-        unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        row_unit<T>(most, unit, down);
     }
     uint32_t seen = 0;
     uint8_t* const row_codes = codes_at(p.m, live ? row : 0, 0) + 8 * (lane & 1);
@@ -183,42 +221,19 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
     const int chunk_bytes = p.m.tile * 16;
     // Piece c of the row, by the whole warp (lanes past the row's end have zeros).
     const auto quantize = [&](int c, const uint32_t (&w)[8], uint32_t most) {
-        uint32_t scale;
-        float s, inv;
         if constexpr (kBlock == 32) {
             most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
             seen = max(seen, most);
-            scale = max(0, static_cast<int>(__float_as_uint(as_f32<T>(most)) >> 23) - 2);
-            inv = __uint_as_float((254u - scale) << 23), s = 0.0f;
-        } else {
-            const float m = as_f32<T>(most) * down, sixth = m * (1.0f / 6.0f);
-            scale = to_e4m3(fmaf(fmaf(-6.0f, sixth, m), 1.0f / 6.0f, sixth));
-            s = from_e4m3(scale) * unit;
-            inv = s > 0.0f ? reciprocal(s) : 0.0f;
         }
-        uint32_t codes[2];
-        const uint64_t r = pair(inv, inv), d = pair(-s, -s);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float t[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = two_f32<T>(w[4 * i + j]);
-                const uint64_t v = pair(f.x, f.y);
-                uint64_t q = mul2(v, r);
-                if constexpr (kBlock == 16) q = fma2(fma2(q, d, v), r, q);
-                const float2 g = parts_of(q);
-                t[2 * j] = g.x, t[2 * j + 1] = g.y;
-            }
-            codes[i] = to_e2m1x8(t);
-        }
+        uint32_t scale;
+        const uint2 codes = encode16<T, kBlock>(w, most, unit, down, scale);
         // four scales a word: of 4 lanes, or of every second of 8
         constexpr int kApart = kBlock / 16;
         if (c >= pieces) scale = 0;
         scale |= __shfl_down_sync(0xFFFFFFFFu, scale, kApart) << 8;
         scale |= __shfl_down_sync(0xFFFFFFFFu, scale, 2 * kApart) << 16;
         if (c < pieces) {
-            *reinterpret_cast<uint2*>(row_codes + static_cast<int64_t>(c / 2) * chunk_bytes) = make_uint2(codes[0], codes[1]);
+            *reinterpret_cast<uint2*>(row_codes + static_cast<int64_t>(c / 2) * chunk_bytes) = codes;
             if (lane % (4 * kApart) == 0) *reinterpret_cast<uint32_t*>(row_scales + static_cast<int64_t>(c / (4 * kApart)) * 512) = scale;
         }
     };
@@ -337,6 +352,56 @@ __global__ void __launch_bounds__(32 * kWarpsQ) read_kernel(const QuantParams p)
     }
 }
 
+// Short rows: p.lanes lanes a row (8 or 16), a piece each, so that a warp has 4 or 2 rows (328153 rows of 122 values: 158 us with a warp a row, 29 so).
+// 16 values that start anywhere are read by the lane itself: neighbours' words are in the same lines, which L1 holds.
+template <typename T, int kBlock>
+__global__ void __launch_bounds__(32 * kWarpsQ) quantize_short_kernel(const QuantParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % p.lanes;
+    pdl_launch_dependents();
+    const int64_t slot = (static_cast<int64_t>(blockIdx.x) * kWarpsQ + warp) * (32 / p.lanes) + lane / p.lanes;
+    const bool live = slot < p.m.rows, mine = live && c < p.m.kp / 16;
+    const int row = live ? static_cast<int>(slot) : 0;
+    const T* const x = static_cast<const T*>(p.x) + row * p.stride;
+    pdl_wait();
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (mine) {
+        if (p.align > 0) {
+            load16(x, c, p.m.k, p.align, w);
+        } else {
+            const Line l(x, c, p.m.k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!l.odd && 2 * i + 1 < l.n) {
+                    w[i] = *reinterpret_cast<const uint32_t*>(l.at + 2 * i);
+                } else {
+                    if (2 * i < l.n) w[i] = l.at[2 * i];
+                    if (2 * i + 1 < l.n) w[i] |= static_cast<uint32_t>(l.at[2 * i + 1]) << 16;
+                }
+            }
+        }
+    }
+    uint32_t most = most16(w), row_most = most;
+    for (int d = p.lanes / 2; d > 0; d >>= 1) row_most = max(row_most, __shfl_xor_sync(0xFFFFFFFFu, row_most, d));
+    if constexpr (kBlock == 32) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+    float unit = 1.0f, down = 1.0f;
+    if constexpr (kBlock == 16) row_unit<T>(row_most, unit, down);
+    uint32_t scale;
+    const uint2 codes = encode16<T, kBlock>(w, most, unit, down, scale);
+    constexpr int kApart = kBlock / 16;
+    if (!mine) scale = 0;
+    scale |= __shfl_down_sync(0xFFFFFFFFu, scale, kApart) << 8;
+    scale |= __shfl_down_sync(0xFFFFFFFFu, scale, 2 * kApart) << 16;
+    if (mine) {
+        *reinterpret_cast<uint2*>(codes_at(p.m, row, c / 2) + 8 * (c & 1)) = codes;
+        if (c % (4 * kApart) == 0) *reinterpret_cast<uint32_t*>(scales_at(p.m, row, c / (4 * kApart))) = scale;
+    }
+    if (live && c == 0) {
+        const bool bad = row_most >= kInfBits<T>;
+        p.m.row_scale[row] = bad ? __int_as_float(0x7FC00000) : unit;
+        if (bad) report(p.status, SGEMV_ERR_NONFINITE);
+    }
+}
+
 // Rows in pieces of 16 values: how the pieces are aligned.
 int row_align(const void* p, int64_t stride, int rows, int k, int size) {
     if (is_aligned(p, 32) && k % 16 == 0 && (rows < 2 || stride * size % 32 == 0)) return 32;
@@ -360,6 +425,20 @@ int launch_rows(const sgemv_fp4_layout& l, QuantParams& p, void (*kern)(const Qu
     const int64_t per = kWarpsQ / p.wpr;
     const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>((used + per - 1) / per)), dim3(32 * kWarpsQ), 0,
                                      static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
+}
+
+// Rows that leave half of a warp's lanes, or more, without a piece; from the tiles of 128 rows on (below, either form is one wave of the GPU).
+bool short_rows(const sgemv_fp4_layout& l) { return l.kp <= 256 && l.tile == 128; }
+
+int launch_short(const sgemv_fp4_layout& l, QuantParams& p, void (*kern)(const QuantParams), void* stream) {
+    DeviceInfo di;
+    const int rc = device_info(&di);
+    if (rc != SGEMV_OK) return rc;
+    p.lanes = l.kp <= 128 ? 8 : 16;
+    const int per = kWarpsQ * 32 / p.lanes;
+    const cudaError_t e =
+        launch_pdl(kern, dim3(static_cast<unsigned>((l.rows + per - 1) / per)), dim3(32 * kWarpsQ), 0, static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }
 
@@ -413,6 +492,11 @@ extern "C" int sgemv_fp4_quantize(const sgemv_fp4_layout* layout, const void* x_
     p.x = x_dev, p.stride = st, p.status = status_dev;
     p.align = row_align(x_dev, st, layout->rows, layout->k, 2);
     const bool half = dtype == SGEMV_F16;
+    if (short_rows(*layout))
+        return launch_short(*layout, p,
+                            layout->block == 16 ? (half ? quantize_short_kernel<__half, 16> : quantize_short_kernel<__nv_bfloat16, 16>)
+                                                : (half ? quantize_short_kernel<__half, 32> : quantize_short_kernel<__nv_bfloat16, 32>),
+                            stream);
     return launch_rows(*layout, p,
                        layout->block == 16 ? (half ? quantize_kernel<__half, 16> : quantize_kernel<__nv_bfloat16, 16>)
                                            : (half ? quantize_kernel<__half, 32> : quantize_kernel<__nv_bfloat16, 32>),

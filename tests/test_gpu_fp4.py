@@ -84,6 +84,30 @@ def test_quantise_matches_oracle(env, rows, k, dtype, block):
 
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("rows,k,offset,stride", [(65, 1, 0, 1), (70, 16, 1, 17), (100, 60, 0, 60), (129, 64, 8, 72), (200, 65, 3, 70), (300, 122, 0, 130), (66, 128, 1, 129),
+                                                  (131, 129, 0, 129), (500, 250, 7, 251), (65, 256, 0, 256), (1000, 200, 0, 200)])
+def test_short_rows(env, rows, k, offset, stride, dtype, block):
+    """Several rows a warp, wherever they start; a row without numbers beside others."""
+    sg, torch = env
+    x = _x(torch, rows, k, dtype, rows + k)
+    wide = torch.full((rows * stride + offset + 8,), float("nan"), dtype=x.dtype, device="cuda")
+    y = wide.as_strided((rows, k), (stride, 1), offset)
+    y.copy_(x)
+    _check_bytes(env, y, block)
+    clean = _quantise(env, y, block)[1]
+    y[7, k - 1] = float("inf")
+    L, data, status = _quantise(env, y, block)
+    assert status == sg.SGEMV_ERR_NONFINITE
+    a, b = (torch.empty((rows, k), device="cuda") for _ in range(2))
+    sg.sgemv_fp4_read(L, clean, a)
+    sg.sgemv_fp4_read(L, data, b)
+    assert torch.isnan(b[7]).all()
+    b[7] = a[7]
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_quantise_edges(env, block, dtype):
     """Ties between codes and between scales, signed zeros, rows of zeros, the smallest and the largest numbers of the type."""
     sg, torch = env
