@@ -260,21 +260,14 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
     }
 }
 
-// The warp's 512 values from column 16 * base on, 16 a lane, as words next to one another.
+// The n values (512 at most) in buf, to where a row starts or 16 values further, by the warp: as words next to one another.
 template <typename T>
-__device__ __forceinline__ void store_line(T* row, int base, int k, int lane, const uint32_t (&w)[8 * sizeof(T) / 2], uint32_t* buf) {
-    constexpr int kWords = 8 * sizeof(T) / 2;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(buf + kWords * lane + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    __syncwarp();
-    const int n = min(512, k - 16 * base);
-    T* const at = row + 16ll * base;
+__device__ __forceinline__ void store_words(T* at, int n, int lane, const uint32_t* buf) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll 4
         for (int i = lane; i < n; i += 32) reinterpret_cast<uint32_t*>(at)[i] = buf[i];
     } else {
-        const bool odd = (reinterpret_cast<uintptr_t>(row) & 2) != 0;
+        const bool odd = (reinterpret_cast<uintptr_t>(at) & 2) != 0;
         unsigned short* const h = reinterpret_cast<unsigned short*>(at);
 #pragma unroll
         for (int i = 0; i < 9; ++i) {
@@ -286,9 +279,65 @@ __device__ __forceinline__ void store_line(T* row, int base, int k, int lane, co
                 *reinterpret_cast<uint32_t*>(h + first) = v;
             } else {
                 if (first >= 0) h[first] = static_cast<unsigned short>(v);
-                if (first + 1 < n) h[first + 1] = static_cast<unsigned short>(v >> 16);
+                if (first + 1 >= 0 && first + 1 < n) h[first + 1] = static_cast<unsigned short>(v >> 16);
             }
         }
+    }
+}
+// The warp's 512 values from column 16 * base on, 16 a lane.
+template <typename T>
+__device__ __forceinline__ void store_line(T* row, int base, int k, int lane, const uint32_t (&w)[8 * sizeof(T) / 2], uint32_t* buf) {
+    constexpr int kWords = 8 * sizeof(T) / 2;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(buf + kWords * lane + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    __syncwarp();
+    store_words(row + 16ll * base, min(512, k - 16 * base), lane, buf);
+}
+
+// The 16 values of 8 bytes of codes.
+template <int kBlock>
+__device__ __forceinline__ void decode16(const uint8_t* at, uint32_t scale, float unit, float (&f)[16]) {
+    const uint2 codes = *reinterpret_cast<const uint2*>(at);
+    const float s = (kBlock == 16 ? from_e4m3(scale) : from_e8m0(scale)) * unit;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t h[4];
+        from_e2m1x8(i ? codes.y : codes.x, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = two_f32<__half>(h[j]);
+            f[8 * i + 2 * j] = v.x * s, f[8 * i + 2 * j + 1] = v.y * s;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void to_words(const float (&f)[16], uint32_t (&w)[8 * sizeof(T) / 2]) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(8 * sizeof(T) / 2); ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+        else w[i] = pack_two<T>(f[2 * i], f[2 * i + 1]);
+    }
+}
+// The first n of a lane's 16 values, to an address of the alignment `align` (32 or 16 bytes).
+template <typename T>
+__device__ __forceinline__ void store16(T* to, int n, int align, const float (&f)[16], const uint32_t (&w)[8 * sizeof(T) / 2]) {
+    if (n >= 16) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(8 * sizeof(T) / 2); i += 8) {
+            if (align == 32) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(to) + i), "r"(w[i]), "r"(w[i + 1]),
+                             "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                             : "memory");
+            } else {
+                reinterpret_cast<uint4*>(to)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                reinterpret_cast<uint4*>(to)[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < n) to[j] = from_f32<T>(f[j]);
     }
 }
 
@@ -308,46 +357,17 @@ __global__ void __launch_bounds__(32 * kWarpsQ) read_kernel(const QuantParams p)
     for (int base = 32 * part; 16 * base < p.m.k; base += 32 * p.wpr) {
         const int c = base + lane;
         const int at = min(c, p.m.kp / 16 - 1);  // (a lane without a piece among others that have one: any)
-        const uint2 codes = *reinterpret_cast<const uint2*>(row_codes + static_cast<int64_t>(at / 2) * chunk_bytes + 8 * (at & 1));
-        const uint32_t sb = row_scales[static_cast<int64_t>(at * 16 / kBlock / 4) * 512 + at * 16 / kBlock % 4];
-        const float s = (kBlock == 16 ? from_e4m3(sb) : from_e8m0(sb)) * unit;
         float f[16];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t h[4];
-            from_e2m1x8(i ? codes.y : codes.x, h);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = two_f32<__half>(h[j]);
-                f[8 * i + 2 * j] = v.x * s, f[8 * i + 2 * j + 1] = v.y * s;
-            }
-        }
+        decode16<kBlock>(row_codes + static_cast<int64_t>(at / 2) * chunk_bytes + 8 * (at & 1),
+                         row_scales[static_cast<int64_t>(at * 16 / kBlock / 4) * 512 + at * 16 / kBlock % 4], unit, f);
         constexpr int kWords = 8 * sizeof(T) / 2;  // of 16 values
         uint32_t w[kWords];
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
-            else w[i] = pack_two<T>(f[2 * i], f[2 * i + 1]);
-        }
+        to_words<T>(f, w);
         T* const to = out + 16 * c;
         if (p.align == 0) {
             store_line(out, base, p.m.k, lane, w, s_line[warp]);
-        } else if (16 * c + 16 <= p.m.k) {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 8) {
-                if (p.align == 32) {
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint32_t*>(to) + i), "r"(w[i]), "r"(w[i + 1]),
-                                 "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
-                                 : "memory");
-                } else {
-                    reinterpret_cast<uint4*>(to)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                    reinterpret_cast<uint4*>(to)[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
-                }
-            }
         } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (16 * c + j < p.m.k) to[j] = from_f32<T>(f[j]);
+            store16(to, p.m.k - 16 * c, p.align, f, w);
         }
     }
 }
@@ -402,6 +422,34 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_short_kernel(const Quan
     }
 }
 
+// The same way back (328153 rows of 122 values: 95 us with a warp a row, 42 so).
+template <typename T, int kBlock>
+__global__ void __launch_bounds__(32 * kWarpsQ) read_short_kernel(const QuantParams p) {
+    constexpr int kWords = 8 * sizeof(T) / 2;
+    __shared__ __align__(16) uint32_t s_line[kWarpsQ][32 * kWords + 4];  // (the word behind a row, whose value is not used, may be behind the last)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % p.lanes;
+    pdl_launch_dependents();
+    const int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarpsQ + warp) * (32 / p.lanes);  // the warp's first row
+    const int64_t slot = base + lane / p.lanes;
+    pdl_wait();
+    uint32_t w[kWords] = {};
+    if (slot < p.m.rows && 16 * c < p.m.k) {
+        const int row = static_cast<int>(slot);
+        float f[16];
+        decode16<kBlock>(codes_at(p.m, row, c / 2) + 8 * (c & 1), scales_at(p.m, row, c * 16 / kBlock / 4)[c * 16 / kBlock % 4], p.m.row_scale[row], f);
+        to_words<T>(f, w);
+        if (p.align > 0) store16(const_cast<T*>(static_cast<const T*>(p.x)) + row * p.stride + 16 * c, p.m.k - 16 * c, p.align, f, w);
+    }
+    if (p.align > 0) return;
+    // rows that start anywhere: by the whole warp, a row after the other
+    uint32_t* const buf = s_line[warp];
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) *reinterpret_cast<uint4*>(buf + kWords * lane + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    __syncwarp();
+    for (int r = 0; r < 32 / p.lanes && base + r < p.m.rows; ++r)
+        store_words(const_cast<T*>(static_cast<const T*>(p.x)) + (base + r) * p.stride, p.m.k, lane, buf + r * p.lanes * kWords);
+}
+
 // Rows in pieces of 16 values: how the pieces are aligned.
 int row_align(const void* p, int64_t stride, int rows, int k, int size) {
     if (is_aligned(p, 32) && k % 16 == 0 && (rows < 2 || stride * size % 32 == 0)) return 32;
@@ -428,7 +476,8 @@ int launch_rows(const sgemv_fp4_layout& l, QuantParams& p, void (*kern)(const Qu
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }
 
-// Rows that leave half of a warp's lanes, or more, without a piece; from the tiles of 128 rows on (below, either form is one wave of the GPU).
+// Rows that leave half of a warp's lanes, or more, without a piece; from the tiles of 128 rows on (below, both
+// are one wave of the GPU: 2.0 to 2.6 us for 64 rows and for 65).
 bool short_rows(const sgemv_fp4_layout& l) { return l.kp <= 256 && l.tile == 128; }
 
 int launch_short(const sgemv_fp4_layout& l, QuantParams& p, void (*kern)(const QuantParams), void* stream) {
@@ -521,6 +570,12 @@ extern "C" int sgemv_fp4_read(const sgemv_fp4_layout* layout, const void* packed
     p.x = out_dev, p.stride = st, p.status = nullptr;
     p.align = row_align(out_dev, st, layout->rows, layout->k, static_cast<int>(size));
     const bool b16 = layout->block == 16;
+    if (short_rows(*layout))
+        return launch_short(*layout, p,
+                            dtype == SGEMV_F16    ? (b16 ? read_short_kernel<__half, 16> : read_short_kernel<__half, 32>)
+                            : dtype == SGEMV_BF16 ? (b16 ? read_short_kernel<__nv_bfloat16, 16> : read_short_kernel<__nv_bfloat16, 32>)
+                                                  : (b16 ? read_short_kernel<float, 16> : read_short_kernel<float, 32>),
+                            stream);
     return launch_rows(*layout, p,
                        dtype == SGEMV_F16    ? (b16 ? read_kernel<__half, 16> : read_kernel<__half, 32>)
                        : dtype == SGEMV_BF16 ? (b16 ? read_kernel<__nv_bfloat16, 16> : read_kernel<__nv_bfloat16, 32>)

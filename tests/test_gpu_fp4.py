@@ -107,6 +107,26 @@ def test_short_rows(env, rows, k, offset, stride, dtype, block):
 
 
 @pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("rows,k,offset,stride", [(65, 1, 0, 1), (70, 16, 1, 17), (100, 60, 0, 60), (129, 64, 8, 72), (200, 65, 3, 70), (300, 122, 0, 130), (66, 128, 1, 129),
+                                                  (131, 129, 0, 129), (500, 250, 7, 251), (65, 256, 0, 256), (1000, 200, 0, 200)])
+def test_reading_short_rows(env, rows, k, offset, stride, block):
+    """Each type is the fp32 form, rounded once; what lies between the rows stays."""
+    sg, torch = env
+    x = _x(torch, rows, k, "bfloat16", rows + 2 * k)
+    x[5] = float("nan")
+    L, data, status = _quantise(env, x, block)
+    assert status == sg.SGEMV_ERR_NONFINITE
+    want = torch.tensor(op.values(op.layout(rows, k, block), data.cpu().numpy()), device="cuda").float()
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        wide = torch.full((rows * stride + offset + 8,), 77.0, dtype=dtype, device="cuda")
+        out = wide.as_strided((rows, k), (stride, 1), offset)
+        sg.sgemv_fp4_read(L, data, out)
+        assert torch.equal(out.nan_to_num(nan=-1e4), want.to(dtype).nan_to_num(nan=-1e4))
+        out.fill_(77.0)
+        assert (wide == 77.0).all()
+
+
+@pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_quantise_edges(env, block, dtype):
     """Ties between codes and between scales, signed zeros, rows of zeros, the smallest and the largest numbers of the type."""
