@@ -103,7 +103,9 @@ typedef struct {
  * softmax's sum and out's sums are held in 32 bits; the softmax's weights are rounded to dtype (11 or 8 bits) before they meet V, as the
  * matrix instruction takes both in one type. lse is the natural logarithm of the softmax's sum.
  * Keys and values that a token does not see do not enter its outputs, whatever they hold. A NaN or infinite element of v that it sees
- * makes that dim of its output NaN or infinite; one of q or k the whole output NaN.
+ * makes that dim of its output NaN or infinite. Scores follow the softmax: with one that is NaN or infinity (NaN elements of q or k,
+ * infinite ones, products that leave binary32) a row's output and lse are NaN; one of minus infinity beside finite ones has weight 0;
+ * where a token sees no other than such, output and lse are NaN.
  * Rows that belong to no request (past start[n_req], or past a request's length) are neither used nor written. Requests of no tokens are
  * allowed. out may be q itself (the same address and strides); out's rows do not overlap one another.
  * The same inputs give the same bits.

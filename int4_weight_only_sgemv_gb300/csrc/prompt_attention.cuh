@@ -429,11 +429,12 @@ __global__ void __launch_bounds__(PromptShape<D>::kThreads, 1)
                 tc_before_sync();
                 mbar_arrive(&p_full[x][tiles & 1]);
             }
+            // Every row sees itself: one without a score above -inf has no softmax (its scores are -inf or NaN) and is NaN, as one with a score of inf or NaN is.
             const float2 lf = parts_of(l2);
-            const float l = lf.x + lf.y;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float l = seen ? lf.x + lf.y : __int_as_float(0x7FC00000);
+            const float inv = 1.0f / l;
             if (live && p.q.lse_dev != nullptr)
-                p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = seen ? (ref + log2f(l)) * p.unscale : -INFINITY;
+                p.q.lse_dev[static_cast<int64_t>(sg.first + i) * p.q.heads_q + a] = (ref + log2f(l)) * p.unscale;
             T* const out = static_cast<T*>(p.q.out_dev) + (sg.first + i) * p.q.out_token_stride + a * p.q.out_head_stride;
             wait(&o_full[x][(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
             __syncwarp();
