@@ -15,8 +15,9 @@
  *             -127; b = 0 where m = 0). The row scale is 1.
  *   block 16  The row scale is 2^e, e the least integer of at least -100 with M <= 2688 * 2^e for the row's largest magnitude M (e = 0
  *             where M = 0). The scale is the e4m3 number nearest to m / 2^e / 6 (ties to even).
- * A code is the nearest to x / (scale * row scale), ties to the even code, magnitudes past 6 to 6; 0 where the scale is 0. A row with an
- * infinite or NaN element has row scale NaN, codes and scales 0: every value that it stands for, and every product with it, is NaN.
+ * A code is the nearest to x / (scale * row scale), ties to the even code, magnitudes past 6 to 6; of magnitude 0 where the scale is 0.
+ * Codes of magnitude 0 may have either sign. A row with an infinite or NaN element has row scale NaN (0x7FC00000), codes and scales 0:
+ * every value that it stands for, and every product with it, is NaN.
  * (The row's power of two stands where other formats of this kind have one scale a tensor: no pass over the tensor comes first, a token
  * does not depend on the others of its call, and as a power of two it rounds nothing.)
  * Bytes, with kp = k up to a multiple of 64, T = 128 rows a tile (a matrix of up to 64 rows: the next power of two, 8 at least):

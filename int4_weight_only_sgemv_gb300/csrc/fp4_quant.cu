@@ -254,6 +254,13 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_kernel(const QuantParam
         }
         bad = seen >= kInfBits<T>;
     }
+    if (bad) {  // zeros over what this lane wrote (a block of 32 is written before its row is known to hold no numbers)
+#pragma unroll 1
+        for (int c = first; c < pieces; c += step) {
+            *reinterpret_cast<uint2*>(row_codes + static_cast<int64_t>(c / 2) * chunk_bytes) = make_uint2(0, 0);
+            if (lane % (kBlock / 4) == 0) *reinterpret_cast<uint32_t*>(row_scales + static_cast<int64_t>(c / (kBlock / 4)) * 512) = 0;
+        }
+    }
     if (live && part == 0 && lane == 0) {
         p.m.row_scale[row] = bad ? __int_as_float(0x7FC00000) : unit;
         if (bad) report(p.status, SGEMV_ERR_NONFINITE);
@@ -406,9 +413,11 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_short_kernel(const Quan
     float unit = 1.0f, down = 1.0f;
     if constexpr (kBlock == 16) row_unit<T>(row_most, unit, down);
     uint32_t scale;
-    const uint2 codes = encode16<T, kBlock>(w, most, unit, down, scale);
+    uint2 codes = encode16<T, kBlock>(w, most, unit, down, scale);
     constexpr int kApart = kBlock / 16;
-    if (!mine) scale = 0;
+    const bool bad = row_most >= kInfBits<T>;
+    if (bad) codes = make_uint2(0, 0);
+    if (bad || !mine) scale = 0;
     scale |= __shfl_down_sync(0xFFFFFFFFu, scale, kApart) << 8;
     scale |= __shfl_down_sync(0xFFFFFFFFu, scale, 2 * kApart) << 16;
     if (mine) {
@@ -416,7 +425,6 @@ __global__ void __launch_bounds__(32 * kWarpsQ) quantize_short_kernel(const Quan
         if (c % (4 * kApart) == 0) *reinterpret_cast<uint32_t*>(scales_at(p.m, row, c / (4 * kApart))) = scale;
     }
     if (live && c == 0) {
-        const bool bad = row_most >= kInfBits<T>;
         p.m.row_scale[row] = bad ? __int_as_float(0x7FC00000) : unit;
         if (bad) report(p.status, SGEMV_ERR_NONFINITE);
     }
