@@ -11,12 +11,16 @@
 // warps 4-7 take the sums out, send, join and write; warp 8 issues the products.
 #pragma once
 
+#include <algorithm>
+
 #include "fp4_tc.cuh"
 
 namespace sgemv {
 
 constexpr int kFewThreads = 288;
-constexpr int kFewSmem = 108 * 1024;   // of the ring: two CTAs an SM
+// Of the ring and what is sent: two CTAs an SM. (With 108 KB, 17 to 32 tokens in blocks of 16 had one place where a tile is split by 5 or more, and copies waited
+// for products: 20 x 4096 x 11008 10.5 us, 9.1 with two; 20 x 5120 x 8192 15.2, 13.0.)
+constexpr int kFewSmem = 112 * 1024;
 constexpr int kFewLeast = 80 * 1024;   // and never three, whose tensor memory (256 columns each) would not fit
 constexpr int kFewMost = 216 * 1024;
 constexpr int kFewCols = 256;
@@ -33,6 +37,24 @@ __host__ __device__ constexpr int few_stage_bytes(int block, int x_tile) {
 // Float4s of sums that a CTA of a cluster joins, and bytes of what the others send it.
 __host__ __device__ inline int few_share(int x_tile, int split) { return (x_tile * 32 + split - 1) / split; }
 __host__ __device__ inline int few_sent(int x_tile, int split) { return (split - 1) * few_share(x_tile, split) * 16; }
+
+// Host: CTAs a tile, places of the ring, and bytes of shared memory, for a call of `tiles` tiles of `stages` stages.
+struct FewPlan {
+    int split, ring, smem;
+};
+inline FewPlan few_plan(int block, int x_tile, int64_t tiles, int stages, int sms) {
+    FewPlan f;
+    // As many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
+    // tiles of 128 tokens are sent leaves one place an SM, and not every SM is in a cluster (512 x 512 x 8192: 6 CTAs 10.5 us, 8 16.9).
+    f.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * sms / tiles, stages / 2})));
+    if (x_tile == 128 && f.split > 4) f.split = std::min(f.split, std::max(4, static_cast<int>(2 * sms / 3 / tiles)));
+    const int stage = few_stage_bytes(block, x_tile), sent = f.split > 1 ? few_sent(x_tile, f.split) : 0;
+    const bool early = few_stage_k(x_tile) == 512;
+    f.ring = std::min({kFewMaxRing, (kFewSmem - (early ? sent : 0)) / stage, (stages + f.split - 1) / f.split});
+    // (the sums of a tile take the ring's place, and in wide tiles what is sent too)
+    f.smem = std::max(early ? std::max(f.ring * stage, x_tile * 512) + sent : std::max(f.ring * stage, x_tile * 512 + sent), kFewLeast);
+    return f;
+}
 
 // 16 bytes into a peer's shared memory, counted on its barrier.
 __device__ __forceinline__ void send16(uint32_t to, float4 v, uint32_t bar) {

@@ -135,16 +135,9 @@ extern "C" int sgemv_fp4_product(const sgemv_fp4_layout* w_layout, const void* w
                                             : (half ? launch_many<__half, 32>(p, wide, sms, s) : launch_many<__nv_bfloat16, 32>(p, wide, sms, s));
         return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
     }
-    // CTAs a tile: as many as fill two places an SM, each with two stages at least (4096 x 4096, one token: 4 CTAs 5.2 us, 8 5.7). From 5 on, what
-    // tiles of 128 tokens are sent leaves one place an SM, and not every SM is in a cluster (512 x 512 x 8192: 6 CTAs 10.5 us, 8 16.9).
-    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, 2 * di.sm_count / tiles, p.k_stages / 2})));
-    if (x.tile == 128 && p.split > 4) p.split = std::min(p.split, std::max(4, static_cast<int>(2 * di.sm_count / 3 / tiles)));
-    const int stage = few_stage_bytes(w.block, x.tile), sent = p.split > 1 ? few_sent(x.tile, p.split) : 0;
-    const bool early = few_stage_k(x.tile) == 512;
-    p.ring = std::min({kFewMaxRing, (kFewSmem - (early ? sent : 0)) / stage, (p.k_stages + p.split - 1) / p.split});
-    // (the sums of a tile take the ring's place, and in wide tiles what is sent too)
-    const int smem = std::max(early ? std::max(p.ring * stage, x.tile * 512) + sent : std::max(p.ring * stage, x.tile * 512 + sent), kFewLeast);
-    const cudaError_t e = w.block == 16 ? (half ? launch_few<__half, 16>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 16>(p, tiles, smem, s))
-                                        : (half ? launch_few<__half, 32>(p, tiles, smem, s) : launch_few<__nv_bfloat16, 32>(p, tiles, smem, s));
+    const FewPlan plan = few_plan(w.block, x.tile, tiles, p.k_stages, di.sm_count);
+    p.split = plan.split, p.ring = plan.ring;
+    const cudaError_t e = w.block == 16 ? (half ? launch_few<__half, 16>(p, tiles, plan.smem, s) : launch_few<__nv_bfloat16, 16>(p, tiles, plan.smem, s))
+                                        : (half ? launch_few<__half, 32>(p, tiles, plan.smem, s) : launch_few<__nv_bfloat16, 32>(p, tiles, plan.smem, s));
     return e == cudaSuccess ? SGEMV_OK : SGEMV_ERR_CUDA;
 }
