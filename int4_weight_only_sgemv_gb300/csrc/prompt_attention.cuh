@@ -67,17 +67,18 @@ struct PromptShape {
 };
 
 // Weights 2^(t - m): the largest is 2^kTop when the reference m is set, which happens anew when a tile's sum passes kBig (or, where the largest score
-// is looked for, when a weight would pass 2^kFar: 128 of those are that sum). fp16's weights end at 2^16 and lose bits below 2^-14, nothing at all
-// being left below 2^(-25 - kTop) of the largest: kTop is low enough that a window's first few keys rarely set a reference that the next tile
-// moves, and high enough for 2^16 keys below that end to add up to no more than a rounding. bf16 has 8 bits of exponent, and there sums of weights
-// stay below 1, so that sums of V do not leave binary32 where V does not; V's elements below 2^-110 lose bits.
+// is looked for, when a weight would pass 2^kFar: 128 of those are that sum). fp16's weights end at 2^16 and have steps of 2^-24 below 2^-14: a row's
+// largest being 2^kTop or more, each is held to 2^(-25 - kTop) of it, and n keys down there add up to n times that (for 2^16 keys as much as the rounding
+// of the others). kTop is low enough that a window's first few keys rarely set a reference that the next tile moves. bf16 has 8 bits of exponent: sums of
+// weights stay below 2^-23 a tile and, over the 2^23 tiles that a request can have, below 1, so that sums of V do not leave binary32 where V does not (with
+// 2^-16 and 1 a tile, seven tiles of 2^127 did); V's elements below 2^-87 lose bits.
 template <typename T>
 struct PromptWeights {
     static constexpr float kTop = 2.0f, kBig = 32768.0f, kFar = 8.0f;
 };
 template <>
 struct PromptWeights<__nv_bfloat16> {
-    static constexpr float kTop = -16.0f, kBig = 1.0f, kFar = -7.0f;
+    static constexpr float kTop = -39.0f, kBig = 1.1920928955078125e-7f, kFar = -30.0f;
 };
 constexpr float kPromptRound = 67108864.0f;  // past this, scores are rounded before the reference comes off
 
