@@ -102,7 +102,9 @@ typedef struct {
 /*
  * sgemv_prompt_attention -- out = softmax(scale * q K^T) V of each request's tokens over its own keys and values: scores, the
  * softmax's sum and out's sums are held in 32 bits; the softmax's weights are rounded to dtype (11 or 8 bits) before they meet V, as the
- * matrix instruction takes both in one type. (bf16 elements of v below 2^-87 lose bits.) lse is the natural logarithm of the softmax's sum.
+ * matrix instruction takes both in one type. In fp16 a weight is also held to no less than 2^-27 of its row's largest (below that it is
+ * 0), which n keys down there add up to n * 2^-27 * max |v| in out; in bf16, elements of v below 2^-87 lose bits. lse is the natural
+ * logarithm of the softmax's sum, of unrounded weights.
  * Keys and values that a token does not see do not enter its outputs, whatever they hold. A NaN or infinite element of v that it sees
  * makes that dim of its output NaN or infinite. Scores follow the softmax: with one that is NaN or infinity (NaN elements of q or k,
  * infinite ones, products that leave binary32) a row's output and lse are NaN; one of minus infinity beside finite ones has weight 0;

@@ -1,8 +1,8 @@
-"""GPU parity of prompt attention at the ends of its weights' range, against binary64: values near the end of bf16 under many tiles of keys, and
-small ones.
+"""GPU parity of prompt attention at the ends of its weights' range, against binary64: values near the end of bf16 under many tiles of keys, small ones,
+and fp16 weights far below a row's largest.
 
 Bound per output as in test_gpu_prompt.py: half a step of sum p |v| for the weights, 2^-14 for exp and the sums, 2 dim 2^-24 of a score's sum of
-magnitudes, half a step for the output."""
+magnitudes, half a step for the output; in fp16 each key's weight is held to 2^-27 of the row's largest at best, which n keys make n 2^-27 max |v|."""
 
 import numpy as np
 import pytest
@@ -24,8 +24,8 @@ def env():
     return sg, torch
 
 
-def _check(env, q, k, v, dtype, scale, rows, causal=True):
-    """One request; only some rows are compared."""
+def _check(env, q, k, v, dtype, scale, rows, causal=True, small=0.0):
+    """One request; only some rows are compared. small: what the weights' lowest steps may add to an output."""
     sg, torch = env
     q, k, v = (t.to(getattr(torch, dtype)) for t in (q, k, v))
     n, heads_q, dim = q.shape
@@ -45,7 +45,7 @@ def _check(env, q, k, v, dtype, scale, rows, causal=True):
             ref, weight = p @ vv, p @ vv.abs()
             size = float((kk.abs() @ q[i, a].double().abs()).max()) * abs(scale)
             noise = 2.0 ** -14 + 2 * dim * 2.0 ** -24 * size
-            tol = HALF_STEP[dtype] * ref.abs() + weight * (HALF_STEP[dtype] + noise)
+            tol = HALF_STEP[dtype] * ref.abs() + weight * (HALF_STEP[dtype] + noise) + small
             err = (out[i, a].double() - ref).abs()
             assert (err <= tol).all(), (i, a, float((err / tol).max()), out[i, a, :4], ref[:4])
             total = float(torch.logsumexp(s, 0))
@@ -71,3 +71,16 @@ def test_values_of_any_size(env, power):
     sg, torch = env
     t = torch.randn((700, 4, 64), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
     _check(env, t[:, :2], t[:, 2:3], t[:, 3:] * 2.0 ** power, "bfloat16", 0.3, (0, 1, 100, 128, 300, 699))
+
+
+@pytest.mark.parametrize("bits", [15, 20, 24, 26])
+def test_fp16_weights_far_below_the_largest(env, bits):
+    """A first key that most of the weight goes to, and 30000 others around 2^-bits of it."""
+    sg, torch = env
+    n, dim, rng = 30000, 64, np.random.default_rng(bits)
+    q, k = torch.zeros((n, 1, dim), device="cuda"), torch.zeros((n, 1, dim), device="cuda")
+    q[:, 0, 0] = 1.0
+    k[0, 0, 0] = bits * 0.6931
+    k[1:, 0, 0] = torch.tensor(rng.uniform(-0.7, 0.7, n - 1), device="cuda").float()
+    v = torch.tensor(rng.standard_normal((n, 1, dim)) + 1.0, device="cuda").float()
+    _check(env, q, k, v, "float16", 1.0, (0, 127, 128, 1000, 29999), small=n * 2.0 ** -27 * float(v.abs().max()))
