@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         if (p.split > 1) {
             if (!kEarly) cluster_arrive();
             cluster_wait();
+            cluster_arrive_relaxed();
         }
     } else if (warp == 8) {
         // Tensor memory only once the kernels before this one have ended: who held some while waiting for them could keep it from one of their CTAs
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         if (p.split > 1) {
             if (!kEarly) cluster_arrive();
             cluster_wait();
+            cluster_arrive_relaxed();
         }
     } else {
         const int me = tid - 128;  // of 128
@@ -218,6 +220,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
                 const uint32_t place = peer_addr(got + share * (rank < to ? rank : rank - 1), to), bar = peer_addr(&sent, to);
                 for (int item = from0 + me; item < from1; item += 128) send16(place + (item - from0) * 16, sums[item], bar);
             }
+            __syncwarp();
+            cluster_arrive_relaxed();  // (this thread sends nothing any more)
             wait(&sent, 0);
         }
         // four weight rows of a token a thread
@@ -245,6 +249,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp4_few_kernel(const ProductPa
         }
     }
     __syncwarp();
+    if (p.split > 1) {
+        // Who gave up waiting for sums does not leave while they may still be sent: not before all have issued theirs, and these have landed. (0 to 0.2 us a
+        // call, as far as this cluster's CTAs are apart.)
+        cluster_wait();
+        if (dead && warp >= 4 && warp < 8) mbar_wait(&sent, 0);
+        __syncwarp();
+    }
     tc_before_sync();
     __syncthreads();
     if (warp == 8) tc_dealloc(s_tmem, kFewCols);

@@ -61,3 +61,10 @@ def test_cases_that_are_split(plan):
     calls = [(16, *c) for c in few.SPLIT]
     for call, (stages, split, ring, *_) in zip(calls, plan(calls), strict=True):
         assert split > 4 and stages // split > ring == 2, (call, stages, split, ring)
+
+
+def test_clusters_of_every_size(plan):
+    """The GPU tests' calls go to clusters of the sizes that they are named by."""
+    import test_gpu_fp4_few as few
+    for split, calls in few.CLUSTERS.items():
+        assert [r[1] for r in plan([(16, *c) for c in calls])] == [split] * len(calls), split
