@@ -126,6 +126,23 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _allocate(stream, make):
+    """make()'s tensor, or dict of them, for a call on `stream`. Where that is not the current one they are allocated there, since on the current
+    one the allocator may hand out memory that work of it still reads, which the call would write at once; and they are kept until work on the
+    current one that has them is done, as if they had been allocated on both."""
+    if stream is None:
+        return make()
+    import torch
+    current = torch.cuda.current_stream()
+    if _stream(stream) == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))):
+        got = make()
+    for t in got.values() if isinstance(got, dict) else (got,):
+        t.record_stream(current)
+    return got
+
+
 # ---------------------------------------------------------------------------------------------- C ABI
 
 def sgemv_abi_version() -> int:
@@ -236,7 +253,7 @@ def pack(w, fmt: int, group: int, status=None, stream=None):
     """Allocate a packed buffer (torch) and pack fp16 w[n][k] into it. Returns (layout, packed)."""
     import torch
     layout = sgemv_layout_query(fmt, w.shape[0], w.shape[1], group)
-    packed = torch.empty(layout.total_bytes, dtype=torch.uint8, device=w.device)
+    packed = _allocate(stream, lambda: torch.empty(layout.total_bytes, dtype=torch.uint8, device=w.device))
     sgemv_pack(layout, w, packed, status, stream)
     return layout, packed
 
@@ -245,7 +262,7 @@ def gemv(layout: Layout, packed, x, out=None, status=None, stream=None):
     """y = Ŵ x for any format (x: fp16 [batch, k]); allocates y unless `out` is given."""
     import torch
     if out is None:
-        out = torch.empty((x.shape[0], layout.n), dtype=torch.float16, device=x.device)
+        out = _allocate(stream, lambda: torch.empty((x.shape[0], layout.n), dtype=torch.float16, device=x.device))
     fn = sgemv_run_dense if layout.format == SGEMV_FMT_DENSE else sgemv_run
     fn(layout, packed, x, out, status, stream)
     return out

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import _check, _lib, _stream
+from . import _allocate, _check, _lib, _stream
 
 SGEMV_F16 = 0
 SGEMV_BF16 = 1
@@ -307,7 +307,7 @@ def kv_workspace(device="cuda"):
 def kv_attention(layout: KvLayout, cache, q, q_start, length, table, max_q: int, scale: float, workspace, window: int = 0,
                  tree=None, status=None, stream=None, lse=None):
     """sgemv_kv_attention into a new contiguous tensor, which it returns; lse: fp32 [tokens, heads_q] to write, or None."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = _allocate(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     sgemv_kv_attention(layout, cache, q, q_start, length, table, out, max_q, scale, workspace, lse, window, tree, status,
                        stream)
     return out
@@ -318,14 +318,19 @@ def logprobs(logits, tokens=None, top: int = 0, full: bool = False, status=None,
     "logp"}."""
     rows, vocab = logits.shape
     f = dict(dtype=torch.float32, device=logits.device)
-    got = {"lse": torch.empty(rows, **f), "entropy": torch.empty(rows, **f)}
-    if tokens is not None:
-        got["tok_logp"] = torch.empty(tokens.shape, **f)
-    if top:
-        got["top_tok"] = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
-        got["top_logp"] = torch.empty((rows, top), **f)
-    if full:
-        got["logp"] = torch.empty((rows, vocab), **f)
+
+    def make():
+        got = {"lse": torch.empty(rows, **f), "entropy": torch.empty(rows, **f)}
+        if tokens is not None:
+            got["tok_logp"] = torch.empty(tokens.shape, **f)
+        if top:
+            got["top_tok"] = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
+            got["top_logp"] = torch.empty((rows, top), **f)
+        if full:
+            got["logp"] = torch.empty((rows, vocab), **f)
+        return got
+
+    got = _allocate(stream, make)
     sgemv_logprobs(logits, tuple(got.get(n) for n in ("tok_logp", "lse", "entropy", "top_tok", "top_logp", "logp")),
                    tokens, status, stream)
     return got

@@ -13,7 +13,7 @@ import struct
 
 import torch
 
-from . import _check, _lib, _stream
+from . import _allocate, _check, _lib, _stream
 from . import kv as _kv
 from .kv import _DTYPE, _device, _flat, _rows
 
@@ -202,20 +202,20 @@ def sgemv_prompt_attention(q, k, v, start, out, scale: float, length=None, lse=N
 def fp4_quantize(x, block: int = 16, status=None, stream=None):
     """(layout, bytes) of the 4-bit matrix of x (fp16 or bf16 [rows, k])."""
     layout = sgemv_fp4_layout_query(x.shape[0], x.shape[1], block)
-    packed = torch.empty(layout.total_bytes, dtype=torch.uint8, device=x.device)
+    packed = _allocate(stream, lambda: torch.empty(layout.total_bytes, dtype=torch.uint8, device=x.device))
     sgemv_fp4_quantize(layout, packed, x, status, stream)
     return layout, packed
 
 
 def fp4_product(w_layout: Fp4Layout, w, x_layout: Fp4Layout, x, dtype=torch.bfloat16, status=None, stream=None):
     """sgemv_fp4_product into a new contiguous tensor [x rows, w rows] of dtype, which it returns."""
-    y = torch.empty((x_layout.rows, w_layout.rows), dtype=dtype, device=w.device)
+    y = _allocate(stream, lambda: torch.empty((x_layout.rows, w_layout.rows), dtype=dtype, device=w.device))
     sgemv_fp4_product(w_layout, w, x_layout, x, y, status, stream)
     return y
 
 
 def prompt_attention(q, k, v, start, scale: float, length=None, lse=None, causal: bool = True, window: int = 0, status=None, stream=None):
     """sgemv_prompt_attention into a new contiguous tensor, which it returns (rows of no request hold anything)."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = _allocate(stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
     sgemv_prompt_attention(q, k, v, start, out, scale, length, lse, causal, window, status, stream)
     return out
