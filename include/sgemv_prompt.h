@@ -86,7 +86,7 @@ typedef struct {
     int32_t n_req, n_tokens;
     int32_t causal;             /* 1: a token sees those up to itself; 0: all of its request */
     int32_t window;             /* 0, or (causal only) each token sees only the last `window` tokens, itself among them */
-    float scale;                /* factor of q . k */
+    float scale;                /* factor of q . k; |scale| up to 2^127 */
     int32_t reserved;
     int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride; /* elements, positive multiples of 8 (below 2^38); that of */
     int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride; /* an axis of length 1 is not used */

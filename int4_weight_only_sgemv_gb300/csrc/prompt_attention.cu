@@ -1,6 +1,7 @@
 // Causal attention over packed prompts: the entry point (argument checks, tensor maps, launch).
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "prompt_attention.cuh"
@@ -9,6 +10,8 @@
 namespace sgemv {
 
 namespace {
+
+constexpr float kLog2E = 1.44269504088896340736f;
 
 // Tiles of `tokens` tokens of `heads` neighbouring heads, 64 dims of a row at a time, swizzled for the tensor cores. (A stride of an axis of
 // length 1 is not used.)
@@ -53,7 +56,7 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
     if (query == nullptr) return SGEMV_ERR_ARG;
     const sgemv_prompt_query& q = *query;
     if ((q.dtype != SGEMV_F16 && q.dtype != SGEMV_BF16) || q.n_req < 0 || q.n_tokens < 0 || q.window < 0 || (q.causal != 0 && q.causal != 1) ||
-        (q.window > 0 && q.causal == 0) || !(q.scale == q.scale))
+        (q.window > 0 && q.causal == 0) || !(std::fabs(q.scale * kLog2E) < INFINITY))
         return SGEMV_ERR_ARG;
     if (q.dim != 64 && q.dim != 128) return SGEMV_ERR_SHAPE;
     if (q.heads < 1 || q.heads_q < q.heads || q.heads_q % q.heads != 0 || q.heads_q > 16384) return SGEMV_ERR_SHAPE;
@@ -115,7 +118,7 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
     p.status = status_dev;
     p.ratio = q.heads_q / q.heads;
     p.out32 = is_aligned(q.out_dev, 32) && (q.n_tokens < 2 || q.out_token_stride % 16 == 0) && (q.heads_q < 2 || q.out_head_stride % 16 == 0);
-    p.scale_log2 = q.scale * 1.44269504088896340736f;
+    p.scale_log2 = q.scale * kLog2E;
     p.unscale = p.scale_log2 == 0.0f ? 0.693147180559945309f : static_cast<float>(static_cast<double>(q.scale) / p.scale_log2);
     p.sub = std::min(p.ratio, 128);
     while (p.ratio % p.sub != 0) --p.sub;

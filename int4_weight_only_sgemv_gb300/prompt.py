@@ -189,7 +189,7 @@ def sgemv_prompt_attention(q, k, v, start, out, scale: float, length=None, lse=N
         query = _QUERY.pack(_DTYPE.get(dtype, -1), heads_q, kv_shape[1], dim, n_req, n, 1 if causal else 0, window, scale, 0, q0, q1, k0, k1, v0, v1,
                             o0, o1, q.data_ptr(), k.data_ptr(), v.data_ptr(), start.data_ptr(), 0 if length is None else length.data_ptr(),
                             out.data_ptr(), 0 if lse is None else lse.data_ptr())
-    except struct.error as e:
+    except (struct.error, OverflowError) as e:  # (a scale that is no binary32 is the latter)
         raise ValueError(f"sgemv_prompt_attention: {e}") from None
     code = _lib.sgemv_prompt_attention(query, None if status is None else status.data_ptr(),
                                        _kv._raw_stream(dev) if stream is None else _stream(stream))
