@@ -114,7 +114,7 @@ typedef struct {
  * The same inputs give the same bits.
  * Device-reported: SGEMV_ERR_ARG (a request with start out of order or out of range, or a length outside 0..start[r + 1] - start[r]: its
  * rows are not written, and nobody's where starts out of order make the others overlap to more than n_tokens); SGEMV_ERR_TIMEOUT (a bounded wait for a copy gave up: out is invalid).
- * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (dim; heads_q; strides; n_tokens times heads_q, or n_req, above 2^30),
+ * Errors returned: SGEMV_ERR_ARG, SGEMV_ERR_SHAPE (dim; heads_q; strides; n_tokens times heads_q above 2^30; n_req above 2^26),
  * SGEMV_ERR_ALIGN, SGEMV_ERR_CUDA.
  */
 int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* status_dev, void* stream);

@@ -60,7 +60,8 @@ extern "C" int sgemv_prompt_attention(const sgemv_prompt_query* query, int32_t* 
         return SGEMV_ERR_ARG;
     if (q.dim != 64 && q.dim != 128) return SGEMV_ERR_SHAPE;
     if (q.heads < 1 || q.heads_q < q.heads || q.heads_q % q.heads != 0 || q.heads_q > 16384) return SGEMV_ERR_SHAPE;
-    if (static_cast<int64_t>(q.n_tokens) * q.heads_q > (1 << 30) || q.n_req > (1 << 30)) return SGEMV_ERR_SHAPE;
+    // (A CTA looks for a segment among n_req / 384 requests, some 80 ns each, while others wait for it with a limit of 200 ms: 14 ms at 2^26.)
+    if (static_cast<int64_t>(q.n_tokens) * q.heads_q > (1 << 30) || q.n_req > (1 << 26)) return SGEMV_ERR_SHAPE;
     if (q.n_req == 0 || q.n_tokens == 0) return SGEMV_OK;
     const void* must[] = {q.q_dev, q.k_dev, q.v_dev, q.start_dev, q.out_dev};
     for (const void* x : must)

@@ -1,5 +1,5 @@
-"""Scales that prompt attention refuses, without a GPU: what is no number, and what leaves binary32 in base 2 (every score of 0 would become NaN). The
-addresses are made up: every call is refused, or has nothing to do."""
+"""Scales and numbers of requests that prompt attention refuses, without a GPU: what is no number, what leaves binary32 in base 2 (every score of 0 would
+become NaN), and more requests than a bounded wait allows for. The addresses are made up: every call is refused, or has nothing to do."""
 
 import ctypes
 
@@ -18,8 +18,8 @@ def sg():
     return sg
 
 
-def _call(sg, scale, n_req):
-    q = sg.PromptQuery(0, 8, 2, 64, n_req, 100, 1, 0, scale, 0, 512, 64, 128, 64, 128, 64, 512, 64, A, A + 0x100000, A + 0x200000, A + 0x300000, None,
+def _call(sg, scale, n_req, n_tokens=100):
+    q = sg.PromptQuery(0, 8, 2, 64, n_req, n_tokens, 1, 0, scale, 0, 512, 64, 128, 64, 128, 64, 512, 64, A, A + 0x100000, A + 0x200000, A + 0x300000, None,
                        A + 0x400000, A + 0x500000)
     return sg._lib.sgemv_prompt_attention(ctypes.byref(q), None, None)
 
@@ -48,3 +48,8 @@ def test_the_binding_refuses_what_binary32_does_not_hold(sg, scale, monkeypatch)
     start = torch.zeros(2, dtype=torch.int32).as_subclass(Cuda)
     with pytest.raises(ValueError):
         sg.sgemv_prompt_attention(t[:, :2], t[:, 2:3], t[:, 3:], start, torch.zeros((4, 2, 64), dtype=torch.float16).as_subclass(Cuda), scale)
+
+
+def test_more_requests_than_can_be_looked_through(sg):
+    assert _call(sg, 0.125, (1 << 26) + 1) == _call(sg, 0.125, (1 << 26) + 1, 0) == sg.SGEMV_ERR_SHAPE
+    assert _call(sg, 0.125, 1 << 26, 0) == 0
