@@ -21,9 +21,9 @@
 //
 // What bounds it now: with heads of 128 a key tile takes some 2950 cycles for both row tiles, of which the tensor cores need 2560 (64 a product
 // of P and V, 96 of Q and K, which reads 8 KB of shared memory) and a row tile's chain (softmax 1030, its hand-over 360, products and their latency
-// 1460) is as long. One prompt of 16384 tokens, 8 KV and 32 query heads of 128: 1362 us, 1610 TFLOP/s. With heads of 64 it is the softmax: 1970 cycles a
-// tile, 1024 of them for exponentials alone (70.5 us for 4096 tokens of the same heads). A segment costs 4500 cycles beside its tiles: 16 prompts of up to
-// 2048 tokens take 185 us, 1150 TFLOP/s.
+// 1460) is as long. One prompt of 16384 tokens, 8 KV and 32 query heads of 128: 1362 to 1440 us, 1530 to 1610 TFLOP/s. With heads of 64 it is the chain
+// of a row tile alone: 1970 cycles a tile, with the tensor cores, the exponentials' pipe (1024) and the issue slots at half each (72 us for 4096 tokens of
+// the same heads). A segment costs 4500 cycles beside its tiles: 16 prompts of up to 2048 tokens take 185 to 200 us, 1070 to 1150 TFLOP/s.
 #pragma once
 
 #include <cuda.h>
