@@ -9,7 +9,8 @@
 //
 // The quotients. x has 11 significant bits, a scale 4, a midpoint between two codes 3: a quotient x / scale is a midpoint or at least 2^-11
 // of one away, so that a binary32 quotient which is exact where it has few bits rounds as the true one does. It is formed by a
-// reciprocal and one correction (the remainder is exact), without a division for each element. The same holds for m / 6 and e4m3.
+// reciprocal and one Newton correction of the quotient, q + (x - q s) / s, whose remainder is exact, without a division for each element.
+// The same holds for m / 6 and e4m3.
 #include "fp4_common.cuh"
 
 namespace sgemv {
