@@ -9,9 +9,10 @@ HOST = os.path.join(ROOT, "tests", "host")
 
 
 def _sources():
-    """The repository's CUDA sources (directories that it does not track start with . or _)."""
+    """The repository's CUDA sources (what git ignores left out)."""
+    ignored = {os.path.join(ROOT, line.strip().strip("/")) for line in open(os.path.join(ROOT, ".gitignore")) if line.strip().endswith("/")}
     for at, dirs, files in os.walk(ROOT):
-        dirs[:] = [d for d in dirs if not d.startswith((".", "_")) and d not in ("baseline", "gpurun_out")]
+        dirs[:] = [d for d in dirs if not d.startswith((".", "_")) and os.path.join(at, d) not in ignored]
         for f in files:
             if f.endswith((".cu", ".cuh")):
                 yield os.path.join(at, f)
